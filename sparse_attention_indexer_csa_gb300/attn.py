@@ -1,0 +1,300 @@
+"""ctypes binding of the operators around the indexer (the C ABI of
+``include/csa_attn.h``, exported by ``libcsa_index.so``): the norm and rotation
+of queries and keys, and causal attention over packed sequences.
+
+Argument marshalling only, as in ``abi.py``.  Every helper takes ``stream``
+(default: the current stream of the tensors' device); tensors it allocates are
+recorded on that stream, so they may be dropped while its work is in flight.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import abi
+from .abi import CSA_BF16, CSA_F32, _check, _stream
+
+CSA_F16 = 2
+
+EXPORTED = (
+    "csa_rope_freqs",
+    "csa_norm_rope",
+    "csa_norm_rope_backward",
+    "csa_norm_rope_workspace_size",
+    "csa_attn_forward",
+    "csa_attn_backward",
+    "csa_attn_workspace_size",
+    "csa_attn_abi_version",
+)
+
+_DTYPES = {torch.bfloat16: CSA_BF16, torch.float32: CSA_F32, torch.float16: CSA_F16}
+
+
+class NormRopeProblem(ctypes.Structure):
+    """Mirror of ``csa_norm_rope_problem`` (strides in elements; 0 = contiguous)."""
+
+    _fields_ = [
+        ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("rot", ctypes.c_int32), ("rot_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+    ]
+
+
+class AttnProblem(ctypes.Structure):
+    """Mirror of ``csa_attn_problem`` (strides in elements; 0 = contiguous)."""
+
+    _fields_ = [
+        ("N", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tk", ctypes.c_int32), ("Hq", ctypes.c_int32),
+        ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+        ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+        ("v_stride_t", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+    ]
+
+
+_ready = None
+
+
+def load() -> ctypes.CDLL:
+    """The library with this header's entry points typed (once)."""
+    global _ready
+    lib = abi.load()
+    if _ready is lib:
+        return lib
+    vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    R, A = ctypes.POINTER(NormRopeProblem), ctypes.POINTER(AttnProblem)
+    lib.csa_rope_freqs.argtypes = [ctypes.c_double, i32, vp]
+    lib.csa_norm_rope.argtypes = [R] + [vp] * 9
+    lib.csa_norm_rope_backward.argtypes = [R] + [vp] * 13 + [sz, vp]
+    lib.csa_norm_rope_workspace_size.argtypes = [R]
+    lib.csa_norm_rope_workspace_size.restype = sz
+    lib.csa_attn_forward.argtypes = [A] + [vp] * 9 + [sz, vp]
+    lib.csa_attn_backward.argtypes = [A] + [vp] * 13 + [sz, vp]
+    lib.csa_attn_workspace_size.argtypes = [A, i32]
+    lib.csa_attn_workspace_size.restype = sz
+    for name in ("csa_rope_freqs", "csa_norm_rope", "csa_norm_rope_backward", "csa_attn_forward",
+                 "csa_attn_backward", "csa_attn_abi_version"):
+        getattr(lib, name).restype = i32
+    _ready = lib
+    return lib
+
+
+# ----------------------------------------------------------------------------- argument checks
+def _dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{what} must be bf16, fp16 or fp32, not {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
+
+
+def _want(t: torch.Tensor, what: str, shape, dtype, device, strided: bool = False):
+    """Shape, type, device and layout of one argument."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must live on the GPU")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's tensors on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if strided:
+        if t.numel() and t.shape[-1] != 1 and t.stride(-1) != 1:
+            raise ValueError(f"the innermost dimension of {what} must be contiguous")
+        if any(t.shape[d] > 1 and t.stride(d) == 0 for d in range(t.dim() - 1)):
+            raise ValueError(f"{what} may not repeat memory (stride 0)")
+    elif not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _on(stream, device):
+    """The stream of a call, as a torch stream of `device`."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An uninitialised tensor that `stream` uses: its memory is not given to
+    other work before what `stream` holds at its release has run."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if t.numel() and stream != torch.cuda.current_stream(device):
+        # the allocator's memory may still be read by work of the current stream
+        stream.wait_stream(torch.cuda.current_stream(device))
+        t.record_stream(stream)
+    return t
+
+
+def _strides(t: torch.Tensor):
+    """Token and head strides (0 where the dimension has one entry)."""
+    return [0 if t.shape[d] <= 1 else int(t.stride(d)) for d in range(2)]
+
+
+# ----------------------------------------------------------------------------- norm + rotation
+def rope_freqs(rot: int, theta: float = 10000.0, device=None) -> torch.Tensor:
+    """Turns per position of the rot/2 pairs, theta^(-2i/rot)/(2 pi), as 64-bit
+    fixed-point fractions: int64 [rot/2] (the bits of uint64) on `device`
+    (default: the current GPU).  Made once and kept by the caller."""
+    host = torch.empty(max(rot // 2, 0), dtype=torch.int64)
+    _check("csa_rope_freqs", load().csa_rope_freqs(float(theta), int(rot), ctypes.c_void_p(host.data_ptr())))
+    return host.to(torch.device("cuda", torch.cuda.current_device()) if device is None else device)
+
+
+def make_norm_rope_problem(q, k, q_weight, freqs, eps=1e-6, rot_offset=0, interleaved=False) -> NormRopeProblem:
+    """Problem of q [T,Hq,D] and k [T,Hk,D] (or None); their strides are passed on."""
+    T, Hq, D = q.shape
+    p = NormRopeProblem(T, Hq, 0 if k is None else k.shape[1], D, 2 * freqs.numel(), int(rot_offset),
+                        1 if interleaved else 0, _dtype(q, "q"), _dtype(q_weight, "q_weight"), float(eps))
+    p.q_stride_t, p.q_stride_h = _strides(q)
+    if k is not None:
+        p.k_stride_t, p.k_stride_h = _strides(k)
+    return p
+
+
+def _check_norm_rope(q, k, q_weight, k_weight, positions, freqs):
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    if (k is None) != (k_weight is None):
+        raise ValueError("k and k_weight come together")
+    T, Hq, D = q.shape
+    dev = q.device
+    _want(q, "q", q.shape, q.dtype, dev, True)
+    _want(q_weight, "q_weight", (D,), q_weight.dtype, dev)
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be [T, Hk, D]")
+        _want(k, "k", (T, k.shape[1], D), q.dtype, dev, True)
+        _want(k_weight, "k_weight", (D,), q_weight.dtype, dev)
+    _want(positions, "positions", (T,), torch.int64, dev)
+    _want(freqs, "freqs", (freqs.numel(),), torch.int64, dev)
+    return dev
+
+
+def norm_rope(q, k, q_weight, k_weight, positions, freqs, eps=1e-6, rot_offset=0, interleaved=False, stream=None):
+    """Norm of every head of q [T,Hq,D] and k [T,Hk,D] with the weights [D], and
+    the rotation of 2*len(freqs) of its values from rot_offset on, by
+    positions [T] int64 -> (q_out, k_out), contiguous, in the inputs' type.
+    k and k_weight may be None (k_out is None).  q and k may be views."""
+    dev = _check_norm_rope(q, k, q_weight, k_weight, positions, freqs)
+    p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
+    with torch.cuda.device(dev):
+        s = _on(stream, dev)
+        q_out = _new(q.shape, q.dtype, dev, s)
+        k_out = None if k is None else _new(k.shape, k.dtype, dev, s)
+        _check("csa_norm_rope", load().csa_norm_rope(
+            ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(freqs),
+            _ptr(q_out), _ptr(k_out), _stream(s)))
+    return q_out, k_out
+
+
+def norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs, eps=1e-6, rot_offset=0,
+                       interleaved=False, workspace=None, stream=None):
+    """Gradients of norm_rope for the cotangents dq_out, dk_out (contiguous) ->
+    (dq, dk, dq_weight, dk_weight): dq, dk contiguous in the inputs' type, the
+    weights' gradients fp32 [D].  Without k: dk_out is None, and so are dk and
+    dk_weight."""
+    dev = _check_norm_rope(q, k, q_weight, k_weight, positions, freqs)
+    _want(dq_out, "dq_out", q.shape, q.dtype, dev)
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out and k come together")
+    if k is not None:
+        _want(dk_out, "dk_out", k.shape, q.dtype, dev)
+    p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
+    with torch.cuda.device(dev):
+        s = _on(stream, dev)
+        D = q.shape[2]
+        dq, dqw = _new(q.shape, q.dtype, dev, s), _new((D,), torch.float32, dev, s)
+        dk = dkw = None
+        if k is not None:
+            dk, dkw = _new(k.shape, k.dtype, dev, s), _new((D,), torch.float32, dev, s)
+        if workspace is None:
+            workspace = _new((int(load().csa_norm_rope_workspace_size(ctypes.byref(p))),), torch.uint8, dev, s)
+        _check("csa_norm_rope_backward", load().csa_norm_rope_backward(
+            ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+            _ptr(positions), _ptr(freqs), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(s)))
+    return dq, dk, dqw, dkw
+
+
+# ----------------------------------------------------------------------------- attention
+def make_attn_problem(q, k, v, cu_q, scale, causal=True) -> AttnProblem:
+    """Problem of q [Tq,Hq,D], k and v [Tk,Hk,D] and len(cu_q)-1 packed
+    sequences; the tensors' strides are passed on."""
+    Tq, Hq, D = q.shape
+    p = AttnProblem(max(0, cu_q.numel() - 1), Tq, k.shape[0], Hq, k.shape[1], D, _dtype(q, "q"), 1 if causal else 0,
+                    float(scale))
+    p.q_stride_t, p.q_stride_h = _strides(q)
+    p.k_stride_t, p.k_stride_h = _strides(k)
+    p.v_stride_t, p.v_stride_h = _strides(v)
+    return p
+
+
+def attn_workspace_size(p: AttnProblem, which: int) -> int:
+    return int(load().csa_attn_workspace_size(ctypes.byref(p), which))
+
+
+def _check_attn(q, k, v, cu_q, cu_k, k_len):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [Tq, Hq, D], k and v [Tk, Hk, D]")
+    dev = q.device
+    _want(q, "q", q.shape, q.dtype, dev, True)
+    _want(k, "k", (k.shape[0], k.shape[1], q.shape[2]), q.dtype, dev, True)
+    _want(v, "v", k.shape, q.dtype, dev, True)
+    n = cu_q.numel()
+    if n < 1:
+        raise ValueError("cu_q and cu_k hold one entry more than there are sequences")
+    _want(cu_q, "cu_q", (n,), torch.int32, dev)
+    _want(cu_k, "cu_k", (n,), torch.int32, dev)
+    if k_len is not None:
+        _want(k_len, "k_len", (n - 1,), torch.int32, dev)
+    return dev
+
+
+def attn_forward(q, k, v, cu_q, cu_k, scale, causal=True, k_len=None, workspace=None, stream=None):
+    """Attention of packed sequences: q [Tq,Hq,D], k and v [Tk,Hk,D] (views
+    allowed), cu_q and cu_k [N+1] int32 -> (out [Tq,Hq,D] in q's type,
+    lse [Tq,Hq] fp32).  With k_len [N] int32 only the first k_len[i] keys of
+    sequence i count: a cache [N,W,Hk,D] is passed as its view [N*W,Hk,D] with
+    cu_k = arange(N+1)*W.  One query row per sequence is the decode step."""
+    dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
+    p = make_attn_problem(q, k, v, cu_q, scale, causal)
+    with torch.cuda.device(dev):
+        s = _on(stream, dev)
+        out = _new(q.shape, q.dtype, dev, s)
+        lse = _new(q.shape[:2], torch.float32, dev, s)
+        if workspace is None:
+            workspace = _new((attn_workspace_size(p, 0),), torch.uint8, dev, s)
+        _check("csa_attn_forward", load().csa_attn_forward(
+            ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(out), _ptr(lse),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(s)))
+    return out, lse
+
+
+def attn_backward(dout, q, k, v, out, lse, cu_q, cu_k, scale, causal=True, k_len=None, workspace=None, stream=None):
+    """Gradients of attn_forward for the cotangent dout of out (contiguous),
+    from the forward's out and lse -> (dq, dk, dv), contiguous, in q's type."""
+    dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
+    _want(dout, "dout", q.shape, q.dtype, dev)
+    _want(out, "out", q.shape, q.dtype, dev)
+    _want(lse, "lse", q.shape[:2], torch.float32, dev)
+    p = make_attn_problem(q, k, v, cu_q, scale, causal)
+    with torch.cuda.device(dev):
+        s = _on(stream, dev)
+        dq = _new(q.shape, q.dtype, dev, s)
+        dk, dv = _new(k.shape, k.dtype, dev, s), _new(v.shape, v.dtype, dev, s)
+        if workspace is None:
+            workspace = _new((attn_workspace_size(p, 1),), torch.uint8, dev, s)
+        _check("csa_attn_backward", load().csa_attn_backward(
+            ctypes.byref(p), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
+            _ptr(k_len), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(s)))
+    return dq, dk, dv

@@ -1,0 +1,99 @@
+// csa_attn_internal.h -- host-side interface between the C ABI of csa_attn.h
+// (csa_attn_api.cu) and the translation units that launch the kernels.
+#pragma once
+
+#include "csa_attn.h"
+#include "csa_internal.h"
+
+namespace csa {
+
+// ----------------------------------------------------------------- norm + rotation
+struct NormRopeParams {
+  long long rows;  // T * (Hq + Hk)
+  int T, Hq, Hk, D, rot, off, w_dtype;
+  float eps, inv_d;
+  const void *q, *k, *qw, *kw;
+  long long q_st, q_sh, k_st, k_sh;  // element strides
+  const int64_t* pos;
+  const uint64_t* freqs;
+  void *yq, *yk;              // outputs (forward) or gradients of q and k (backward)
+  const void *gq, *gk;        // cotangents (backward)
+  float *dqw, *dkw;           // gradients of the weights (backward)
+  float* part;                // partial sums of them, [blocks][2][D] (backward)
+};
+constexpr int kNormRopeBlocks = 152 * 4;  // blocks (and partial sums) of the backward at most
+cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);
+cudaError_t launch_norm_rope_backward(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);
+
+// ----------------------------------------------------------------- attention
+struct AttnParams {
+  int N, Tq, Tk, Hq, Hk, g, D;  // g = Hq / Hk
+  int causal;
+  float scale;
+  const void *q, *k, *v;
+  long long q_st, q_sh, k_st, k_sh, v_st, v_sh;
+  const int32_t *cu_q, *cu_k, *k_len;
+  void* out;
+  float* lse;
+  // backward
+  const void* dout;
+  float* delta;  // [Tq,Hq]: sum over D of dout * out
+  void *dq, *dk, *dv;
+};
+cudaError_t launch_attn_forward(const AttnParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_backward(const AttnParams& p, int dtype, cudaStream_t stream);
+cudaError_t take_status_attn(uint32_t* out, cudaStream_t stream);
+
+// ----------------------------------------------------------------- packed sequences (device)
+// Extents of one sequence, clamped to the tensors: query rows q0..q1-1, keys
+// k0..k0+lk-1.  A row r (counted from q0) sees the keys j < see(r).
+struct SeqExt {
+  int q0, q1, k0, lk;
+};
+
+__device__ __forceinline__ SeqExt seq_extent(const AttnParams& p, int i) {
+  const int a = p.cu_q[i], b = p.cu_q[i + 1], c = p.cu_k[i], d = p.cu_k[i + 1];
+  SeqExt s;
+  s.q0 = min(max(a, 0), p.Tq);
+  s.q1 = min(max(b, s.q0), p.Tq);
+  s.k0 = min(max(c, 0), p.Tk);
+  const int k1 = min(max(d, s.k0), p.Tk);
+  s.lk = k1 - s.k0;
+  bool bad = a != s.q0 || b != s.q1 || c != s.k0 || d != k1;
+  if (p.k_len != nullptr) {
+    const int n = p.k_len[i], m = min(max(n, 0), s.lk);
+    bad |= n != m;
+    s.lk = m;
+  }
+  if (bad) record_error(kErrDevice);
+  return s;
+}
+
+// Looks over every sequence's entries once (one block of a launch): what is
+// out of order or range is recorded even where no row or key meets it.
+__device__ __forceinline__ void check_sequences(const AttnParams& p) {
+  for (int i = threadIdx.x; i < p.N; i += blockDim.x) seq_extent(p, i);
+}
+
+// Number of keys row r (0-based in its sequence) sees.
+__device__ __forceinline__ int keys_seen(const AttnParams& p, const SeqExt& s, int r) {
+  if (!p.causal) return s.lk;
+  return max(0, min(s.lk, r + 1 + s.lk - (s.q1 - s.q0)));
+}
+
+// Sequence holding row t: the last i with cu[i] <= t (n sequences), or -1
+// for a row outside all of them.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
+  if (n == 0 || t < cu[0] || t >= cu[n]) return -1;
+  int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace csa
