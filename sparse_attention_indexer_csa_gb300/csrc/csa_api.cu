@@ -598,14 +598,15 @@ csa_status csa_index_gather(const csa_problem* p, const void* k, const int32_t* 
 }
 
 csa_status csa_index_device_status(void* stream) {
-  uint32_t a = 0, b = 0, c = 0, d = 0, e = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (take_status_prefill(&a, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_other(&b, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_gather(&c, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_backward(&d, s) != cudaSuccess) return CSA_ERR_CUDA;
-  if (take_status_attn(&e, s) != cudaSuccess) return CSA_ERR_CUDA;
-  const uint32_t v = a | b | c | d | e;
+  if (take_status_attn_fwd(&e, s) != cudaSuccess) return CSA_ERR_CUDA;
+  if (take_status_attn_bwd(&f, s) != cudaSuccess) return CSA_ERR_CUDA;
+  const uint32_t v = a | b | c | d | e | f;
   if (v & kErrTimeout) return CSA_ERR_TIMEOUT;
   if (v != 0u) return CSA_ERR_DEVICE;
   return CSA_OK;

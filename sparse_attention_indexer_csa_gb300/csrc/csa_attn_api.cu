@@ -91,6 +91,7 @@ bool attn_supported(const csa_attn_problem* p) {
   if (p->D != 64 && p->D != 128) return false;
   if (p->dtype != CSA_BF16 && p->dtype != CSA_F16) return false;
   if (p->Hq / p->Hk > 128 || p->Hq > 65535) return false;
+  if (static_cast<double>(p->q_stride_h) * (p->Hq / p->Hk) > static_cast<double>(1ll << 38)) return false;
   const double rows = std::max(static_cast<double>(p->Tq) * p->Hq, static_cast<double>(p->Tk) * p->Hk);
   return rows < 8.0e9 && p->N < (1 << 30);
 }
@@ -132,7 +133,10 @@ csa_status check_attn_inputs(const csa_attn_problem* p, const void* q, const voi
 size_t attn_workspace_bytes(const csa_attn_problem* p, int which) {
   if (check_attn(p) != CSA_OK) return 0;
   if (which == 1) return (static_cast<size_t>(p->Tq) * p->Hq * 4 + 255) / 256 * 256;
-  return 0;
+  if (which != 0 || p->Tq == 0 || !attn_supported(p)) return 0;
+  // split keys: fp32 outputs and lse of each share
+  const AttnPlan plan = attn_plan(p->N, p->Tq, p->Tk, p->Hk, p->Hq / p->Hk);
+  return plan.n_split > 1 ? static_cast<size_t>(plan.n_split) * p->Tq * p->Hq * (p->D + 1) * 4 : 0;
 }
 
 }  // namespace
@@ -223,7 +227,7 @@ csa_status csa_attn_forward(const csa_attn_problem* p, const void* q, const void
   AttnParams a = attn_params(p, q, k, v, cu_q, cu_k, k_len);
   a.out = out;
   a.lse = lse;
-  if (launch_attn_forward(a, p->dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSA_ERR_CUDA;
+  if (launch_attn_forward(a, p->dtype, workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSA_ERR_CUDA;
   return CSA_OK;
 }
 

@@ -1,18 +1,17 @@
-// csa_attn.cu -- causal attention over packed sequences: forward and
-// gradients, one warp per query row and head (forward, dq) or per key and key
-// head (dk, dv).
+// csa_attn_bwd.cu -- gradients of causal attention over packed sequences, one
+// warp per query row and head (dq) or per key and key head (dk, dv).
 //
-//   s_j = scale q.k_j, out = sum_j p_j v_j with p = softmax(s), lse = log sum exp(s)
 //   delta = dout.out;  p_j = exp(s_j - lse);  ds_j = p_j (dout.v_j - delta)
 //   dq = scale sum_j ds_j k_j;  dk_j = scale sum_rows ds_j q;  dv_j = sum_rows p_j dout
 //
 // A warp takes 32 keys (rows) at a time: lane j forms the dot products of
 // key (row) j, then every lane adds the 32 weighted rows into its own D/32
-// values.  The softmax runs over the tiles with a running maximum and sum.
+// values.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "csa_attn_internal.h"
+#include "csa_attn_tiles.cuh"
 
 namespace csa {
 namespace {
@@ -30,11 +29,6 @@ __device__ __forceinline__ __half from_f<__half>(float x) {
   return __float2half(x);
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -49,43 +43,6 @@ __device__ __forceinline__ float dot(const X* a, const float* b) {
 #pragma unroll 16
   for (int d = 0; d < D; ++d) s = fmaf(to_f(a[d]), b[d], s);
   return s;
-}
-
-template <typename X, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_fwd_kernel(const AttnParams p) {
-  __shared__ float qs[kWarps][D];
-  if (blockIdx.x == 0) check_sequences(p);
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (item >= static_cast<long long>(p.Tq) * p.Hq) return;
-  const int t = static_cast<int>(item / p.Hq), h = static_cast<int>(item % p.Hq), hk = h / p.g;
-  const X* q = static_cast<const X*>(p.q) + t * p.q_st + h * p.q_sh;
-  for (int d = lane; d < D; d += 32) qs[w][d] = to_f(q[d]);
-  __syncwarp();
-  float acc[D / 32] = {}, m = -INFINITY, l = 0.f;
-  const int i = find_seq(p.cu_q, p.N, t);
-  if (i >= 0) {
-    const SeqExt e = seq_extent(p, i);
-    const int see = keys_seen(p, e, t - e.q0);
-    const X* k = static_cast<const X*>(p.k) + e.k0 * p.k_st + hk * p.k_sh;
-    const X* v = static_cast<const X*>(p.v) + e.k0 * p.v_st + hk * p.v_sh;
-    for (int j0 = 0; j0 < see; j0 += 32) {
-      const int j = j0 + lane;
-      const float s = j < see ? dot<X, D>(k + j * p.k_st, qs[w]) * p.scale : -INFINITY;
-      const float mn = fmaxf(m, warp_max(s)), ms = mn == -INFINITY ? 0.f : mn;
-      const float pj = expf(s - ms), f = expf(m - ms);
-      m = mn;
-      l = l * f + warp_sum(pj);
-      for (int d = 0; d < D / 32; ++d) acc[d] *= f;
-      for (int u = 0; u < min(32, see - j0); ++u) {
-        const float pu = __shfl_sync(0xffffffffu, pj, u);
-        for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(pu, to_f(v[(j0 + u) * p.v_st + d * 32 + lane]), acc[d]);
-      }
-    }
-  }
-  X* out = static_cast<X*>(p.out) + item * D;
-  for (int d = 0; d < D / 32; ++d) out[d * 32 + lane] = from_f<X>(l == 0.f ? 0.f : acc[d] / l);
-  if (lane == 0) p.lse[item] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 template <typename X, int D>
@@ -188,12 +145,6 @@ __global__ void __launch_bounds__(kWarps * 32) attn_dkv_kernel(const AttnParams 
 unsigned blocks_of(long long items) { return static_cast<unsigned>((items + kWarps - 1) / kWarps); }
 
 template <typename X, int D>
-cudaError_t fwd(const AttnParams& p, cudaStream_t s) {
-  if (p.Tq > 0)
-    attn_fwd_kernel<X, D><<<blocks_of(static_cast<long long>(p.Tq) * p.Hq), kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
-}
-template <typename X, int D>
 cudaError_t bwd(const AttnParams& p, cudaStream_t s) {
   if (p.Tq > 0) {
     const unsigned n = blocks_of(static_cast<long long>(p.Tq) * p.Hq);
@@ -206,22 +157,11 @@ cudaError_t bwd(const AttnParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attn_forward(const AttnParams& p, int dtype, cudaStream_t s) {
-  if (dtype == CSA_BF16) return p.D == 128 ? fwd<__nv_bfloat16, 128>(p, s) : fwd<__nv_bfloat16, 64>(p, s);
-  return p.D == 128 ? fwd<__half, 128>(p, s) : fwd<__half, 64>(p, s);
-}
 cudaError_t launch_attn_backward(const AttnParams& p, int dtype, cudaStream_t s) {
   if (dtype == CSA_BF16) return p.D == 128 ? bwd<__nv_bfloat16, 128>(p, s) : bwd<__nv_bfloat16, 64>(p, s);
   return p.D == 128 ? bwd<__half, 128>(p, s) : bwd<__half, 64>(p, s);
 }
 
-cudaError_t take_status_attn(uint32_t* out, cudaStream_t stream) {
-  uint32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_status, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-  return e;
-}
+cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
 
 }  // namespace csa

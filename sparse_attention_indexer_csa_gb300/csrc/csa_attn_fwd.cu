@@ -1,0 +1,438 @@
+// csa_attn_fwd.cu -- causal attention over packed sequences on the tensor
+// cores: forward, and the join of split keys.
+//
+//   s_j = scale q.k_j over the keys a row sees, out = sum_j p_j v_j with
+//   p = softmax(s), lse = log sum_j exp(s_j).
+//
+// A CTA takes TILES blocks of 128 query rows of one sequence and one key head
+// and walks the keys in tiles of 128, in one pass with a running reference m
+// and sum l:
+//   S = Q . K^T     (A = q block, B = k tile, both in shared memory, to TMEM)
+//   P = 2^(c (S - m)) in the storage type, c = scale log2(e), written over S
+//   O += P . V      (A = P in TMEM, B = v tile read MN-major, O in TMEM)
+// and at the end out = O / l, lse = scale m + ln l.
+//
+// Rows: the g = Hq/Hk query heads that share a key head are rows of the same
+// block (row = token * g + head), so a block holds 128/g consecutive tokens,
+// K and V are read once per group, and one token of g heads (decoding) is a
+// block like any other.
+//
+// m is not the running maximum but the maximum when it was last raised: it is
+// raised, and O and l rescaled, only when the maximum has grown by more than
+// 8 in the exponent.  P then stays below 2^8, in range of fp16 too, and the
+// quotient O / l is the same; the rescaling of O in TMEM, 128 values a row,
+// nearly never runs after the first tiles.
+//
+// Roles (TILES = 2: 12 warps, one CTA per SM; TILES = 1: 6 warps, two CTAs
+// per SM):
+//   warps 0..4 TILES-1  softmax: one thread per row, all 128 scores of a tile
+//                       in registers; then the division and the stores
+//   next warp           issuer of the products, one thread
+//   next warp           TMA producer, one thread
+// With two blocks the tensor cores form S and O of one while the softmax of
+// the other runs; TMEM holds S0 S1 O0 O1 (512 columns).  With one block the
+// second CTA on the SM does the same.
+//
+// Keys may be split over gridDim.z CTAs (few rows, long caches): each writes
+// its normalised O and lse in fp32, and a second kernel joins them.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "csa_attn_internal.h"
+#include "csa_attn_tiles.cuh"
+
+namespace csa {
+namespace {
+
+template <int D, int TILES>
+struct FwdCfg {
+  static constexpr uint32_t kTile = kChunkBytes * (D / 64);  // 128 rows x D, 64 columns per 16 KB chunk
+  static constexpr int kStages = TILES == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+  static constexpr int kWarps = TILES == 2 ? 12 : 6;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kMmaWarp = 4 * TILES, kTmaWarp = kMmaWarp + 1;
+  static constexpr uint32_t kOffQ = 0, kOffKv = kOffQ + TILES * kTile, kOffBar = kOffKv + kStages * kTile;
+  // barriers: q full [TILES], kv full / empty [stages], s full, p full, o full [TILES], done
+  static constexpr int kBarQ = 0, kBarFull = TILES, kBarEmpty = kBarFull + kStages, kBarS = kBarEmpty + kStages,
+                       kBarP = kBarS + TILES, kBarO = kBarP + TILES, kBarDone = kBarO + TILES,
+                       kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 64 + 1024;
+  static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
+  static constexpr uint32_t kO = 128 * TILES;  // first column of O
+};
+static_assert(FwdCfg<128, 2>::kSmem <= 227 * 1024 && FwdCfg<64, 2>::kSmem <= 227 * 1024, "one CTA per SM");
+static_assert(2 * FwdCfg<128, 1>::kSmem <= 226 * 1024 && 2 * FwdCfg<64, 1>::kSmem <= 226 * 1024, "two CTAs per SM");
+
+struct FwdArgs {
+  AttnParams a;
+  int tq;        // tokens per block of 128 rows
+  int nb;        // ceil(Tq / (TILES * tq))
+  int n_split;
+  float c;       // scale * log2(e)
+  float lag;     // 8 / c: how far the reference may fall behind the maximum
+  float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
+  float* part_lse;  // [n_split][Tq * Hq]
+  unsigned long long wait_ns;
+};
+
+template <typename X, int D, int TILES>
+__global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const FwdArgs f) {
+  using C = FwdCfg<D, TILES>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
+  RowItem* item = reinterpret_cast<RowItem*>(base + C::kOffMisc + 16);
+  const AttnParams& a = f.a;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+  const int hk = static_cast<int>(blockIdx.x % a.Hk);
+
+  if (warp == C::kMmaWarp) {
+    // blocks are taken from the last one on: the rows that see most keys first
+    const RowItem it = find_row_item(a, TILES * f.tq, f.nb, f.nb + a.N - static_cast<int>(blockIdx.x / a.Hk));
+    if (lane == 0) *item = it;
+    if (blockIdx.x == 0 && blockIdx.z == 0)
+      for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < TILES; ++i) {
+      mbar_init(bars + C::kBarQ + i, 1);
+      mbar_init(bars + C::kBarS + i, 1);
+      mbar_init(bars + C::kBarP + i, 4);
+      mbar_init(bars + C::kBarO + i, 1);
+    }
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(bars + C::kBarFull + i, 1);
+      mbar_init(bars + C::kBarEmpty + i, 1);
+    }
+    mbar_init(bars + C::kBarDone, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const RowItem it = *item;
+  if (it.t0 >= it.t1) return;  // no row here (two borders fall together)
+
+  // key tiles of this CTA's share: block w walks lo .. hi[w]-1
+  int n_tok[TILES], hi[TILES], lo = 0, top = 0;
+#pragma unroll
+  for (int w = 0; w < TILES; ++w) {
+    n_tok[w] = min(f.tq, max(0, it.t1 - it.t0 - w * f.tq));
+    const int see = n_tok[w] > 0 ? keys_seen(a, it.s, it.t0 + w * f.tq + n_tok[w] - 1 - it.s.q0) : 0;
+    hi[w] = (see + 127) >> 7;
+    top = max(top, hi[w]);
+  }
+  if (f.n_split > 1) {
+    const int share = (top + f.n_split - 1) / f.n_split;
+    lo = static_cast<int>(blockIdx.z) * share;
+#pragma unroll
+    for (int w = 0; w < TILES; ++w) hi[w] = max(lo, min(hi[w], lo + share));
+    top = max(lo, min(top, lo + share));
+  }
+  const bool work = top > lo;
+
+  if (work && warp == C::kMmaWarp) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = work ? *tmem_slot : 0u;
+  const WaitCtl ctl{abort_flag, f.wait_ns};
+
+  if (warp == C::kTmaWarp) {
+    reg_shrink<TILES == 2>();
+    if (work && lane == 0) {  // ------------------------------------------- TMA producer
+      const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
+      for (int w = 0; w < TILES; ++w) {
+        if (hi[w] <= lo) continue;
+        mbar_arrive_expect_tx(bars + C::kBarQ + w, static_cast<uint32_t>(f.tq * a.g) * 128u * (D / 64));
+        for (int ch = 0; ch < D / 64; ++ch)
+          tma_load_4d_hint(base + C::kOffQ + w * C::kTile + ch * kChunkBytes, &tmap_q, bars + C::kBarQ + w, ch * 64, 0,
+                           it.t0 + w * f.tq, hk, q_pol);
+      }
+      uint32_t n = 0;
+      for (int j = lo; j < top; ++j)
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const uint32_t st = n % C::kStages;
+          if (!mbar_wait(bars + C::kBarEmpty + st, ((n / C::kStages) & 1u) ^ 1u, ctl)) continue;
+          mbar_arrive_expect_tx(bars + C::kBarFull + st, C::kTile);
+          for (int ch = 0; ch < D / 64; ++ch)
+            tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k,
+                             bars + C::kBarFull + st, ch * 64, it.s.k0 + j * 128, hk, kv_pol);
+        }
+      // no copy is in flight when the CTA ends: the last use of each stage has landed
+      volatile uint32_t dummy = 0;
+      const WaitCtl dctl{&dummy, ctl.limit_ns};
+      if (*abort_flag == 0u)
+        for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < n; ++i)
+          mbar_wait(bars + C::kBarFull + (n - 1 - i) % C::kStages, ((n - 1 - i) / C::kStages) & 1u, dctl);
+    }
+  } else if (warp == C::kMmaWarp) {
+    reg_shrink<TILES == 2>();
+    if (work && lane == 0) {  // ------------------------------------------- issuer of the products
+      const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
+      const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffKv), 128);
+      const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffKv), kChunkBytes, 1024u);
+      constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false), kIdO = idesc_f16<X>(128, D, true);
+      bool alive = true;
+      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
+      auto scores = [&](int w, uint32_t st) {  // S_w = Q_w . K^T
+        tc_fence_after();
+        if (alive) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
+            umma_bf16(tmem + w * 128, qd + static_cast<uint64_t>(w * (C::kTile >> 4)) + o,
+                      kd + static_cast<uint64_t>(st * (C::kTile >> 4)) + o, kIdS, ks != 0 ? 1u : 0u);
+          }
+        }
+        umma_commit(bars + C::kBarS + w);
+      };
+      uint32_t n = 0;  // index of the key tile in the ring (the value tile is n + 1)
+      auto full = [&](uint32_t i) { wait(C::kBarFull + static_cast<int>(i % C::kStages), (i / C::kStages) & 1u); };
+      full(0);
+      for (int w = 0; w < TILES; ++w)
+        if (hi[w] > lo) {
+          wait(C::kBarQ + w, 0u);
+          scores(w, 0);
+        }
+      umma_commit(bars + C::kBarEmpty + 0);
+      for (int j = lo; j < top; ++j, n += 2) {
+        const uint32_t sv = (n + 1) % C::kStages, sk = (n + 2) % C::kStages;
+        full(n + 1);
+        bool have_k = false;
+        for (int w = 0; w < TILES; ++w) {
+          if (j >= hi[w]) continue;
+          wait(C::kBarP + w, static_cast<uint32_t>(j - lo) & 1u);
+          tc_fence_after();
+          if (alive) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_bf16_tmem_a(tmem + C::kO + w * 128, tmem + w * 128 + 8u * ks,
+                               vd + static_cast<uint64_t>(sv * (C::kTile >> 4)) + static_cast<uint64_t>(128 * ks), kIdO,
+                               (j != lo || ks != 0) ? 1u : 0u);
+          }
+          if (j + 1 < hi[w]) {
+            if (!have_k) full(n + 2);
+            have_k = true;
+            scores(w, sk);
+          } else {
+            umma_commit(bars + C::kBarO + w);
+          }
+        }
+        umma_commit(bars + C::kBarEmpty + sv);
+        if (j + 1 < top) umma_commit(bars + C::kBarEmpty + sk);
+      }
+      umma_commit(bars + C::kBarDone);
+      volatile uint32_t dummy = 0;
+      const WaitCtl dctl{&dummy, ctl.limit_ns};
+      mbar_wait(bars + C::kBarDone, 0u, dctl);
+    }
+  } else if (warp < 4 * TILES) {  // ----------------------------------------- softmax, output
+    reg_grow<TILES == 2>();
+    const int w = warp >> 2, row = (warp & 3) * 32 + static_cast<int>(lane);
+    const int tok = row / a.g, head = row - tok * a.g;
+    const bool row_ok = tok < (w == 0 ? n_tok[0] : n_tok[TILES - 1]);
+    const int my_hi = w == 0 ? hi[0] : hi[TILES - 1], lo_hi = hi[0];
+    const int t = it.t0 + w * f.tq + tok;
+    const int see = row_ok ? keys_seen(a, it.s, t - it.s.q0) : 0;
+    // every row of the block sees the keys below this
+    const int see_all = my_hi > lo ? keys_seen(a, it.s, it.t0 + w * f.tq - it.s.q0) : 0;
+    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 128;
+    const uint32_t to = ts + (C::kO - w * 128) + w * 128;
+    const float c = f.c;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = lo; j < my_hi; ++j) {
+      ok = ok && mbar_wait(bars + C::kBarS + w, static_cast<uint32_t>(j - lo) & 1u, ctl);
+      tc_fence_after();
+      float s[4][32];
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_wait32(s[i]);
+        if ((j + 1) * 128 > see_all) {
+          const int lim = see - j * 128;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
+        }
+        const float mt = row_max(s);
+        if (j == lo) {
+          m = mt;
+        } else if (__any_sync(0xffffffffu, mt > m + f.lag)) {
+          // the former tiles' product with V has completed: its commit preceded this tile's scores
+          const float mn = fmaxf(m, mt);
+          const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
+          m = mn;
+          l *= r;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        const float2 c2 = make_float2(c, c), b2 = make_float2(-ms * c, -ms * c);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float2 x = ffma2(make_float2(s[i][2 * u], s[i][2 * u + 1]), c2, b2);
+            const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum[u & 1] = fadd2(sum[u & 1], p);
+            pk[u] = pack_pair<X>(p.x, p.y);
+          }
+          tmem_st16(ts + 16 * i, pk);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_wait_st();
+        if ((j + 1) * 128 > it.s.lk && (w == 0 || j >= lo_hi)) {
+          // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
+          const uint32_t nv = 2u * static_cast<uint32_t>(j - lo) + 1u, sv = nv % C::kStages;
+          if (mbar_wait(bars + C::kBarFull + sv, (nv / C::kStages) & 1u, ctl))
+            clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, it.s.lk - j * 128, threadIdx.x & 127, 128);
+          fence_proxy_async_shared();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarP + w);
+    }
+    // ------------------------------------------------------------------ output
+    const bool any = my_hi > lo;
+    if (any) {
+      ok = ok && mbar_wait(bars + C::kBarO + w, 0u, ctl);
+      tc_fence_after();
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const long long at = static_cast<long long>(t) * a.Hq + hk * a.g + head;
+    const float lse = l > 0.f || l != l ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      float o[32];
+      if (any && ok) {
+        tmem_ld32_start(to + 32 * i, o);
+        tmem_wait32(o);
+      }
+      if (!row_ok) continue;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) o[u] = any && ok && inv != 0.f ? o[u] * inv : 0.f;
+      if (f.n_split > 1) {
+        float4* dst = reinterpret_cast<float4*>(
+            f.part_o + (static_cast<long long>(blockIdx.z) * a.Tq * a.Hq + at) * D + 32 * i);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<X*>(a.out) + at * D + 32 * i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          dst[u] = make_uint4(pack_pair<X>(o[8 * u], o[8 * u + 1]), pack_pair<X>(o[8 * u + 2], o[8 * u + 3]),
+                              pack_pair<X>(o[8 * u + 4], o[8 * u + 5]), pack_pair<X>(o[8 * u + 6], o[8 * u + 7]));
+      }
+    }
+    if (row_ok) {
+      if (f.n_split > 1)
+        f.part_lse[static_cast<long long>(blockIdx.z) * a.Tq * a.Hq + at] = lse;
+      else
+        a.lse[at] = lse;
+    }
+  } else {
+    reg_shrink<TILES == 2>();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (work && warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+// out = sum_z w_z O_z / sum_z w_z with w_z = exp(lse_z - max lse): D/4 threads
+// per row and head, four values each.  Bytes: n_split (D + 1) fp32 read per
+// row and head.
+template <typename X, int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams a, const float* part_o, const float* part_lse,
+                                                       int n_split) {
+  constexpr int PER = 256 / (D / 4);
+  const long long rows = static_cast<long long>(a.Tq) * a.Hq;
+  const long long r = static_cast<long long>(blockIdx.x) * PER + threadIdx.x / (D / 4);
+  const int l = threadIdx.x % (D / 4);
+  if (r >= rows) return;
+  float m = -INFINITY;
+  for (int z = 0; z < n_split; ++z) m = fmaxf(m, part_lse[z * rows + r]);
+  const float ms = m == -INFINITY ? 0.f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int z = 0; z < n_split; ++z) {
+    const float lz = part_lse[z * rows + r];
+    if (lz == -INFINITY) continue;
+    const float w = exp2_approx((lz - ms) * 1.4426950408889634f);
+    const float4 o = reinterpret_cast<const float4*>(part_o + (z * rows + r) * D)[l];
+    sum += w;
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2 u;
+  u.x = pack_pair<X>(acc.x * inv, acc.y * inv);
+  u.y = pack_pair<X>(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(static_cast<X*>(a.out) + r * D)[l] = u;
+  if (l == 0) a.lse[r] = sum == 0.f ? -INFINITY : ms + logf(sum);
+}
+
+template <typename X, int D, int TILES>
+cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t stream) {
+  using C = FwdCfg<D, TILES>;
+  CUtensorMap tq, tk, tv;
+  FwdArgs f;
+  f.a = p;
+  f.tq = 128 / p.g;
+  f.nb = static_cast<int>((static_cast<long long>(p.Tq) + TILES * f.tq - 1) / (TILES * f.tq));
+  f.n_split = n_split;
+  f.c = p.scale * 1.4426950408889634f;
+  f.lag = 8.f / f.c;
+  f.part_o = static_cast<float*>(workspace);
+  f.part_lse = f.part_o + static_cast<long long>(n_split) * p.Tq * p.Hq * D;
+  f.wait_ns = kAttnWaitNs;
+  if (!make_rows_map(&tq, p, p.q, p.q_st, p.q_sh, f.tq) || !make_keys_map(&tk, p, p.k, p.k_st, p.k_sh) ||
+      !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh))
+    return cudaErrorInvalidValue;
+  cudaError_t e = smem_limit_once<attn_fwd_kernel<X, D, TILES>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  attn_fwd_kernel<X, D, TILES>
+      <<<dim3(static_cast<unsigned>(grid), 1, n_split), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+  if ((e = cudaGetLastError()) != cudaSuccess || n_split == 1) return e;
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+  constexpr int PER = 256 / (D / 4);
+  attn_join_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER), 256, 0, stream>>>(p, f.part_o, f.part_lse,
+                                                                                          n_split);
+  return cudaGetLastError();
+}
+
+template <typename X>
+cudaError_t by_size(const AttnParams& p, const AttnPlan& plan, void* ws, cudaStream_t s) {
+  if (p.D == 128)
+    return plan.tiles == 2 ? run<X, 128, 2>(p, plan.n_split, ws, s) : run<X, 128, 1>(p, plan.n_split, ws, s);
+  return plan.tiles == 2 ? run<X, 64, 2>(p, plan.n_split, ws, s) : run<X, 64, 1>(p, plan.n_split, ws, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t s) {
+  const AttnPlan plan = attn_plan(p.N, p.Tq, p.Tk, p.Hk, p.g);
+  return dtype == CSA_BF16 ? by_size<__nv_bfloat16>(p, plan, workspace, s) : by_size<__half>(p, plan, workspace, s);
+}
+
+cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
+
+}  // namespace csa

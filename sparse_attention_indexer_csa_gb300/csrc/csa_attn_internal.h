@@ -40,9 +40,32 @@ struct AttnParams {
   float* delta;  // [Tq,Hq]: sum over D of dout * out
   void *dq, *dk, *dv;
 };
-cudaError_t launch_attn_forward(const AttnParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_backward(const AttnParams& p, int dtype, cudaStream_t stream);
-cudaError_t take_status_attn(uint32_t* out, cudaStream_t stream);
+cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream);
+cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream);
+
+// How the forward cuts its work, from the sizes the host knows (the lengths
+// stand on the device).
+struct AttnPlan {
+  int tiles;    // blocks of 128 rows per CTA (2: one CTA per SM, 1: two)
+  int n_split;  // CTAs that share the keys of a block
+};
+inline AttnPlan attn_plan(int N, int Tq, int Tk, int Hk, int g) {
+  const int tok = 128 / g;
+  const long long seqs = std::max(1, std::min(N, Tq));
+  AttnPlan p;
+  // sequences whose rows fit one block leave a second one empty
+  p.tiles = Tq <= seqs * tok ? 1 : 2;
+  p.n_split = 1;
+  const long long step = static_cast<long long>(p.tiles) * tok;
+  const long long items = std::max(seqs, (Tq + step - 1) / step) * Hk;
+  const long long key_tiles = (Tk / std::max(1, N) + 127) / 128;  // of an average sequence
+  const long long want = p.tiles == 1 ? 4 * 304 : 152;
+  if (items < want && key_tiles >= 8)
+    p.n_split = static_cast<int>(std::min<long long>((want + items - 1) / items, key_tiles / 4));
+  return p;
+}
 
 // ----------------------------------------------------------------- packed sequences (device)
 // Extents of one sequence, clamped to the tensors: query rows q0..q1-1, keys
