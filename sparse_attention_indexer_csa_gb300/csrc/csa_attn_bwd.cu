@@ -1,12 +1,38 @@
-// csa_attn_bwd.cu -- gradients of causal attention over packed sequences, one
-// warp per query row and head (dq) or per key and key head (dk, dv).
+// csa_attn_bwd.cu -- gradients of causal attention over packed sequences on
+// the tensor cores.
 //
-//   delta = dout.out;  p_j = exp(s_j - lse);  ds_j = p_j (dout.v_j - delta)
-//   dq = scale sum_j ds_j k_j;  dk_j = scale sum_rows ds_j q;  dv_j = sum_rows p_j dout
+//   delta = dout.out  (per row and head)
+//   p_j = exp(s_j - lse),  ds_j = p_j (dout.v_j - delta)
+//   dq = scale sum_j ds_j k_j,  dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dout
 //
-// A warp takes 32 keys (rows) at a time: lane j forms the dot products of
-// key (row) j, then every lane adds the 32 weighted rows into its own D/32
-// values.
+// Three kernels: delta (one pass over dout and out), dq, and dk with dv.  The
+// scores are formed again from q, k and lse in both of the latter; P and dS
+// never leave the SM.  That is seven products per tile where one kernel
+// for everything needs five, but every output is summed by one CTA in a fixed
+// order: no atomics (the same bits on every call), no fp32 dq in memory, and
+// dk, dv of a key head sum over its g query heads in place.
+//
+//   attn_dkv_kernel  a CTA takes up to 128 keys of one sequence and key head
+//     and walks the rows that see them in blocks of 128 (rows = token * g +
+//     head, as in the forward):
+//       S^T = K Q^T, dP^T = V dO^T           (operands in shared memory)
+//       P^T, dS^T in the storage type over S^T, dP^T in TMEM
+//       dV += P^T dO, dK += dS^T Q           (A in TMEM, B read MN-major)
+//     TMEM: S^T, dP^T, dV, dK, 128 columns each.  The issue order dV(i),
+//     S^T(i+1), dK(i), dP^T(i+1) leaves the elementwise warps the time of two
+//     products for each of their two halves.
+//   attn_dq_kernel   a CTA takes a block of 128 rows and walks the key tiles:
+//       S = Q K^T, dP = dO V^T, dS over dP in TMEM, dQ += dS K
+//     TMEM: S, two dP, dQ.
+//
+// Warps (12): 0-7 elementwise (TMEM lanes 32 (w % 4) .., column half w / 4) and
+// output; 8 issuer of the products; 9 TMA producer; 10 row statistics of the
+// coming block (dkv) and what must be cleared in a tile's end; 11 none.
+//
+// A tile's end that belongs to another sequence may hold NaN, which a zero
+// factor does not cancel: rows (dkv) or keys (dq) past the end are cleared in
+// shared memory before any product reads them: such a tile lands on a barrier
+// of its own, and the warp that cleared its end completes the tile's in the ring.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -16,150 +42,661 @@
 namespace csa {
 namespace {
 
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename X>
-__device__ __forceinline__ X from_f(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
-  return __float2bfloat16(x);
-}
-template <>
-__device__ __forceinline__ __half from_f<__half>(float x) {
-  return __float2half(x);
-}
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kPrepWarp = 10;
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+struct BwdArgs {
+  AttnParams a;
+  int tq;  // tokens per block of 128 rows
+  int nb;  // dq: ceil(Tq / tq); dkv: ceil(Tk / 128)
+  float c;
+  unsigned long long wait_ns;
+};
 
-constexpr int kWarps = 4;
+// The walks' two resident tiles (dq: Q, dO; dkv: K, V) and two stages of two
+// tiles (dq: K, V; dkv: Q, dO).
+template <int D>
+struct BwdCfg {
+  static constexpr uint32_t kTile = kChunkBytes * (D / 64);
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kOffA = 0, kOffB = kTile, kOffSt = 2 * kTile;  // stage s: kOffSt + 2 s kTile
+  static constexpr uint32_t kOffStat = kOffSt + 2 * kStages * kTile;      // [2][2][128] fp32: -lse log2 e, delta
+  static constexpr uint32_t kOffBar = kOffStat + 2 * 2 * 128 * 4;
+  static constexpr int kBarRes = 0, kBarFull = 1, kBarEmpty = kBarFull + kStages, kBarLast = kBarEmpty + kStages,
+                       kBarStat = kBarLast + 1, kBarStatFree = kBarStat + 2, kBarS = kBarStatFree + 2,
+                       kBarP = kBarS + 1, kBarDp = kBarP + 1, kBarDs = kBarDp + 2, kBarAcc = kBarDs + 2,
+                       kBarDone = kBarAcc + 1, kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 64 + 1024;
+};
+static_assert(BwdCfg<128>::kSmem <= 227 * 1024, "shared memory");
 
-template <typename X, int D>
-__device__ __forceinline__ float dot(const X* a, const float* b) {
-  float s = 0.f;
-#pragma unroll 16
-  for (int d = 0; d < D; ++d) s = fmaf(to_f(a[d]), b[d], s);
-  return s;
-}
+template <int D>
+struct Cta {
+  uint8_t* base;
+  uint64_t* bars;
+  WaitCtl ctl;
+  uint32_t tmem;
+};
 
-template <typename X, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_delta_kernel(const AttnParams p) {
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (item >= static_cast<long long>(p.Tq) * p.Hq) return;
-  float s = 0.f;
-  for (int d = lane; d < D; d += 32)
-    s = fmaf(to_f(static_cast<const X*>(p.dout)[item * D + d]), to_f(static_cast<const X*>(p.out)[item * D + d]), s);
-  s = warp_sum(s);
-  if (lane == 0) p.delta[item] = s;
-}
-
-template <typename X, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_dq_kernel(const AttnParams p) {
-  __shared__ float qs[kWarps][D], ds_[kWarps][D];
-  if (blockIdx.x == 0) check_sequences(p);
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (item >= static_cast<long long>(p.Tq) * p.Hq) return;
-  const int t = static_cast<int>(item / p.Hq), h = static_cast<int>(item % p.Hq), hk = h / p.g;
-  const X* q = static_cast<const X*>(p.q) + t * p.q_st + h * p.q_sh;
-  for (int d = lane; d < D; d += 32) {
-    qs[w][d] = to_f(q[d]);
-    ds_[w][d] = to_f(static_cast<const X*>(p.dout)[item * D + d]);
+// Common set-up: barriers, TMEM.  `work` is uniform over the CTA.
+template <int D>
+__device__ __forceinline__ void init_barriers(uint64_t* bars) {
+  using C = BwdCfg<D>;
+  for (int i = 0; i < C::kBars; ++i) {
+    int n = 1;
+    if (i == C::kBarStatFree || i == C::kBarStatFree + 1 || i == C::kBarP || i == C::kBarDs || i == C::kBarDs + 1)
+      n = kEpiWarps;
+    mbar_init(bars + i, n);
   }
-  __syncwarp();
-  float acc[D / 32] = {};
-  const int i = find_seq(p.cu_q, p.N, t);
-  if (i >= 0) {
-    const SeqExt e = seq_extent(p, i);
-    const int see = keys_seen(p, e, t - e.q0);
-    const float lse = p.lse[item], delta = p.delta[item];
-    const X* k = static_cast<const X*>(p.k) + e.k0 * p.k_st + hk * p.k_sh;
-    const X* v = static_cast<const X*>(p.v) + e.k0 * p.v_st + hk * p.v_sh;
-    for (int j0 = 0; j0 < see; j0 += 32) {
-      const int j = j0 + lane;
-      float ds = 0.f;
-      if (j < see)
-        ds = expf(dot<X, D>(k + j * p.k_st, qs[w]) * p.scale - lse) * (dot<X, D>(v + j * p.v_st, ds_[w]) - delta);
-      for (int u = 0; u < min(32, see - j0); ++u) {
-        const float du = __shfl_sync(0xffffffffu, ds, u);
-        for (int d = 0; d < D / 32; ++d) acc[d] = fmaf(du, to_f(k[(j0 + u) * p.k_st + d * 32 + lane]), acc[d]);
-      }
+  fence_mbar_init();
+}
+
+// S or dP of one tile: D[128,128] = A . B^T, both K-major over D.
+template <typename X, int D>
+__device__ __forceinline__ void product_abt(uint32_t d, uint64_t ad, uint64_t bd) {
+  constexpr uint32_t kId = idesc_f16<X>(128, 128, false);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
+    umma_bf16(d, ad + o, bd + o, kId, ks != 0 ? 1u : 0u);
+  }
+}
+// Acc[128,D] (+)= A . B with A in TMEM (two halves of 64 in columns 0.. and
+// 64.. of `x`) and B [128,D] read MN-major.
+template <typename X, int D>
+__device__ __forceinline__ void product_acc(uint32_t acc, uint32_t x, uint64_t bd, bool first) {
+  constexpr uint32_t kId = idesc_f16<X>(128, D, true);
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks)
+    umma_bf16_tmem_a(acc, x + 64u * (ks >> 2) + 8u * (ks & 3), bd + static_cast<uint64_t>(128 * ks), kId,
+                     (!first || ks != 0) ? 1u : 0u);
+}
+
+// Waits until nothing that the producer started is in flight.
+template <int D>
+__device__ __forceinline__ void drain_stages(const Cta<D>& ct, uint32_t n) {
+  using C = BwdCfg<D>;
+  if (*ct.ctl.abort_flag != 0u) return;
+  volatile uint32_t dummy = 0;
+  const WaitCtl dctl{&dummy, ct.ctl.limit_ns};
+  for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < n; ++i)
+    mbar_wait(ct.bars + C::kBarFull + (n - 1 - i) % C::kStages, ((n - 1 - i) / C::kStages) & 1u, dctl);
+}
+
+// One accumulator lane (D fp32 values times f) to D values of X at dst.
+template <typename X, int D>
+__device__ __forceinline__ void store_lane(uint32_t t, float f, X* dst, bool some, bool write) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    float o[32];
+    __syncwarp();
+    if (some) {
+      tmem_ld32_start(t + 32 * i, o);
+      tmem_wait32(o);
+    }
+    if (!write) continue;
+#pragma unroll
+    for (int u = 0; u < 32; ++u) o[u] = some ? o[u] * f : 0.f;
+    uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * i);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      d4[u] = make_uint4(pack_pair<X>(o[8 * u], o[8 * u + 1]), pack_pair<X>(o[8 * u + 2], o[8 * u + 3]),
+                         pack_pair<X>(o[8 * u + 4], o[8 * u + 5]), pack_pair<X>(o[8 * u + 6], o[8 * u + 7]));
+  }
+}
+
+// ----------------------------------------------------------------- delta
+// delta = dout.out: D/8 lanes per row and head, 16 bytes of each tensor a lane.
+template <typename X, int D>
+__global__ void __launch_bounds__(256) attn_delta_kernel(const AttnParams p) {
+  constexpr int G = D / 8;
+  const long long r = static_cast<long long>(blockIdx.x) * (256 / G) + threadIdx.x / G;
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+  const int l = threadIdx.x % G;
+  float s = 0.f;
+  if (r < rows) {
+    const uint4 x = reinterpret_cast<const uint4*>(static_cast<const X*>(p.dout) + r * D)[l];
+    const uint4 y = reinterpret_cast<const uint4*>(static_cast<const X*>(p.out) + r * D)[l];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpack_pair<X>(xs[i]), b = unpack_pair<X>(ys[i]);
+      s = fmaf(a.x, b.x, s);
+      s = fmaf(a.y, b.y, s);
     }
   }
-  X* dq = static_cast<X*>(p.dq) + item * D;
-  for (int d = 0; d < D / 32; ++d) dq[d * 32 + lane] = from_f<X>(acc[d] * p.scale);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (r < rows && l == 0) p.delta[r] = s;
 }
 
+// ----------------------------------------------------------------- dk, dv
 template <typename X, int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_dkv_kernel(const AttnParams p) {
-  __shared__ float ks[kWarps][D], vs[kWarps][D];
-  if (blockIdx.x == 0) check_sequences(p);
-  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (item >= static_cast<long long>(p.Tk) * p.Hk) return;
-  const int t = static_cast<int>(item / p.Hk), hk = static_cast<int>(item % p.Hk);
-  for (int d = lane; d < D; d += 32) {
-    ks[w][d] = to_f((static_cast<const X*>(p.k) + t * p.k_st + hk * p.k_sh)[d]);
-    vs[w][d] = to_f((static_cast<const X*>(p.v) + t * p.v_st + hk * p.v_sh)[d]);
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
+                    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                    const BwdArgs f) {
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
+  RowItem* item = reinterpret_cast<RowItem*>(base + C::kOffMisc + 16);
+  const AttnParams& a = f.a;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+  const int hk = static_cast<int>(blockIdx.x % a.Hk);
+
+  if (warp == kMmaWarp) {
+    const RowItem it = find_key_item(a, 128, f.nb, static_cast<int>(blockIdx.x / a.Hk));
+    if (lane == 0) *item = it;
+    if (blockIdx.x == 0)
+      for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
   }
-  __syncwarp();
-  float ak[D / 32] = {}, av[D / 32] = {};
-  const int i = find_seq(p.cu_k, p.N, t);
-  if (i >= 0) {
-    const SeqExt e = seq_extent(p, i);
-    const int j = t - e.k0, lq = e.q1 - e.q0;
-    const int r_lo = j >= e.lk ? lq : (p.causal ? max(0, j - (e.lk - lq)) : 0);
-    const long long n = static_cast<long long>(max(0, lq - r_lo)) * p.g;
-    for (long long u0 = 0; u0 < n; u0 += 32) {
-      const long long u = u0 + lane;
-      float pj = 0.f, ds = 0.f;
-      const auto row = [&](long long x) { return e.q0 + r_lo + x / p.g; };
-      const auto head = [&](long long x) { return hk * p.g + x % p.g; };
-      if (u < n) {
-        const long long qi = row(u) * p.Hq + head(u);
-        pj = expf(dot<X, D>(static_cast<const X*>(p.q) + row(u) * p.q_st + head(u) * p.q_sh, ks[w]) * p.scale -
-                  p.lse[qi]);
-        ds = pj * (dot<X, D>(static_cast<const X*>(p.dout) + qi * D, vs[w]) - p.delta[qi]);
+  if (threadIdx.x == 0) {
+    init_barriers<D>(bars);
+    *abort_flag = 0u;
+  }
+  __syncthreads();
+  const RowItem it = *item;  // keys it.t0 .. it.t1-1 of the tensor
+  if (it.t0 >= it.t1) return;
+
+  // keys of the sequence among them, and the rows (tokens of the sequence) that see the first
+  const int j0 = it.t0 - it.s.k0, lq = it.s.q1 - it.s.q0;
+  const int n_key = max(0, min(it.t1 - it.t0, it.s.lk - j0));
+  const int r_lo = n_key > 0 ? (a.causal ? min(lq, max(0, j0 - (it.s.lk - lq))) : 0) : lq;
+  const int n_blk = (lq - r_lo + f.tq - 1) / f.tq;
+  const bool work = n_blk > 0;
+  const int rows_blk = f.tq * a.g;  // rows of a full block (128 when g divides it)
+
+  if (work && rows_blk < 128)  // rows that no copy writes: zero factors must meet finite values
+    for (int s = 0; s < 2 * C::kStages; ++s)
+      clear_tile_rows<D>(base + C::kOffSt + s * C::kTile, rows_blk, static_cast<int>(threadIdx.x), kThreads);
+  fence_proxy_async_shared();
+  if (work && warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Cta<D> ct{base, bars, WaitCtl{abort_flag, f.wait_ns}, work ? *tmem_slot : 0u};
+  const uint32_t t_s = ct.tmem, t_dp = ct.tmem + 128, t_dv = ct.tmem + 256, t_dk = ct.tmem + 384;
+  const WaitCtl& ctl = ct.ctl;
+  // the last block may hold fewer tokens than tq
+  const int tail = lq - r_lo - (n_blk - 1) * f.tq;
+
+  if (warp == kTmaWarp) {
+    if (work && lane == 0) {
+      const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
+      mbar_arrive_expect_tx(bars + C::kBarRes, 2 * C::kTile);
+      for (int ch = 0; ch < D / 64; ++ch) {
+        tma_load_3d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_k, bars + C::kBarRes, ch * 64, it.t0, hk, first);
+        tma_load_3d_hint(base + C::kOffB + ch * kChunkBytes, &tmap_v, bars + C::kBarRes, ch * 64, it.t0, hk, first);
       }
-      for (int x = 0; x < static_cast<int>(min(32ll, n - u0)); ++x) {
-        const float px = __shfl_sync(0xffffffffu, pj, x), dx = __shfl_sync(0xffffffffu, ds, x);
-        const X* q = static_cast<const X*>(p.q) + row(u0 + x) * p.q_st + head(u0 + x) * p.q_sh;
-        const X* o = static_cast<const X*>(p.dout) + (row(u0 + x) * p.Hq + head(u0 + x)) * D;
-        for (int d = 0; d < D / 32; ++d) {
-          ak[d] = fmaf(dx, to_f(q[d * 32 + lane]), ak[d]);
-          av[d] = fmaf(px, to_f(o[d * 32 + lane]), av[d]);
+      for (int i = 0; i < n_blk; ++i) {
+        const int st = i % C::kStages;
+        if (!mbar_wait(bars + C::kBarEmpty + st, ((i / C::kStages) & 1u) ^ 1u, ctl)) continue;
+        uint8_t* dst = base + C::kOffSt + 2 * st * C::kTile;
+        uint64_t* bar = bars + (i == n_blk - 1 && tail < f.tq ? C::kBarLast : C::kBarFull + st);
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows_blk) * 256u * (D / 64));
+        for (int ch = 0; ch < D / 64; ++ch) {
+          tma_load_4d_hint(dst + ch * kChunkBytes, &tmap_q, bar, ch * 64, 0, it.s.q0 + r_lo + i * f.tq, hk, last);
+          tma_load_4d_hint(dst + C::kTile + ch * kChunkBytes, &tmap_do, bar, ch * 64, 0, it.s.q0 + r_lo + i * f.tq, hk,
+                           last);
+        }
+      }
+      drain_stages<D>(ct, n_blk);
+      mbar_wait(bars + C::kBarRes, 0u, ctl);
+    }
+  } else if (warp == kMmaWarp) {
+    if (work && lane == 0) {
+      const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
+      const uint64_t vd = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
+      const uint64_t sk = smem_desc_kmajor(smem_u32(base + C::kOffSt), 128);
+      const uint64_t sm = smem_desc_mn_sw128(smem_u32(base + C::kOffSt), kChunkBytes, 1024u);
+      constexpr uint64_t kT = C::kTile >> 4;
+      bool alive = true;
+      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
+      auto ready = [&](int i) {
+        wait(C::kBarFull + i % C::kStages, (i / C::kStages) & 1u);
+        tc_fence_after();
+      };
+      wait(C::kBarRes, 0u);
+      ready(0);
+      if (alive) product_abt<X, D>(t_s, kd, sk);
+      umma_commit(bars + C::kBarS);
+      if (alive) product_abt<X, D>(t_dp, vd, sk + kT);
+      umma_commit(bars + C::kBarDp);
+      for (int i = 0; i < n_blk; ++i) {
+        const uint64_t st = static_cast<uint64_t>(i % C::kStages) * (2 * kT);
+        const uint64_t nx = static_cast<uint64_t>((i + 1) % C::kStages) * (2 * kT);
+        wait(C::kBarP, static_cast<uint32_t>(i) & 1u);
+        tc_fence_after();
+        if (alive) product_acc<X, D>(t_dv, t_s, sm + st + kT, i == 0);
+        if (i + 1 < n_blk) {
+          ready(i + 1);
+          if (alive) product_abt<X, D>(t_s, kd, sk + nx);
+          umma_commit(bars + C::kBarS);
+        }
+        wait(C::kBarDs, static_cast<uint32_t>(i) & 1u);
+        tc_fence_after();
+        if (alive) product_acc<X, D>(t_dk, t_dp, sm + st, i == 0);
+        umma_commit(bars + C::kBarEmpty + i % C::kStages);
+        if (i + 1 < n_blk) {
+          if (alive) product_abt<X, D>(t_dp, vd, sk + nx + kT);
+          umma_commit(bars + C::kBarDp);
+        }
+      }
+      umma_commit(bars + C::kBarAcc);
+      umma_commit(bars + C::kBarDone);
+      volatile uint32_t dummy = 0;
+      const WaitCtl dctl{&dummy, ctl.limit_ns};
+      mbar_wait(bars + C::kBarDone, 0u, dctl);
+    }
+  } else if (warp == kPrepWarp) {
+    if (work) {
+      for (int i = 0; i < n_blk; ++i) {
+        const int b = i & 1, t0 = it.s.q0 + r_lo + i * f.tq;
+        const int rows = (i == n_blk - 1 ? tail : f.tq) * a.g;
+        float* st = reinterpret_cast<float*>(base + C::kOffStat) + b * 256;
+        const bool ok = mbar_wait(bars + C::kBarStatFree + b, ((i >> 1) & 1u) ^ 1u, ctl);
+        if (ok) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = u * 32 + static_cast<int>(lane), tok = r / a.g;
+            float nl = -INFINITY, de = 0.f;
+            if (r < rows) {
+              const long long at = static_cast<long long>(t0 + tok) * a.Hq + hk * a.g + (r - tok * a.g);
+              const float l = a.lse[at];
+              if (l != -INFINITY) {
+                nl = -l * 1.4426950408889634f;
+                de = a.delta[at];
+              }
+            }
+            st[r] = nl;
+            st[128 + r] = de;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
+        if (i == n_blk - 1 && tail < f.tq) {
+          const int sg = i % C::kStages;
+          if (mbar_wait(bars + C::kBarLast, 0u, ctl)) {
+            clear_tile_rows<D>(base + C::kOffSt + 2 * sg * C::kTile, rows, static_cast<int>(lane), 32);
+            clear_tile_rows<D>(base + C::kOffSt + (2 * sg + 1) * C::kTile, rows, static_cast<int>(lane), 32);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::kBarFull + sg);
         }
       }
     }
+  } else if (warp < kEpiWarps) {
+    const int hf = warp >> 2, key = (warp & 3) * 32 + static_cast<int>(lane);
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = t_s + lane_off + 64 * hf, tp = t_dp + lane_off + 64 * hf;
+    const float2 c2 = make_float2(f.c, f.c);
+    // the first token (relative to r_lo) that sees this key, as a row; and the first that sees all keys
+    const int first_row = a.causal ? (j0 + key - (it.s.lk - lq) - r_lo) * a.g : 0;
+    const int all_rows = a.causal ? (j0 + n_key - 1 - (it.s.lk - lq) - r_lo) * a.g : 0;
+    bool ok = true;
+    for (int i = 0; i < n_blk; ++i) {
+      const int b = i & 1;
+      const float4* st4 = reinterpret_cast<const float4*>(base + C::kOffStat + b * 1024) + 16 * hf;
+      ok = ok && mbar_wait(bars + C::kBarStat + b, (i >> 1) & 1u, ctl);
+      ok = ok && mbar_wait(bars + C::kBarS, static_cast<uint32_t>(i) & 1u, ctl);
+      tc_fence_after();
+      float p[2][32];
+      if (ok) {
+        tmem_ld32_start(ts, p[0]);
+        tmem_ld32_start(ts + 32, p[1]);
+        tmem_wait32(p[0]);
+        tmem_wait32(p[1]);
+        if (i * rows_blk < all_rows) {
+          const int skip = first_row - i * rows_blk - 64 * hf;  // columns before the first row that sees this key
+#pragma unroll
+          for (int u = 0; u < 64; ++u)
+            if (u < skip) p[u >> 5][u & 31] = -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float4 nl = st4[8 * h + u];
+            float* x = p[h] + 4 * u;
+            const float2 e0 = ffma2(make_float2(x[0], x[1]), c2, make_float2(nl.x, nl.y));
+            const float2 e1 = ffma2(make_float2(x[2], x[3]), c2, make_float2(nl.z, nl.w));
+            x[0] = exp2_approx(e0.x);
+            x[1] = exp2_approx(e0.y);
+            x[2] = exp2_approx(e1.x);
+            x[3] = exp2_approx(e1.y);
+            pk[2 * u] = pack_pair<X>(x[0], x[1]);
+            pk[2 * u + 1] = pack_pair<X>(x[2], x[3]);
+          }
+          tmem_st16(ts + 16 * h, pk);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarP);
+      ok = ok && mbar_wait(bars + C::kBarDp, static_cast<uint32_t>(i) & 1u, ctl);
+      tc_fence_after();
+      if (ok) {
+        float d[2][32];
+        tmem_ld32_start(tp, d[0]);
+        tmem_ld32_start(tp + 32, d[1]);
+        tmem_wait32(d[0]);
+        tmem_wait32(d[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float4 de = st4[32 + 8 * h + u];
+            const float* x = p[h] + 4 * u;
+            const float* y = d[h] + 4 * u;
+            const float2 a0 = fmul2(make_float2(x[0], x[1]), fadd2(make_float2(y[0], y[1]), make_float2(-de.x, -de.y)));
+            const float2 a1 = fmul2(make_float2(x[2], x[3]), fadd2(make_float2(y[2], y[3]), make_float2(-de.z, -de.w)));
+            pk[2 * u] = pack_pair<X>(a0.x, a0.y);
+            pk[2 * u + 1] = pack_pair<X>(a1.x, a1.y);
+          }
+          tmem_st16(tp + 16 * h, pk);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + C::kBarDs);
+        mbar_arrive(bars + C::kBarStatFree + b);
+      }
+    }
+    // output: the first four warps dv, the others dk
+    if (work) {
+      ok = ok && mbar_wait(bars + C::kBarAcc, 0u, ctl);
+      tc_fence_after();
+    }
+    const bool write = key < it.t1 - it.t0;
+    const long long at = (static_cast<long long>(it.t0 + key) * a.Hk + hk) * D;
+    // keys the sequence does not hold (past k_len, or outside every sequence) get zeros
+    const float fac = hf == 0 ? 1.f : a.scale;
+    store_lane<X, D>((hf == 0 ? t_dv : t_dk) + lane_off, fac, static_cast<X*>(hf == 0 ? a.dv : a.dk) + at, work && ok,
+                     write && key < n_key);
+    if (write && key >= n_key) {
+      uint4* d4 = reinterpret_cast<uint4*>(static_cast<X*>(hf == 0 ? a.dv : a.dk) + at);
+      for (int u = 0; u < D / 8; ++u) d4[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
-  for (int d = 0; d < D / 32; ++d) {
-    (static_cast<X*>(p.dk) + item * D)[d * 32 + lane] = from_f<X>(ak[d] * p.scale);
-    (static_cast<X*>(p.dv) + item * D)[d * 32 + lane] = from_f<X>(av[d]);
-  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (work && warp == kMmaWarp) tmem_dealloc(ct.tmem, 512);
 }
 
-unsigned blocks_of(long long items) { return static_cast<unsigned>((items + kWarps - 1) / kWarps); }
-
+// ----------------------------------------------------------------- dq
 template <typename X, int D>
-cudaError_t bwd(const AttnParams& p, cudaStream_t s) {
-  if (p.Tq > 0) {
-    const unsigned n = blocks_of(static_cast<long long>(p.Tq) * p.Hq);
-    attn_delta_kernel<X, D><<<n, kWarps * 32, 0, s>>>(p);
-    attn_dq_kernel<X, D><<<n, kWarps * 32, 0, s>>>(p);
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
+                   const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                   const BwdArgs f) {
+  using C = BwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
+  RowItem* item = reinterpret_cast<RowItem*>(base + C::kOffMisc + 16);
+  const AttnParams& a = f.a;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+  const int hk = static_cast<int>(blockIdx.x % a.Hk);
+
+  if (warp == kMmaWarp) {
+    const RowItem it = find_row_item(a, f.tq, f.nb, f.nb + a.N - static_cast<int>(blockIdx.x / a.Hk));
+    if (lane == 0) *item = it;
+    if (blockIdx.x == 0)
+      for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
   }
-  if (p.Tk > 0) attn_dkv_kernel<X, D><<<blocks_of(static_cast<long long>(p.Tk) * p.Hk), kWarps * 32, 0, s>>>(p);
+  if (threadIdx.x == 0) {
+    init_barriers<D>(bars);
+    *abort_flag = 0u;
+  }
+  __syncthreads();
+  const RowItem it = *item;
+  if (it.t0 >= it.t1) return;
+  const int n_tok = min(f.tq, it.t1 - it.t0);
+  const int top = (keys_seen(a, it.s, it.t0 + n_tok - 1 - it.s.q0) + 127) >> 7;  // key tiles
+  const bool work = top > 0;
+  if (work && warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Cta<D> ct{base, bars, WaitCtl{abort_flag, f.wait_ns}, work ? *tmem_slot : 0u};
+  const uint32_t t_s = ct.tmem, t_dp = ct.tmem + 128, t_dq = ct.tmem + 384;  // two dP buffers
+  const WaitCtl& ctl = ct.ctl;
+  const bool fix = top * 128 > it.s.lk;  // the last tile reaches past the sequence's keys
+
+  if (warp == kTmaWarp) {
+    if (work && lane == 0) {
+      const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
+      mbar_arrive_expect_tx(bars + C::kBarRes, static_cast<uint32_t>(f.tq * a.g) * 256u * (D / 64));
+      for (int ch = 0; ch < D / 64; ++ch) {
+        tma_load_4d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_q, bars + C::kBarRes, ch * 64, 0, it.t0, hk, first);
+        tma_load_4d_hint(base + C::kOffB + ch * kChunkBytes, &tmap_do, bars + C::kBarRes, ch * 64, 0, it.t0, hk, first);
+      }
+      for (int j = 0; j < top; ++j) {
+        const int st = j % C::kStages;
+        if (!mbar_wait(bars + C::kBarEmpty + st, ((j / C::kStages) & 1u) ^ 1u, ctl)) continue;
+        uint8_t* dst = base + C::kOffSt + 2 * st * C::kTile;
+        uint64_t* bar = bars + (j == top - 1 && fix ? C::kBarLast : C::kBarFull + st);
+        mbar_arrive_expect_tx(bar, 2 * C::kTile);
+        for (int ch = 0; ch < D / 64; ++ch) {
+          tma_load_3d_hint(dst + ch * kChunkBytes, &tmap_k, bar, ch * 64, it.s.k0 + j * 128, hk, last);
+          tma_load_3d_hint(dst + C::kTile + ch * kChunkBytes, &tmap_v, bar, ch * 64, it.s.k0 + j * 128, hk, last);
+        }
+      }
+      drain_stages<D>(ct, top);
+      mbar_wait(bars + C::kBarRes, 0u, ctl);
+    }
+  } else if (warp == kMmaWarp) {
+    if (work && lane == 0) {
+      const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
+      const uint64_t od = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
+      const uint64_t sk = smem_desc_kmajor(smem_u32(base + C::kOffSt), 128);
+      const uint64_t sm = smem_desc_mn_sw128(smem_u32(base + C::kOffSt), kChunkBytes, 1024u);
+      constexpr uint64_t kT = C::kTile >> 4;
+      bool alive = true;
+      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
+      auto scores = [&](int j) {  // S(j) and dP(j); dP(j-2), whose buffer this is, went into dQ before
+        const uint64_t st = static_cast<uint64_t>(j % C::kStages) * (2 * kT);
+        wait(C::kBarFull + j % C::kStages, (j / C::kStages) & 1u);
+        tc_fence_after();
+        if (alive) product_abt<X, D>(t_s, qd, sk + st);
+        umma_commit(bars + C::kBarS);
+        if (alive) product_abt<X, D>(t_dp + 128 * (j & 1), od, sk + st + kT);
+        umma_commit(bars + C::kBarDp + (j & 1));
+      };
+      wait(C::kBarRes, 0u);
+      scores(0);
+      for (int j = 0; j < top; ++j) {
+        if (j + 1 < top) {
+          wait(C::kBarP, static_cast<uint32_t>(j) & 1u);  // S(j) is in registers
+          scores(j + 1);
+        }
+        wait(C::kBarDs + (j & 1), static_cast<uint32_t>(j >> 1) & 1u);
+        tc_fence_after();
+        if (alive)
+          product_acc<X, D>(t_dq, t_dp + 128 * (j & 1), sm + static_cast<uint64_t>(j % C::kStages) * (2 * kT), j == 0);
+        umma_commit(bars + C::kBarEmpty + j % C::kStages);
+      }
+      umma_commit(bars + C::kBarAcc);
+      umma_commit(bars + C::kBarDone);
+      volatile uint32_t dummy = 0;
+      const WaitCtl dctl{&dummy, ctl.limit_ns};
+      mbar_wait(bars + C::kBarDone, 0u, dctl);
+    }
+  } else if (warp == kPrepWarp) {
+    if (work && fix) {
+      const int j = top - 1, st = j % C::kStages;
+      const bool ok = mbar_wait(bars + C::kBarLast, 0u, ctl);
+      if (ok) {
+        clear_tile_rows<D>(base + C::kOffSt + 2 * st * C::kTile, it.s.lk - j * 128, static_cast<int>(lane), 32);
+        clear_tile_rows<D>(base + C::kOffSt + (2 * st + 1) * C::kTile, it.s.lk - j * 128, static_cast<int>(lane), 32);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarFull + st);
+    }
+  } else if (warp < kEpiWarps) {
+    const int hf = warp >> 2, row = (warp & 3) * 32 + static_cast<int>(lane);
+    const int tok = row / a.g, head = row - tok * a.g;
+    const bool row_ok = tok < n_tok;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = t_s + lane_off + 64 * hf;
+    const long long at = static_cast<long long>(it.t0 + tok) * a.Hq + hk * a.g + head;
+    float nl = -INFINITY, de = 0.f;
+    if (row_ok) {
+      const float l = a.lse[at];
+      if (l != -INFINITY) {
+        nl = -l * 1.4426950408889634f;
+        de = a.delta[at];
+      }
+    }
+    const int see = row_ok ? keys_seen(a, it.s, it.t0 + tok - it.s.q0) : 0;
+    const int see_all = keys_seen(a, it.s, it.t0 - it.s.q0);
+    const float2 c2 = make_float2(f.c, f.c), nl2 = make_float2(nl, nl), nd2 = make_float2(-de, -de);
+    bool ok = true;
+    for (int j = 0; j < top; ++j) {
+      ok = ok && mbar_wait(bars + C::kBarS, static_cast<uint32_t>(j) & 1u, ctl);
+      tc_fence_after();
+      float p[2][32];
+      if (ok) {
+        tmem_ld32_start(ts, p[0]);
+        tmem_ld32_start(ts + 32, p[1]);
+        tmem_wait32(p[0]);
+        tmem_wait32(p[1]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarP);
+      if (ok) {
+        if ((j + 1) * 128 > see_all) {
+          const int lim = see - j * 128 - 64 * hf;
+#pragma unroll
+          for (int u = 0; u < 64; ++u)
+            if (u >= lim) p[u >> 5][u & 31] = -INFINITY;
+        }
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          float* x = p[u >> 4] + 2 * (u & 15);
+          const float2 e = ffma2(make_float2(x[0], x[1]), c2, nl2);
+          x[0] = exp2_approx(e.x);
+          x[1] = exp2_approx(e.y);
+        }
+      }
+      ok = ok && mbar_wait(bars + C::kBarDp + (j & 1), static_cast<uint32_t>(j >> 1) & 1u, ctl);
+      tc_fence_after();
+      if (ok) {
+        const uint32_t tp = t_dp + 128 * (j & 1) + lane_off + 64 * hf;
+        float d[2][32];
+        tmem_ld32_start(tp, d[0]);
+        tmem_ld32_start(tp + 32, d[1]);
+        tmem_wait32(d[0]);
+        tmem_wait32(d[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float2 y = fadd2(make_float2(d[h][2 * u], d[h][2 * u + 1]), nd2);
+            const float2 z = fmul2(make_float2(p[h][2 * u], p[h][2 * u + 1]), y);
+            pk[u] = pack_pair<X>(z.x, z.y);
+          }
+          tmem_st16(tp + 16 * h, pk);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarDs + (j & 1));
+    }
+    if (work) {
+      ok = ok && mbar_wait(bars + C::kBarAcc, 0u, ctl);
+      tc_fence_after();
+    }
+    // output: each half of the warps takes half of the columns; rows that see nothing get zeros
+    const bool none = nl == -INFINITY;
+    X* dst = static_cast<X*>(a.dq) + at * D + (D / 2) * hf;
+    store_lane<X, D / 2>(t_dq + lane_off + (D / 2) * hf, none ? 0.f : a.scale, dst, work && ok, row_ok && !none);
+    if (row_ok && none) {
+      uint4* d4 = reinterpret_cast<uint4*>(dst);
+      for (int u = 0; u < D / 16; ++u) d4[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (work && warp == kMmaWarp) tmem_dealloc(ct.tmem, 512);
+}
+
+// ----------------------------------------------------------------- launches
+template <typename X, int D>
+cudaError_t run(const AttnParams& p, cudaStream_t stream) {
+  using C = BwdCfg<D>;
+  BwdArgs f;
+  f.a = p;
+  f.tq = 128 / p.g;
+  f.c = p.scale * 1.4426950408889634f;
+  f.wait_ns = kAttnWaitNs;
+  cudaError_t e;
+  if ((e = smem_limit_once<attn_dq_kernel<X, D>>(C::kSmem)) != cudaSuccess) return e;
+  if ((e = smem_limit_once<attn_dkv_kernel<X, D>>(C::kSmem)) != cudaSuccess) return e;
+  CUtensorMap tq, to, tk, tv;
+  if (p.Tq > 0) {
+    if (!make_rows_map(&tq, p, p.q, p.q_st, p.q_sh, f.tq) ||
+        !make_rows_map(&to, p, p.dout, static_cast<long long>(p.Hq) * D, D, f.tq))
+      return cudaErrorInvalidValue;
+    if (!make_keys_map(&tk, p, p.k, p.k_st, p.k_sh) || !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh))
+      return cudaErrorInvalidValue;
+    const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+    constexpr int PER = 256 / (D / 8);
+    attn_delta_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER), 256, 0, stream>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (p.Tk > 0) {
+    // without any query row nothing is seen: the maps describe rows that nothing loads
+    if (p.Tq == 0) {
+      const size_t n = static_cast<size_t>(p.Tk) * p.Hk * D * sizeof(X);
+      if ((e = cudaMemsetAsync(p.dk, 0, n, stream)) != cudaSuccess) return e;
+      return cudaMemsetAsync(p.dv, 0, n, stream);
+    }
+    f.nb = static_cast<int>((static_cast<long long>(p.Tk) + 127) / 128);
+    const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk;
+    if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    attn_dkv_kernel<X, D><<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  f.nb = static_cast<int>((static_cast<long long>(p.Tq) + f.tq - 1) / f.tq);
+  const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  attn_dq_kernel<X, D><<<static_cast<unsigned>(grid), kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attn_backward(const AttnParams& p, int dtype, cudaStream_t s) {
-  if (dtype == CSA_BF16) return p.D == 128 ? bwd<__nv_bfloat16, 128>(p, s) : bwd<__nv_bfloat16, 64>(p, s);
-  return p.D == 128 ? bwd<__half, 128>(p, s) : bwd<__half, 64>(p, s);
+  if (dtype == CSA_BF16) return p.D == 128 ? run<__nv_bfloat16, 128>(p, s) : run<__nv_bfloat16, 64>(p, s);
+  return p.D == 128 ? run<__half, 128>(p, s) : run<__half, 64>(p, s);
 }
 
 cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }

@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       float o[32];
+      __syncwarp();
       if (any && ok) {
         tmem_ld32_start(to + 32 * i, o);
         tmem_wait32(o);

@@ -92,31 +92,10 @@ __device__ __forceinline__ SeqExt seq_extent(const AttnParams& p, int i) {
   return s;
 }
 
-// Looks over every sequence's entries once (one block of a launch): what is
-// out of order or range is recorded even where no row or key meets it.
-__device__ __forceinline__ void check_sequences(const AttnParams& p) {
-  for (int i = threadIdx.x; i < p.N; i += blockDim.x) seq_extent(p, i);
-}
-
 // Number of keys row r (0-based in its sequence) sees.
 __device__ __forceinline__ int keys_seen(const AttnParams& p, const SeqExt& s, int r) {
   if (!p.causal) return s.lk;
   return max(0, min(s.lk, r + 1 + s.lk - (s.q1 - s.q0)));
-}
-
-// Sequence holding row t: the last i with cu[i] <= t (n sequences), or -1
-// for a row outside all of them.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int n, int t) {
-  if (n == 0 || t < cu[0] || t >= cu[n]) return -1;
-  int lo = 0, hi = n;  // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
 }
 
 }  // namespace csa

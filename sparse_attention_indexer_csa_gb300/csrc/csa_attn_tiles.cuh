@@ -71,9 +71,12 @@ struct RowItem {
 // search for how many multiples are among the first x+1 borders, 32 probes at
 // a time.  A warp; every lane gets the result.  Entries out of order give some
 // other runs inside 0..Tq.
-__device__ __forceinline__ RowItem find_row_item(const AttnParams& a, int step, int nb, int x) {
+template <bool KEYS>
+__device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int nb, int x) {
   const int lane = static_cast<int>(lane_id());
-  auto start = [&](int i) { return min(max(a.cu_q[i], 0), a.Tq); };  // 0 <= i <= N
+  const int T = KEYS ? a.Tk : a.Tq;
+  const int32_t* cu = KEYS ? a.cu_k : a.cu_q;
+  auto start = [&](int i) { return min(max(cu[i], 0), T); };  // 0 <= i <= N
   const bool seqs = a.N > 0;
   const int nB = seqs ? a.N + 1 : 0;
   // the largest i whose i-th multiple is among the first k borders (a multiple
@@ -97,16 +100,24 @@ __device__ __forceinline__ RowItem find_row_item(const AttnParams& a, int step, 
   const int i = lo, j = k - lo;
   RowItem r;
   r.t0 = 0;
-  if (i > 0) r.t0 = static_cast<int>(min(static_cast<long long>(a.Tq), static_cast<long long>(i - 1) * step));
+  if (i > 0) r.t0 = static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(i - 1) * step));
   if (j > 0) r.t0 = max(r.t0, start(j - 1));
-  r.t1 = static_cast<int>(min(static_cast<long long>(a.Tq), i < nb ? static_cast<long long>(i) * step : a.Tq));
+  r.t1 = i < nb ? static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(i) * step)) : T;
   if (j < nB) r.t1 = min(r.t1, start(j));
-  r.s = SeqExt{r.t0, r.t1, 0, 0};
+  r.s = KEYS ? SeqExt{0, 0, r.t0, 0} : SeqExt{r.t0, r.t1, 0, 0};
   if (seqs && j > 0 && j <= a.N) r.s = seq_extent(a, j - 1);
   // entries out of order: a run never leaves its sequence
-  r.t0 = max(r.t0, r.s.q0);
-  r.t1 = min(r.t1, r.s.q1);
+  r.t0 = max(r.t0, KEYS ? r.s.k0 : r.s.q0);
+  if (!KEYS) r.t1 = min(r.t1, r.s.q1);
+  if (r.t1 - r.t0 > step) r.t1 = r.t0 + step;
   return r;
+}
+__device__ __forceinline__ RowItem find_row_item(const AttnParams& a, int step, int nb, int x) {
+  return find_item<false>(a, step, nb, x);
+}
+// The same over the keys: t0 .. t1-1 count from the tensor's first key.
+__device__ __forceinline__ RowItem find_key_item(const AttnParams& a, int step, int nb, int x) {
+  return find_item<true>(a, step, nb, x);
 }
 
 // ----------------------------------------------------------------- register splits
@@ -161,6 +172,13 @@ __device__ __forceinline__ uint32_t pack_pair(float a, float b) {
     const __half2 v = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
+}
+template <typename X>
+__device__ __forceinline__ float2 unpack_pair(uint32_t u) {
+  if constexpr (is_bf16<X>())
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
