@@ -53,20 +53,24 @@ struct BwdArgs {
   unsigned long long wait_ns;
 };
 
-// The walks' two resident tiles (dq: Q, dO; dkv: K, V) and two stages of two
-// tiles (dq: K, V; dkv: Q, dO).
+// Two resident tiles (dq: Q, dO; dkv: K, V) and two rings of tiles: E, whose
+// tile is used first and last in a step (dq: K for S and dQ; dkv: Q for S^T and
+// dK), and F (dq: V for dP; dkv: dO for dP^T and dV), which is free earlier.
+// With three E and two F tiles each copy has the time of three to six products
+// to arrive (two stages of both together left it two: 6000 cycles a step where
+// the products need 2048).
 template <int D>
 struct BwdCfg {
   static constexpr uint32_t kTile = kChunkBytes * (D / 64);
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr uint32_t kOffA = 0, kOffB = kTile, kOffSt = 2 * kTile;  // stage s: kOffSt + 2 s kTile
-  static constexpr uint32_t kOffStat = kOffSt + 2 * kStages * kTile;      // [2][2][128] fp32: -lse log2 e, delta
+  static constexpr int kE = D == 128 ? 3 : 5, kF = D == 128 ? 2 : 4;
+  static constexpr uint32_t kOffA = 0, kOffB = kTile, kOffE = 2 * kTile, kOffF = kOffE + kE * kTile;
+  static constexpr uint32_t kOffStat = kOffF + kF * kTile;  // [2][2][128] fp32: -lse log2 e, delta
   static constexpr uint32_t kOffBar = kOffStat + 2 * 2 * 128 * 4;
-  static constexpr int kBarRes = 0, kBarFull = 1, kBarEmpty = kBarFull + kStages, kBarLast = kBarEmpty + kStages,
-                       kBarStat = kBarLast + 1, kBarStatFree = kBarStat + 2, kBarS = kBarStatFree + 2,
-                       kBarP = kBarS + 1, kBarDp = kBarP + 1, kBarDs = kBarDp + 2, kBarAcc = kBarDs + 2,
-                       kBarDone = kBarAcc + 1, kBars = kBarDone + 1;
-  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 64 + 1024;
+  static constexpr int kBarRes = 0, kBarE = 1, kBarF = kBarE + kE, kBarFreeE = kBarF + kF, kBarFreeF = kBarFreeE + kE,
+                       kBarLast = kBarFreeF + kF, kBarStat = kBarLast + 2, kBarStatFree = kBarStat + 2,
+                       kBarS = kBarStatFree + 2, kBarP = kBarS + 1, kBarDp = kBarP + 1, kBarDs = kBarDp + 2,
+                       kBarAcc = kBarDs + 2, kBarDone = kBarAcc + 1, kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 64;
 };
 static_assert(BwdCfg<128>::kSmem <= 227 * 1024, "shared memory");
 
@@ -112,15 +116,46 @@ __device__ __forceinline__ void product_acc(uint32_t acc, uint32_t x, uint64_t b
                      (!first || ks != 0) ? 1u : 0u);
 }
 
-// Waits until nothing that the producer started is in flight.
-template <int D>
-__device__ __forceinline__ void drain_stages(const Cta<D>& ct, uint32_t n) {
-  using C = BwdCfg<D>;
-  if (*ct.ctl.abort_flag != 0u) return;
+// Position in a ring of n tiles.
+struct Ring {
+  int n, at;
+  uint32_t phase;
+  __device__ explicit Ring(int size) : n(size), at(0), phase(0u) {}
+  __device__ void next() {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Waits until the copies of the first `used` tiles of a ring have landed.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int n, int used, const WaitCtl& ctl) {
+  if (*ctl.abort_flag != 0u) return;
   volatile uint32_t dummy = 0;
-  const WaitCtl dctl{&dummy, ct.ctl.limit_ns};
-  for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < n; ++i)
-    mbar_wait(ct.bars + C::kBarFull + (n - 1 - i) % C::kStages, ((n - 1 - i) / C::kStages) & 1u, dctl);
+  const WaitCtl dctl{&dummy, ctl.limit_ns};
+  for (int i = 0; i < n && i < used; ++i)
+    mbar_wait(full + (used - 1 - i) % n, (static_cast<uint32_t>(used - 1 - i) / n) & 1u, dctl);
+}
+
+// Copies tile i of a ring (rows: a block of query rows; else 128 keys).  The
+// last tile lands on `last` instead when its end has to be cleared.
+template <int D>
+__device__ __forceinline__ void load_ring(uint8_t* base, uint32_t off, uint64_t* full, uint64_t* free, uint64_t* last,
+                                          const Ring& r, const CUtensorMap* map, bool rows, int at, int hk,
+                                          uint32_t bytes, uint64_t pol, const WaitCtl& ctl) {
+  constexpr uint32_t kTile = kChunkBytes * (D / 64);
+  if (!mbar_wait(free + r.at, r.phase ^ 1u, ctl)) return;
+  uint64_t* bar = last != nullptr ? last : full + r.at;
+  uint8_t* dst = base + off + r.at * kTile;
+  mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+  for (int ch = 0; ch < D / 64; ++ch) {
+    if (rows)
+      tma_load_4d_hint(dst + ch * kChunkBytes, map, bar, ch * 64, 0, at, hk, pol);
+    else
+      tma_load_3d_hint(dst + ch * kChunkBytes, map, bar, ch * 64, at, hk, pol);
+  }
 }
 
 // One accumulator lane (D fp32 values times f) to D values of X at dst.
@@ -177,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                     const BwdArgs f) {
   using C = BwdCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
@@ -196,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     init_barriers<D>(bars);
+    if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
     *abort_flag = 0u;
   }
   __syncthreads();
@@ -211,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows_blk = f.tq * a.g;  // rows of a full block (128 when g divides it)
 
   if (work && rows_blk < 128)  // rows that no copy writes: zero factors must meet finite values
-    for (int s = 0; s < 2 * C::kStages; ++s)
-      clear_tile_rows<D>(base + C::kOffSt + s * C::kTile, rows_blk, static_cast<int>(threadIdx.x), kThreads);
+    for (int s = 0; s < C::kE + C::kF; ++s)
+      clear_tile_rows<D>(base + C::kOffE + s * C::kTile, rows_blk, static_cast<int>(threadIdx.x), kThreads);
   fence_proxy_async_shared();
   if (work && warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
@@ -235,59 +270,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_k, bars + C::kBarRes, ch * 64, it.t0, hk, first);
         tma_load_3d_hint(base + C::kOffB + ch * kChunkBytes, &tmap_v, bars + C::kBarRes, ch * 64, it.t0, hk, first);
       }
+      Ring e(C::kE), o(C::kF);
+      const uint32_t bytes = static_cast<uint32_t>(rows_blk) * 128u * (D / 64);
       for (int i = 0; i < n_blk; ++i) {
-        const int st = i % C::kStages;
-        if (!mbar_wait(bars + C::kBarEmpty + st, ((i / C::kStages) & 1u) ^ 1u, ctl)) continue;
-        uint8_t* dst = base + C::kOffSt + 2 * st * C::kTile;
-        uint64_t* bar = bars + (i == n_blk - 1 && tail < f.tq ? C::kBarLast : C::kBarFull + st);
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(rows_blk) * 256u * (D / 64));
-        for (int ch = 0; ch < D / 64; ++ch) {
-          tma_load_4d_hint(dst + ch * kChunkBytes, &tmap_q, bar, ch * 64, 0, it.s.q0 + r_lo + i * f.tq, hk, last);
-          tma_load_4d_hint(dst + C::kTile + ch * kChunkBytes, &tmap_do, bar, ch * 64, 0, it.s.q0 + r_lo + i * f.tq, hk,
-                           last);
-        }
+        const bool cut = i == n_blk - 1 && tail < f.tq;
+        const int t = it.s.q0 + r_lo + i * f.tq;
+        load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, cut ? bars + C::kBarLast : nullptr, e, &tmap_q,
+                     true, t, hk, bytes, last, ctl);
+        load_ring<D>(base, C::kOffF, bars + C::kBarF, bars + C::kBarFreeF, cut ? bars + C::kBarLast + 1 : nullptr, o,
+                     &tmap_do, true, t, hk, bytes, last, ctl);
+        e.next();
+        o.next();
       }
-      drain_stages<D>(ct, n_blk);
+      drain_ring(bars + C::kBarE, C::kE, n_blk, ctl);
+      drain_ring(bars + C::kBarF, C::kF, n_blk, ctl);
       mbar_wait(bars + C::kBarRes, 0u, ctl);
     }
   } else if (warp == kMmaWarp) {
     if (work && lane == 0) {
       const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
       const uint64_t vd = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
-      const uint64_t sk = smem_desc_kmajor(smem_u32(base + C::kOffSt), 128);
-      const uint64_t sm = smem_desc_mn_sw128(smem_u32(base + C::kOffSt), kChunkBytes, 1024u);
+      const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffE), 128);
+      const uint64_t od = smem_desc_kmajor(smem_u32(base + C::kOffF), 128);
+      const uint64_t qm = smem_desc_mn_sw128(smem_u32(base + C::kOffE), kChunkBytes, 1024u);
+      const uint64_t om = smem_desc_mn_sw128(smem_u32(base + C::kOffF), kChunkBytes, 1024u);
       constexpr uint64_t kT = C::kTile >> 4;
       bool alive = true;
       auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
-      auto ready = [&](int i) {
-        wait(C::kBarFull + i % C::kStages, (i / C::kStages) & 1u);
+      Ring e(C::kE), o(C::kF);  // e: the coming block's Q; o: this block's dO
+      auto scores = [&](Ring& r) {
+        wait(C::kBarE + r.at, r.phase);
         tc_fence_after();
+        if (alive) product_abt<X, D>(t_s, kd, qd + static_cast<uint64_t>(r.at) * kT);
+        umma_commit(bars + C::kBarS);
+      };
+      auto dprob = [&](const Ring& r) {
+        wait(C::kBarF + r.at, r.phase);
+        tc_fence_after();
+        if (alive) product_abt<X, D>(t_dp, vd, od + static_cast<uint64_t>(r.at) * kT);
+        umma_commit(bars + C::kBarDp);
       };
       wait(C::kBarRes, 0u);
-      ready(0);
-      if (alive) product_abt<X, D>(t_s, kd, sk);
-      umma_commit(bars + C::kBarS);
-      if (alive) product_abt<X, D>(t_dp, vd, sk + kT);
-      umma_commit(bars + C::kBarDp);
+      scores(e);
+      dprob(o);
       for (int i = 0; i < n_blk; ++i) {
-        const uint64_t st = static_cast<uint64_t>(i % C::kStages) * (2 * kT);
-        const uint64_t nx = static_cast<uint64_t>((i + 1) % C::kStages) * (2 * kT);
+        const int q_at = e.at, o_at = o.at;
+        e.next();
+        o.next();
         wait(C::kBarP, static_cast<uint32_t>(i) & 1u);
         tc_fence_after();
-        if (alive) product_acc<X, D>(t_dv, t_s, sm + st + kT, i == 0);
-        if (i + 1 < n_blk) {
-          ready(i + 1);
-          if (alive) product_abt<X, D>(t_s, kd, sk + nx);
-          umma_commit(bars + C::kBarS);
-        }
+        if (alive) product_acc<X, D>(t_dv, t_s, om + static_cast<uint64_t>(o_at) * kT, i == 0);
+        umma_commit(bars + C::kBarFreeF + o_at);
+        if (i + 1 < n_blk) scores(e);
         wait(C::kBarDs, static_cast<uint32_t>(i) & 1u);
         tc_fence_after();
-        if (alive) product_acc<X, D>(t_dk, t_dp, sm + st, i == 0);
-        umma_commit(bars + C::kBarEmpty + i % C::kStages);
-        if (i + 1 < n_blk) {
-          if (alive) product_abt<X, D>(t_dp, vd, sk + nx + kT);
-          umma_commit(bars + C::kBarDp);
-        }
+        if (alive) product_acc<X, D>(t_dk, t_dp, qm + static_cast<uint64_t>(q_at) * kT, i == 0);
+        umma_commit(bars + C::kBarFreeE + q_at);
+        if (i + 1 < n_blk) dprob(o);
       }
       umma_commit(bars + C::kBarAcc);
       umma_commit(bars + C::kBarDone);
@@ -301,35 +340,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = i & 1, t0 = it.s.q0 + r_lo + i * f.tq;
         const int rows = (i == n_blk - 1 ? tail : f.tq) * a.g;
         float* st = reinterpret_cast<float*>(base + C::kOffStat) + b * 256;
-        const bool ok = mbar_wait(bars + C::kBarStatFree + b, ((i >> 1) & 1u) ^ 1u, ctl);
-        if (ok) {
+        // all eight loads in flight before the buffer is waited for: one latency per block, off its path
+        float l[4], de[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = u * 32 + static_cast<int>(lane), tok = r / a.g;
+          const long long at = static_cast<long long>(t0 + tok) * a.Hq + hk * a.g + (r - tok * a.g);
+          l[u] = -INFINITY;
+          de[u] = 0.f;
+          if (r < rows) {
+            l[u] = __ldg(a.lse + at);
+            de[u] = __ldg(a.delta + at);
+          }
+        }
+        if (mbar_wait(bars + C::kBarStatFree + b, ((i >> 1) & 1u) ^ 1u, ctl)) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const int r = u * 32 + static_cast<int>(lane), tok = r / a.g;
-            float nl = -INFINITY, de = 0.f;
-            if (r < rows) {
-              const long long at = static_cast<long long>(t0 + tok) * a.Hq + hk * a.g + (r - tok * a.g);
-              const float l = a.lse[at];
-              if (l != -INFINITY) {
-                nl = -l * 1.4426950408889634f;
-                de = a.delta[at];
-              }
-            }
-            st[r] = nl;
-            st[128 + r] = de;
+            const int r = u * 32 + static_cast<int>(lane);
+            const bool none = l[u] == -INFINITY;
+            st[r] = none ? -INFINITY : -l[u] * 1.4426950408889634f;
+            st[128 + r] = none ? 0.f : de[u];
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
         if (i == n_blk - 1 && tail < f.tq) {
-          const int sg = i % C::kStages;
-          if (mbar_wait(bars + C::kBarLast, 0u, ctl)) {
-            clear_tile_rows<D>(base + C::kOffSt + 2 * sg * C::kTile, rows, static_cast<int>(lane), 32);
-            clear_tile_rows<D>(base + C::kOffSt + (2 * sg + 1) * C::kTile, rows, static_cast<int>(lane), 32);
+          for (int x = 0; x < 2; ++x) {  // Q, dO
+            const int at = i % (x ? C::kF : C::kE);
+            if (mbar_wait(bars + C::kBarLast + x, 0u, ctl))
+              clear_tile_rows<D>(base + (x ? C::kOffF : C::kOffE) + at * C::kTile, rows, static_cast<int>(lane), 32);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + (x ? C::kBarF : C::kBarE) + at);
           }
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars + C::kBarFull + sg);
         }
       }
     }
@@ -445,8 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                    const BwdArgs f) {
   using C = BwdCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
@@ -464,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     init_barriers<D>(bars);
+    if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
     *abort_flag = 0u;
   }
   __syncthreads();
@@ -492,37 +535,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_q, bars + C::kBarRes, ch * 64, 0, it.t0, hk, first);
         tma_load_4d_hint(base + C::kOffB + ch * kChunkBytes, &tmap_do, bars + C::kBarRes, ch * 64, 0, it.t0, hk, first);
       }
+      Ring k(C::kE), v(C::kF);
       for (int j = 0; j < top; ++j) {
-        const int st = j % C::kStages;
-        if (!mbar_wait(bars + C::kBarEmpty + st, ((j / C::kStages) & 1u) ^ 1u, ctl)) continue;
-        uint8_t* dst = base + C::kOffSt + 2 * st * C::kTile;
-        uint64_t* bar = bars + (j == top - 1 && fix ? C::kBarLast : C::kBarFull + st);
-        mbar_arrive_expect_tx(bar, 2 * C::kTile);
-        for (int ch = 0; ch < D / 64; ++ch) {
-          tma_load_3d_hint(dst + ch * kChunkBytes, &tmap_k, bar, ch * 64, it.s.k0 + j * 128, hk, last);
-          tma_load_3d_hint(dst + C::kTile + ch * kChunkBytes, &tmap_v, bar, ch * 64, it.s.k0 + j * 128, hk, last);
-        }
+        const bool cut = j == top - 1 && fix;
+        load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, cut ? bars + C::kBarLast : nullptr, k, &tmap_k,
+                     false, it.s.k0 + j * 128, hk, C::kTile, last, ctl);
+        load_ring<D>(base, C::kOffF, bars + C::kBarF, bars + C::kBarFreeF, cut ? bars + C::kBarLast + 1 : nullptr, v,
+                     &tmap_v, false, it.s.k0 + j * 128, hk, C::kTile, last, ctl);
+        k.next();
+        v.next();
       }
-      drain_stages<D>(ct, top);
+      drain_ring(bars + C::kBarE, C::kE, top, ctl);
+      drain_ring(bars + C::kBarF, C::kF, top, ctl);
       mbar_wait(bars + C::kBarRes, 0u, ctl);
     }
   } else if (warp == kMmaWarp) {
     if (work && lane == 0) {
       const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
       const uint64_t od = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
-      const uint64_t sk = smem_desc_kmajor(smem_u32(base + C::kOffSt), 128);
-      const uint64_t sm = smem_desc_mn_sw128(smem_u32(base + C::kOffSt), kChunkBytes, 1024u);
+      const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffE), 128);
+      const uint64_t vd = smem_desc_kmajor(smem_u32(base + C::kOffF), 128);
+      const uint64_t km = smem_desc_mn_sw128(smem_u32(base + C::kOffE), kChunkBytes, 1024u);
       constexpr uint64_t kT = C::kTile >> 4;
       bool alive = true;
       auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
-      auto scores = [&](int j) {  // S(j) and dP(j); dP(j-2), whose buffer this is, went into dQ before
-        const uint64_t st = static_cast<uint64_t>(j % C::kStages) * (2 * kT);
-        wait(C::kBarFull + j % C::kStages, (j / C::kStages) & 1u);
+      Ring k(C::kE), v(C::kF);
+      int free_at = 0;
+      auto scores = [&](int j) {  // S(j) and dP(j); dS(j-2), whose buffer this is, went into dQ before
+        wait(C::kBarE + k.at, k.phase);
         tc_fence_after();
-        if (alive) product_abt<X, D>(t_s, qd, sk + st);
+        if (alive) product_abt<X, D>(t_s, qd, kd + static_cast<uint64_t>(k.at) * kT);
         umma_commit(bars + C::kBarS);
-        if (alive) product_abt<X, D>(t_dp + 128 * (j & 1), od, sk + st + kT);
+        wait(C::kBarF + v.at, v.phase);
+        tc_fence_after();
+        if (alive) product_abt<X, D>(t_dp + 128 * (j & 1), od, vd + static_cast<uint64_t>(v.at) * kT);
         umma_commit(bars + C::kBarDp + (j & 1));
+        umma_commit(bars + C::kBarFreeF + v.at);
+        k.next();
+        v.next();
       };
       wait(C::kBarRes, 0u);
       scores(0);
@@ -534,8 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(C::kBarDs + (j & 1), static_cast<uint32_t>(j >> 1) & 1u);
         tc_fence_after();
         if (alive)
-          product_acc<X, D>(t_dq, t_dp + 128 * (j & 1), sm + static_cast<uint64_t>(j % C::kStages) * (2 * kT), j == 0);
-        umma_commit(bars + C::kBarEmpty + j % C::kStages);
+          product_acc<X, D>(t_dq, t_dp + 128 * (j & 1), km + static_cast<uint64_t>(free_at) * kT, j == 0);
+        umma_commit(bars + C::kBarFreeE + free_at);
+        if (++free_at == C::kE) free_at = 0;
       }
       umma_commit(bars + C::kBarAcc);
       umma_commit(bars + C::kBarDone);
@@ -545,15 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kPrepWarp) {
     if (work && fix) {
-      const int j = top - 1, st = j % C::kStages;
-      const bool ok = mbar_wait(bars + C::kBarLast, 0u, ctl);
-      if (ok) {
-        clear_tile_rows<D>(base + C::kOffSt + 2 * st * C::kTile, it.s.lk - j * 128, static_cast<int>(lane), 32);
-        clear_tile_rows<D>(base + C::kOffSt + (2 * st + 1) * C::kTile, it.s.lk - j * 128, static_cast<int>(lane), 32);
+      const int j = top - 1;
+      for (int x = 0; x < 2; ++x) {  // K, V
+        const int at = j % (x ? C::kF : C::kE);
+        if (mbar_wait(bars + C::kBarLast + x, 0u, ctl))
+          clear_tile_rows<D>(base + (x ? C::kOffF : C::kOffE) + at * C::kTile, it.s.lk - j * 128,
+                             static_cast<int>(lane), 32);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + (x ? C::kBarF : C::kBarE) + at);
       }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + C::kBarFull + st);
     }
   } else if (warp < kEpiWarps) {
     const int hf = warp >> 2, row = (warp & 3) * 32 + static_cast<int>(lane);
@@ -657,6 +709,7 @@ cudaError_t run(const AttnParams& p, cudaStream_t stream) {
   f.tq = 128 / p.g;
   f.c = p.scale * 1.4426950408889634f;
   f.wait_ns = kAttnWaitNs;
+  static_assert(C::kOffA % 1024 == 0 && C::kTile % 1024 == 0, "swizzled tiles start on 1024 bytes");
   cudaError_t e;
   if ((e = smem_limit_once<attn_dq_kernel<X, D>>(C::kSmem)) != cudaSuccess) return e;
   if ((e = smem_limit_once<attn_dkv_kernel<X, D>>(C::kSmem)) != cudaSuccess) return e;
