@@ -17,11 +17,11 @@
 // K and V are read once per group, and one token of g heads (decoding) is a
 // block like any other.
 //
-// m is not the running maximum but the maximum when it was last raised: it is
-// raised, and O and l rescaled, only when the maximum has grown by more than
-// 8 in the exponent.  P then stays below 2^8, in range of fp16 too, and the
-// quotient O / l is the same; the rescaling of O in TMEM, 128 values a row,
-// nearly never runs after the first tiles.
+// m is a reference, not the running maximum: the maximum of the first tile,
+// raised to the maximum so far (with O and l rescaled and the tile's P formed
+// again) only when a tile's sum of P exceeds 2^12.  Up to there P is in range of
+// fp16 too, its relative precision is the same and so is the quotient O / l; no
+// maximum is taken in the tiles that follow.
 //
 // Roles (TILES = 2: 12 warps, one CTA per SM; TILES = 1: 6 warps, two CTAs
 // per SM):
@@ -43,6 +43,8 @@
 
 namespace csa {
 namespace {
+
+constexpr float kRaise = 4096.f;  // a tile's sum of P above which the reference is raised
 
 template <int D, int TILES>
 struct FwdCfg {
@@ -69,7 +71,6 @@ struct FwdArgs {
   int nb;        // ceil(Tq / (TILES * tq))
   int n_split;
   float c;       // scale * log2(e)
-  float lag;     // 8 / c: how far the reference may fall behind the maximum
   float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
   float* part_lse;  // [n_split][Tq * Hq]
   unsigned long long wait_ns;
@@ -202,11 +203,10 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
           wait(C::kBarQ + w, 0u);
           scores(w, 0);
         }
-      umma_commit(bars + C::kBarEmpty + 0);
       for (int j = lo; j < top; ++j, n += 2) {
         const uint32_t sv = (n + 1) % C::kStages, sk = (n + 2) % C::kStages;
         full(n + 1);
-        bool have_k = false;
+        if (j + 1 < top) full(n + 2);
         for (int w = 0; w < TILES; ++w) {
           if (j >= hi[w]) continue;
           wait(C::kBarP + w, static_cast<uint32_t>(j - lo) & 1u);
@@ -218,16 +218,11 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
                                vd + static_cast<uint64_t>(sv * (C::kTile >> 4)) + static_cast<uint64_t>(128 * ks), kIdO,
                                (j != lo || ks != 0) ? 1u : 0u);
           }
-          if (j + 1 < hi[w]) {
-            if (!have_k) full(n + 2);
-            have_k = true;
+          if (j + 1 < hi[w])
             scores(w, sk);
-          } else {
+          else
             umma_commit(bars + C::kBarO + w);
-          }
         }
-        umma_commit(bars + C::kBarEmpty + sv);
-        if (j + 1 < top) umma_commit(bars + C::kBarEmpty + sk);
       }
       umma_commit(bars + C::kBarDone);
       volatile uint32_t dummy = 0;
@@ -249,9 +244,18 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
     const float c = f.c;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    // The last block's scores of a tile are formed last: when they stand, all products with this key tile and
+    // the former value tile are done, and one thread gives both back to the producer.  (A commit of the issuing
+    // thread for each would hold up its next products.)
+    const bool frees = my_hi == top && (w == TILES - 1 || n_tok[TILES - 1] <= 0) && (threadIdx.x & 127) == 0;
     for (int j = lo; j < my_hi; ++j) {
       ok = ok && mbar_wait(bars + C::kBarS + w, static_cast<uint32_t>(j - lo) & 1u, ctl);
       tc_fence_after();
+      if (frees) {
+        const uint32_t n = 2u * static_cast<uint32_t>(j - lo);
+        mbar_arrive(bars + C::kBarEmpty + n % C::kStages);
+        if (j > lo) mbar_arrive(bars + C::kBarEmpty + (n - 1) % C::kStages);
+      }
       float s[4][32];
       if (ok) {
 #pragma unroll
@@ -264,34 +268,41 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
           for (int i = 0; i < 128; ++i)
             if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
         }
-        const float mt = row_max(s);
-        if (j == lo) {
-          m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + f.lag)) {
+        if (j == lo) m = row_max(s);
+        float tile;
+        // P of the tile, over the scores in TMEM; the scores stay in s
+        auto probs = [&] {
+          const float b = m == -INFINITY ? 0.f : -m * c;
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+              const float2 x = ffma2(make_float2(s[i][2 * u], s[i][2 * u + 1]), make_float2(c, c), make_float2(b, b));
+              const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+              sum[u & 1] = fadd2(sum[u & 1], p);
+              pk[u] = pack_pair<X>(p.x, p.y);
+            }
+            tmem_st16(ts + 16 * i, pk);
+          }
+          tile = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        };
+        probs();
+        if (__any_sync(0xffffffffu, tile > kRaise)) {
           // the former tiles' product with V has completed: its commit preceded this tile's scores
-          const float mn = fmaxf(m, mt);
+          const float mn = fmaxf(m, row_max(s));
           const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
           m = mn;
           l *= r;
+          tmem_wait_st();
+          if (j != lo) {
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
-        }
-        const float ms = m == -INFINITY ? 0.f : m;
-        const float2 c2 = make_float2(c, c), b2 = make_float2(-ms * c, -ms * c);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            const float2 x = ffma2(make_float2(s[i][2 * u], s[i][2 * u + 1]), c2, b2);
-            const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            sum[u & 1] = fadd2(sum[u & 1], p);
-            pk[u] = pack_pair<X>(p.x, p.y);
+            for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
           }
-          tmem_st16(ts + 16 * i, pk);
+          probs();
         }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        l += tile;
         tmem_wait_st();
         if ((j + 1) * 128 > it.s.lk && (w == 0 || j >= lo_hi)) {
           // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
@@ -399,7 +410,6 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
   f.nb = static_cast<int>((static_cast<long long>(p.Tq) + TILES * f.tq - 1) / (TILES * f.tq));
   f.n_split = n_split;
   f.c = p.scale * 1.4426950408889634f;
-  f.lag = 8.f / f.c;
   f.part_o = static_cast<float*>(workspace);
   f.part_lse = f.part_o + static_cast<long long>(n_split) * p.Tq * p.Hq * D;
   f.wait_ns = kAttnWaitNs;
