@@ -195,28 +195,38 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
         }
         umma_commit(bars + C::kBarS + w);
       };
-      uint32_t n = 0;  // index of the key tile in the ring (the value tile is n + 1)
-      auto full = [&](uint32_t i) { wait(C::kBarFull + static_cast<int>(i % C::kStages), (i / C::kStages) & 1u); };
-      full(0);
+      // positions in the ring, kept without divisions: this thread's own time is on the products' path
+      uint32_t at = 0, phase = 0;
+      auto full = [&]() -> uint32_t {  // waits for the ring's next tile and returns its stage
+        const uint32_t st = at;
+        wait(C::kBarFull + static_cast<int>(st), phase);
+        if (++at == static_cast<uint32_t>(C::kStages)) {
+          at = 0;
+          phase ^= 1u;
+        }
+        return st;
+      };
+      uint32_t sk = full();
       for (int w = 0; w < TILES; ++w)
         if (hi[w] > lo) {
           wait(C::kBarQ + w, 0u);
-          scores(w, 0);
+          scores(w, sk);
         }
-      for (int j = lo; j < top; ++j, n += 2) {
-        const uint32_t sv = (n + 1) % C::kStages, sk = (n + 2) % C::kStages;
-        full(n + 1);
-        if (j + 1 < top) full(n + 2);
+      uint32_t ph = 0;
+      for (int j = lo; j < top; ++j, ph ^= 1u) {
+        const uint32_t sv = full();
+        if (j + 1 < top) sk = full();
+        const uint64_t v = vd + static_cast<uint64_t>(sv * (C::kTile >> 4));
+#pragma unroll
         for (int w = 0; w < TILES; ++w) {
           if (j >= hi[w]) continue;
-          wait(C::kBarP + w, static_cast<uint32_t>(j - lo) & 1u);
+          wait(C::kBarP + w, ph);
           tc_fence_after();
           if (alive) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_bf16_tmem_a(tmem + C::kO + w * 128, tmem + w * 128 + 8u * ks,
-                               vd + static_cast<uint64_t>(sv * (C::kTile >> 4)) + static_cast<uint64_t>(128 * ks), kIdO,
-                               (j != lo || ks != 0) ? 1u : 0u);
+              umma_bf16_tmem_a(tmem + C::kO + w * 128, tmem + w * 128 + 8u * ks, v + static_cast<uint64_t>(128 * ks),
+                               kIdO, (j != lo || ks != 0) ? 1u : 0u);
           }
           if (j + 1 < hi[w])
             scores(w, sk);
@@ -256,52 +266,57 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
         mbar_arrive(bars + C::kBarEmpty + n % C::kStages);
         if (j > lo) mbar_arrive(bars + C::kBarEmpty + (n - 1) % C::kStages);
       }
-      float s[4][32];
       if (ok) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_wait32(s[i]);
-        if ((j + 1) * 128 > see_all) {
-          const int lim = see - j * 128;
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
-        }
-        if (j == lo) m = row_max(s);
         float tile;
-        // P of the tile, over the scores in TMEM; the scores stay in s
-        auto probs = [&] {
+        uint32_t pk[4][16];
+        // the row's 128 scores, those it does not see at -inf
+        auto load = [&](float (&s)[4][32]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_wait32(s[i]);
+          if ((j + 1) * 128 > see_all) {
+            const int lim = see - j * 128;
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
+          }
+        };
+        auto probs = [&](const float (&s)[4][32]) {
           const float b = m == -INFINITY ? 0.f : -m * c;
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-              const float2 x = ffma2(make_float2(s[i][2 * u], s[i][2 * u + 1]), make_float2(c, c), make_float2(b, b));
-              const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-              sum[u & 1] = fadd2(sum[u & 1], p);
-              pk[u] = pack_pair<X>(p.x, p.y);
-            }
-            tmem_st16(ts + 16 * i, pk);
+          for (int u = 0; u < 64; ++u) {
+            const float* x = s[u >> 4] + 2 * (u & 15);
+            const float2 e = ffma2(make_float2(x[0], x[1]), make_float2(c, c), make_float2(b, b));
+            const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            sum[u & 1] = fadd2(sum[u & 1], p);
+            pk[u >> 4][u & 15] = pack_pair<X>(p.x, p.y);
           }
           tile = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         };
-        probs();
+        {
+          float s[4][32];
+          load(s);
+          if (j == lo) m = row_max(s);
+          probs(s);
+        }
         if (__any_sync(0xffffffffu, tile > kRaise)) {
+          float s[4][32];
+          load(s);
           // the former tiles' product with V has completed: its commit preceded this tile's scores
           const float mn = fmaxf(m, row_max(s));
           const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
           m = mn;
           l *= r;
-          tmem_wait_st();
           if (j != lo) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
           }
-          probs();
+          probs(s);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_st16(ts + 16 * i, pk[i]);
         l += tile;
         tmem_wait_st();
         if ((j + 1) * 128 > it.s.lk && (w == 0 || j >= lo_hi)) {
