@@ -4,8 +4,8 @@
 //   s_j = scale q.k_j over the keys a row sees, out = sum_j p_j v_j with
 //   p = softmax(s), lse = log sum_j exp(s_j).
 //
-// A CTA takes TILES blocks of 128 query rows of one sequence and one key head
-// and walks the keys in tiles of 128, in one pass with a running reference m
+// An item is TILES blocks of 128 query rows of one sequence and one key head; a
+// CTA walks the keys in tiles of 128, in one pass with a running reference m
 // and sum l:
 //   S = Q . K^T     (A = q block, B = k tile, both in shared memory, to TMEM)
 //   P = 2^(c (S - m)) in the storage type, c = scale log2(e), written over S
@@ -23,17 +23,21 @@
 // fp16 too, its relative precision is the same and so is the quotient O / l; no
 // maximum is taken in the tiles that follow.
 //
-// Roles (TILES = 2: 12 warps, one CTA per SM; TILES = 1: 6 warps, two CTAs
+// Roles (TILES = 2: 12 warps, one CTA per SM; TILES = 1: 8 warps, two CTAs
 // per SM):
 //   warps 0..4 TILES-1  softmax: one thread per row, all 128 scores of a tile
 //                       in registers; then the division and the stores
 //   next warp           issuer of the products, one thread
 //   next warp           TMA producer, one thread
+//   next warp           items: a CTA that has one more item to come takes it from
+//                       the blocks of the grid that have not started (cluster
+//                       launch control), so its rows, first tiles and query
+//                       block are on their way while the former item ends
 // With two blocks the tensor cores form S and O of one while the softmax of
 // the other runs; TMEM holds S0 S1 O0 O1 (512 columns).  With one block the
 // second CTA on the SM does the same.
 //
-// Keys may be split over gridDim.z CTAs (few rows, long caches): each writes
+// Keys may be split over n_split items (few rows, long caches): each writes
 // its normalised O and lse in fp32, and a second kernel joins them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,20 +54,22 @@ template <int D, int TILES>
 struct FwdCfg {
   static constexpr uint32_t kTile = kChunkBytes * (D / 64);  // 128 rows x D, 64 columns per 16 KB chunk
   static constexpr int kStages = TILES == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
-  static constexpr int kWarps = TILES == 2 ? 12 : 6;
+  static constexpr int kWarps = TILES == 2 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kMmaWarp = 4 * TILES, kTmaWarp = kMmaWarp + 1;
+  static constexpr int kMmaWarp = 4 * TILES, kTmaWarp = kMmaWarp + 1, kItemWarp = kMmaWarp + 2;
   static constexpr uint32_t kOffQ = 0, kOffKv = kOffQ + TILES * kTile, kOffBar = kOffKv + kStages * kTile;
-  // barriers: q full [TILES], kv full / empty [stages], s full, p full, o full [TILES], done
-  static constexpr int kBarQ = 0, kBarFull = TILES, kBarEmpty = kBarFull + kStages, kBarS = kBarEmpty + kStages,
-                       kBarP = kBarS + TILES, kBarO = kBarP + TILES, kBarDone = kBarO + TILES,
-                       kBars = kBarDone + 1;
-  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 64 + 1024;
+  static constexpr int kSlots = 2;  // items ahead
+  static constexpr int kBarQ = 0, kBarQFree = TILES, kBarFull = 2 * TILES, kBarEmpty = kBarFull + kStages,
+                       kBarS = kBarEmpty + kStages, kBarP = kBarS + TILES, kBarO = kBarP + TILES,
+                       kBarItem = kBarO + TILES, kBarItemFree = kBarItem + kSlots, kBarNext = kBarItemFree + kSlots,
+                       kBarDone = kBarNext + 1, kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16, kOffItem = kOffMisc + 32;
+  static constexpr uint32_t kSmem = kOffItem + kSlots * 64;
   static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
   static constexpr uint32_t kO = 128 * TILES;  // first column of O
 };
 static_assert(FwdCfg<128, 2>::kSmem <= 227 * 1024 && FwdCfg<64, 2>::kSmem <= 227 * 1024, "one CTA per SM");
-static_assert(2 * FwdCfg<128, 1>::kSmem <= 226 * 1024 && 2 * FwdCfg<64, 1>::kSmem <= 226 * 1024, "two CTAs per SM");
+static_assert(2 * (FwdCfg<128, 1>::kSmem + 1024) <= 228 * 1024 && 2 * (FwdCfg<64, 1>::kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 
 struct FwdArgs {
   AttnParams a;
@@ -76,308 +82,432 @@ struct FwdArgs {
   unsigned long long wait_ns;
 };
 
+// One item: a run of at most TILES * tq query rows of one sequence (or of rows
+// outside all of them: lk = 0), one key head, one share of the keys.
+struct FwdItem {
+  SeqExt s;
+  int t0, t1;     // rows; t0 >= t1: no more items
+  int lo, hi[2];  // block w walks the key tiles lo .. hi[w]-1
+  int n_tok[2];   // tokens of each block
+  int hk, z;      // key head, share
+};
+static_assert(sizeof(FwdItem) <= 64, "a slot");
+
+// A warp; every lane gets the result.
+template <int TILES>
+__device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
+  const AttnParams& a = f.a;
+  FwdItem it;
+  const uint32_t rest = id / static_cast<uint32_t>(a.Hk);
+  it.hk = static_cast<int>(id - rest * static_cast<uint32_t>(a.Hk));
+  const uint32_t x = rest / static_cast<uint32_t>(f.n_split);
+  it.z = static_cast<int>(rest - x * static_cast<uint32_t>(f.n_split));
+  // rows are taken from the last ones on: those that see most keys first
+  const RowItem r = find_row_item(a, TILES * f.tq, f.nb, f.nb + a.N - static_cast<int>(x));
+  it.s = r.s;
+  it.t0 = r.t0;
+  it.t1 = r.t1;
+  it.lo = 0;
+  int top = 0;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    it.n_tok[w] = w < TILES ? min(f.tq, max(0, r.t1 - r.t0 - w * f.tq)) : 0;
+    const int see = it.n_tok[w] > 0 ? keys_seen(a, r.s, r.t0 + w * f.tq + it.n_tok[w] - 1 - r.s.q0) : 0;
+    it.hi[w] = (see + 127) >> 7;
+    top = max(top, it.hi[w]);
+  }
+  if (f.n_split > 1) {
+    const int share = (top + f.n_split - 1) / f.n_split;
+    it.lo = it.z * share;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) it.hi[w] = max(it.lo, min(it.hi[w], it.lo + share));
+  }
+  return it;
+}
+
 template <typename X, int D, int TILES>
 __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const FwdArgs f) {
   using C = FwdCfg<D, TILES>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
-  RowItem* item = reinterpret_cast<RowItem*>(base + C::kOffMisc + 16);
+  uint8_t* next_slot = base + C::kOffMisc;  // 16 bytes: the answer to a request for the next item
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc + 16);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 20);
   const AttnParams& a = f.a;
   const int warp = threadIdx.x / 32;
   const uint32_t lane = lane_id();
-  const int hk = static_cast<int>(blockIdx.x % a.Hk);
 
-  if (warp == C::kMmaWarp) {
-    // blocks are taken from the last one on: the rows that see most keys first
-    const RowItem it = find_row_item(a, TILES * f.tq, f.nb, f.nb + a.N - static_cast<int>(blockIdx.x / a.Hk));
-    if (lane == 0) *item = it;
-    if (blockIdx.x == 0 && blockIdx.z == 0)
-      for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
-  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < TILES; ++i) {
-      mbar_init(bars + C::kBarQ + i, 1);
-      mbar_init(bars + C::kBarS + i, 1);
-      mbar_init(bars + C::kBarP + i, 4);
-      mbar_init(bars + C::kBarO + i, 1);
+    for (int i = 0; i < C::kBars; ++i) {
+      int n = 1;
+      if (i >= C::kBarP && i < C::kBarP + TILES) n = 4;
+      if (i >= C::kBarItemFree && i < C::kBarItemFree + C::kSlots) n = 2 + 4 * TILES;
+      mbar_init(bars + i, n);
     }
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(bars + C::kBarFull + i, 1);
-      mbar_init(bars + C::kBarEmpty + i, 1);
-    }
-    mbar_init(bars + C::kBarDone, 1);
+    if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  __syncthreads();
-  const RowItem it = *item;
-  if (it.t0 >= it.t1) return;  // no row here (two borders fall together)
-
-  // key tiles of this CTA's share: block w walks lo .. hi[w]-1
-  int n_tok[TILES], hi[TILES], lo = 0, top = 0;
-#pragma unroll
-  for (int w = 0; w < TILES; ++w) {
-    n_tok[w] = min(f.tq, max(0, it.t1 - it.t0 - w * f.tq));
-    const int see = n_tok[w] > 0 ? keys_seen(a, it.s, it.t0 + w * f.tq + n_tok[w] - 1 - it.s.q0) : 0;
-    hi[w] = (see + 127) >> 7;
-    top = max(top, hi[w]);
+  if (warp == C::kTmaWarp && lane == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
   }
-  if (f.n_split > 1) {
-    const int share = (top + f.n_split - 1) / f.n_split;
-    lo = static_cast<int>(blockIdx.z) * share;
-#pragma unroll
-    for (int w = 0; w < TILES; ++w) hi[w] = max(lo, min(hi[w], lo + share));
-    top = max(lo, min(top, lo + share));
-  }
-  const bool work = top > lo;
-
-  if (work && warp == C::kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = work ? *tmem_slot : 0u;
+  const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, f.wait_ns};
+  // the role's next item; null after the last one or a wait that gave up.  Its slot is the role's until
+  // give_item(): fields are read where they are needed instead of being held in registers
+  uint32_t n_item = 0;
+  auto next_item = [&]() -> const volatile FwdItem* {
+    const uint32_t sl = n_item & 1u;
+    if (!mbar_wait(bars + C::kBarItem + sl, (n_item >> 1) & 1u, ctl)) return nullptr;
+    const volatile FwdItem* it = reinterpret_cast<const volatile FwdItem*>(base + C::kOffItem + 64 * sl);
+    return it->t0 < it->t1 ? it : nullptr;
+  };
+  auto give_item = [&] {
+    mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
+    ++n_item;
+  };
 
-  if (warp == C::kTmaWarp) {
-    reg_shrink<TILES == 2>();
-    if (work && lane == 0) {  // ------------------------------------------- TMA producer
-      const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
-      for (int w = 0; w < TILES; ++w) {
-        if (hi[w] <= lo) continue;
-        mbar_arrive_expect_tx(bars + C::kBarQ + w, static_cast<uint32_t>(f.tq * a.g) * 128u * (D / 64));
-        for (int ch = 0; ch < D / 64; ++ch)
-          tma_load_4d_hint(base + C::kOffQ + w * C::kTile + ch * kChunkBytes, &tmap_q, bars + C::kBarQ + w, ch * 64, 0,
-                           it.t0 + w * f.tq, hk, q_pol);
+  if (warp == C::kItemWarp) {
+    reg_shrink<TILES>();
+    // ----------------------------------------------------------------------- items
+    // Prepared one ahead of the other roles: the search for a run of rows is a chain of global loads.
+    if (blockIdx.x == 0)
+      for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
+    uint32_t id = blockIdx.x, n = 0, asked = 0;
+    bool more = true;
+    while (more) {
+      if (lane == 0) request_next(next_slot, bars + C::kBarNext);
+      const FwdItem it = make_item<TILES>(f, id);
+      if (it.t0 < it.t1) {  // two borders may fall together: no row
+        const uint32_t sl = n & 1u;
+        more = mbar_wait(bars + C::kBarItemFree + sl, ((n >> 1) & 1u) ^ 1u, ctl);
+        if (lane == 0) *reinterpret_cast<FwdItem*>(base + C::kOffItem + 64 * sl) = it;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarItem + sl);
+        ++n;
       }
-      uint32_t n = 0;
-      for (int j = lo; j < top; ++j)
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t st = n % C::kStages;
-          if (!mbar_wait(bars + C::kBarEmpty + st, ((n / C::kStages) & 1u) ^ 1u, ctl)) continue;
-          mbar_arrive_expect_tx(bars + C::kBarFull + st, C::kTile);
+      volatile uint32_t dummy = 0;  // the answer is waited for even when a role gave up: it writes shared memory
+      const WaitCtl dctl{&dummy, ctl.limit_ns};
+      const bool got = mbar_wait(bars + C::kBarNext, asked & 1u, dctl);
+      ++asked;
+      more = got && more && answer_next(next_slot, id);
+    }
+    if (*abort_flag == 0u) {
+      const uint32_t sl = n & 1u;
+      mbar_wait(bars + C::kBarItemFree + sl, ((n >> 1) & 1u) ^ 1u, ctl);
+      if (lane == 0) reinterpret_cast<FwdItem*>(base + C::kOffItem + 64 * sl)->t1 = INT32_MIN;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarItem + sl);
+    }
+  } else if (warp == C::kTmaWarp) {
+    reg_shrink<TILES>();
+    if (lane == 0) {  // --------------------------------------------------- TMA producer
+      const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
+      uint32_t at = 0, phase = 1, used = 0, nq[TILES] = {};
+      while (const volatile FwdItem* it = next_item()) {
+        const int lo = it->lo, hi[2] = {it->hi[0], it->hi[1]}, top = max(hi[0], hi[1]);
+        const int t0 = it->t0, k0 = it->s.k0, hk = it->hk;
+        give_item();
+        for (int w = 0; w < TILES; ++w) {
+          if (hi[w] <= lo) continue;
+          if (!mbar_wait(bars + C::kBarQFree + w, (nq[w] & 1u) ^ 1u, ctl)) continue;
+          ++nq[w];
+          mbar_arrive_expect_tx(bars + C::kBarQ + w, static_cast<uint32_t>(f.tq * a.g) * 128u * (D / 64));
           for (int ch = 0; ch < D / 64; ++ch)
-            tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k,
-                             bars + C::kBarFull + st, ch * 64, it.s.k0 + j * 128, hk, kv_pol);
+            tma_load_4d_hint(base + C::kOffQ + w * C::kTile + ch * kChunkBytes, &tmap_q, bars + C::kBarQ + w, ch * 64, 0,
+                             t0 + w * f.tq, hk, q_pol);
         }
+        for (int j = lo; j < top; ++j)
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t st = at, ph = phase;
+            if (++at == static_cast<uint32_t>(C::kStages)) {
+              at = 0;
+              phase ^= 1u;
+            }
+            ++used;
+            if (!mbar_wait(bars + C::kBarEmpty + st, ph, ctl)) continue;
+            mbar_arrive_expect_tx(bars + C::kBarFull + st, C::kTile);
+            for (int ch = 0; ch < D / 64; ++ch)
+              tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k,
+                               bars + C::kBarFull + st, ch * 64, k0 + j * 128, hk, kv_pol);
+          }
+      }
       // no copy is in flight when the CTA ends: the last use of each stage has landed
       volatile uint32_t dummy = 0;
       const WaitCtl dctl{&dummy, ctl.limit_ns};
       if (*abort_flag == 0u)
-        for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < n; ++i)
-          mbar_wait(bars + C::kBarFull + (n - 1 - i) % C::kStages, ((n - 1 - i) / C::kStages) & 1u, dctl);
+        for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < used; ++i)
+          mbar_wait(bars + C::kBarFull + (used - 1 - i) % C::kStages, ((used - 1 - i) / C::kStages) & 1u, dctl);
     }
   } else if (warp == C::kMmaWarp) {
-    reg_shrink<TILES == 2>();
-    if (work && lane == 0) {  // ------------------------------------------- issuer of the products
-      const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
-      const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffKv), 128);
-      const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffKv), kChunkBytes, 1024u);
-      constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false), kIdO = idesc_f16<X>(128, D, true);
-      bool alive = true;
-      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
-      auto scores = [&](int w, uint32_t st) {  // S_w = Q_w . K^T
-        tc_fence_after();
+    reg_shrink<TILES>();
+    // ----------------------------------------------------------------------- issuer of the products
+    // The warp runs as one (uniform operands: a descriptor moved to uniform registers for each product made the
+    // products wait for their issue), one elected thread issues.
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
+    const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffKv), 128);
+    const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffKv), kChunkBytes, 1024u);
+    constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false), kIdO = idesc_f16<X>(128, D, true), kT = C::kTile >> 4;
+    bool alive = true;
+    auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
+    // S_w = Q_w . K^T
+    auto scores = [&](int w, uint32_t st) {
+      tc_fence_after();
+      if (elect_one()) {
         if (alive) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
-            umma_bf16(tmem + w * 128, qd + static_cast<uint64_t>(w * (C::kTile >> 4)) + o,
-                      kd + static_cast<uint64_t>(st * (C::kTile >> 4)) + o, kIdS, ks != 0 ? 1u : 0u);
+            umma_bf16(tm + w * 128, qd + static_cast<uint64_t>(w * kT) + o, kd + static_cast<uint64_t>(st * kT) + o, kIdS,
+                      ks != 0 ? 1u : 0u);
           }
         }
         umma_commit(bars + C::kBarS + w);
-      };
-      // positions in the ring, kept without divisions: this thread's own time is on the products' path
-      uint32_t at = 0, phase = 0;
-      auto full = [&]() -> uint32_t {  // waits for the ring's next tile and returns its stage
-        const uint32_t st = at;
-        wait(C::kBarFull + static_cast<int>(st), phase);
-        if (++at == static_cast<uint32_t>(C::kStages)) {
-          at = 0;
-          phase ^= 1u;
-        }
-        return st;
-      };
-      uint32_t sk = full();
+      }
+      __syncwarp();
+    };
+    // positions in the ring, kept without divisions; `seen` is what the look ahead found
+    uint32_t at = 0, phase = 0;
+    auto full = [&](bool seen) -> uint32_t {  // waits for the ring's next tile and returns its stage
+      const uint32_t st = at;
+      if (!seen) wait(C::kBarFull + static_cast<int>(st), phase);
+      if (++at == static_cast<uint32_t>(C::kStages)) {
+        at = 0;
+        phase ^= 1u;
+      }
+      return st;
+    };
+    uint32_t p_par[TILES] = {}, q_par[TILES] = {};  // parities of P and Q
+    while (const volatile FwdItem* it = next_item()) {
+      const int lo = uniform(it->lo), hi[2] = {uniform(it->hi[0]), uniform(it->hi[1])}, top = max(hi[0], hi[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
+      ++n_item;
+      if (top <= lo) continue;
+      uint32_t sk = full(false);
+#pragma unroll
       for (int w = 0; w < TILES; ++w)
         if (hi[w] > lo) {
-          wait(C::kBarQ + w, 0u);
+          wait(C::kBarQ + w, q_par[w]);
+          q_par[w] ^= 1u;
           scores(w, sk);
         }
-      uint32_t ph = 0;
-      for (int j = lo; j < top; ++j, ph ^= 1u) {
-        const uint32_t sv = full();
-        if (j + 1 < top) sk = full();
-        const uint64_t v = vd + static_cast<uint64_t>(sv * (C::kTile >> 4));
+      for (int j = lo; j < top; ++j) {
+        const uint32_t sv = full(false);
+        if (j + 1 < top) sk = full(false);
 #pragma unroll
         for (int w = 0; w < TILES; ++w) {
           if (j >= hi[w]) continue;
-          wait(C::kBarP + w, ph);
+          wait(C::kBarP + w, p_par[w]);
+          p_par[w] ^= 1u;
           tc_fence_after();
-          if (alive) {
+          if (elect_one()) {
+            if (alive) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_bf16_tmem_a(tmem + C::kO + w * 128, tmem + w * 128 + 8u * ks, v + static_cast<uint64_t>(128 * ks),
-                               kIdO, (j != lo || ks != 0) ? 1u : 0u);
+              for (int ks = 0; ks < 8; ++ks)
+                umma_bf16_tmem_a(tm + C::kO + w * 128, tm + w * 128 + 8u * ks,
+                                 vd + static_cast<uint64_t>(sv * kT) + static_cast<uint64_t>(128 * ks), kIdO,
+                                 (j != lo || ks != 0) ? 1u : 0u);
+            }
+            if (j + 1 >= hi[w]) umma_commit(bars + C::kBarO + w);
           }
-          if (j + 1 < hi[w])
-            scores(w, sk);
-          else
-            umma_commit(bars + C::kBarO + w);
+          __syncwarp();
+          if (j + 1 < hi[w]) scores(w, sk);
         }
       }
-      umma_commit(bars + C::kBarDone);
-      volatile uint32_t dummy = 0;
-      const WaitCtl dctl{&dummy, ctl.limit_ns};
-      mbar_wait(bars + C::kBarDone, 0u, dctl);
     }
+    if (elect_one()) umma_commit(bars + C::kBarDone);
+    __syncwarp();
+    volatile uint32_t dummy = 0;
+    const WaitCtl dctl{&dummy, ctl.limit_ns};
+    mbar_wait(bars + C::kBarDone, 0u, dctl);
   } else if (warp < 4 * TILES) {  // ----------------------------------------- softmax, output
-    reg_grow<TILES == 2>();
+    reg_grow<TILES>();
     const int w = warp >> 2, row = (warp & 3) * 32 + static_cast<int>(lane);
     const int tok = row / a.g, head = row - tok * a.g;
-    const bool row_ok = tok < (w == 0 ? n_tok[0] : n_tok[TILES - 1]);
-    const int my_hi = w == 0 ? hi[0] : hi[TILES - 1], lo_hi = hi[0];
-    const int t = it.t0 + w * f.tq + tok;
-    const int see = row_ok ? keys_seen(a, it.s, t - it.s.q0) : 0;
-    // every row of the block sees the keys below this
-    const int see_all = my_hi > lo ? keys_seen(a, it.s, it.t0 + w * f.tq - it.s.q0) : 0;
     const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 128;
     const uint32_t to = ts + (C::kO - w * 128) + w * 128;
     const float c = f.c;
-    float m = -INFINITY, l = 0.f;
+    uint32_t s_phase = 0, o_phase = 0, ring = 0;  // ring: tiles of the ring before this item
     bool ok = true;
-    // The last block's scores of a tile are formed last: when they stand, all products with this key tile and
-    // the former value tile are done, and one thread gives both back to the producer.  (A commit of the issuing
-    // thread for each would hold up its next products.)
-    const bool frees = my_hi == top && (w == TILES - 1 || n_tok[TILES - 1] <= 0) && (threadIdx.x & 127) == 0;
-    for (int j = lo; j < my_hi; ++j) {
-      ok = ok && mbar_wait(bars + C::kBarS + w, static_cast<uint32_t>(j - lo) & 1u, ctl);
-      tc_fence_after();
-      if (frees) {
-        const uint32_t n = 2u * static_cast<uint32_t>(j - lo);
-        mbar_arrive(bars + C::kBarEmpty + n % C::kStages);
-        if (j > lo) mbar_arrive(bars + C::kBarEmpty + (n - 1) % C::kStages);
+    while (const volatile FwdItem* it = next_item()) {
+      const int lo = it->lo, my_hi = it->hi[w], top = max(it->hi[0], it->hi[1]), lk = it->s.lk;
+      const bool row_ok = tok < it->n_tok[w];
+      int see = 0, see_all = 0;  // keys this row sees; keys every row of the block sees
+      if (my_hi > lo) {
+        const SeqExt e{it->s.q0, it->s.q1, it->s.k0, lk};
+        const int r = it->t0 + w * f.tq - e.q0;
+        see_all = keys_seen(a, e, r);
+        if (row_ok) see = keys_seen(a, e, r + tok);
       }
-      if (ok) {
-        float tile;
-        uint32_t pk[4][16];
-        // the row's 128 scores, those it does not see at -inf
-        auto load = [&](float (&s)[4][32]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s[i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_wait32(s[i]);
-          if ((j + 1) * 128 > see_all) {
-            const int lim = see - j * 128;
-#pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
-          }
-        };
-        auto probs = [&](const float (&s)[4][32]) {
-          const float b = m == -INFINITY ? 0.f : -m * c;
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int u = 0; u < 64; ++u) {
-            const float* x = s[u >> 4] + 2 * (u & 15);
-            const float2 e = ffma2(make_float2(x[0], x[1]), make_float2(c, c), make_float2(b, b));
-            const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-            sum[u & 1] = fadd2(sum[u & 1], p);
-            pk[u >> 4][u & 15] = pack_pair<X>(p.x, p.y);
-          }
-          tile = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        };
-        {
-          float s[4][32];
-          load(s);
-          if (j == lo) m = row_max(s);
-          probs(s);
+      float m = -INFINITY, l = 0.f;
+      // The last block's scores of a tile are formed last: when they stand, all products with this key tile and
+      // the former value tile are done, and one thread gives both back to the producer.  (A commit of the issuing
+      // thread for each would hold up its next products.)
+      const bool first_thread = (threadIdx.x & 127) == 0;
+      const bool frees = my_hi == top && (w == TILES - 1 || it->n_tok[TILES - 1] <= 0) && first_thread;
+      for (int j = lo; j < my_hi; ++j) {
+        ok = ok && mbar_wait(bars + C::kBarS + w, s_phase, ctl);
+        s_phase ^= 1u;
+        tc_fence_after();
+        const uint32_t nk = ring + 2u * static_cast<uint32_t>(j - lo);
+        if (frees) {
+          mbar_arrive(bars + C::kBarEmpty + nk % C::kStages);
+          if (j > lo) mbar_arrive(bars + C::kBarEmpty + (nk - 1) % C::kStages);
         }
-        if (__any_sync(0xffffffffu, tile > kRaise)) {
-          float s[4][32];
-          load(s);
-          // the former tiles' product with V has completed: its commit preceded this tile's scores
-          const float mn = fmaxf(m, row_max(s));
-          const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
-          m = mn;
-          l *= r;
-          if (j != lo) {
+        if (j == my_hi - 1 && first_thread) mbar_arrive(bars + C::kBarQFree + w);  // the last product with Q
+        if (ok) {
+          float tile;
+          uint32_t pk[4][16];
+          // the row's 128 scores, those it does not see at -inf
+          auto load = [&](float (&s)[4][32]) {
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
+            for (int i = 0; i < 4; ++i) tmem_ld32_start(ts + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_wait32(s[i]);
+            if ((j + 1) * 128 > see_all) {
+              const int lim = see - j * 128;
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
+            }
+          };
+          auto probs = [&](const float (&s)[4][32]) {
+            const float b = m == -INFINITY ? 0.f : -m * c;
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int u = 0; u < 64; ++u) {
+              const float* x = s[u >> 4] + 2 * (u & 15);
+              const float2 e = ffma2(make_float2(x[0], x[1]), make_float2(c, c), make_float2(b, b));
+              const float2 p = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+              sum[u & 1] = fadd2(sum[u & 1], p);
+              pk[u >> 4][u & 15] = pack_pair<X>(p.x, p.y);
+            }
+            tile = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          };
+          {
+            float s[4][32];
+            load(s);
+            if (j == lo) m = row_max(s);
+            probs(s);
           }
-          probs(s);
-        }
+          if (__any_sync(0xffffffffu, tile > kRaise)) {
+            float s[4][32];
+            load(s);
+            // the former tiles' product with V has completed: its commit preceded this tile's scores
+            const float mn = fmaxf(m, row_max(s));
+            const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
+            m = mn;
+            l *= r;
+            if (j != lo) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_st16(ts + 16 * i, pk[i]);
-        l += tile;
-        tmem_wait_st();
-        if ((j + 1) * 128 > it.s.lk && (w == 0 || j >= lo_hi)) {
-          // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
-          const uint32_t nv = 2u * static_cast<uint32_t>(j - lo) + 1u, sv = nv % C::kStages;
-          if (mbar_wait(bars + C::kBarFull + sv, (nv / C::kStages) & 1u, ctl))
-            clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, it.s.lk - j * 128, threadIdx.x & 127, 128);
-          fence_proxy_async_shared();
+              for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
+            }
+            probs(s);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_st16(ts + 16 * i, pk[i]);
+          l += tile;
+          tmem_wait_st();
+          if ((j + 1) * 128 > lk && (w == 0 || j >= it->hi[0])) {
+            // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
+            const uint32_t nv = nk + 1u, sv = nv % C::kStages;
+            if (mbar_wait(bars + C::kBarFull + sv, (nv / C::kStages) & 1u, ctl))
+              clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, lk - j * 128, threadIdx.x & 127, 128);
+            fence_proxy_async_shared();
+          }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarP + w);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + C::kBarP + w);
-    }
-    // ------------------------------------------------------------------ output
-    const bool any = my_hi > lo;
-    if (any) {
-      ok = ok && mbar_wait(bars + C::kBarO + w, 0u, ctl);
-      tc_fence_after();
-    }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    const long long at = static_cast<long long>(t) * a.Hq + hk * a.g + head;
-    const float lse = l > 0.f || l != l ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float o[32];
-      __syncwarp();
-      if (any && ok) {
-        tmem_ld32_start(to + 32 * i, o);
-        tmem_wait32(o);
+      ring += 2u * static_cast<uint32_t>(max(0, top - lo));
+      // ---------------------------------------------------------------- output
+      const bool any = my_hi > lo;
+      if (any) {
+        ok = ok && mbar_wait(bars + C::kBarO + w, o_phase, ctl);
+        o_phase ^= 1u;
+        tc_fence_after();
+        if (frees) mbar_arrive(bars + C::kBarEmpty + (ring - 1u) % C::kStages);
       }
-      if (!row_ok) continue;
+      const bool seen = any && ok && (l > 0.f || l != l);
+      const float inv = seen ? 1.f / l : 0.f;
+      const float lse = seen ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      const long long rows = static_cast<long long>(a.Tq) * a.Hq;
+      // element offset of row `r` of the block (and -1 for a row it does not hold)
+      const int t_blk = it->t0 + w * f.tq, hk = it->hk, z = it->z;
+      const long long at = row_ok ? static_cast<long long>(t_blk + tok) * a.Hq + hk * a.g + head : -1;
+      if (at >= 0) {
+        if (f.n_split > 1)
+          f.part_lse[z * rows + at] = lse;
+        else
+          a.lse[at] = lse;
+      }
+      // Lanes 4 i .. 4 i + 3 exchange their rows' 16-byte pieces, so that four lanes store 64 bytes of one row:
+      // a store of 16 bytes by each of 32 rows takes as many passes through L1 as it has rows.
+      long long at4[4];
 #pragma unroll
-      for (int u = 0; u < 32; ++u) o[u] = any && ok && inv != 0.f ? o[u] * inv : 0.f;
-      if (f.n_split > 1) {
-        float4* dst = reinterpret_cast<float4*>(
-            f.part_o + (static_cast<long long>(blockIdx.z) * a.Tq * a.Hq + at) * D + 32 * i);
+      for (int u = 0; u < 4; ++u) at4[u] = __shfl_sync(0xffffffffu, at, (lane & ~3u) + u);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<X*>(a.out) + at * D + 32 * i);
+      for (int i = 0; i < D / 32; ++i) {
+        float o[32];
+        __syncwarp();
+        if (any) {
+          tmem_ld32_start(to + 32 * i, o);
+          tmem_wait32(o);
+        }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          dst[u] = make_uint4(pack_pair<X>(o[8 * u], o[8 * u + 1]), pack_pair<X>(o[8 * u + 2], o[8 * u + 3]),
+        for (int u = 0; u < 32; ++u) o[u] = seen ? o[u] * inv : 0.f;
+        if (f.n_split > 1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 16 fp32 values: four pieces
+            uint4 q[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              q[u] = make_uint4(__float_as_uint(o[16 * h + 4 * u]), __float_as_uint(o[16 * h + 4 * u + 1]),
+                                __float_as_uint(o[16 * h + 4 * u + 2]), __float_as_uint(o[16 * h + 4 * u + 3]));
+            transpose4(q, lane);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (at4[u] >= 0)
+                reinterpret_cast<uint4*>(f.part_o + (z * rows + at4[u]) * D + 32 * i + 16 * h)[lane & 3] = q[u];
+          }
+        } else {
+          uint4 q[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            q[u] = make_uint4(pack_pair<X>(o[8 * u], o[8 * u + 1]), pack_pair<X>(o[8 * u + 2], o[8 * u + 3]),
                               pack_pair<X>(o[8 * u + 4], o[8 * u + 5]), pack_pair<X>(o[8 * u + 6], o[8 * u + 7]));
+          transpose4(q, lane);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (at4[u] >= 0) reinterpret_cast<uint4*>(static_cast<X*>(a.out) + at4[u] * D + 32 * i)[lane & 3] = q[u];
+        }
       }
-    }
-    if (row_ok) {
-      if (f.n_split > 1)
-        f.part_lse[static_cast<long long>(blockIdx.z) * a.Tq * a.Hq + at] = lse;
-      else
-        a.lse[at] = lse;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
+      ++n_item;
     }
   } else {
-    reg_shrink<TILES == 2>();
+    reg_shrink<TILES>();
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (work && warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // out = sum_z w_z O_z / sum_z w_z with w_z = exp(lse_z - max lse): D/4 threads
@@ -433,10 +563,9 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
     return cudaErrorInvalidValue;
   cudaError_t e = smem_limit_once<attn_fwd_kernel<X, D, TILES>>(C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk;
+  const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk * n_split;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  attn_fwd_kernel<X, D, TILES>
-      <<<dim3(static_cast<unsigned>(grid), 1, n_split), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+  attn_fwd_kernel<X, D, TILES><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
   if ((e = cudaGetLastError()) != cudaSuccess || n_split == 1) return e;
   const long long rows = static_cast<long long>(p.Tq) * p.Hq;
   constexpr int PER = 256 / (D / 4);

@@ -120,16 +120,89 @@ __device__ __forceinline__ RowItem find_key_item(const AttnParams& a, int step, 
   return find_item<true>(a, step, nb, x);
 }
 
-// ----------------------------------------------------------------- register splits
-// 384 threads start with 168 registers each (64512): 256 of them grow to 200,
-// 128 shrink to 104 (51200 + 13312 = 64512).
-template <bool ON>
-__device__ __forceinline__ void reg_grow() {
-  if constexpr (ON) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+// ----------------------------------------------------------------- next item
+// Cluster launch control: asks for one block of the grid that has not started;
+// the 16-byte answer at `slot` completes on `bar`.  One thread.
+__device__ __forceinline__ void request_next(uint8_t* slot, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16u);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(slot)),
+      "r"(smem_u32(bar))
+      : "memory");
 }
-template <bool ON>
+// The answer: false when none was left (no further request may follow), else
+// `id` is the index of the block, which will not be launched.
+__device__ __forceinline__ bool answer_next(const uint8_t* slot, uint32_t& id) {
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(slot))
+      : "memory");
+  id = x;
+  fence_proxy_async_shared();  // the next answer is written by the async proxy
+  return ok != 0u;
+}
+
+// ----------------------------------------------------------------- waits on the critical path
+// As mbar_wait, by a whole warp whose control flow stays uniform (what follows
+// keeps its operands in uniform registers), and polling without suspending the
+// threads: suspended ones take longer to come back than the tensor pipe has
+// work queued.  The limit is looked at every 1024 polls.
+__device__ __forceinline__ bool mbar_look_warp(uint64_t* bar, uint32_t parity) {
+  return __any_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
+}
+__device__ __forceinline__ bool mbar_spin_warp(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_look_warp(bar, parity)) return true;
+    if ((n & 1023u) == 1023u) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      const bool late = t - t0 > ctl.limit_ns;
+      if (__any_sync(0xffffffffu, late || *ctl.abort_flag != 0u)) {
+        *ctl.abort_flag = 1u;
+        if (late) record_error(kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(x));
+  return x != 0u;
+}
+// Lane 0's value, as one the compiler knows to be the same in all lanes.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// ----------------------------------------------------------------- register splits
+// TILES = 2: 384 threads start with 168 registers each (64512): 256 of them grow
+// to 216, 128 shrink to 72 (55296 + 9216 = 64512).  TILES = 1, two CTAs per SM:
+// 256 threads start with 128 (32768): 128 grow to 184, 128 shrink to 72 (32768).
+template <int TILES>
+__device__ __forceinline__ void reg_grow() {
+  if constexpr (TILES == 2)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+}
+template <int TILES>
 __device__ __forceinline__ void reg_shrink() {
-  if constexpr (ON) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if constexpr (TILES == 2)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
 }
 
 // ----------------------------------------------------------------- small helpers
@@ -147,6 +220,31 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   const uint32_t t = is_bf16<X>() ? 1u : 0u;  // operand type: 0 f16, 1 bf16
   return (1u << 4) | (t << 7) | (t << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The products of csa_ptx.cuh with descriptors given as their low words (start
+// address; the high words are the same for every tile): the issuing thread
+// then adds 32-bit offsets instead of holding 64-bit sums in registers.
+__device__ __forceinline__ uint32_t desc_hi(uint64_t d) { return static_cast<uint32_t>(d >> 32); }
+__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_lo_tmem_a(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -208,6 +306,27 @@ __device__ __forceinline__ void tmem_scale16(uint32_t t, float r) {
     for (int i = 0; i < 8; ++i) u[8 * h + i] = __float_as_uint(v[i] * r);
   }
   tmem_st16(t, u);
+}
+
+// Lanes 4 i + r (r = 0..3) hold four pieces each; afterwards lane 4 i + r holds
+// piece r of the lanes 4 i .. 4 i + 3, in their order.
+__device__ __forceinline__ void transpose4(uint4 (&q)[4], uint32_t lane) {
+  auto swap = [&](uint4& x, uint4& y, uint32_t mask) {  // upper lane gives x, lower lane gives y
+    const bool up = (lane & mask) != 0u;
+    uint4 s = up ? x : y;
+    s.x = __shfl_xor_sync(0xffffffffu, s.x, mask);
+    s.y = __shfl_xor_sync(0xffffffffu, s.y, mask);
+    s.z = __shfl_xor_sync(0xffffffffu, s.z, mask);
+    s.w = __shfl_xor_sync(0xffffffffu, s.w, mask);
+    if (up)
+      x = s;
+    else
+      y = s;
+  };
+  swap(q[0], q[1], 1u);
+  swap(q[2], q[3], 1u);
+  swap(q[0], q[2], 2u);
+  swap(q[1], q[3], 2u);
 }
 
 // Clears the rows from `first` on of a 128-row tile (D/64 chunks), by
