@@ -287,7 +287,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bars + C::kBarRes, 0u, ctl);
     }
   } else if (warp == kMmaWarp) {
-    if (work && lane == 0) {
+    // the warp runs as one, with uniform operands; an elected thread issues the products
+    if (work) {
+      const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(ct.tmem)));
+      const uint32_t m_s = tm, m_dp = tm + 128, m_dv = tm + 256, m_dk = tm + 384;
+      const int n = uniform(n_blk);
       const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
       const uint64_t vd = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
       const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffE), 128);
@@ -296,40 +300,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t om = smem_desc_mn_sw128(smem_u32(base + C::kOffF), kChunkBytes, 1024u);
       constexpr uint64_t kT = C::kTile >> 4;
       bool alive = true;
-      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
+      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
       Ring e(C::kE), o(C::kF);  // e: the coming block's Q; o: this block's dO
-      auto scores = [&](Ring& r) {
+      auto scores = [&](const Ring& r) {
         wait(C::kBarE + r.at, r.phase);
         tc_fence_after();
-        if (alive) product_abt<X, D>(t_s, kd, qd + static_cast<uint64_t>(r.at) * kT);
-        umma_commit(bars + C::kBarS);
+        if (elect_one()) {
+          if (alive) product_abt<X, D>(m_s, kd, qd + static_cast<uint64_t>(r.at) * kT);
+          umma_commit(bars + C::kBarS);
+        }
+        __syncwarp();
       };
       auto dprob = [&](const Ring& r) {
         wait(C::kBarF + r.at, r.phase);
         tc_fence_after();
-        if (alive) product_abt<X, D>(t_dp, vd, od + static_cast<uint64_t>(r.at) * kT);
-        umma_commit(bars + C::kBarDp);
+        if (elect_one()) {
+          if (alive) product_abt<X, D>(m_dp, vd, od + static_cast<uint64_t>(r.at) * kT);
+          umma_commit(bars + C::kBarDp);
+        }
+        __syncwarp();
       };
       wait(C::kBarRes, 0u);
       scores(e);
       dprob(o);
-      for (int i = 0; i < n_blk; ++i) {
+      for (int i = 0; i < n; ++i) {
         const int q_at = e.at, o_at = o.at;
         e.next();
         o.next();
         wait(C::kBarP, static_cast<uint32_t>(i) & 1u);
         tc_fence_after();
-        if (alive) product_acc<X, D>(t_dv, t_s, om + static_cast<uint64_t>(o_at) * kT, i == 0);
-        umma_commit(bars + C::kBarFreeF + o_at);
-        if (i + 1 < n_blk) scores(e);
+        if (elect_one()) {
+          if (alive) product_acc<X, D>(m_dv, m_s, om + static_cast<uint64_t>(o_at) * kT, i == 0);
+          umma_commit(bars + C::kBarFreeF + o_at);
+        }
+        __syncwarp();
+        if (i + 1 < n) scores(e);
         wait(C::kBarDs, static_cast<uint32_t>(i) & 1u);
         tc_fence_after();
-        if (alive) product_acc<X, D>(t_dk, t_dp, qm + static_cast<uint64_t>(q_at) * kT, i == 0);
-        umma_commit(bars + C::kBarFreeE + q_at);
-        if (i + 1 < n_blk) dprob(o);
+        if (elect_one()) {
+          if (alive) product_acc<X, D>(m_dk, m_dp, qm + static_cast<uint64_t>(q_at) * kT, i == 0);
+          umma_commit(bars + C::kBarFreeE + q_at);
+        }
+        __syncwarp();
+        if (i + 1 < n) dprob(o);
       }
-      umma_commit(bars + C::kBarAcc);
-      umma_commit(bars + C::kBarDone);
+      if (elect_one()) {
+        umma_commit(bars + C::kBarAcc);
+        umma_commit(bars + C::kBarDone);
+      }
+      __syncwarp();
       volatile uint32_t dummy = 0;
       const WaitCtl dctl{&dummy, ctl.limit_ns};
       mbar_wait(bars + C::kBarDone, 0u, dctl);
@@ -550,7 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bars + C::kBarRes, 0u, ctl);
     }
   } else if (warp == kMmaWarp) {
-    if (work && lane == 0) {
+    // the warp runs as one, with uniform operands; an elected thread issues the products
+    if (work) {
+      const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(ct.tmem)));
+      const int n = uniform(top);
       const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffA), 128);
       const uint64_t od = smem_desc_kmajor(smem_u32(base + C::kOffB), 128);
       const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffE), 128);
@@ -558,38 +580,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t km = smem_desc_mn_sw128(smem_u32(base + C::kOffE), kChunkBytes, 1024u);
       constexpr uint64_t kT = C::kTile >> 4;
       bool alive = true;
-      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_wait(bars + bar, parity, ctl); };
+      auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
       Ring k(C::kE), v(C::kF);
       int free_at = 0;
       auto scores = [&](int j) {  // S(j) and dP(j); dS(j-2), whose buffer this is, went into dQ before
         wait(C::kBarE + k.at, k.phase);
         tc_fence_after();
-        if (alive) product_abt<X, D>(t_s, qd, kd + static_cast<uint64_t>(k.at) * kT);
-        umma_commit(bars + C::kBarS);
+        if (elect_one()) {
+          if (alive) product_abt<X, D>(tm, qd, kd + static_cast<uint64_t>(k.at) * kT);
+          umma_commit(bars + C::kBarS);
+        }
+        __syncwarp();
         wait(C::kBarF + v.at, v.phase);
         tc_fence_after();
-        if (alive) product_abt<X, D>(t_dp + 128 * (j & 1), od, vd + static_cast<uint64_t>(v.at) * kT);
-        umma_commit(bars + C::kBarDp + (j & 1));
-        umma_commit(bars + C::kBarFreeF + v.at);
+        if (elect_one()) {
+          if (alive) product_abt<X, D>(tm + 128 + 128 * (j & 1), od, vd + static_cast<uint64_t>(v.at) * kT);
+          umma_commit(bars + C::kBarDp + (j & 1));
+          umma_commit(bars + C::kBarFreeF + v.at);
+        }
+        __syncwarp();
         k.next();
         v.next();
       };
       wait(C::kBarRes, 0u);
       scores(0);
-      for (int j = 0; j < top; ++j) {
-        if (j + 1 < top) {
+      for (int j = 0; j < n; ++j) {
+        if (j + 1 < n) {
           wait(C::kBarP, static_cast<uint32_t>(j) & 1u);  // S(j) is in registers
           scores(j + 1);
         }
         wait(C::kBarDs + (j & 1), static_cast<uint32_t>(j >> 1) & 1u);
         tc_fence_after();
-        if (alive)
-          product_acc<X, D>(t_dq, t_dp + 128 * (j & 1), km + static_cast<uint64_t>(free_at) * kT, j == 0);
-        umma_commit(bars + C::kBarFreeE + free_at);
+        if (elect_one()) {
+          if (alive)
+            product_acc<X, D>(tm + 384, tm + 128 + 128 * (j & 1), km + static_cast<uint64_t>(free_at) * kT, j == 0);
+          umma_commit(bars + C::kBarFreeE + free_at);
+        }
+        __syncwarp();
         if (++free_at == C::kE) free_at = 0;
       }
-      umma_commit(bars + C::kBarAcc);
-      umma_commit(bars + C::kBarDone);
+      if (elect_one()) {
+        umma_commit(bars + C::kBarAcc);
+        umma_commit(bars + C::kBarDone);
+      }
+      __syncwarp();
       volatile uint32_t dummy = 0;
       const WaitCtl dctl{&dummy, ctl.limit_ns};
       mbar_wait(bars + C::kBarDone, 0u, dctl);
