@@ -132,7 +132,7 @@ csa_status check_attn_inputs(const csa_attn_problem* p, const void* q, const voi
 }
 size_t attn_workspace_bytes(const csa_attn_problem* p, int which) {
   if (check_attn(p) != CSA_OK) return 0;
-  if (which == 1) return (static_cast<size_t>(p->Tq) * p->Hq * 4 + 255) / 256 * 256;
+  if (which == 1) return attn_bwd_plan(p->N, p->Tq, p->Tk, p->Hq, p->Hk, p->D).total;
   if (which != 0 || p->Tq == 0 || !attn_supported(p)) return 0;
   // split keys: fp32 outputs and lse of each share
   const AttnPlan plan = attn_plan(p->N, p->Tq, p->Tk, p->Hk, p->Hq / p->Hk);
@@ -250,11 +250,10 @@ csa_status csa_attn_backward(const csa_attn_problem* p, const void* dout, const 
   a.dout = dout;
   a.out = const_cast<void*>(out);
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(workspace);
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  if (launch_attn_backward(a, p->dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSA_ERR_CUDA;
+  if (launch_attn_backward(a, p->dtype, workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return CSA_ERR_CUDA;
   return CSA_OK;
 }
 

@@ -62,7 +62,7 @@ struct FwdCfg {
   static constexpr int kBarQ = 0, kBarQFree = TILES, kBarFull = 2 * TILES, kBarEmpty = kBarFull + kStages,
                        kBarS = kBarEmpty + kStages, kBarP = kBarS + TILES, kBarO = kBarP + TILES,
                        kBarItem = kBarO + TILES, kBarItemFree = kBarItem + kSlots, kBarNext = kBarItemFree + kSlots,
-                       kBarDone = kBarNext + 1, kBars = kBarDone + 1;
+                       kBarSoon = kBarNext + 1, kBarDone = kBarSoon + 1, kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16, kOffItem = kOffMisc + 32;
   static constexpr uint32_t kSmem = kOffItem + kSlots * 64;
   static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
@@ -181,27 +181,30 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
   if (warp == C::kItemWarp) {
     reg_shrink<TILES>();
     // ----------------------------------------------------------------------- items
-    // Prepared one ahead of the other roles: the search for a run of rows is a chain of global loads.
+    // Prepared ahead of the other roles: the search for a run of rows is a chain of global loads.
     if (blockIdx.x == 0)
       for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
     uint32_t id = blockIdx.x, n = 0, asked = 0;
     bool more = true;
     while (more) {
-      if (lane == 0) request_next(next_slot, bars + C::kBarNext);
       const FwdItem it = make_item<TILES>(f, id);
       if (it.t0 < it.t1) {  // two borders may fall together: no row
-        const uint32_t sl = n & 1u;
-        more = mbar_wait(bars + C::kBarItemFree + sl, ((n >> 1) & 1u) ^ 1u, ctl);
-        if (lane == 0) *reinterpret_cast<FwdItem*>(base + C::kOffItem + 64 * sl) = it;
+        if (lane == 0) *reinterpret_cast<FwdItem*>(base + C::kOffItem + 64 * (n & 1u)) = it;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + C::kBarItem + sl);
+        if (lane == 0) mbar_arrive(bars + C::kBarItem + (n & 1u));
         ++n;
+        // Another one is asked for when the copies of this one have all been started, two or three tiles before
+        // its end: an item that a CTA holds ahead is one that no idle CTA can take.
+        more = mbar_wait(bars + C::kBarSoon, (n - 1u) & 1u, ctl) &&
+               mbar_wait(bars + C::kBarItemFree + (n & 1u), ((n >> 1) & 1u) ^ 1u, ctl);
       }
+      if (!more) break;
+      if (lane == 0) request_next(next_slot, bars + C::kBarNext);
       volatile uint32_t dummy = 0;  // the answer is waited for even when a role gave up: it writes shared memory
       const WaitCtl dctl{&dummy, ctl.limit_ns};
       const bool got = mbar_wait(bars + C::kBarNext, asked & 1u, dctl);
       ++asked;
-      more = got && more && answer_next(next_slot, id);
+      more = got && answer_next(next_slot, id);
     }
     if (*abort_flag == 0u) {
       const uint32_t sl = n & 1u;
@@ -242,6 +245,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
               tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k,
                                bars + C::kBarFull + st, ch * 64, k0 + j * 128, hk, kv_pol);
           }
+        mbar_arrive(bars + C::kBarSoon);
       }
       // no copy is in flight when the CTA ends: the last use of each stage has landed
       volatile uint32_t dummy = 0;

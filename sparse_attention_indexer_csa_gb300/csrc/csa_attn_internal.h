@@ -41,7 +41,7 @@ struct AttnParams {
   void *dq, *dk, *dv;
 };
 cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
-cudaError_t launch_attn_backward(const AttnParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_backward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
 cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream);
 cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream);
 
@@ -64,6 +64,29 @@ inline AttnPlan attn_plan(int N, int Tq, int Tk, int Hk, int g) {
   const long long want = p.tiles == 1 ? 4 * 304 : 152;
   if (items < want && key_tiles >= 8)
     p.n_split = static_cast<int>(std::min<long long>((want + items - 1) / items, key_tiles / 4));
+  return p;
+}
+
+// How the backward cuts the dk, dv work, and what its workspace holds: delta,
+// the order of the runs of keys, the shares' sums.
+struct AttnBwdPlan {
+  int n_split;   // shares of the rows that see a run of 128 keys
+  bool ordered;  // more items than SMs: the longest first
+  size_t off_order, off_part, total;
+};
+inline AttnBwdPlan attn_bwd_plan(int N, int Tq, int Tk, int Hq, int Hk, int D) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  AttnBwdPlan p;
+  const long long runs = std::max<long long>((static_cast<long long>(Tk) + 127) / 128, std::min(N, Tk));
+  const long long items = std::max<long long>(1, runs * Hk);
+  // blocks of 128 rows that an average run of keys meets
+  const long long blocks = static_cast<long long>(Tq / std::max(1, std::min(N, Tq))) * (Hq / Hk) / 128;
+  p.n_split = 1;
+  if (items < 2 * 152) p.n_split = static_cast<int>(std::max<long long>(1, std::min((3 * 152 + items - 1) / items, blocks / 16)));
+  p.ordered = items * p.n_split > 152;
+  p.off_order = up(static_cast<size_t>(Tq) * Hq * 4);
+  p.off_part = up(p.off_order + (p.ordered ? (static_cast<size_t>((static_cast<long long>(Tk) + 127) / 128) + N + 1) * 4 : 0));
+  p.total = p.off_part + (p.n_split > 1 ? static_cast<size_t>(p.n_split) * Tk * Hk * D * 8 : 0);
   return p;
 }
 

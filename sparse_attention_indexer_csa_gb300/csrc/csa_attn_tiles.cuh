@@ -69,9 +69,9 @@ struct RowItem {
 // between the x-th and the next of those borders in ascending order (two
 // borders that fall together leave an empty run).  The x-th is found by a
 // search for how many multiples are among the first x+1 borders, 32 probes at
-// a time.  A warp; every lane gets the result.  Entries out of order give some
+// a time by a warp, whose lanes all get the result (or by one thread).  Entries out of order give some
 // other runs inside 0..Tq.
-template <bool KEYS>
+template <bool KEYS, bool WARP = true>
 __device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int nb, int x) {
   const int lane = static_cast<int>(lane_id());
   const int T = KEYS ? a.Tk : a.Tq;
@@ -84,6 +84,13 @@ __device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int 
   const int k = x + 1;
   int lo = max(0, k - nB), hi = min(k, nb);
   if (lo > hi) return RowItem{0, 0, SeqExt{0, 0, 0, 0}};
+  while (!WARP && lo < hi) {  // one thread: by halves
+    const int i = (lo + hi + 1) >> 1;
+    if (static_cast<long long>(i - 1) * step <= start(k - i))
+      lo = i;
+    else
+      hi = i - 1;
+  }
   while (lo < hi) {
     const int span = hi - lo, stride = (span + 31) / 32;
     const int i = lo + min(span, (lane + 1) * stride);  // lo < i <= hi, so 0 <= k - i < nB
