@@ -36,7 +36,6 @@ NormRopeParams norm_rope_params(const csa_norm_rope_problem* p, const void* q, c
                                 const void* kw, const int64_t* pos, const uint64_t* freqs) {
   NormRopeParams n;
   std::memset(&n, 0, sizeof(n));
-  n.rows = static_cast<long long>(p->T) * (p->Hq + p->Hk);
   n.T = p->T;
   n.Hq = p->Hq;
   n.Hk = p->Hk;

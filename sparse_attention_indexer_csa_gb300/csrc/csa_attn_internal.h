@@ -9,7 +9,6 @@ namespace csa {
 
 // ----------------------------------------------------------------- norm + rotation
 struct NormRopeParams {
-  long long rows;  // T * (Hq + Hk)
   int T, Hq, Hk, D, rot, off, w_dtype;
   float eps, inv_d;
   const void *q, *k, *qw, *kw;
@@ -19,7 +18,9 @@ struct NormRopeParams {
   void *yq, *yk;              // outputs (forward) or gradients of q and k (backward)
   const void *gq, *gk;        // cotangents (backward)
   float *dqw, *dkw;           // gradients of the weights (backward)
-  float* part;                // partial sums of them, [blocks][2][D] (backward)
+  float* part;                // partial sums of them, [blocks][D] (backward)
+  int q_blocks;               // blocks that work on q; the others work on k
+  int cs_tokens;              // tokens whose cosines and sines a chunk of rows needs at most
 };
 constexpr int kNormRopeBlocks = 152 * 4;  // blocks (and partial sums) of the backward at most
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);
