@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import abi
-from .abi import CSA_BF16, CSA_F32, _check, _stream
+from .abi import CSA_BF16, CSA_F32, _check
 
 CSA_F16 = 2
 
@@ -63,9 +63,9 @@ _ready = None
 def load() -> ctypes.CDLL:
     """The library with this header's entry points typed (once)."""
     global _ready
+    if _ready is not None:
+        return _ready
     lib = abi.load()
-    if _ready is lib:
-        return lib
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     R, A = ctypes.POINTER(NormRopeProblem), ctypes.POINTER(AttnProblem)
     lib.csa_rope_freqs.argtypes = [ctypes.c_double, i32, vp]
@@ -86,57 +86,86 @@ def load() -> ctypes.CDLL:
 
 # ----------------------------------------------------------------------------- argument checks
 def _dtype(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be bf16, fp16 or fp32, not {t.dtype}")
-    return _DTYPES[t.dtype]
+    return code
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None or t.numel() == 0 else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr() or None
 
 
 def _want(t: torch.Tensor, what: str, shape, dtype, device, strided: bool = False):
     """Shape, type, device and layout of one argument."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must live on the GPU")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's tensors on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.device != device or t.dtype != dtype or t.shape != shape or device.type != "cuda":
+        if not t.is_cuda:
+            raise ValueError(f"{what} must live on the GPU")
+        if t.device != device:
+            raise ValueError(f"{what} is on {t.device}, the call's tensors on {device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
         raise ValueError(f"{what} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if strided:
-        if t.numel() and t.shape[-1] != 1 and t.stride(-1) != 1:
-            raise ValueError(f"the innermost dimension of {what} must be contiguous")
-        if any(t.shape[d] > 1 and t.stride(d) == 0 for d in range(t.dim() - 1)):
-            raise ValueError(f"{what} may not repeat memory (stride 0)")
-    elif not t.is_contiguous():
+    if t.is_contiguous():
+        return
+    if not strided:
         raise ValueError(f"{what} must be contiguous")
+    st = t.stride()
+    if t.numel() and shape[-1] != 1 and st[-1] != 1:
+        raise ValueError(f"the innermost dimension of {what} must be contiguous")
+    if any(n > 1 and x == 0 for n, x in zip(shape[:-1], st)):
+        raise ValueError(f"{what} may not repeat memory (stride 0)")
 
 
-def _on(stream, device):
-    """The stream of a call, as a torch stream of `device`."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
+def _current_stream(device) -> int:
+    """Handle of the current stream (without the stream object where torch has a call for that)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and device.index is not None:
+        return raw(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An uninitialised tensor that `stream` uses: its memory is not given to
-    other work before what `stream` holds at its release has run."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if t.numel() and stream != torch.cuda.current_stream(device):
-        # the allocator's memory may still be read by work of the current stream
-        stream.wait_stream(torch.cuda.current_stream(device))
-        t.record_stream(stream)
-    return t
+class _Call:
+    """Device and stream of one call: the stream as the library takes it, and
+    the memory that the call allocates."""
+
+    __slots__ = ("device", "stream", "handle", "guard")
+
+    def __init__(self, stream, device):
+        self.device = device
+        # kernels go to the current device, so it has to be the tensors' one
+        self.guard = None
+        if device.index is not None and torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+            self.guard.__enter__()
+        self.stream = None  # a stream other than the current one
+        self.handle = _current_stream(device)
+        if stream is not None:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            if handle != self.handle:
+                self.stream = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+                # the allocator's memory may still be in use by work of the current stream
+                self.stream.wait_stream(torch.cuda.current_stream(device))
+                self.handle = handle
+
+    def new(self, shape, dtype) -> torch.Tensor:
+        """An uninitialised tensor; its memory is not given to other work
+        before what the call's stream holds at its release has run."""
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.stream is not None and t.numel():
+            t.record_stream(self.stream)
+        return t
+
+    def done(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
 
 
 def _strides(t: torch.Tensor):
     """Token and head strides (0 where the dimension has one entry)."""
-    return [0 if t.shape[d] <= 1 else int(t.stride(d)) for d in range(2)]
+    n, m = t.shape[0], t.shape[1]
+    a, b, _ = t.stride()
+    return 0 if n <= 1 else a, 0 if m <= 1 else b
 
 
 # ----------------------------------------------------------------------------- norm + rotation
@@ -186,13 +215,15 @@ def norm_rope(q, k, q_weight, k_weight, positions, freqs, eps=1e-6, rot_offset=0
     k and k_weight may be None (k_out is None).  q and k may be views."""
     dev = _check_norm_rope(q, k, q_weight, k_weight, positions, freqs)
     p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
-    with torch.cuda.device(dev):
-        s = _on(stream, dev)
-        q_out = _new(q.shape, q.dtype, dev, s)
-        k_out = None if k is None else _new(k.shape, k.dtype, dev, s)
+    c = _Call(stream, dev)
+    try:
+        q_out = c.new(q.shape, q.dtype)
+        k_out = None if k is None else c.new(k.shape, k.dtype)
         _check("csa_norm_rope", load().csa_norm_rope(
             ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(freqs),
-            _ptr(q_out), _ptr(k_out), _stream(s)))
+            _ptr(q_out), _ptr(k_out), c.handle))
+    finally:
+        c.done()
     return q_out, k_out
 
 
@@ -209,19 +240,21 @@ def norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, freq
     if k is not None:
         _want(dk_out, "dk_out", k.shape, q.dtype, dev)
     p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
-    with torch.cuda.device(dev):
-        s = _on(stream, dev)
+    c = _Call(stream, dev)
+    try:
         D = q.shape[2]
-        dq, dqw = _new(q.shape, q.dtype, dev, s), _new((D,), torch.float32, dev, s)
+        dq, dqw = c.new(q.shape, q.dtype), c.new((D,), torch.float32)
         dk = dkw = None
         if k is not None:
-            dk, dkw = _new(k.shape, k.dtype, dev, s), _new((D,), torch.float32, dev, s)
+            dk, dkw = c.new(k.shape, k.dtype), c.new((D,), torch.float32)
         if workspace is None:
-            workspace = _new((int(load().csa_norm_rope_workspace_size(ctypes.byref(p))),), torch.uint8, dev, s)
+            workspace = c.new((int(load().csa_norm_rope_workspace_size(ctypes.byref(p))),), torch.uint8)
         _check("csa_norm_rope_backward", load().csa_norm_rope_backward(
             ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
             _ptr(positions), _ptr(freqs), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(s)))
+            workspace.numel() * workspace.element_size(), c.handle))
+    finally:
+        c.done()
     return dq, dk, dqw, dkw
 
 
@@ -267,15 +300,18 @@ def attn_forward(q, k, v, cu_q, cu_k, scale, causal=True, k_len=None, workspace=
     cu_k = arange(N+1)*W.  One query row per sequence is the decode step."""
     dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
     p = make_attn_problem(q, k, v, cu_q, scale, causal)
-    with torch.cuda.device(dev):
-        s = _on(stream, dev)
-        out = _new(q.shape, q.dtype, dev, s)
-        lse = _new(q.shape[:2], torch.float32, dev, s)
+    c = _Call(stream, dev)
+    try:
+        out = c.new(q.shape, q.dtype)
+        lse = c.new(q.shape[:2], torch.float32)
         if workspace is None:
-            workspace = _new((attn_workspace_size(p, 0),), torch.uint8, dev, s)
+            need = attn_workspace_size(p, 0)
+            workspace = c.new((need,), torch.uint8) if need else None
         _check("csa_attn_forward", load().csa_attn_forward(
             ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(k_len), _ptr(out), _ptr(lse),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(s)))
+            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), c.handle))
+    finally:
+        c.done()
     return out, lse
 
 
@@ -287,14 +323,16 @@ def attn_backward(dout, q, k, v, out, lse, cu_q, cu_k, scale, causal=True, k_len
     _want(out, "out", q.shape, q.dtype, dev)
     _want(lse, "lse", q.shape[:2], torch.float32, dev)
     p = make_attn_problem(q, k, v, cu_q, scale, causal)
-    with torch.cuda.device(dev):
-        s = _on(stream, dev)
-        dq = _new(q.shape, q.dtype, dev, s)
-        dk, dv = _new(k.shape, k.dtype, dev, s), _new(v.shape, v.dtype, dev, s)
+    c = _Call(stream, dev)
+    try:
+        dq = c.new(q.shape, q.dtype)
+        dk, dv = c.new(k.shape, k.dtype), c.new(v.shape, v.dtype)
         if workspace is None:
-            workspace = _new((attn_workspace_size(p, 1),), torch.uint8, dev, s)
+            workspace = c.new((attn_workspace_size(p, 1),), torch.uint8)
         _check("csa_attn_backward", load().csa_attn_backward(
             ctypes.byref(p), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_q), _ptr(cu_k),
             _ptr(k_len), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(s)))
+            workspace.numel() * workspace.element_size(), c.handle))
+    finally:
+        c.done()
     return dq, dk, dv
