@@ -256,7 +256,8 @@ __device__ __forceinline__ void store_lanes(uint32_t t, float f, X* dst, long lo
   long long at4[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) at4[u] = __shfl_sync(0xffffffffu, at, (lane & ~3u) + u);
-#pragma unroll
+  // (not unrolled: this runs once per item, and its time is that of fetching its instructions)
+#pragma unroll 1
   for (int i = 0; i < N / 32; ++i) {
     float o[32];
     __syncwarp();
@@ -656,8 +657,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i * rows_blk < all_rows) {
             const int skip = first_row - i * rows_blk - 64 * hf;  // columns before the first row that sees this key
 #pragma unroll
-            for (int u = 0; u < 64; ++u)
-              if (u < skip) p[u >> 5][u & 31] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t drop = low_bits(skip - 32 * h);
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                if ((drop & (1u << u)) != 0u) p[h][u] = -INFINITY;
+            }
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -960,8 +965,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((j + 1) * 128 > see_all) {
             const int lim = see - j * 128 - 64 * hf;
 #pragma unroll
-            for (int u = 0; u < 64; ++u)
-              if (u >= lim) p[u >> 5][u & 31] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t keep = low_bits(lim - 32 * h);
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                if ((keep & (1u << u)) == 0u) p[h][u] = -INFINITY;
+            }
           }
 #pragma unroll
           for (int u = 0; u < 32; ++u) {

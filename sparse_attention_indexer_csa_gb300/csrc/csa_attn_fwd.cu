@@ -125,7 +125,8 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
   return it;
 }
 
-template <typename X, int D, int TILES>
+// SPLIT: items are shares of the keys, and their outputs go to the workspace.
+template <typename X, int D, int TILES, bool SPLIT>
 __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const FwdArgs f) {
@@ -384,8 +385,12 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
             if ((j + 1) * 128 > see_all) {
               const int lim = see - j * 128;
 #pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t keep = low_bits(lim - 32 * i);
+#pragma unroll
+                for (int u = 0; u < 32; ++u)
+                  if ((keep & (1u << u)) == 0u) s[i][u] = -INFINITY;
+              }
             }
           };
           auto probs = [&](const float (&s)[4][32]) {
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
       const int t_blk = it->t0 + w * f.tq, hk = it->hk, z = it->z;
       const long long at = row_ok ? static_cast<long long>(t_blk + tok) * a.Hq + hk * a.g + head : -1;
       if (at >= 0) {
-        if (f.n_split > 1)
+        if constexpr (SPLIT)
           f.part_lse[z * rows + at] = lse;
         else
           a.lse[at] = lse;
@@ -464,7 +469,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
       long long at4[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) at4[u] = __shfl_sync(0xffffffffu, at, (lane & ~3u) + u);
-#pragma unroll
+      // (not unrolled: this runs once per item, and its time is that of fetching its instructions)
+#pragma unroll 1
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
         __syncwarp();
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
         }
 #pragma unroll
         for (int u = 0; u < 32; ++u) o[u] = seen ? o[u] * inv : 0.f;
-        if (f.n_split > 1) {
+        if constexpr (SPLIT) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 16 fp32 values: four pieces
             uint4 q[4];
@@ -565,12 +571,17 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
   if (!make_rows_map(&tq, p, p.q, p.q_st, p.q_sh, f.tq) || !make_keys_map(&tk, p, p.k, p.k_st, p.k_sh) ||
       !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh))
     return cudaErrorInvalidValue;
-  cudaError_t e = smem_limit_once<attn_fwd_kernel<X, D, TILES>>(C::kSmem);
-  if (e != cudaSuccess) return e;
   const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk * n_split;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  attn_fwd_kernel<X, D, TILES><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
-  if ((e = cudaGetLastError()) != cudaSuccess || n_split == 1) return e;
+  cudaError_t e;
+  if (n_split == 1) {
+    if ((e = smem_limit_once<attn_fwd_kernel<X, D, TILES, false>>(C::kSmem)) != cudaSuccess) return e;
+    attn_fwd_kernel<X, D, TILES, false><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+    return cudaGetLastError();
+  }
+  if ((e = smem_limit_once<attn_fwd_kernel<X, D, TILES, true>>(C::kSmem)) != cudaSuccess) return e;
+  attn_fwd_kernel<X, D, TILES, true><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(p.Tq) * p.Hq;
   constexpr int PER = 256 / (D / 4);
   attn_join_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER), 256, 0, stream>>>(p, f.part_o, f.part_lse,

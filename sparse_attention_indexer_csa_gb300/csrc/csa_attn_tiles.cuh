@@ -302,6 +302,11 @@ __device__ __forceinline__ float row_max(const float (&s)[4][32]) {
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
+// The n lowest bits (n of any size, below 1: none; above 31: all).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // Multiplies 16 TMEM columns of this thread's lane by r.
 __device__ __forceinline__ void tmem_scale16(uint32_t t, float r) {
   float v[8];
