@@ -50,14 +50,21 @@ namespace {
 
 constexpr float kRaise = 4096.f;  // a tile's sum of P above which the reference is raised
 
-template <int D, int TILES>
+// ROWS: rows of a block that may be used.  32 (with TILES = 1) keeps a smaller query block in shared memory and a
+// third key or value tile in its place; the products read 128 rows all the same, and what they read past the
+// block reaches only the unused rows of S.
+template <int D, int TILES, int ROWS>
 struct FwdCfg {
   static constexpr uint32_t kTile = kChunkBytes * (D / 64);  // 128 rows x D, 64 columns per 16 KB chunk
-  static constexpr int kStages = TILES == 2 ? (D == 128 ? 5 : 10) : (D == 128 ? 2 : 5);
+  static constexpr uint32_t kQChunk = ROWS * 128, kQTile = kQChunk * (D / 64);  // 64 columns of the query block; all
+  static constexpr int kStages = TILES == 2 ? (D == 128 ? 4 : 8) : ROWS == 32 ? (D == 128 ? 3 : 6) : (D == 128 ? 2 : 5);
   static constexpr int kWarps = TILES == 2 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kMmaWarp = 4 * TILES, kTmaWarp = kMmaWarp + 1, kItemWarp = kMmaWarp + 2;
-  static constexpr uint32_t kOffQ = 0, kOffKv = kOffQ + TILES * kTile, kOffBar = kOffKv + kStages * kTile;
+  static constexpr uint32_t kOffQ = 0, kOffKv = kOffQ + TILES * kQTile;
+  // TILES = 2: 64 columns of each block's output on their way to memory
+  static constexpr uint32_t kOffOut = kOffKv + kStages * kTile;
+  static constexpr uint32_t kOffBar = kOffOut + (TILES == 2 ? 2 * kChunkBytes : 0);
   static constexpr int kSlots = 2;  // items ahead
   static constexpr int kBarQ = 0, kBarQFree = TILES, kBarFull = 2 * TILES, kBarEmpty = kBarFull + kStages,
                        kBarS = kBarEmpty + kStages, kBarP = kBarS + TILES, kBarO = kBarP + TILES,
@@ -68,8 +75,11 @@ struct FwdCfg {
   static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
   static constexpr uint32_t kO = 128 * TILES;  // first column of O
 };
-static_assert(FwdCfg<128, 2>::kSmem <= 227 * 1024 && FwdCfg<64, 2>::kSmem <= 227 * 1024, "one CTA per SM");
-static_assert(2 * (FwdCfg<128, 1>::kSmem + 1024) <= 228 * 1024 && 2 * (FwdCfg<64, 1>::kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(FwdCfg<128, 2, 128>::kSmem <= 227 * 1024 && FwdCfg<64, 2, 128>::kSmem <= 227 * 1024, "one CTA per SM");
+constexpr bool two_fit(uint32_t smem) { return 2 * (smem + 1024) <= 228 * 1024; }
+static_assert(two_fit(FwdCfg<128, 1, 128>::kSmem) && two_fit(FwdCfg<64, 1, 128>::kSmem) &&
+                  two_fit(FwdCfg<128, 1, 32>::kSmem) && two_fit(FwdCfg<64, 1, 32>::kSmem),
+              "two CTAs per SM");
 
 struct FwdArgs {
   AttnParams a;
@@ -126,11 +136,12 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
 }
 
 // SPLIT: items are shares of the keys, and their outputs go to the workspace.
-template <typename X, int D, int TILES, bool SPLIT>
-__global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2)
+template <typename X, int D, int TILES, int ROWS, bool SPLIT>
+__global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ? 1 : 2)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                    const __grid_constant__ CUtensorMap tmap_v, const FwdArgs f) {
-  using C = FwdCfg<D, TILES>;
+                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_out,
+                    const FwdArgs f) {
+  using C = FwdCfg<D, TILES, ROWS>;
   extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   uint8_t* next_slot = base + C::kOffMisc;  // 16 bytes: the answer to a request for the next item
@@ -155,6 +166,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
+    if (TILES == 2 && !SPLIT) prefetch_tmap(&tmap_out);
   }
   if (warp == C::kMmaWarp) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -229,7 +241,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
           ++nq[w];
           mbar_arrive_expect_tx(bars + C::kBarQ + w, static_cast<uint32_t>(f.tq * a.g) * 128u * (D / 64));
           for (int ch = 0; ch < D / 64; ++ch)
-            tma_load_4d_hint(base + C::kOffQ + w * C::kTile + ch * kChunkBytes, &tmap_q, bars + C::kBarQ + w, ch * 64, 0,
+            tma_load_4d_hint(base + C::kOffQ + w * C::kQTile + ch * C::kQChunk, &tmap_q, bars + C::kBarQ + w, ch * 64, 0,
                              t0 + w * f.tq, hk, q_pol);
         }
         for (int j = lo; j < top; ++j)
@@ -275,7 +287,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
-            umma_bf16(tm + w * 128, qd + static_cast<uint64_t>(w * kT) + o, kd + static_cast<uint64_t>(st * kT) + o, kIdS,
+            const uint64_t oq = static_cast<uint64_t>(((ks >> 2) * C::kQChunk + (ks & 3) * 32) >> 4);
+            umma_bf16(tm + w * 128, qd + static_cast<uint64_t>(w * (C::kQTile >> 4)) + oq, kd + static_cast<uint64_t>(st * kT) + o, kIdS,
                       ks != 0 ? 1u : 0u);
           }
         }
@@ -345,6 +358,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
     const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + w * 128;
     const uint32_t to = ts + (C::kO - w * 128) + w * 128;
     const float c = f.c;
+    const bool has_rows = (warp & 3) * 32 < ROWS;  // of a warp without rows nothing is used
     uint32_t s_phase = 0, o_phase = 0, ring = 0;  // ring: tiles of the ring before this item
     bool ok = true;
     while (const volatile FwdItem* it = next_item()) {
@@ -373,7 +387,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
           if (j > lo) mbar_arrive(bars + C::kBarEmpty + (nk - 1) % C::kStages);
         }
         if (j == my_hi - 1 && first_thread) mbar_arrive(bars + C::kBarQFree + w);  // the last product with Q
-        if (ok) {
+          if (ok && has_rows) {
           float tile;
           uint32_t pk[4][16];
           // the row's 128 scores, those it does not see at -inf
@@ -385,12 +399,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
             if ((j + 1) * 128 > see_all) {
               const int lim = see - j * 128;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t keep = low_bits(lim - 32 * i);
-#pragma unroll
-                for (int u = 0; u < 32; ++u)
-                  if ((keep & (1u << u)) == 0u) s[i][u] = -INFINITY;
-              }
+              for (int i = 0; i < 128; ++i)
+                if (i >= lim) s[i >> 5][i & 31] = -INFINITY;
             }
           };
           auto probs = [&](const float (&s)[4][32]) {
@@ -434,7 +444,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
             // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
             const uint32_t nv = nk + 1u, sv = nv % C::kStages;
             if (mbar_wait(bars + C::kBarFull + sv, (nv / C::kStages) & 1u, ctl))
-              clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, lk - j * 128, threadIdx.x & 127, 128);
+              clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, lk - j * 128, threadIdx.x & (ROWS - 1), ROWS);
             fence_proxy_async_shared();
           }
         }
@@ -463,6 +473,47 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
           f.part_lse[z * rows + at] = lse;
         else
           a.lse[at] = lse;
+      }
+      if constexpr (TILES == 2 && !SPLIT) {
+        // A full block goes through shared memory, 64 columns at a time, and is stored by TMA: a quarter of the
+        // instructions of the stores below, which run once per item and wait for being fetched.
+        if (it->n_tok[w] == f.tq) {
+          uint8_t* mine = base + C::kOffOut + w * kChunkBytes;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 64; ++ch) {
+            if (first_thread) bulk_wait_group_read<0>();  // what was staged before has been read
+            named_bar_sync(1 + w, 128);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float o[32];
+              if (any) {
+                tmem_ld32_start(to + 64 * ch + 32 * h, o);
+                tmem_wait32(o);
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (seen)
+                  q = make_uint4(pack_pair<X>(o[8 * u] * inv, o[8 * u + 1] * inv),
+                                 pack_pair<X>(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                 pack_pair<X>(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                 pack_pair<X>(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+                *reinterpret_cast<uint4*>(mine + row * 128 + (((4 * h + u) ^ (row & 7)) * 16)) = q;
+              }
+            }
+            fence_proxy_async_shared();
+            named_bar_sync(1 + w, 128);
+            if (first_thread) {
+              tma_store_4d(&tmap_out, mine, ch * 64, 0, t_blk, hk);
+              bulk_commit_group();
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
+          ++n_item;
+          continue;
+        }
       }
       // Lanes 4 i .. 4 i + 3 exchange their rows' 16-byte pieces, so that four lanes store 64 bytes of one row:
       // a store of 16 bytes by each of 32 rows takes as many passes through L1 as it has rows.
@@ -506,10 +557,12 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
             if (at4[u] >= 0) reinterpret_cast<uint4*>(static_cast<X*>(a.out) + at4[u] * D + 32 * i)[lane & 3] = q[u];
         }
       }
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
       ++n_item;
     }
+    if (TILES == 2 && !SPLIT && (threadIdx.x & 127) == 0) bulk_wait_group_all();
   } else {
     reg_shrink<TILES>();
   }
@@ -520,48 +573,76 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES>::kThreads, TILES == 2 ? 1 : 2
   if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
-// out = sum_z w_z O_z / sum_z w_z with w_z = exp(lse_z - max lse): D/4 threads
-// per row and head, four values each.  Bytes: n_split (D + 1) fp32 read per
-// row and head.
+// out = sum_z w_z O_z / sum_z w_z with w_z = exp(lse_z - max lse).  A block per
+// row and head: 256 / (D/4) groups of threads take every so many shares, four
+// values a thread, and their sums are added in order.  Bytes: n_split (D + 1)
+// fp32 read per row and head.  (One group for all shares took longer than the
+// attention itself where a single sequence is cut into many.)
 template <typename X, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnParams a, const float* part_o, const float* part_lse,
                                                        int n_split) {
-  constexpr int PER = 256 / (D / 4);
-  const long long rows = static_cast<long long>(a.Tq) * a.Hq;
-  const long long r = static_cast<long long>(blockIdx.x) * PER + threadIdx.x / (D / 4);
-  const int l = threadIdx.x % (D / 4);
-  if (r >= rows) return;
-  float m = -INFINITY;
-  for (int z = 0; z < n_split; ++z) m = fmaxf(m, part_lse[z * rows + r]);
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float w[kMaxSplit], top[8], total[8];
+  __shared__ float4 acc[GROUPS][LANES];
+  const long long rows = static_cast<long long>(a.Tq) * a.Hq, r = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid / 32;
+  const float lz = tid < n_split ? part_lse[tid * rows + r] : -INFINITY;  // n_split <= kMaxSplit = 256
+  float m = lz;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) top[warp] = m;
+  __syncthreads();
+  m = top[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, top[i]);
   const float ms = m == -INFINITY ? 0.f : m;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int z = 0; z < n_split; ++z) {
-    const float lz = part_lse[z * rows + r];
-    if (lz == -INFINITY) continue;
-    const float w = exp2_approx((lz - ms) * 1.4426950408889634f);
+  const float wz = exp2_approx((lz - ms) * 1.4426950408889634f);  // 0 for a share that saw nothing
+  float s = wz;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (tid < n_split) w[tid] = wz;
+  if ((tid & 31) == 0) total[warp] = s;
+  __syncthreads();
+  s = ((total[0] + total[1]) + (total[2] + total[3])) + ((total[4] + total[5]) + (total[6] + total[7]));
+  const int g = tid / LANES, l = tid % LANES;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int z = g; z < n_split; z += GROUPS) {
+    const float f = w[z];
     const float4 o = reinterpret_cast<const float4*>(part_o + (z * rows + r) * D)[l];
-    sum += w;
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+    if (f != 0.f) {
+      v.x = fmaf(f, o.x, v.x);
+      v.y = fmaf(f, o.y, v.y);
+      v.z = fmaf(f, o.z, v.z);
+      v.w = fmaf(f, o.w, v.w);
+    }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  acc[g][l] = v;
+  __syncthreads();
+  if (g != 0) return;
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 o = acc[i][l];
+    v.x += o.x;
+    v.y += o.y;
+    v.z += o.z;
+    v.w += o.w;
+  }
+  const float inv = s == 0.f ? 0.f : 1.f / s;
   uint2 u;
-  u.x = pack_pair<X>(acc.x * inv, acc.y * inv);
-  u.y = pack_pair<X>(acc.z * inv, acc.w * inv);
+  u.x = pack_pair<X>(v.x * inv, v.y * inv);
+  u.y = pack_pair<X>(v.z * inv, v.w * inv);
   reinterpret_cast<uint2*>(static_cast<X*>(a.out) + r * D)[l] = u;
-  if (l == 0) a.lse[r] = sum == 0.f ? -INFINITY : ms + logf(sum);
+  if (l == 0) a.lse[r] = s == 0.f ? -INFINITY : ms + logf(s);
 }
 
-template <typename X, int D, int TILES>
+template <typename X, int D, int TILES, int ROWS>
 cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t stream) {
-  using C = FwdCfg<D, TILES>;
-  CUtensorMap tq, tk, tv;
+  using C = FwdCfg<D, TILES, ROWS>;
+  CUtensorMap tq, tk, tv, to;
   FwdArgs f;
   f.a = p;
-  f.tq = 128 / p.g;
+  f.tq = ROWS / p.g;
   f.nb = static_cast<int>((static_cast<long long>(p.Tq) + TILES * f.tq - 1) / (TILES * f.tq));
   f.n_split = n_split;
   f.c = p.scale * 1.4426950408889634f;
@@ -569,38 +650,40 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
   f.part_lse = f.part_o + static_cast<long long>(n_split) * p.Tq * p.Hq * D;
   f.wait_ns = kAttnWaitNs;
   if (!make_rows_map(&tq, p, p.q, p.q_st, p.q_sh, f.tq) || !make_keys_map(&tk, p, p.k, p.k_st, p.k_sh) ||
-      !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh))
+      !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh) ||
+      !make_rows_map(&to, p, p.out, static_cast<long long>(p.Hq) * D, D, f.tq))
     return cudaErrorInvalidValue;
   const long long grid = (static_cast<long long>(f.nb) + p.N + 1) * p.Hk * n_split;
-  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+  if (grid > 0x7FFFFFFFll || (n_split > 1 && rows > 0x7FFFFFFFll)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (n_split == 1) {
-    if ((e = smem_limit_once<attn_fwd_kernel<X, D, TILES, false>>(C::kSmem)) != cudaSuccess) return e;
-    attn_fwd_kernel<X, D, TILES, false><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+    constexpr auto kernel = attn_fwd_kernel<X, D, TILES, ROWS, false>;
+    if ((e = smem_limit_once<kernel>(C::kSmem)) != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, to, f);
     return cudaGetLastError();
   }
-  if ((e = smem_limit_once<attn_fwd_kernel<X, D, TILES, true>>(C::kSmem)) != cudaSuccess) return e;
-  attn_fwd_kernel<X, D, TILES, true><<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, f);
+  constexpr auto kernel = attn_fwd_kernel<X, D, TILES, ROWS, true>;
+  if ((e = smem_limit_once<kernel>(C::kSmem)) != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(grid), C::kThreads, C::kSmem, stream>>>(tq, tk, tv, to, f);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
-  constexpr int PER = 256 / (D / 4);
-  attn_join_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER), 256, 0, stream>>>(p, f.part_o, f.part_lse,
-                                                                                          n_split);
+  attn_join_kernel<X, D><<<static_cast<unsigned>(rows), 256, 0, stream>>>(p, f.part_o, f.part_lse, n_split);
   return cudaGetLastError();
 }
 
-template <typename X>
-cudaError_t by_size(const AttnParams& p, const AttnPlan& plan, void* ws, cudaStream_t s) {
-  if (p.D == 128)
-    return plan.tiles == 2 ? run<X, 128, 2>(p, plan.n_split, ws, s) : run<X, 128, 1>(p, plan.n_split, ws, s);
-  return plan.tiles == 2 ? run<X, 64, 2>(p, plan.n_split, ws, s) : run<X, 64, 1>(p, plan.n_split, ws, s);
+template <typename X, int D>
+cudaError_t by_plan(const AttnParams& p, void* ws, cudaStream_t s) {
+  const AttnPlan plan = attn_plan(p.N, p.Tq, p.Tk, p.Hk, p.g);
+  if (plan.tiles == 2) return run<X, D, 2, 128>(p, plan.n_split, ws, s);
+  return plan.rows == 32 ? run<X, D, 1, 32>(p, plan.n_split, ws, s) : run<X, D, 1, 128>(p, plan.n_split, ws, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t s) {
-  const AttnPlan plan = attn_plan(p.N, p.Tq, p.Tk, p.Hk, p.g);
-  return dtype == CSA_BF16 ? by_size<__nv_bfloat16>(p, plan, workspace, s) : by_size<__half>(p, plan, workspace, s);
+  if (dtype == CSA_BF16)
+    return p.D == 128 ? by_plan<__nv_bfloat16, 128>(p, workspace, s) : by_plan<__nv_bfloat16, 64>(p, workspace, s);
+  return p.D == 128 ? by_plan<__half, 128>(p, workspace, s) : by_plan<__half, 64>(p, workspace, s);
 }
 
 cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }

@@ -48,23 +48,34 @@ cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream);
 
 // How the forward cuts its work, from the sizes the host knows (the lengths
 // stand on the device).
+constexpr int kMaxSplit = 256;
 struct AttnPlan {
-  int tiles;    // blocks of 128 rows per CTA (2: one CTA per SM, 1: two)
+  int tiles;    // blocks of rows per CTA (2: one CTA per SM, 1: two)
+  int rows;     // rows of a block: 128, or 32 (tiles = 1)
   int n_split;  // CTAs that share the keys of a block
 };
 inline AttnPlan attn_plan(int N, int Tq, int Tk, int Hk, int g) {
-  const int tok = 128 / g;
   const long long seqs = std::max(1, std::min(N, Tq));
   AttnPlan p;
-  // sequences whose rows fit one block leave a second one empty
-  p.tiles = Tq <= seqs * tok ? 1 : 2;
-  p.n_split = 1;
-  const long long step = static_cast<long long>(p.tiles) * tok;
+  // Sequences whose rows fit one block would leave a second one empty; those
+  // whose rows fit a quarter of one (decoding) leave room for a third tile of
+  // keys in flight.
+  p.tiles = Tq <= seqs * (128 / g) ? 1 : 2;
+  p.rows = g <= 32 && Tq <= seqs * (32 / g) ? 32 : 128;
+  const long long step = static_cast<long long>(p.tiles) * (p.rows / g);
   const long long items = std::max(seqs, (Tq + step - 1) / step) * Hk;
   const long long key_tiles = (Tk / std::max(1, N) + 127) / 128;  // of an average sequence
-  const long long want = p.tiles == 1 ? 4 * 304 : 152;
-  if (items < want && key_tiles >= 8)
-    p.n_split = static_cast<int>(std::min<long long>((want + items - 1) / items, key_tiles / 4));
+  // Few items: as many shares as fill the GPU once.  With more, shares even out
+  // what the sequences' lengths leave uneven (64 sequences of 2048 to 8192 keys,
+  // 8 key heads: 287 us in one share, 258 in three, 251 in five, 254 in eight);
+  // a share of fewer than four (eight) tiles costs more than it gains.
+  const long long slots = p.tiles == 1 ? 304 : 152;
+  long long n = 1;
+  if (2 * items <= slots)
+    n = std::min(slots / items, key_tiles / 4);
+  else if (p.tiles == 1 && items < 8 * slots)
+    n = std::min((8 * slots + items - 1) / items, key_tiles / 8);
+  p.n_split = static_cast<int>(std::max<long long>(1, std::min<long long>(n, kMaxSplit)));
   return p;
 }
 

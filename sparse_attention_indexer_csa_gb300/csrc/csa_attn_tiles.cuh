@@ -127,6 +127,14 @@ __device__ __forceinline__ RowItem find_key_item(const AttnParams& a, int step, 
   return find_item<true>(a, step, nb, x);
 }
 
+// TMA store of a 4-D box from shared memory, tracked by the bulk async-group of
+// the issuing thread.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(m),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
 // ----------------------------------------------------------------- next item
 // Cluster launch control: asks for one block of the grid that has not started;
 // the 16-byte answer at `slot` completes on `bar`.  One thread.
