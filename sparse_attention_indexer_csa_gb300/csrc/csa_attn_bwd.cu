@@ -77,7 +77,7 @@ struct BwdCfg {
                        kBarS = kBarStatFree + 2, kBarP = kBarS + 1, kBarDp = kBarP + 1, kBarDs = kBarDp + 1,
                        kBarAcc = kBarDs + 1, kBarResFree = kBarAcc + 1, kBarCopied = kBarResFree + 1,
                        kBarItem = kBarCopied + 1, kBarItemFree = kBarItem + 2, kBarNext = kBarItemFree + 2,
-                       kBarSoon = kBarNext + 1, kBarDone = kBarSoon + 1, kBars = kBarDone + 1;
+                       kBarSoon = kBarNext + 1, kBarMeet = kBarSoon + 1, kBarDone = kBarMeet + 4, kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16, kOffItem = kOffMisc + 32;
   static constexpr uint32_t kSmem = kOffItem + 2 * 64;
 };
@@ -104,6 +104,7 @@ __device__ __forceinline__ void init_barriers(uint64_t* bars) {
     int n = 1;
     if (i == C::kBarStatFree || i == C::kBarStatFree + 1 || i == C::kBarP || i == C::kBarDs || i == C::kBarCopied)
       n = kEpiWarps;
+    if (i >= C::kBarMeet && i < C::kBarMeet + 4) n = 2;
     if (i == C::kBarItemFree || i == C::kBarItemFree + 1) n = kEpiWarps + 3;  // + issuer, producer, preparer
     mbar_init(bars + i, n);
   }
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = t_s + lane_off + 64 * hf, tp = t_dp + lane_off + 64 * hf;
     const float2 c2 = make_float2(f.c, f.c);
-    uint32_t step = 0, item = 0;
+    uint32_t step = 0, item = 0, met = 0;
     bool ok = true;
     while (const volatile BwdItem* it = ct.next()) {
       const int n = it->n;
@@ -945,7 +946,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + C::kBarCopied);
         ++item;
       }
-      const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(-de, -de);
+      const float2 nl2 = make_float2(nl, nl);
+      float2 nd2 = make_float2(-de, -de);
+      if (n == 1) {
+        // All the keys these rows see are in one tile: delta = sum p dP, without the rounding of out that dout.out
+        // has (and that shows where a row averages few values).  The dk, dv kernel uses it too.  The tile's scores
+        // and dP are read once more below (in the loop itself this took registers from every tile).
+        ok = ok && mbar_wait(bars + C::kBarS, step, ctl);
+        ok = ok && mbar_wait(bars + C::kBarDp, step, ctl);
+        tc_fence_after();
+        float sum = 0.f;
+        if (ok) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x[32], d[32];
+            tmem_ld32_start(ts + 32 * h, x);
+            tmem_ld32_start(tp + 32 * h, d);
+            tmem_wait32(x);
+            tmem_wait32(d);
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              if (64 * hf + 32 * h + u < see) sum = fmaf(exp2_approx(fmaf(x[u], f.c, nl)), d[u], sum);
+          }
+        }
+        float* xch = reinterpret_cast<float*>(base + C::kOffStat) + row;
+        xch[128 * hf] = sum;
+        meet(bars + C::kBarMeet + (warp & 3), met, ctl);
+        const float delta = xch[0] + xch[128];
+        meet(bars + C::kBarMeet + (warp & 3), met, ctl);
+        if (nl != -INFINITY) {
+          nd2 = make_float2(-delta, -delta);
+          if (hf == 0) a.delta[at] = delta;
+        }
+      }
       for (int j = 0; j < n; ++j, step ^= 1u) {
         ok = ok && mbar_wait(bars + C::kBarS, step, ctl);
         tc_fence_after();
@@ -1060,27 +1093,26 @@ cudaError_t run(const AttnParams& p, const AttnBwdPlan& plan, uint8_t* ws, cudaS
   attn_delta_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER + (order != nullptr)), 256, 0, stream>>>(
       p, order, static_cast<int>(runs_k), nb_k, f.tq);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.Tk > 0) {
-    f.nb = nb_k;
-    const unsigned grid = static_cast<unsigned>(runs_k * p.Hk * plan.n_split);
-    if (plan.n_split > 1) {
-      if ((e = smem_limit_once<attn_dkv_kernel<X, D, true>>(C::kSmem)) != cudaSuccess) return e;
-      attn_dkv_kernel<X, D, true><<<grid, kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
-    } else {
-      if ((e = smem_limit_once<attn_dkv_kernel<X, D, false>>(C::kSmem)) != cudaSuccess) return e;
-      attn_dkv_kernel<X, D, false><<<grid, kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
-    }
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (plan.n_split > 1) {
-      const long long keys = static_cast<long long>(p.Tk) * p.Hk;
-      constexpr int PER_J = 256 / (D / 4);
-      attn_join_dkv_kernel<X, D><<<static_cast<unsigned>((keys + PER_J - 1) / PER_J), 256, 0, stream>>>(
-          p, f.part_dk, f.part_dv, plan.n_split);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-  }
+  // dq first: it improves delta for the rows of few keys
   f.nb = nb_q;
   attn_dq_kernel<X, D><<<static_cast<unsigned>(runs_q * p.Hk), kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
+  if ((e = cudaGetLastError()) != cudaSuccess || p.Tk == 0) return e;
+  f.nb = nb_k;
+  const unsigned grid = static_cast<unsigned>(runs_k * p.Hk * plan.n_split);
+  if (plan.n_split > 1) {
+    if ((e = smem_limit_once<attn_dkv_kernel<X, D, true>>(C::kSmem)) != cudaSuccess) return e;
+    attn_dkv_kernel<X, D, true><<<grid, kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
+  } else {
+    if ((e = smem_limit_once<attn_dkv_kernel<X, D, false>>(C::kSmem)) != cudaSuccess) return e;
+    attn_dkv_kernel<X, D, false><<<grid, kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (plan.n_split > 1) {
+    const long long keys = static_cast<long long>(p.Tk) * p.Hk;
+    constexpr int PER_J = 256 / (D / 4);
+    attn_join_dkv_kernel<X, D><<<static_cast<unsigned>((keys + PER_J - 1) / PER_J), 256, 0, stream>>>(
+        p, f.part_dk, f.part_dv, plan.n_split);
+  }
   return cudaGetLastError();
 }
 

@@ -69,7 +69,7 @@ struct FwdCfg {
   static constexpr int kBarQ = 0, kBarQFree = TILES, kBarFull = 2 * TILES, kBarEmpty = kBarFull + kStages,
                        kBarS = kBarEmpty + kStages, kBarP = kBarS + TILES, kBarO = kBarP + TILES,
                        kBarItem = kBarO + TILES, kBarItemFree = kBarItem + kSlots, kBarNext = kBarItemFree + kSlots,
-                       kBarSoon = kBarNext + 1, kBarDone = kBarSoon + 1, kBars = kBarDone + 1;
+                       kBarSoon = kBarNext + 1, kBarMeet = kBarSoon + 1, kBarDone = kBarMeet + TILES, kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16, kOffItem = kOffMisc + 32;
   static constexpr uint32_t kSmem = kOffItem + kSlots * 64;
   static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kBars; ++i) {
       int n = 1;
-      if (i >= C::kBarP && i < C::kBarP + TILES) n = 4;
+      if ((i >= C::kBarP && i < C::kBarP + TILES) || (i >= C::kBarMeet && i < C::kBarMeet + TILES)) n = 4;
       if (i >= C::kBarItemFree && i < C::kBarItemFree + C::kSlots) n = 2 + 4 * TILES;
       mbar_init(bars + i, n);
     }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
     const uint32_t to = ts + (C::kO - w * 128) + w * 128;
     const float c = f.c;
     const bool has_rows = (warp & 3) * 32 < ROWS;  // of a warp without rows nothing is used
-    uint32_t s_phase = 0, o_phase = 0, ring = 0;  // ring: tiles of the ring before this item
+    uint32_t s_phase = 0, o_phase = 0, met = 0, ring = 0;  // ring: tiles of the ring before this item
     bool ok = true;
     while (const volatile FwdItem* it = next_item()) {
       const int lo = it->lo, my_hi = it->hi[w], top = max(it->hi[0], it->hi[1]), lk = it->s.lk;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
 #pragma unroll 1
           for (int ch = 0; ch < D / 64; ++ch) {
             if (first_thread) bulk_wait_group_read<0>();  // what was staged before has been read
-            named_bar_sync(1 + w, 128);
+            meet(bars + C::kBarMeet + w, met, ctl);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float o[32];
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
               }
             }
             fence_proxy_async_shared();
-            named_bar_sync(1 + w, 128);
+            meet(bars + C::kBarMeet + w, met, ctl);
             if (first_thread) {
               tma_store_4d(&tmap_out, mine, ch * 64, 0, t_blk, hk);
               bulk_commit_group();

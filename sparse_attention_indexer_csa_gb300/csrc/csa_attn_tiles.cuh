@@ -201,6 +201,16 @@ __device__ __forceinline__ bool elect_one() {
 // Lane 0's value, as one the compiler knows to be the same in all lanes.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
+// A meeting of warps at `bar` (initialised to their number), bounded as every
+// wait is: named barriers would wait for a warp that gave up.  What the warps
+// wrote to shared memory before is visible after; phase is kept by each warp.
+__device__ __forceinline__ void meet(uint64_t* bar, uint32_t& phase, const WaitCtl& ctl) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+  mbar_wait(bar, phase, ctl);
+  phase ^= 1u;
+}
+
 // ----------------------------------------------------------------- register splits
 // TILES = 2: 384 threads start with 168 registers each (64512): 256 of them grow
 // to 216, 128 shrink to 72 (55296 + 9216 = 64512).  TILES = 1, two CTAs per SM:
