@@ -33,6 +33,7 @@
 //                       the blocks of the grid that have not started (cluster
 //                       launch control), so its rows, first tiles and query
 //                       block are on their way while the former item ends
+//   next warp           value tiles that hold keys hidden from some row
 // With two blocks the tensor cores form S and O of one while the softmax of
 // the other runs; TMEM holds S0 S1 O0 O1 (512 columns).  With one block the
 // second CTA on the SM does the same.
@@ -69,7 +70,8 @@ struct FwdCfg {
   static constexpr int kBarQ = 0, kBarQFree = TILES, kBarFull = 2 * TILES, kBarEmpty = kBarFull + kStages,
                        kBarS = kBarEmpty + kStages, kBarP = kBarS + TILES, kBarO = kBarP + TILES,
                        kBarItem = kBarO + TILES, kBarItemFree = kBarItem + kSlots, kBarNext = kBarItemFree + kSlots,
-                       kBarSoon = kBarNext + 1, kBarMeet = kBarSoon + 1, kBarDone = kBarMeet + TILES, kBars = kBarDone + 1;
+                       kBarSoon = kBarNext + 1, kBarMeet = kBarSoon + 1, kBarLast = kBarMeet + TILES,
+                       kBarDone = kBarLast + kStages, kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = (kOffBar + 8 * kBars + 15) / 16 * 16, kOffItem = kOffMisc + 32;
   static constexpr uint32_t kSmem = kOffItem + kSlots * 64;
   static constexpr uint32_t kTmemCols = TILES == 2 ? 512 : 256;
@@ -100,6 +102,8 @@ struct FwdItem {
   int lo, hi[2];  // block w walks the key tiles lo .. hi[w]-1
   int n_tok[2];   // tokens of each block
   int hk, z;      // key head, share
+  int open;       // keys that all rows see: the value tiles past them are mended before their products
+  int odd;        // first key tile of which values were taken out (see mend_values)
 };
 static_assert(sizeof(FwdItem) <= 64, "a slot");
 
@@ -117,6 +121,8 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
   it.s = r.s;
   it.t0 = r.t0;
   it.t1 = r.t1;
+  it.odd = INT32_MAX;
+  it.open = r.t0 < r.t1 ? keys_seen(a, r.s, r.t0 - r.s.q0) : 0;
   it.lo = 0;
   int top = 0;
 #pragma unroll
@@ -133,6 +139,61 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
     for (int w = 0; w < 2; ++w) it.hi[w] = max(it.lo, min(it.hi[w], it.lo + share));
   }
   return it;
+}
+
+// What the products of a value tile may not meet, since a hidden key's P of 0
+// does not cancel it.  Rows from `held` on are not the sequence's: cleared.
+// Rows from `open` on are hidden from some row of the item: what is infinite
+// or NaN among them is taken out, and `odd` remembers the tile (patch_row adds
+// it to the rows that see it).  By a warp of its own, between the tile's arrival
+// and the products: in the softmax warps it cost 5 to 8 % of a prompt's time.
+template <typename X, int D>
+__device__ __forceinline__ void mend_values(uint8_t* tile, int held, int open, int* odd, int j) {
+  constexpr uint32_t kExp = is_bf16<X>() ? 0x7f807f80u : 0x7c007c00u, kOne = is_bf16<X>() ? 0x00800080u : 0x04000400u;
+  constexpr int P = D / 8;  // 16-byte pieces of a row; piece `q` of row `row` (whatever the swizzle makes of it)
+  auto at = [&](int row, int q) {
+    return reinterpret_cast<uint4*>(tile + (q >> 3) * kChunkBytes + row * 128 + ((q & 7) * 16));
+  };
+  const int lane = static_cast<int>(lane_id()), first = max(0, min(open, held)), last = min(held, 128);
+  // an exponent of all ones carries into the sign's place when one is added to it
+  uint32_t found = 0u;
+#pragma unroll 4
+  for (int i = lane; i < (last - first) * P; i += 32) {
+    const uint4 v = *at(first + i / P, i % P);
+    found |= ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+  }
+  if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0u)) {
+    if (lane == 0) atomicMin(odd, j);
+    auto finite = [&](uint32_t x) {
+      const uint32_t bad = ((x & kExp) + kOne) & 0x80008000u;  // a bit for each half to take out
+      return x & ~((bad >> 15) * 0xffffu);
+    };
+#pragma unroll 1
+    for (int i = lane; i < (last - first) * P; i += 32) {
+      uint4* p = at(first + i / P, i % P);
+      const uint4 v = *p;
+      *p = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
+    }
+  }
+#pragma unroll 4
+  for (int i = lane; i < (128 - max(0, held)) * P; i += 32) *at(max(0, held) + i / P, i % P) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Adds to a row's stored output (type Y) what mend_values took out and the row
+// sees: the infinite and NaN values of its keys first .. see-1.  (In line: a
+// call would take registers from the loop over the tiles.)
+template <typename X, int D, typename Y>
+__device__ __forceinline__ void patch_row(const X* v, long long v_st, int first, int see, Y* out) {
+  constexpr uint32_t kExp = is_bf16<X>() ? 0x7f80u : 0x7c00u;
+#pragma unroll 1
+  for (int key = first; key < see; ++key) {
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+      const X* x = v + key * v_st + d;
+      if ((*reinterpret_cast<const uint16_t*>(x) & kExp) != kExp) continue;
+      out[d] = static_cast<Y>(static_cast<float>(out[d]) + static_cast<float>(*x));
+    }
+  }
 }
 
 // SPLIT: items are shares of the keys, and their outputs go to the workspace.
@@ -155,7 +216,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
     for (int i = 0; i < C::kBars; ++i) {
       int n = 1;
       if ((i >= C::kBarP && i < C::kBarP + TILES) || (i >= C::kBarMeet && i < C::kBarMeet + TILES)) n = 4;
-      if (i >= C::kBarItemFree && i < C::kBarItemFree + C::kSlots) n = 2 + 4 * TILES;
+      if (i >= C::kBarItemFree && i < C::kBarItemFree + C::kSlots) n = 3 + 4 * TILES;
       mbar_init(bars + i, n);
     }
     if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
@@ -233,7 +294,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
       uint32_t at = 0, phase = 1, used = 0, nq[TILES] = {};
       while (const volatile FwdItem* it = next_item()) {
         const int lo = it->lo, hi[2] = {it->hi[0], it->hi[1]}, top = max(hi[0], hi[1]);
-        const int t0 = it->t0, k0 = it->s.k0, hk = it->hk;
+        const int t0 = it->t0, k0 = it->s.k0, hk = it->hk, open = it->open;
         give_item();
         for (int w = 0; w < TILES; ++w) {
           if (hi[w] <= lo) continue;
@@ -253,10 +314,12 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             }
             ++used;
             if (!mbar_wait(bars + C::kBarEmpty + st, ph, ctl)) continue;
-            mbar_arrive_expect_tx(bars + C::kBarFull + st, C::kTile);
+            // a value tile that is mended lands on the stage's other barrier; who mends it completes the first
+            uint64_t* bar = bars + (kv && (j + 1) * 128 > open ? C::kBarLast : C::kBarFull) + st;
+            mbar_arrive_expect_tx(bar, C::kTile);
             for (int ch = 0; ch < D / 64; ++ch)
-              tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k,
-                               bars + C::kBarFull + st, ch * 64, k0 + j * 128, hk, kv_pol);
+              tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k, bar, ch * 64,
+                               k0 + j * 128, hk, kv_pol);
           }
         mbar_arrive(bars + C::kBarSoon);
       }
@@ -440,13 +503,6 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
           for (int i = 0; i < 4; ++i) tmem_st16(ts + 16 * i, pk[i]);
           l += tile;
           tmem_wait_st();
-          if ((j + 1) * 128 > lk && (w == 0 || j >= it->hi[0])) {
-            // what stands in the value tile past the sequence's keys is cleared: 0 * NaN would reach the sums
-            const uint32_t nv = nk + 1u, sv = nv % C::kStages;
-            if (mbar_wait(bars + C::kBarFull + sv, (nv / C::kStages) & 1u, ctl))
-              clear_tile_rows<D>(base + C::kOffKv + sv * C::kTile, lk - j * 128, threadIdx.x & (ROWS - 1), ROWS);
-            fence_proxy_async_shared();
-          }
         }
         tc_fence_before();
         __syncwarp();
@@ -508,6 +564,13 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
               bulk_commit_group();
             }
           }
+          if (it->odd < my_hi) {
+            if (first_thread) bulk_wait_group_all();
+            meet(bars + C::kBarMeet + w, met, ctl);
+            if (seen && at >= 0)
+              patch_row<X, D>(static_cast<const X*>(a.v) + it->s.k0 * a.v_st + hk * a.v_sh, a.v_st, it->odd * 128, see,
+                              static_cast<X*>(a.out) + at * D);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
@@ -557,14 +620,42 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             if (at4[u] >= 0) reinterpret_cast<uint4*>(static_cast<X*>(a.out) + at4[u] * D + 32 * i)[lane & 3] = q[u];
         }
       }
+      if (it->odd < my_hi) {
+        __syncwarp();  // the row's stores may have been another lane's
+        __threadfence_block();
+        if (seen && at >= 0) {
+          const X* v = static_cast<const X*>(a.v) + it->s.k0 * a.v_st + hk * a.v_sh;
+          if constexpr (SPLIT)
+            patch_row<X, D>(v, a.v_st, it->odd * 128, min(see, my_hi * 128), f.part_o + (z * rows + at) * D);
+          else
+            patch_row<X, D>(v, a.v_st, it->odd * 128, see, static_cast<X*>(a.out) + at * D);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
       ++n_item;
     }
     if (TILES == 2 && !SPLIT && (threadIdx.x & 127) == 0) bulk_wait_group_all();
-  } else {
+  } else {  // ---------------------------------------------------------------- mender
     reg_shrink<TILES>();
+    uint32_t ring = 0, last_par = 0;
+    while (const volatile FwdItem* it = next_item()) {
+      const int lo = it->lo, top = max(it->hi[0], it->hi[1]), open = it->open, lk = it->s.lk;
+      for (int j = max(lo, open >> 7); j < top; ++j) {
+        const uint32_t st = (ring + 2u * static_cast<uint32_t>(j - lo) + 1u) % C::kStages;
+        if (mbar_wait(bars + C::kBarLast + st, (last_par >> st) & 1u, ctl))
+          mend_values<X, D>(base + C::kOffKv + st * C::kTile, lk - j * 128, open - j * 128, const_cast<int*>(&it->odd), j);
+        last_par ^= 1u << st;
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarFull + st);
+      }
+      ring += 2u * static_cast<uint32_t>(max(0, top - lo));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarItemFree + (n_item & 1u));
+      ++n_item;
+    }
   }
   __syncwarp();
   tc_fence_before();

@@ -200,6 +200,39 @@ def test_other_sequences_do_not_leak():
         assert torch.equal(a[~bad_rows.cuda()], b[~bad_rows.cuda()])
 
 
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,dt", [([200], [200], 8, 1, 128, BF), ([300, 40], [300, 90], 4, 4, 64, FP16),
+                                              ([24], [5000], 8, 1, 128, BF), ([3], [700], 6, 2, 64, FP16)])
+def test_hidden_keys_of_the_sequence_do_not_leak(lq, lk, Hq, Hk, D, dt):
+    """Infinite and NaN keys and values reach the rows that see them and no others."""
+    q, k, v, _ = _inputs(lq, lk, Hq, Hk, D, dt, seed=31)
+    cu_q, cu_k = _cu(lq).cuda(), _cu(lk).cuda()
+    run = lambda: csa.attn_forward(q.cuda(), k.cuda(), v.cuda(), cu_q, cu_k, D ** -0.5)  # noqa: E731
+    good, good_lse = run()
+    first = lk[0] - lq[0]                 # the last key that row 0 sees
+    at = first + lq[0] // 2               # seen from row lq/2 on
+    rows = lq[0] // 2
+    v[at, 0, 3], v[at, 0, 5], v[at, 0, 60] = float("inf"), -float("inf"), float("nan")
+    v[lk[0] - 1, Hk - 1, 7] = float("nan")   # seen by the last row alone
+    out, lse = run()
+    torch.cuda.synchronize()
+    assert csa.device_status() == csa.CSA_OK
+    assert torch.equal(lse, good_lse)
+    g = Hq // Hk
+    changed = torch.zeros_like(out, dtype=torch.bool)
+    changed[rows:lq[0], :g, 3] = changed[rows:lq[0], :g, 5] = changed[rows:lq[0], :g, 60] = True
+    changed[lq[0] - 1, Hq - g:, 7] = True
+    assert torch.equal(out[~changed], good[~changed])
+    assert (out[rows:lq[0], :g, 3] == float("inf")).all() and (out[rows:lq[0], :g, 5] == -float("inf")).all()
+    assert out[rows:lq[0], :g, 60].isnan().all() and out[lq[0] - 1, Hq - g:, 7].isnan().all()
+    # a NaN key: the rows that see it are NaN, the others keep their bits
+    k[lk[0] - 1, 0, 0] = float("nan")
+    out2, lse2 = run()
+    same = torch.ones(sum(lq), Hq, dtype=torch.bool, device="cuda")
+    same[lq[0] - 1, :g] = False
+    assert torch.equal(lse2[same], good_lse[same]) and lse2[~same].isnan().all() and out2[lq[0] - 1, :g].isnan().all()
+    assert torch.equal(out2[same].nan_to_num(3.0), out[same].nan_to_num(3.0))
+
+
 def test_rows_outside_every_sequence():
     q, k, v, do = _inputs([50], [60], 4, 2, 64, BF, seed=7)
     cu_q, cu_k = torch.tensor([10, 30, 41], dtype=torch.int32), torch.tensor([5, 20, 51], dtype=torch.int32)
