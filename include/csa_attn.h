@@ -89,7 +89,11 @@ size_t csa_norm_rope_workspace_size(const csa_norm_rope_problem* p);
  * A row that sees no key, and a row outside every sequence, gives out = 0 and
  * lse = -inf.  Lengths of zero are allowed on either side.
  * What a sequence does not hold is never part of its results: rows of other
- * sequences and cache entries past k_len may hold anything, also NaN.
+ * sequences and cache entries past k_len may hold anything, also NaN.  Keys of
+ * the sequence itself that are hidden from a row (later ones) do not reach its
+ * out and lse either, whatever they hold.  The gradients of a sequence that
+ * holds infinite or NaN values are not specified; those of the others are
+ * unaffected.
  *   cu_q, cu_k [N+1] int32 ascending in 0..Tq, 0..Tk; k_len [N] int32 or NULL.
  *   They are device memory; entries out of order or range are clamped, never
  *   followed, and record CSA_ERR_DEVICE in the device status word.

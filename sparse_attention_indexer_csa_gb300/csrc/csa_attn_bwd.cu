@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Cta<D> ct{base, bars, ctl, 0u};
 
   if (warp == kItemWarp) {
-    reg_shrink<2>();
+    reg_shrink();
     if (blockIdx.x == 0)
       for (int i = static_cast<int>(lane); i < a.N; i += 32) seq_extent(a, i);
     run_items<D>(ct, [&](uint32_t id) {
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return it;
     });
   } else if (warp == kTmaWarp) {
-    reg_shrink<2>();
+    reg_shrink();
     const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
     Ring k(C::kE), v(C::kF);
     uint32_t n_res = 0;
@@ -815,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n_res > 0) mbar_wait(bars + C::kBarRes, (n_res - 1u) & 1u, ctl);
     }
   } else if (warp == kMmaWarp) {
-    reg_shrink<2>();
+    reg_shrink();
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffE), 128);
     const uint64_t vd = smem_desc_kmajor(smem_u32(base + C::kOffF), 128);
@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const WaitCtl dctl{&dummy, ctl.limit_ns};
     mbar_wait(bars + C::kBarDone, 0u, dctl);
   } else if (warp == kPrepWarp) {
-    reg_shrink<2>();
+    reg_shrink();
     uint32_t last_par = 0;
     int used = 0;
     while (const volatile BwdItem* it = ct.next()) {

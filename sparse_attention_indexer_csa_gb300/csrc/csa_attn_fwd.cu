@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
   };
 
   if (warp == C::kItemWarp) {
-    reg_shrink<TILES>();
+    reg_shrink();
     // ----------------------------------------------------------------------- items
     // Prepared ahead of the other roles: the search for a run of rows is a chain of global loads.
     if (blockIdx.x == 0)
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
       if (lane == 0) mbar_arrive(bars + C::kBarItem + sl);
     }
   } else if (warp == C::kTmaWarp) {
-    reg_shrink<TILES>();
+    reg_shrink();
     if (lane == 0) {  // --------------------------------------------------- TMA producer
       const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
       uint32_t at = 0, phase = 1, used = 0, nq[TILES] = {};
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
           mbar_wait(bars + C::kBarFull + (used - 1 - i) % C::kStages, ((used - 1 - i) / C::kStages) & 1u, dctl);
     }
   } else if (warp == C::kMmaWarp) {
-    reg_shrink<TILES>();
+    reg_shrink();
     // ----------------------------------------------------------------------- issuer of the products
     // The warp runs as one (uniform operands: a descriptor moved to uniform registers for each product made the
     // products wait for their issue), one elected thread issues.
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
     }
     if (TILES == 2 && !SPLIT && (threadIdx.x & 127) == 0) bulk_wait_group_all();
   } else {  // ---------------------------------------------------------------- mender
-    reg_shrink<TILES>();
+    reg_shrink();
     uint32_t ring = 0, last_par = 0;
     while (const volatile FwdItem* it = next_item()) {
       const int lo = it->lo, top = max(it->hi[0], it->hi[1]), open = it->open, lk = it->s.lk;

@@ -69,8 +69,8 @@ struct RowItem {
 // between the x-th and the next of those borders in ascending order (two
 // borders that fall together leave an empty run).  The x-th is found by a
 // search for how many multiples are among the first x+1 borders, 32 probes at
-// a time by a warp, whose lanes all get the result (or by one thread).  Entries out of order give some
-// other runs inside 0..Tq.
+// a time by a warp, whose lanes all get the result (or by one thread).
+// Entries out of order give some other runs inside 0..Tq.
 template <bool KEYS, bool WARP = true>
 __device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int nb, int x) {
   const int lane = static_cast<int>(lane_id());
@@ -222,13 +222,7 @@ __device__ __forceinline__ void reg_grow() {
   else
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
 }
-template <int TILES>
-__device__ __forceinline__ void reg_shrink() {
-  if constexpr (TILES == 2)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-}
+__device__ __forceinline__ void reg_shrink() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
 
 // ----------------------------------------------------------------- small helpers
 template <typename X>
@@ -245,31 +239,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   const uint32_t t = is_bf16<X>() ? 1u : 0u;  // operand type: 0 f16, 1 bf16
   return (1u << 4) | (t << 7) | (t << 10) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// The products of csa_ptx.cuh with descriptors given as their low words (start
-// address; the high words are the same for every tile): the issuing thread
-// then adds 32-bit offsets instead of holding 64-bit sums in registers.
-__device__ __forceinline__ uint32_t desc_hi(uint64_t d) { return static_cast<uint32_t>(d >> 32); }
-__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(a_hi), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void umma_lo_tmem_a(uint32_t d, uint32_t a, uint32_t b, uint32_t b_hi, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
-      "mov.b64 y, {%2, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
