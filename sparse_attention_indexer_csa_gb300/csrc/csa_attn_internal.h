@@ -8,6 +8,13 @@
 namespace csa {
 
 // ----------------------------------------------------------------- norm + rotation
+// How the rows (token, head) of q or of k are dealt to groups of lanes: unit n
+// (R consecutive rows) goes to group n % groups, so that all groups together
+// read and write one window that moves through memory.
+struct RowDeal {
+  int groups, R, rounds;
+  int skip, dt, dh;  // rows between two units of a group; the same in tokens and heads
+};
 struct NormRopeParams {
   int T, Hq, Hk, D, rot, off, w_dtype;
   float eps, inv_d;
@@ -20,7 +27,7 @@ struct NormRopeParams {
   float *dqw, *dkw;           // gradients of the weights (backward)
   float* part;                // partial sums of them, [blocks][D] (backward)
   int q_blocks;               // blocks that work on q; the others work on k
-  int cs_tokens;              // tokens whose cosines and sines a chunk of rows needs at most
+  RowDeal deal_q, deal_k;
 };
 constexpr int kNormRopeBlocks = 152 * 4;  // blocks (and partial sums) of the backward at most
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);

@@ -10,14 +10,18 @@
 // norm of a head is a sum over values that are read anyway).  A row (one
 // token, one head) is held by G lanes, eight values each, so every access is
 // 16 bytes wide (8 for 16-bit halves) and the mean is a shuffle within G lanes.
-// Both values of a pair are in the same lane.  Rows are walked head-fastest,
-// so a block's rows belong to a few tokens whose cosines and sines it computes
-// once, into shared memory.
+// Both values of a pair are in the same lane.  A group of lanes takes rows in
+// units of up to eight consecutive ones (head-fastest) and forms the cosines and
+// sines of a token itself when it comes to it: four pairs a lane, once for the
+// token's heads in the unit.  (In shared memory, once per block, they cost a
+// barrier and its wait per chunk: 126 us against 98 for 16384 tokens.)  The units
+// of all groups lie side by side in memory: one long run of rows for each group
+// took 122 us, since as many places of the memory were open as there are groups.
 //
 // Measured (bf16, 64 + 8 heads of 128): forward, 16384 tokens, all values
-// rotated, 126 us (4.8 TB/s, a plain copy gives 6.7); 32768 tokens, half
-// rotated in neighbouring pairs, 216 us (5.6 TB/s), gradients 376 us (4.8
-// TB/s).  64 tokens: 5 us, a launch.
+// rotated, 98 us (6.15 TB/s, a plain copy gives 6.69); 32768 tokens, half
+// rotated in neighbouring pairs, 189 us (6.4 TB/s), gradients 294 us (6.2
+// TB/s).  64 tokens: 4.6 us, a launch.
 //
 // Angles: position * freq modulo 2^64 is the fraction of a turn with 64 bits
 // after the point, whatever the position; its upper 32 bits, as a signed
@@ -33,7 +37,11 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsFwd = 4, kRowsBwd = 3;  // rows of a thread in a chunk
+// Rows of a thread on their way (gradients of 32768 tokens: 3, 313 us; 4, 294; fp32 has registers for two).
+template <typename X, bool BWD>
+constexpr int kRows = BWD && sizeof(X) == 4 ? 2 : 4;
+// Consecutive rows of a group of lanes, at most (16384 tokens: 4, 104 us; 8, 98; 16, 124; 32, 120).
+constexpr int kUnit = 8;
 // Blocks per SM (the registers a thread has): fp32 rows take twice the
 // registers while they are on their way, and spill at three.
 template <typename X, bool BWD>
@@ -136,41 +144,23 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// Cosines and sines of the tokens t0 .. t0+n-1, rot/2 of each.  A lane takes
-// four pairs of a token; pair p stands at (p % 4) * (rot/8) + p / 4, so that the
-// lanes of a row read consecutive words (in the pairs' own order they meet in
-// two to four banks).
-__device__ __forceinline__ void fill_angles(const NormRopeParams& p, int t0, int n, float2* cs) {
-  const int half = p.rot / 2, lanes = half / 4;
-  for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int t = i / half, j = i - t * half;
-    const uint64_t turns = static_cast<uint64_t>(p.pos[t0 + t]) * p.freqs[j];
-    const float x = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    float s, c;
-    sincospif(x, &s, &c);
-    cs[t * half + (j & 3) * lanes + (j >> 2)] = make_float2(c, s);
-  }
-}
-
 // Turning as two products: value <- value * c + partner * s, both values of a
 // pair being in the same lane, with s of the sign that its place asks for.  In
-// the forward the weights are part of c and s (the partner's of s), formed once
-// per token; rows of a token follow each other.  Values that are not turned
-// have c = 1 (the weight) and s = 0.
+// the forward the weights are part of c and s (the partner's of s).  Values
+// that are not turned have c = 1 (the weight) and s = 0.
 template <bool INTER, bool BWD>
 struct Turn {
-  bool in;     // the values are turned
-  int first;   // the lane's place among those of the pairs
-  int lanes;   // lanes of the pairs
-  int token;   // whose c and s are held
+  const uint64_t* freqs;  // of the lane's four pairs; null: its values are not turned
   float2 c[4], s[4];
 
-  __device__ __forceinline__ Turn(const NormRopeParams& p, const Lane& ln) {
+  __device__ __forceinline__ Turn(const NormRopeParams& p, const Lane& ln, const V8& w) {
     const int r = ln.e - p.off;
-    in = r >= 0 && r < (INTER ? p.rot : p.rot / 2);
-    lanes = p.rot / 8;
-    first = in ? r / (INTER ? 8 : 4) : 0;
-    token = -1;
+    freqs = r >= 0 && r < (INTER ? p.rot : p.rot / 2) ? p.freqs + (INTER ? r / 2 : r) : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = BWD ? make_float2(1.f, 1.f) : w.p[i];
+      s[i] = make_float2(0.f, 0.f);
+    }
   }
   // The partners of v's values.
   __device__ __forceinline__ static V8 partners(const V8& v) {
@@ -179,26 +169,25 @@ struct Turn {
     for (int i = 0; i < 4; ++i) o.p[i] = INTER ? make_float2(v.p[i].y, v.p[i].x) : v.p[i ^ 2];
     return o;
   }
-  // c and s of token `tok` of those in `all`; w: this lane's weights (forward)
-  __device__ __forceinline__ void hold(const float2* all, int tok, const V8& w) {
-    if (tok == token) return;
-    token = tok;
+  // c and s of a position; w: this lane's weights (forward)
+  __device__ __forceinline__ void set(int64_t pos, const V8& w) {
+    if (freqs == nullptr) return;
+    float2 a[4];  // cosine and sine of each pair
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t turns = static_cast<uint64_t>(pos) * freqs[i];
+      sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &a[i].y, &a[i].x);  // 2^-31
+    }
     const V8 wo = partners(w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      c[i] = make_float2(1.f, 1.f);
-      s[i] = make_float2(0.f, 0.f);
-      if (in) {
-        if constexpr (INTER) {
-          const float2 a = all[(tok * 4 + i) * lanes + first];
-          c[i] = make_float2(a.x, a.x);
-          s[i] = BWD ? make_float2(a.y, -a.y) : make_float2(-a.y, a.y);
-        } else {
-          const int k = 2 * (i & 1);
-          const float2 a = all[(tok * 4 + k) * lanes + first], b = all[(tok * 4 + k + 1) * lanes + first];
-          c[i] = make_float2(a.x, b.x);
-          s[i] = ((i < 2) != BWD) ? make_float2(-a.y, -b.y) : make_float2(a.y, b.y);
-        }
+      if constexpr (INTER) {
+        c[i] = make_float2(a[i].x, a[i].x);
+        s[i] = BWD ? make_float2(a[i].y, -a[i].y) : make_float2(-a[i].y, a[i].y);
+      } else {
+        const int k = 2 * (i & 1);
+        c[i] = make_float2(a[k].x, a[k + 1].x);
+        s[i] = ((i < 2) != BWD) ? make_float2(-a[k].y, -a[k + 1].y) : make_float2(a[k].y, a[k + 1].y);
       }
       if constexpr (!BWD) {
         c[i] = fmul2(c[i], w.p[i]);
@@ -243,129 +232,129 @@ __device__ __forceinline__ Part<X> make_part(const NormRopeParams& p) {
   return a;
 }
 
-// Position (token, head) of a row, moved on by a fixed number of rows without
-// divisions; next() says whether the head count was passed.
-struct Walk {
-  int t, h, H, dt, dh;
-  __device__ __forceinline__ Walk(long long row, int heads, int step) : H(heads) {
-    t = static_cast<int>(row / heads);
-    h = static_cast<int>(row - static_cast<long long>(t) * heads);
-    dt = step / heads;
-    dh = step - dt * heads;
-  }
-  __device__ __forceinline__ bool next() {
-    t += dt;
-    h += dh;
-    const bool wrap = h >= H;
-    if (wrap) {
+// A stretch of n() rows: one token's from head h on, in a unit of which k rows are left.
+struct Stretch {
+  int t, h, k;
+  __device__ __forceinline__ int n(int H) const { return min(H - h, k); }
+  // The one that follows; true where it opens the group's next unit.
+  __device__ __forceinline__ bool advance(const RowDeal& d, int H) {
+    const int m = n(H);
+    if (k > m) {
+      ++t;
+      h = 0;
+      k -= m;
+      return false;
+    }
+    t += d.dt;
+    h += m + d.dh;
+    if (h >= H) {
       h -= H;
       ++t;
     }
-    return wrap;
+    k = d.R;
+    return true;
   }
 };
 
-// A block takes a run of chunks of PER * U consecutive rows; a thread's row u of
-// the next chunk is requested as soon as row u of this one is taken from its
-// registers, so loads are always in flight, and the next chunk's cosines and
-// sines are formed while this one is worked on (one barrier a chunk).
+// A row is requested U rows before it is worked on, as soon as its registers
+// are free.  All groups walk as far (the shuffles need whole warps); what lies
+// past a group's rows is neither read nor written.
 template <typename X, int G, bool INTER, int U, bool BWD>
 __global__ void __launch_bounds__(kThreads, kBlocks<X, BWD>) norm_rope_kernel(const NormRopeParams p) {
-  extern __shared__ float2 cs_all[];
-  constexpr int PER = kThreads / G, CHUNK = PER * U;
+  constexpr int PER = kThreads / G;
   const Part<X> a = make_part<X>(p);
   const Lane ln = make_lane<INTER>(p, threadIdx.x % G);
   const int e = ln.e, gap = ln.gap;
   const bool lane_ok = e < p.D;
-  const long long chunks = (a.rows + CHUNK - 1) / CHUNK;
-  const long long c0 = chunks * a.block / a.blocks, c1 = chunks * (a.block + 1) / a.blocks;
+  const int group = a.block * PER + threadIdx.x / G;
+  const RowDeal deal = a.is_q ? p.deal_q : p.deal_k;
+  // rows of this group: only its last unit may be short
+  const long long last = a.rows - (static_cast<long long>(deal.rounds - 1) * deal.groups + group) * deal.R;
+  int left = (deal.rounds - 1) * deal.R + static_cast<int>(min(max(last, 0ll), static_cast<long long>(deal.R)));
+  int left_ahead = left;
+  const V8 w = load_weight(a.w, p.w_dtype, e, gap, p.D);
+  Turn<INTER, BWD> tn(p, ln, w);
+  const long long row0 = static_cast<long long>(group) * deal.R;
+  const int t0 = a.rows < 0x7FFFFFFFll ? static_cast<int>(row0) / a.H : static_cast<int>(row0 / a.H);
+  Stretch now{t0, static_cast<int>(row0 - static_cast<long long>(t0) * a.H), deal.R};  // of the row worked on
+  Stretch ahead = now;                                                                // of the row requested
+  const X* xp = a.x + ahead.t * a.st + ahead.h * a.sh + e;
+  const X* gp = BWD ? a.g + row0 * p.D + e : nullptr;
+  X* yp = a.y + row0 * p.D + e;
   float2 acc[4] = {};  // gradients of the weights
-  if (c0 < c1) {
-    const int half = p.rot / 2, cs_size = p.cs_tokens * half;
-    const V8 w = load_weight(a.w, p.w_dtype, e, gap, p.D);
-    Turn<INTER, BWD> tn(p, ln);
-    // Pointers and 32-bit counts instead of row numbers: the integer work of a row is half of its instructions.
-    const long long row0 = c0 * CHUNK + threadIdx.x / G, end = min(a.rows, c1 * CHUNK);
-    Walk blk(c0 * CHUNK, a.H, CHUNK);  // first row of the chunk whose angles are formed
-    Walk cur(row0, a.H, PER);          // the row worked on
-    Walk ahead = cur;                  // the row requested
-    int left = row0 < end ? static_cast<int>(min((end - row0 + PER - 1) / PER, 0x3fffffffll)) : 0, left_ahead = left;
-    const X* xp = a.x + ahead.t * a.st + ahead.h * a.sh + e;
-    const X* gp = BWD ? a.g + row0 * p.D + e : nullptr;
-    X* yp = a.y + row0 * p.D + e;
-    const long long step = ahead.dt * a.st + ahead.dh * a.sh, wrap = a.st - a.H * a.sh;
-    const int lin = PER * p.D, nc = static_cast<int>(c1 - c0);
-    Raw8<X> rx[U], rg[BWD ? U : 1];
-    auto request = [&](int u) {
-      rx[u] = Raw8<X>{};
-      if constexpr (BWD) rg[u] = Raw8<X>{};
-      if (left_ahead > 0 && lane_ok) {
-        rx[u] = load8<X, INTER>(xp, gap);
-        if constexpr (BWD) rg[u] = load8<X, INTER>(gp, gap);
-      }
-      --left_ahead;
-      xp += step;
-      if (ahead.next()) xp += wrap;
-      if constexpr (BWD) gp += lin;
-    };
-    auto angles = [&](float2* cs) {
-      // tokens blk.t .. of this chunk's rows
-      const int n = blk.dt + (blk.h + blk.dh > 0 ? 1 : 0) + (blk.h + blk.dh > a.H ? 1 : 0);
-      fill_angles(p, blk.t, min(n, p.T - blk.t), cs);
-    };
+  Raw8<X> rx[U], rg[BWD ? U : 1];
+  int n_ahead = ahead.n(a.H), n_now = n_ahead;
+  auto request = [&](int u) {
+    rx[u] = Raw8<X>{};
+    if constexpr (BWD) rg[u] = Raw8<X>{};
+    if (left_ahead > 0 && lane_ok) {
+      rx[u] = load8<X, INTER>(xp, gap);
+      if constexpr (BWD) rg[u] = load8<X, INTER>(gp, gap);
+    }
+    --left_ahead;
+    xp += a.sh;
+    if constexpr (BWD) gp += p.D;
+    if (--n_ahead == 0) {
+      const bool jump = ahead.advance(deal, a.H);
+      n_ahead = ahead.n(a.H);
+      xp = a.x + ahead.t * a.st + ahead.h * a.sh + e;
+      if (BWD && jump) gp += static_cast<long long>(deal.skip) * p.D;
+    }
+  };
+  // the position of the coming stretch is on its way while this one's heads are worked on
+  auto position = [&](const Stretch& s) { return static_cast<unsigned>(s.t) < static_cast<unsigned>(p.T) ? p.pos[s.t] : 0; };
+  auto coming = [&]() {
+    Stretch s = now;
+    s.advance(deal, a.H);
+    return position(s);
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u) request(u);
-    cur.t -= blk.t;  // counted from the chunk's first token
-    int buf = 0;
-    angles(cs_all);
-    __syncthreads();
-    for (int c = 0; c < nc; ++c) {
-      const int t_first = blk.t;
-      blk.next();
-      const float2* cs = cs_all + buf * cs_size;
-      if (c + 1 < nc) angles(cs_all + (buf ^ 1) * cs_size);
-      tn.token = -1;
+  for (int u = 0; u < U; ++u) request(u);
+  int64_t pos = coming();
+  tn.set(position(now), w);
+  const int most = deal.rounds * deal.R;  // all groups walk as far
+  for (int i = 0; i < most; i += U) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const Raw8<X> raw = BWD ? rg[BWD ? u : 0] : rx[u];  // what is turned: the cotangent, or the row
-        V8 x = widen(rx[u]);
-        const V8 v = BWD ? widen(raw) : x;
-        request(u);
-        const bool ok = left > 0;
-        tn.hold(cs, ok ? cur.t : 0, w);
-        float2 ss = fmul2(x.p[0], x.p[0]);
+    for (int u = 0; u < U; ++u) {
+      const Raw8<X> raw = BWD ? rg[BWD ? u : 0] : rx[u];  // what is turned: the cotangent, or the row
+      V8 x = widen(rx[u]);
+      const V8 v = BWD ? widen(raw) : x;
+      request(u);
+      const bool ok = left > 0;
+      float2 ss = fmul2(x.p[0], x.p[0]);
 #pragma unroll
-        for (int i = 1; i < 4; ++i) ss = ffma2(x.p[i], x.p[i], ss);
-        float r = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
-        if (BWD && !ok) r = 0.f;  // no row: nothing may reach the weights' sums (eps may be 0)
-        const float2 r2 = make_float2(r, r);
-        V8 y;
-        if constexpr (BWD) {
-          float2 dot = make_float2(0.f, 0.f);
+      for (int i = 1; i < 4; ++i) ss = ffma2(x.p[i], x.p[i], ss);
+      float r = rsqrtf(group_sum<G>(ss.x + ss.y) * p.inv_d + p.eps);
+      if (BWD && !ok) r = 0.f;  // no row: nothing may reach the weights' sums (eps may be 0)
+      const float2 r2 = make_float2(r, r);
+      V8 y;
+      if constexpr (BWD) {
+        float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 z = tn.turned(v, i), xh = fmul2(x.p[i], r2);
-            const float2 zx = fmul2(z, xh);
-            acc[i] = fadd2(acc[i], zx);
-            dot = ffma2(zx, w.p[i], dot);
-            y.p[i] = fmul2(z, w.p[i]);
-            x.p[i] = xh;
-          }
-          const float m = -group_sum<G>(dot.x + dot.y) * p.inv_d;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y.p[i] = fmul2(r2, ffma2(x.p[i], make_float2(m, m), y.p[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y.p[i] = fmul2(r2, tn.turned(x, i));
+        for (int i = 0; i < 4; ++i) {
+          const float2 z = tn.turned(v, i), xh = fmul2(x.p[i], r2);
+          const float2 zx = fmul2(z, xh);
+          acc[i] = fadd2(acc[i], zx);
+          dot = ffma2(zx, w.p[i], dot);
+          y.p[i] = fmul2(z, w.p[i]);
+          x.p[i] = xh;
         }
-        if (ok && lane_ok) store8<X, INTER>(yp, gap, y);
-        cur.next();
-        --left;
-        yp += lin;
+        const float m = -group_sum<G>(dot.x + dot.y) * p.inv_d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.p[i] = fmul2(r2, ffma2(x.p[i], make_float2(m, m), y.p[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.p[i] = fmul2(r2, tn.turned(x, i));
       }
-      cur.t -= blk.t - t_first;
-      buf ^= 1;
-      __syncthreads();
+      if (ok && lane_ok) store8<X, INTER>(yp, gap, y);
+      --left;
+      yp += p.D;
+      if (--n_now == 0) {
+        if (now.advance(deal, a.H)) yp += static_cast<long long>(deal.skip) * p.D;
+        n_now = now.n(a.H);
+        tn.set(pos, w);
+        pos = coming();
+      }
     }
   }
   if constexpr (BWD) {
@@ -404,9 +393,22 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, i
   }
 }
 
+// See RowDeal; rows > 0, groups > 0.
+RowDeal deal_rows(long long rows, long long groups, int H) {
+  RowDeal d;
+  const long long rounds = (rows + groups * kUnit - 1) / (groups * kUnit);
+  d.groups = static_cast<int>(groups);
+  d.rounds = static_cast<int>(rounds);
+  d.R = static_cast<int>((rows + groups * rounds - 1) / (groups * rounds));  // at most kUnit: only the last round is short
+  d.skip = static_cast<int>((groups - 1) * d.R);
+  d.dt = d.skip / H;
+  d.dh = d.skip % H;
+  return d;
+}
+
 template <typename X, int G, bool INTER, bool BWD>
 cudaError_t run(NormRopeParams p, cudaStream_t stream) {
-  constexpr int PER = kThreads / G, U = BWD ? kRowsBwd : kRowsFwd, CHUNK = PER * U;
+  constexpr int PER = kThreads / G, U = kRows<X, BWD>, CHUNK = PER * U;
   // blocks of q and k in proportion to their chunks, all on the GPU at once
   auto chunks = [&](int H) { return (static_cast<long long>(p.T) * H + CHUNK - 1) / CHUNK; };
   const long long cq = chunks(p.Hq), ck = chunks(p.Hk), most = 152 * kBlocks<X, BWD>;
@@ -416,14 +418,10 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
     nq = std::min<long long>(cq, std::max<long long>(1, most - nk));
   }
   p.q_blocks = static_cast<int>(nq);
-  // tokens that a chunk can meet, for both parts
-  auto tokens = [&](int H) { return H > 0 ? std::min<long long>(p.T, (CHUNK - 1 + H - 1) / H + 1) : 0; };
-  p.cs_tokens = static_cast<int>(std::max(tokens(p.Hq), tokens(p.Hk)));
-  const size_t smem = static_cast<size_t>(2) * p.cs_tokens * (p.rot / 2) * sizeof(float2);
-  cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024 && (e = smem_limit_once<norm_rope_kernel<X, G, INTER, U, BWD>>(80 * 1024)) != cudaSuccess) return e;
-  norm_rope_kernel<X, G, INTER, U, BWD><<<static_cast<unsigned>(nq + nk), kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+  p.deal_q = deal_rows(static_cast<long long>(p.T) * p.Hq, nq * PER, p.Hq);
+  if (nk > 0) p.deal_k = deal_rows(static_cast<long long>(p.T) * p.Hk, nk * PER, p.Hk);
+  norm_rope_kernel<X, G, INTER, U, BWD><<<static_cast<unsigned>(nq + nk), kThreads, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !BWD) return e;
   norm_rope_dw_kernel<<<dim3((p.D + 31) / 32, p.Hk > 0 ? 2 : 1), 1024, 0, stream>>>(
       p.part, static_cast<int>(nq), static_cast<int>(nk), p.D, p.dqw, p.dkw);

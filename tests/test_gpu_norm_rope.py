@@ -90,6 +90,21 @@ def test_forward_and_gradients(case):
         _close(dw, rw, mw, 2.0 ** -15)
 
 
+# More rows than one round over the GPU holds, the last one short, tokens across units: every group of lanes
+# goes on to further rows.
+ROUNDS = [
+    (1601, 45, 7, 128, 64, 64, True, BF, BF, 11),
+    (3001, 13, 1, 256, 256, 0, False, FP16, F32, 0),
+    (20011, 3, 2, 128, 128, 0, False, F32, F32, 900001),
+    (300007, 1, 1, 32, 32, 0, False, BF, BF, 5),
+]
+
+
+@pytest.mark.parametrize("case", ROUNDS, ids=str)
+def test_several_rounds(case):
+    test_forward_and_gradients(case)
+
+
 def test_gradient_by_differences():
     # directional difference of sum(y * g) in fp32 against <dx, d> + <dw, e>
     gen = torch.Generator().manual_seed(3)
