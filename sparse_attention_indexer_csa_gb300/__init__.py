@@ -1,5 +1,7 @@
 """GB300 (sm_103a) CSA indexer: per-row top-k selection of compressed KV
-entries by the head-reduced score  sum_h w[b,s,h] * ReLU(scale * q.k).
+entries by the head-reduced score  sum_h w[b,s,h] * ReLU(scale * q.k), and the
+operators around it: norm and rotation of queries and keys, attention of packed
+sequences, with their gradients.
 
 The compute lives in ``libcsa_index.so`` (hand-written CUDA behind the C ABIs
 of ``include/csa_index.h`` and ``include/csa_attn.h``); this package is its

@@ -36,6 +36,12 @@
 // factor does not cancel: rows (dkv) or keys (dq) past the end are cleared in
 // shared memory before any product reads them: such a tile lands on a barrier
 // of its own, and the warp that cleared its end completes the tile's in the ring.
+//
+// Measured (bf16, 64 + 8 heads of 128, 8192 tokens in 5 documents): 0.828 ms,
+// 1025 TFLOP/s of the five products that count, 1435 of the seven executed (a
+// library product: 1885).  dkv 0.405 ms, tensor pipe active 79 %: the products;
+// dq 0.366 ms, 62 %: the elementwise warps' way between two products, and short
+// items; delta 0.042 ms, 6.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
