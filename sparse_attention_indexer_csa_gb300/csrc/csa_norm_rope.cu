@@ -409,7 +409,8 @@ RowDeal deal_rows(long long rows, long long groups, int H) {
 template <typename X, int G, bool INTER, bool BWD>
 cudaError_t run(NormRopeParams p, cudaStream_t stream) {
   constexpr int PER = kThreads / G, U = kRows<X, BWD>, CHUNK = PER * U;
-  // blocks of q and k in proportion to their chunks, all on the GPU at once
+  // Blocks of q and k in proportion to their chunks, all on the GPU at once.  A
+  // small call has U rows for each group of lanes (64 tokens: 4.7 us; one row for each, 7.1).
   auto chunks = [&](int H) { return (static_cast<long long>(p.T) * H + CHUNK - 1) / CHUNK; };
   const long long cq = chunks(p.Hq), ck = chunks(p.Hk), most = 152 * kBlocks<X, BWD>;
   long long nq = cq, nk = ck;
