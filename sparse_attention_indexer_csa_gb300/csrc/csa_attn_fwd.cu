@@ -111,6 +111,7 @@ struct FwdItem {
   int n_tok[2];   // tokens of each block
   int hk, z;      // key head, share
   int open;       // keys that all rows see: the value tiles past them are mended before their products
+  int seen;       // keys that some row sees
   int odd;        // first key tile of which values were taken out (see mend_values)
 };
 static_assert(sizeof(FwdItem) <= 64, "a slot");
@@ -133,12 +134,14 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
   it.open = r.t0 < r.t1 ? keys_seen(a, r.s, r.t0 - r.s.q0) : 0;
   it.lo = 0;
   int top = 0;
+  it.seen = 0;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     it.n_tok[w] = w < TILES ? min(f.tq, max(0, r.t1 - r.t0 - w * f.tq)) : 0;
     const int see = it.n_tok[w] > 0 ? keys_seen(a, r.s, r.t0 + w * f.tq + it.n_tok[w] - 1 - r.s.q0) : 0;
     it.hi[w] = (see + 127) >> 7;
     top = max(top, it.hi[w]);
+    it.seen = max(it.seen, see);
   }
   if (f.n_split > 1) {
     const int share = (top + f.n_split - 1) / f.n_split;
@@ -150,8 +153,8 @@ __device__ __forceinline__ FwdItem make_item(const FwdArgs& f, uint32_t id) {
 }
 
 // What the products of a value tile may not meet, since a hidden key's P of 0
-// does not cancel it.  Rows from `held` on are not the sequence's: cleared.
-// Rows from `open` on are hidden from some row of the item: what is infinite
+// does not cancel it.  Rows from `held` on are the sequence's no more, or hidden
+// from every row of the item: cleared.  Those from `open` on are hidden from some: what is infinite
 // or NaN among them is taken out, and `odd` remembers the tile (patch_row adds
 // it to the rows that see it).  By a warp of its own, between the tile's arrival
 // and the products: 2.72 -> 2.77 ms for a prompt of 16384 tokens, 1.26 -> 1.33
@@ -650,11 +653,11 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
     reg_shrink();
     uint32_t ring = 0, last_par = 0;
     while (const volatile FwdItem* it = next_item()) {
-      const int lo = it->lo, top = max(it->hi[0], it->hi[1]), open = it->open, lk = it->s.lk;
+      const int lo = it->lo, top = max(it->hi[0], it->hi[1]), open = it->open, seen = it->seen;
       for (int j = max(lo, open >> 7); j < top; ++j) {
         const uint32_t st = (ring + 2u * static_cast<uint32_t>(j - lo) + 1u) % C::kStages;
         if (mbar_wait(bars + C::kBarLast + st, (last_par >> st) & 1u, ctl))
-          mend_values<X, D>(base + C::kOffKv + st * C::kTile, lk - j * 128, open - j * 128, const_cast<int*>(&it->odd), j);
+          mend_values<X, D>(base + C::kOffKv + st * C::kTile, seen - j * 128, open - j * 128, const_cast<int*>(&it->odd), j);
         last_par ^= 1u << st;
         fence_proxy_async_shared();
         __syncwarp();
