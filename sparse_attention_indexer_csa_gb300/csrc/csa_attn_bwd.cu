@@ -644,9 +644,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = it->n;
       int first_row, all_rows;  // the first row (from the share's first on) that sees this key; that sees all keys
       {
-        const int d = it->t0 - it->s.k0 - (it->s.lk - (it->s.q1 - it->s.q0)) - it->r_lo - it->lo * f.tq;
-        first_row = a.causal ? (d + key) * a.g : 0;
-        all_rows = a.causal ? (d + it->own - 1) * a.g : 0;
+        // in tokens, and clamped there: a key far before the first row is seen from it on, and the distance times the
+        // heads need not fit 32 bits
+        const int d = max(it->t0 - it->s.k0 - (it->s.lk - (it->s.q1 - it->s.q0)), -128) - it->r_lo - it->lo * f.tq;
+        first_row = a.causal ? max(0, d + key) * a.g : 0;
+        all_rows = a.causal ? max(0, d + it->own - 1) * a.g : 0;
       }
       for (int i = 0; i < n; ++i, ++blk) {
         const uint32_t b = blk & 1u;

@@ -1,0 +1,90 @@
+"""Attention on the GPU where lengths, magnitudes or infinities are extreme.
+
+Each tolerance counts the roundings named beside it; u = eps/2 of the storage
+type, and ds = 2^-16 of the largest scale*|q|.|k| bounds a score's error (fp32
+sums of exact products).
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_indexer_csa_gb300 as csa
+from oracle import attn_oracle as A
+
+pytestmark = pytest.mark.gpu
+
+BF, FP16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    csa.load()
+
+
+def _cu(*lengths):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+
+
+def _ok():
+    torch.cuda.synchronize()
+    assert csa.device_status() == csa.CSA_OK
+
+
+def test_gradients_of_keys_far_before_the_rows():
+    """One row of 128 heads over 17 million keys: the distance of an early key from the row, times
+    the heads, passes 2^31.
+
+    All keys and values are zero but for a few, so that the definition is a sum over those and one more term of
+    weight n0.  The forward's out and lse are the definition's, rounded.  dk and dv: the roundings of p or of ds
+    (u), the score's error (2 ds), delta from the rounded out (u sum |dout||out|), fp32 sums of 64
+    products (2^-15), the output's own (u).
+    """
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 20 GB of device memory")
+    lk, H, D, scale = 17_000_000, 128, 64, 0.125
+    gen = torch.Generator().manual_seed(41)
+    r = lambda *s: torch.randn(*s, generator=gen).to(BF)  # noqa: E731
+    at = [0, 5, 200, lk // 2, lk - 1]
+    n0 = lk - len(at)
+    q, do, kt, vt = r(1, H, D), r(1, H, D), r(len(at), D), r(len(at), D)
+    q[..., 0], kt[3, 0] = 4.0, 32.0  # one key weighs as much as all the zero ones
+    Q, G, K, V = A.f64(q)[0], A.f64(do)[0], A.f64(kt), A.f64(vt)
+    s = scale * Q @ K.T
+    z = np.exp(s).sum(1) + n0
+    p, p0 = np.exp(s) / z[:, None], 1 / z
+    out = torch.from_numpy(p @ V).to(BF)
+    O = A.f64(out)
+    k, v = (torch.zeros(lk, 1, D, dtype=BF, device="cuda") for _ in range(2))
+    k[at, 0], v[at, 0] = kt.cuda(), vt.cuda()
+    dq, dk, dv = csa.attn_backward(do.cuda(), q.cuda(), k, v, out[None].cuda(),
+                                   torch.from_numpy(np.log(z)).float()[None].cuda(), _cu(1), _cu(lk), scale)
+    _ok()
+    u = 2.0 ** -8
+    ds = 2.0 ** -16 * scale * (np.abs(Q) @ np.abs(K).T).max()
+    delta = (G * (p @ V)).sum(1)
+    err = u * (np.abs(G) * np.abs(O)).sum(1)  # of delta
+    def grads(p, dp, dpm):  # of one key, from its weight in each head, dP and the magnitudes of dP's sum
+        d = p * (dp - delta)
+        dm = np.abs(d) * (u + 2 * ds) + p * (err + 2.0 ** -15 * dpm)
+        gk, gv = scale * d @ Q, p @ G
+        return (gk, u * np.abs(gk) + scale * dm @ np.abs(Q) + 2.0 ** -15 * np.abs(scale * d) @ np.abs(Q),
+                gv, u * np.abs(gv) + (u + 2 * ds + 2.0 ** -15) * p @ np.abs(G))
+    for i, j in enumerate(at):
+        gk, bk, gv, bv = grads(p[:, i], G @ V[i], np.abs(G) @ np.abs(V[i]))
+        assert (np.abs(A.f64(dk[j, 0]) - gk) <= bk).all() and (np.abs(A.f64(dv[j, 0]) - gv) <= bv).all(), j
+    rest = torch.ones(lk, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    gk, bk, gv, bv = grads(p0, 0.0, 0.0)
+    for got, want, bound in ((dk, gk, bk), (dv, gv, bv)):
+        # all zero keys have the same gradients: every one lies between the extremes of its column
+        lo = torch.where(rest[:, None], got[:, 0], float("inf")).amin(0)
+        hi = torch.where(rest[:, None], got[:, 0], float("-inf")).amax(0)
+        assert (np.abs(A.f64(lo) - want) <= bound).all() and (np.abs(A.f64(hi) - want) <= bound).all()
+        assert np.abs(want).min() > 0
+    mag = np.abs(p * (G @ V.T - delta[:, None])) @ np.abs(K)
+    want = scale * (p * (G @ V.T - delta[:, None])) @ K
+    bound = u * np.abs(want) + scale * (mag * (u + 2 * ds) + (p * (err[:, None] + 2.0 ** -15 * (np.abs(G) @ np.abs(V).T)))
+                                        @ np.abs(K)) + 2.0 ** -15 * scale * mag
+    assert (np.abs(A.f64(dq[0]) - want) <= bound).all()
