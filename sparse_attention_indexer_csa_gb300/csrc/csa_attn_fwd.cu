@@ -21,7 +21,9 @@
 // raised to the maximum so far (with O and l rescaled and the tile's P formed
 // again) only when a tile's sum of P exceeds 2^12.  Up to there P is in range of
 // fp16 too, its relative precision is the same and so is the quotient O / l; no
-// maximum is taken in the tiles that follow.
+// maximum is taken in the tiles that follow.  Where a first tile's scores are
+// all -inf, m is f.lowest, so that the first score above gives an infinite P
+// and raises it (asking each tile for rows without a reference took 2 %).
 //
 // Roles (TILES = 2: 12 warps, one CTA per SM; TILES = 1: 8 warps, two CTAs
 // per SM):
@@ -97,6 +99,7 @@ struct FwdArgs {
   int nb;        // ceil(Tq / (TILES * tq))
   int n_split;
   float c;       // scale * log2(e)
+  float lowest;  // the least reference of a row: c * lowest is finite
   float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
   float* part_lse;  // [n_split][Tq * Hq]
   unsigned long long wait_ns;
@@ -479,7 +482,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             }
           };
           auto probs = [&](const float (&s)[4][32]) {
-            const float b = m == -INFINITY ? 0.f : -m * c;
+            const float b = -m * c;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int u = 0; u < 64; ++u) {
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
           {
             float s[4][32];
             load(s);
-            if (j == lo) m = row_max(s);
+            if (j == lo) m = fmaxf(row_max(s), f.lowest);
             probs(s);
           }
           if (__any_sync(0xffffffffu, tile > kRaise)) {
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             load(s);
             // the former tiles' product with V has completed: its commit preceded this tile's scores
             const float mn = fmaxf(m, row_max(s));
-            const float r = m == -INFINITY ? 0.f : exp2_approx((m - mn) * c);
+            const float r = exp2_approx((m - mn) * c);
             m = mn;
             l *= r;
             if (j != lo) {
@@ -749,6 +752,7 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
   f.nb = static_cast<int>((static_cast<long long>(p.Tq) + TILES * f.tq - 1) / (TILES * f.tq));
   f.n_split = n_split;
   f.c = p.scale * 1.4426950408889634f;
+  f.lowest = -3.3e38f / std::max(1.f, f.c);
   f.part_o = static_cast<float*>(workspace);
   f.part_lse = f.part_o + static_cast<long long>(n_split) * p.Tq * p.Hq * D;
   f.wait_ns = kAttnWaitNs;

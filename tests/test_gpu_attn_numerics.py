@@ -88,3 +88,31 @@ def test_gradients_of_keys_far_before_the_rows():
     bound = u * np.abs(want) + scale * (mag * (u + 2 * ds) + (p * (err[:, None] + 2.0 ** -15 * (np.abs(G) @ np.abs(V).T)))
                                         @ np.abs(K)) + 2.0 ** -15 * scale * mag
     assert (np.abs(A.f64(dq[0]) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("hidden", [128, 300])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,dt", [(5, 700, 8, 1, 128, BF), (200, 900, 6, 2, 64, FP16), (40, 500, 2, 2, 128, FP16),
+                                              (1, 9000, 8, 1, 128, BF), (150, 640, 32, 1, 64, BF)])
+def test_first_keys_of_no_weight(lq, lk, Hq, Hk, D, dt, hidden):
+    """The first keys a row sees score -inf (a key holds -inf) and weigh nothing: the result is that
+    of the other keys alone, whatever their scores' size.
+
+    Tolerances of out and lse as for any row: p's rounding and the output's (u), the score's error (2 ds),
+    exponentials and sums (2^-18); fp16 loses p below 2^-25.
+    """
+    gen = torch.Generator().manual_seed(hidden + lq)
+    r = lambda *s: torch.randn(*s, generator=gen).to(dt)  # noqa: E731
+    q, k, v = r(lq, Hq, D), r(lk, Hk, D), r(lk, Hk, D)
+    q[..., 0] = 1.0
+    k[:hidden, :, 0] = float("-inf")
+    scale, u, tiny = D ** -0.5, torch.finfo(dt).eps / 2, 2.0 ** -25 if dt == FP16 else 0.0
+    for shift in (0.0, -400.0, 300.0):  # of all the other scores
+        k[hidden:, :, 0] = shift / scale
+        out, lse = csa.attn_forward(q.cuda(), k.cuda(), v.cuda(), _cu(lq), _cu(lk), scale)
+        _ok()
+        ref = A.attention(A.f64(q), A.f64(k[hidden:]), A.f64(v[hidden:]), [0, lq], [0, lk - hidden], scale)
+        ds = 2.0 ** -16 * ref["smax"]
+        err = np.abs(A.f64(out) - ref["out"])
+        bound = u * np.abs(ref["out"]) + (u + 2 * ds[..., None] + 2.0 ** -18) * ref["mag_out"] + tiny * ref["vsum"]
+        assert (err <= bound).all(), (shift, float((err / bound).max()))
+        assert (np.abs(A.f64(lse) - ref["lse"]) <= ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(ref["lse"])).all(), shift
