@@ -19,7 +19,7 @@
 //
 // m is a reference, not the running maximum: the maximum of the first tile,
 // raised to the maximum so far (with O and l rescaled and the tile's P formed
-// again) only when a tile's sum of P exceeds 2^12.  Up to there P is in range of
+// again) only when a tile's sum of P exceeds kRaise.  Up to there P is in range of
 // fp16 too, its relative precision is the same and so is the quotient O / l; no
 // maximum is taken in the tiles that follow.  Where a first tile's scores are
 // all -inf, m is f.lowest, so that the first score above gives an infinite P
@@ -58,7 +58,13 @@
 namespace csa {
 namespace {
 
-constexpr float kRaise = 4096.f;  // a tile's sum of P above which the reference is raised
+// P is formed 2^kShift times its size, so that fp16 holds weights down to 2^-33 of the reference's (at 2^-25, as they
+// come, 131072 keys of that weight would be in l and not in O); O and l share the factor.  The reference is raised
+// when a tile's sum of P exceeds kRaise: P stays in range, and a first tile (128 at most, unshifted) never asks for it.
+template <typename X>
+constexpr int kShift = is_bf16<X>() ? 0 : 8;
+template <typename X>
+constexpr float kRaise = is_bf16<X>() ? 4096.f : 32768.f;
 
 // ROWS: rows of a block that may be used.  32 (with TILES = 1) keeps a smaller
 // query block in shared memory and a third key or value tile in its place; the
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             }
           };
           auto probs = [&](const float (&s)[4][32]) {
-            const float b = -m * c;
+            const float b = static_cast<float>(kShift<X>) - m * c;
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int u = 0; u < 64; ++u) {
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
             if (j == lo) m = fmaxf(row_max(s), f.lowest);
             probs(s);
           }
-          if (__any_sync(0xffffffffu, tile > kRaise)) {
+          if (__any_sync(0xffffffffu, tile > kRaise<X>)) {
             float s[4][32];
             load(s);
             // the former tiles' product with V has completed: its commit preceded this tile's scores
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
       }
       const bool seen = any && ok && (l > 0.f || l != l);
       const float inv = seen ? 1.f / l : 0.f;
-      const float lse = seen ? (m * c + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+      const float lse = seen ? (m * c + __log2f(l * (1.f / (1 << kShift<X>)))) * 0.6931471805599453f : -INFINITY;
       const long long rows = static_cast<long long>(a.Tq) * a.Hq;
       // element offset of row `r` of the block (and -1 for a row it does not hold)
       const int t_blk = it->t0 + w * f.tq, hk = it->hk, z = it->z;

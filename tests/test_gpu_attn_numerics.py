@@ -116,3 +116,31 @@ def test_first_keys_of_no_weight(lq, lk, Hq, Hk, D, dt, hidden):
         bound = u * np.abs(ref["out"]) + (u + 2 * ds[..., None] + 2.0 ** -18) * ref["mag_out"] + tiny * ref["vsum"]
         assert (err <= bound).all(), (shift, float((err / bound).max()))
         assert (np.abs(A.f64(lse) - ref["lse"]) <= ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(ref["lse"])).all(), shift
+
+
+@pytest.mark.parametrize("top", [17.3, 19.0])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D", [(1, 131072, 8, 1, 128), (3, 60000, 2, 2, 64), (200, 20000, 4, 1, 64)])
+def test_many_small_weights_in_fp16(lq, lk, Hq, Hk, D, top):
+    """A dominant first key whose value is zero, and many keys whose weights are near or below 2^-25 of its own:
+    the output is the sum of what those bring.
+
+    u for p's rounding and for the output's, 2 ds for the score's error, 2^-18 for exponentials; the sum of
+    weights adds up to a thousand tiles in fp32 (2^-24 each: 2^-14).  A weight below 2^-33 of the first tile's largest
+    is lost.
+    """
+    gen = torch.Generator().manual_seed(lk)
+    r = lambda *s: torch.randn(*s, generator=gen).to(FP16)  # noqa: E731
+    q, k, v = r(lq, Hq, D), r(lk, Hk, D), 1 + 0.1 * r(lk, Hk, D)
+    scale = D ** -0.5
+    q[..., 0] = 1.0
+    k[..., 0], k[0] = 0.0, 0.0
+    k[0, :, 0], v[0] = top / scale, 0.0
+    out, lse = csa.attn_forward(q.cuda(), k.cuda(), v.cuda(), _cu(lq), _cu(lk), scale)
+    _ok()
+    ref = A.attention(A.f64(q), A.f64(k), A.f64(v), [0, lq], [0, lk], scale)
+    u, ds = 2.0 ** -11, 2.0 ** -16 * ref["smax"]
+    err = np.abs(A.f64(out) - ref["out"])
+    bound = (u * np.abs(ref["out"]) + (u + 2 * ds[..., None] + 2.0 ** -18 + 2.0 ** -14) * ref["mag_out"]
+             + 2.0 ** -33 * ref["vsum"])
+    assert (err <= bound).all(), float((err / bound).max())
+    assert (np.abs(A.f64(lse) - ref["lse"]) <= ds + 2.0 ** -14 + 2.0 ** -22 * np.abs(ref["lse"])).all()
