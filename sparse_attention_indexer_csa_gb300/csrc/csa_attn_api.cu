@@ -131,7 +131,7 @@ csa_status check_attn_inputs(const csa_attn_problem* p, const void* q, const voi
 }
 size_t attn_workspace_bytes(const csa_attn_problem* p, int which) {
   if (check_attn(p) != CSA_OK) return 0;
-  if (which == 1) return attn_bwd_plan(p->N, p->Tq, p->Tk, p->Hq, p->Hk, p->D).total;
+  if (which == 1) return attn_bwd_plan(p->N, p->Tq, p->Tk, p->Hq, p->Hk, p->D, p->dtype == CSA_F16).total;
   if (which != 0 || p->Tq == 0 || !attn_supported(p)) return 0;
   // split keys: fp32 outputs and lse of each share
   const AttnPlan plan = attn_plan(p->N, p->Tq, p->Tk, p->Hk, p->Hq / p->Hk);

@@ -37,6 +37,14 @@
 // shared memory before any product reads them: such a tile lands on a barrier
 // of its own, and the warp that cleared its end completes the tile's in the ring.
 //
+// fp16 holds neither dS of a scaled loss's cotangent (p (dP - delta) passes 65504
+// where the gradients do not) nor that of a small one.  |dP - delta| is at most
+// 2 |dout_r| max_j |v_j|: dS is formed times a power of two that brings this bound
+// to 2^15, and dq and dk are taken back in fp32.  dq has a power for each row, dk,
+// which sums over rows, one for each sequence and key head: nothing of another
+// sequence has a part in it.  attn_range_kernel takes the norms and delta in one
+// pass (56 us for delta's 42 at the size below); bf16 has the range and none of this.
+//
 // Measured (bf16, 64 + 8 heads of 128, 8192 tokens in 5 documents): 0.828 ms,
 // 1025 TFLOP/s of the five products that count, 1435 of the seven executed (a
 // library product: 1885).  dkv 0.405 ms, tensor pipe active 79 %: the products;
@@ -100,6 +108,7 @@ struct BwdItem {
   int z;       // dkv: share
   int own;     // tokens (dq) or keys of the sequence (dkv) among t0 .. t1-1
   int r_lo;    // dkv: first row that sees a key of the run
+  float fit;   // fp16: dq: the largest |v|^2 of the sequence; dkv: the power of two that dS is formed with
 };
 static_assert(sizeof(BwdItem) <= 64, "a slot");
 
@@ -210,6 +219,13 @@ __device__ __forceinline__ void product_acc(uint32_t acc, uint32_t x, uint64_t b
     umma_bf16_tmem_a(acc, x + 64u * (ks >> 2) + 8u * (ks & 3), bd + static_cast<uint64_t>(128 * ks), kId,
                      (!first || ks != 0) ? 1u : 0u);
 }
+
+// fp16: 2 |dout| |v| < 2^E for the squares of the two norms.
+__device__ __forceinline__ int ds_exponent(float dout2, float v2) {
+  const int e = static_cast<int>((__float_as_uint(2.f * sqrtf(dout2 * v2)) >> 23) & 255u) - 126;
+  return min(max(e, -60), 60);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Position in a ring of n tiles.
 struct Ring {
@@ -377,6 +393,77 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const AttnParams p, 
   if (r < rows && l == 0) p.delta[r] = s;
 }
 
+// The same for fp16, with what dS can reach: the squares of the norms of dout's
+// rows, and the largest of dout and of v for each sequence and key head.  A block
+// takes a run of rows (or of keys, past `row_blocks`) of one sequence and key head
+// and raises its maximum once: looked at for each row, the few words of a batch of
+// long sequences took four times as long as the values.
+template <typename X, int D>
+__global__ void __launch_bounds__(256, 4)
+    attn_range_kernel(const AttnParams p, int32_t* order, int n_runs, int nb_k, int nb_q, int tq, unsigned row_blocks) {
+  constexpr int G = D / 8, PER = 256 / G, U = 4;
+  __shared__ uint32_t most;
+  if (order != nullptr && blockIdx.x == 0) {
+    order_runs(p, order, n_runs, nb_k, tq);
+    return;
+  }
+  unsigned block = order != nullptr ? blockIdx.x - 1u : blockIdx.x;
+  const bool values = block >= row_blocks;
+  if (values) block -= row_blocks;
+  const int x = static_cast<int>(block / static_cast<unsigned>(p.Hk)), hk = static_cast<int>(block % static_cast<unsigned>(p.Hk));
+  const RowItem it = values ? find_key_item(p, 128, nb_k, x) : find_row_item(p, tq, nb_q, x);
+  if (it.seq < 0 || it.t0 >= it.t1) return;  // the same for the whole block
+  if (threadIdx.x == 0) most = 0u;
+  __syncthreads();
+  const int l = threadIdx.x % G;
+  // keys past k_len are not the sequence's
+  const int rows = values ? max(0, min(it.t1 - it.t0, it.s.lk - (it.t0 - it.s.k0))) : (it.t1 - it.t0) * p.g;
+  float top = 0.f;
+  for (int r0 = threadIdx.x / G; r0 < 128; r0 += U * PER) {
+    uint4 a[U], b[U];
+    long long at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * PER, tok = values ? r : r / p.g;
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+      at[u] = static_cast<long long>(it.t0 + tok) * p.Hq + hk * p.g + (r - tok * p.g);
+      if (r >= rows) continue;
+      if (values) {
+        a[u] = reinterpret_cast<const uint4*>(static_cast<const X*>(p.v) + (it.t0 + tok) * p.v_st + hk * p.v_sh)[l];
+      } else {
+        a[u] = reinterpret_cast<const uint4*>(static_cast<const X*>(p.dout) + at[u] * D)[l];
+        b[u] = reinterpret_cast<const uint4*>(static_cast<const X*>(p.out) + at[u] * D)[l];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t xs[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, ys[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+      float s = 0.f, n2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack_pair<X>(xs[i]), w = unpack_pair<X>(ys[i]);
+        s = fmaf(v.x, w.x, s);
+        s = fmaf(v.y, w.y, s);
+        n2 = fmaf(v.x, v.x, fmaf(v.y, v.y, n2));
+      }
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      }
+      if (l == 0 && !values && r0 + u * PER < rows) {
+        p.delta[at[u]] = s;
+        p.norm2[at[u]] = n2;
+      }
+      top = fmaxf(top, n2);
+    }
+  }
+  // not negative: ordered as their bits
+  if (l == 0) atomicMax(&most, __float_as_uint(top));
+  __syncthreads();
+  if (threadIdx.x == 0) atomicMax(p.range + (static_cast<long long>(it.seq) * p.Hk + hk) * 2 + values, most);
+}
+
 // dk, dv = the sums of the shares, in order: D/4 threads per key and key head.
 template <typename X, int D>
 __global__ void __launch_bounds__(256) attn_join_dkv_kernel(const AttnParams a, const float* part_dk, const float* part_dv,
@@ -470,6 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all = key_run_blocks(a, r, f.tq), share = (all + f.n_split - 1) / f.n_split;
       it.lo = min(all, it.z * share);
       it.n = min(all, it.lo + share) - it.lo;
+      it.fit = 1.f;
+      if (!is_bf16<X>() && r.seq >= 0) {
+        const uint32_t* m = a.range + (static_cast<long long>(r.seq) * a.Hk + it.hk) * 2;
+        it.fit = power_of_two(15 - ds_exponent(__uint_as_float(m[0]), __uint_as_float(m[1])));
+      }
       return it;
     });
   } else if (warp == kTmaWarp) {
@@ -588,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring e(C::kE), o(C::kF);
     while (const volatile BwdItem* it = ct.next()) {
       const int n = it->n, hk = it->hk, q0 = it->s.q0 + it->r_lo + it->lo * f.tq, all = it->s.q1 - q0;
+      const float fit = is_bf16<X>() ? 1.f : it->fit;
       for (int i = 0; i < n; ++i, ++blk) {
         const uint32_t b = blk & 1u;
         const int t0 = q0 + i * f.tq, rows = min(f.tq, all - i * f.tq) * a.g;
@@ -611,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = u * 32 + static_cast<int>(lane);
             const bool none = l[u] == -INFINITY;
             st[r] = none ? -INFINITY : -l[u] * 1.4426950408889634f;
-            st[128 + r] = none ? 0.f : de[u];
+            st[128 + r] = none ? 0.f : is_bf16<X>() ? de[u] : de[u] * fit;
           }
         }
         __syncwarp();
@@ -650,6 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         first_row = a.causal ? max(0, d + key) * a.g : 0;
         all_rows = a.causal ? max(0, d + it->own - 1) * a.g : 0;
       }
+      const float fit = is_bf16<X>() ? 1.f : it->fit;
+      // dP - delta, for fp16 times the item's power of two (delta comes with it)
+      auto less_delta = [&](float2 dp, float2 de) {
+        return is_bf16<X>() ? fadd2(dp, make_float2(-de.x, -de.y))
+                            : ffma2(dp, make_float2(fit, fit), make_float2(-de.x, -de.y));
+      };
       for (int i = 0; i < n; ++i, ++blk) {
         const uint32_t b = blk & 1u;
         // (loads in program order: hoisted ones would take the registers of the scores)
@@ -710,8 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 de = lds_f4(st4 + 512u + 16u * (8 * h + u));
               const float* x = p[h] + 4 * u;
               const float* y = d + 4 * u;
-              const float2 a0 = fmul2(make_float2(x[0], x[1]), fadd2(make_float2(y[0], y[1]), make_float2(-de.x, -de.y)));
-              const float2 a1 = fmul2(make_float2(x[2], x[3]), fadd2(make_float2(y[2], y[3]), make_float2(-de.z, -de.w)));
+              const float2 a0 = fmul2(make_float2(x[0], x[1]), less_delta(make_float2(y[0], y[1]), make_float2(de.x, de.y)));
+              const float2 a1 = fmul2(make_float2(x[2], x[3]), less_delta(make_float2(y[2], y[3]), make_float2(de.z, de.w)));
               pk[2 * u] = pack_pair<X>(a0.x, a0.y);
               pk[2 * u + 1] = pack_pair<X>(a1.x, a1.y);
             }
@@ -735,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int t0 = it->t0;
       const long long at = key < it->t1 - t0 ? (static_cast<long long>(t0 + key) * a.Hk + it->hk) * D : -1;
-      const float fac = key < it->own ? (hf == 0 ? 1.f : a.scale) : 0.f;
+      const float fac = key < it->own ? (hf == 0 ? 1.f : is_bf16<X>() ? a.scale : a.scale / fit) : 0.f;
       const uint32_t src = (hf == 0 ? t_dv : t_dk) + lane_off;
       if constexpr (SPLIT)
         store_lanes<float, D>(src, fac, (hf == 0 ? f.part_dv : f.part_dk) + it->z * (static_cast<long long>(a.Tk) * a.Hk * D),
@@ -783,6 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.own = min(f.tq, r.t1 - r.t0);
       it.n = it.own > 0 ? (keys_seen(a, r.s, r.t0 + it.own - 1 - r.s.q0) + 127) >> 7 : 0;
       it.r_lo = it.lo = it.z = 0;
+      it.fit = 0.f;
+      if (!is_bf16<X>() && r.seq >= 0) it.fit = __uint_as_float(a.range[(static_cast<long long>(r.seq) * a.Hk + it.hk) * 2 + 1]);
       return it;
     });
   } else if (warp == kTmaWarp) {
@@ -917,10 +1018,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = tok < it->own;
       const long long at = row_ok ? static_cast<long long>(it->t0 + tok) * a.Hq + it->hk * a.g + head : -1;
       float nl = -INFINITY, de = 0.f;
-      int see = 0, see_all = 0;
+      int see = 0, see_all = 0, fit = 0;  // fit: exponent of the row's power of two
       if (n > 0) {
         if (row_ok) {
           const float l = a.lse[at], d = a.delta[at];
+          if constexpr (!is_bf16<X>()) fit = 15 - ds_exponent(a.norm2[at], it->fit);
           if (l != -INFINITY) {
             nl = -l * 1.4426950408889634f;
             de = d;
@@ -954,7 +1056,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + C::kBarCopied);
         ++item;
       }
-      const float2 nl2 = make_float2(nl, nl);
+      const float nf = is_bf16<X>() ? nl : nl + static_cast<float>(fit);
+      const float2 nl2 = make_float2(nf, nf);
       float2 nd2 = make_float2(-de, -de);
       if (n == 1) {
         // All the keys these rows see are in one tile: delta = sum p dP, without the rounding of out that dout.out
@@ -1051,7 +1154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       // output: each half of the warps takes half of the columns; rows that see nothing get zeros
-      store_lanes<X, D / 2>(t_dq + lane_off + (D / 2) * hf, nl == -INFINITY ? 0.f : a.scale,
+      store_lanes<X, D / 2>(t_dq + lane_off + (D / 2) * hf,
+                            nl == -INFINITY ? 0.f : is_bf16<X>() ? a.scale : a.scale * power_of_two(-fit),
                             static_cast<X*>(a.dq) + (D / 2) * hf, at >= 0 ? at * D : -1, n > 0 && ok);
       tc_fence_before();
       ct.give();
@@ -1098,8 +1202,16 @@ cudaError_t run(const AttnParams& p, const AttnBwdPlan& plan, uint8_t* ws, cudaS
   if (runs_k * p.Hk * plan.n_split > 0x7FFFFFFFll || runs_q * p.Hk > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   const long long rows = static_cast<long long>(p.Tq) * p.Hq;
   constexpr int PER = 256 / (D / 8);
-  attn_delta_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER + (order != nullptr)), 256, 0, stream>>>(
-      p, order, static_cast<int>(runs_k), nb_k, f.tq);
+  if constexpr (is_bf16<X>()) {
+    attn_delta_kernel<X, D><<<static_cast<unsigned>((rows + PER - 1) / PER + (order != nullptr)), 256, 0, stream>>>(
+        p, order, static_cast<int>(runs_k), nb_k, f.tq);
+  } else {
+    if (p.N > 0 && (e = cudaMemsetAsync(p.range, 0, static_cast<size_t>(p.N) * p.Hk * 8, stream)) != cudaSuccess) return e;
+    const long long row_blocks = runs_q * p.Hk, blocks = (order != nullptr) + row_blocks + runs_k * p.Hk;
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    attn_range_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+        p, order, static_cast<int>(runs_k), nb_k, nb_q, f.tq, static_cast<unsigned>(row_blocks));
+  }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // dq first: it improves delta for the rows of few keys
   f.nb = nb_q;
@@ -1127,10 +1239,12 @@ cudaError_t run(const AttnParams& p, const AttnBwdPlan& plan, uint8_t* ws, cudaS
 }  // namespace
 
 cudaError_t launch_attn_backward(const AttnParams& p, int dtype, void* workspace, cudaStream_t s) {
-  const AttnBwdPlan plan = attn_bwd_plan(p.N, p.Tq, p.Tk, p.Hq, p.Hk, p.D);
+  const AttnBwdPlan plan = attn_bwd_plan(p.N, p.Tq, p.Tk, p.Hq, p.Hk, p.D, dtype == CSA_F16);
   AttnParams a = p;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.delta = reinterpret_cast<float*>(ws);
+  a.norm2 = reinterpret_cast<float*>(ws + plan.off_norm2);
+  a.range = reinterpret_cast<uint32_t*>(ws + plan.off_range);
   if (dtype == CSA_BF16)
     return p.D == 128 ? run<__nv_bfloat16, 128>(a, plan, ws, s) : run<__nv_bfloat16, 64>(a, plan, ws, s);
   return p.D == 128 ? run<__half, 128>(a, plan, ws, s) : run<__half, 64>(a, plan, ws, s);

@@ -46,6 +46,9 @@ struct AttnParams {
   // backward
   const void* dout;
   float* delta;  // [Tq,Hq]: sum over D of dout * out
+  // fp16: what dS can reach (see ds_exponent)
+  float* norm2;     // [Tq,Hq]: sum over D of dout^2
+  uint32_t* range;  // [N,Hk,2]: the largest of a sequence's rows of dout, and of v (bits of fp32)
   void *dq, *dk, *dv;
 };
 cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
@@ -87,13 +90,14 @@ inline AttnPlan attn_plan(int N, int Tq, int Tk, int Hk, int g) {
 }
 
 // How the backward cuts the dk, dv work, and what its workspace holds: delta,
-// the order of the runs of keys, the shares' sums.
+// for fp16 the norms of dout's rows and the sequences' largest, the order of the
+// runs of keys, the shares' sums.
 struct AttnBwdPlan {
   int n_split;   // shares of the rows that see a run of 128 keys
   bool ordered;  // more items than SMs: the longest first
-  size_t off_order, off_part, total;
+  size_t off_norm2, off_range, off_order, off_part, total;
 };
-inline AttnBwdPlan attn_bwd_plan(int N, int Tq, int Tk, int Hq, int Hk, int D) {
+inline AttnBwdPlan attn_bwd_plan(int N, int Tq, int Tk, int Hq, int Hk, int D, bool fp16) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   AttnBwdPlan p;
   const long long runs = std::max<long long>((static_cast<long long>(Tk) + 127) / 128, std::min(N, Tk));
@@ -103,7 +107,10 @@ inline AttnBwdPlan attn_bwd_plan(int N, int Tq, int Tk, int Hq, int Hk, int D) {
   p.n_split = 1;
   if (items < 2 * 152) p.n_split = static_cast<int>(std::max<long long>(1, std::min((3 * 152 + items - 1) / items, blocks / 16)));
   p.ordered = items * p.n_split > 152;
-  p.off_order = up(static_cast<size_t>(Tq) * Hq * 4);
+  const size_t per_row = up(static_cast<size_t>(Tq) * Hq * 4);
+  p.off_norm2 = per_row;
+  p.off_range = per_row * (fp16 ? 2 : 1);
+  p.off_order = up(p.off_range + (fp16 ? static_cast<size_t>(N) * Hk * 8 : 0));
   p.off_part = up(p.off_order + (p.ordered ? (static_cast<size_t>((static_cast<long long>(Tk) + 127) / 128) + N + 1) * 4 : 0));
   p.total = p.off_part + (p.n_split > 1 ? static_cast<size_t>(p.n_split) * Tk * Hk * D * 8 : 0);
   return p;

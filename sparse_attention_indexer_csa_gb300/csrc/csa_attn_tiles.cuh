@@ -62,6 +62,7 @@ inline bool make_keys_map(CUtensorMap* m, const AttnParams& p, const void* x, lo
 struct RowItem {
   int t0, t1;
   SeqExt s;
+  int seq;  // its sequence (-1: none)
 };
 
 // The runs are what the multiples of `step` (nb of them below Tq) and the
@@ -83,7 +84,7 @@ __device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int 
   // goes before a start of the same value)
   const int k = x + 1;
   int lo = max(0, k - nB), hi = min(k, nb);
-  if (lo > hi) return RowItem{0, 0, SeqExt{0, 0, 0, 0}};
+  if (lo > hi) return RowItem{0, 0, SeqExt{0, 0, 0, 0}, -1};
   while (!WARP && lo < hi) {  // one thread: by halves
     const int i = (lo + hi + 1) >> 1;
     if (static_cast<long long>(i - 1) * step <= start(k - i))
@@ -112,7 +113,8 @@ __device__ __forceinline__ RowItem find_item(const AttnParams& a, int step, int 
   r.t1 = i < nb ? static_cast<int>(min(static_cast<long long>(T), static_cast<long long>(i) * step)) : T;
   if (j < nB) r.t1 = min(r.t1, start(j));
   r.s = KEYS ? SeqExt{0, 0, r.t0, 0} : SeqExt{r.t0, r.t1, 0, 0};
-  if (seqs && j > 0 && j <= a.N) r.s = seq_extent(a, j - 1);
+  r.seq = seqs && j > 0 && j <= a.N ? j - 1 : -1;
+  if (r.seq >= 0) r.s = seq_extent(a, r.seq);
   // entries out of order: a run never leaves its sequence
   r.t0 = max(r.t0, KEYS ? r.s.k0 : r.s.q0);
   if (!KEYS) r.t1 = min(r.t1, r.s.q1);

@@ -144,3 +144,52 @@ def test_many_small_weights_in_fp16(lq, lk, Hq, Hk, D, top):
              + 2.0 ** -33 * ref["vsum"])
     assert (err <= bound).all(), float((err / bound).max())
     assert (np.abs(A.f64(lse) - ref["lse"]) <= ds + 2.0 ** -14 + 2.0 ** -22 * np.abs(ref["lse"])).all()
+
+
+def _gradients(lq, lk, Hq, Hk, D, size, seed, vsize=1.0, qk=1.0):
+    """(got, ref) of the fp16 gradients for cotangents of the given size; qk: size of q and k, at scores of unit size."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    q, k, v = ((r(*s) * m).to(FP16) for s, m in (((sum(lq), Hq, D), qk), ((sum(lk), Hk, D), qk), ((sum(lk), Hk, D), vsize)))
+    do = (r(sum(lq), Hq, D) * size).to(FP16)
+    cu_q, cu_k, scale = _cu(*lq), _cu(*lk), D ** -0.5 / qk ** 2
+    args = [t.cuda() for t in (q, k, v)]
+    out, lse = csa.attn_forward(*args, cu_q, cu_k, scale)
+    got = csa.attn_backward(do.cuda(), *args, out, lse, cu_q, cu_k, scale)
+    _ok()
+    ref = A.attention(A.f64(q), A.f64(k), A.f64(v), cu_q.cpu().numpy(), cu_k.cpu().numpy(), scale, dout=A.f64(do))
+    return dict(zip(("dq", "dk", "dv"), got)), ref
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D", [([2, 1, 3], [2, 1, 3], 4, 4, 128), ([64, 40], [64, 90], 2, 2, 128),
+                                           ([150], [400], 6, 2, 64), ([20], [9000], 4, 2, 64)])
+def test_fp16_gradients_of_large_cotangents(lq, lk, Hq, Hk, D):
+    """Cotangents of a scaled loss: p (dP - delta) passes fp16's range in places, the gradients do not.
+
+    u for the rounding of p or ds and one of delta's, 2 ds, 2^-15 for the sums, u for the output's.
+    """
+    got, ref = _gradients(lq, lk, Hq, Hk, D, 2.0 ** 13, 7 * D + lk[0], vsize=3.0)
+    u, top = 2.0 ** -11, 2.0 ** -15 * ref["smax"].max()
+    for n in ("dq", "dk", "dv"):
+        want = ref[n]
+        assert np.abs(want).max() < 65000, n  # the inputs are chosen so
+        bound = u * np.abs(want) + ((u if n == "dv" else 2 * u) + top + 2.0 ** -15) * ref["mag_" + n]
+        err = np.abs(A.f64(got[n]) - want)
+        assert (err <= bound + 2.0 ** -25).all(), (n, float((err / (bound + 2.0 ** -25)).max()))
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,size", [([40], [6000], 4, 2, 64, 2.0 ** -10), ([30, 9], [4000, 2500], 2, 2, 128, 2.0 ** -12),
+                                                ([300], [3000], 4, 1, 64, 2.0 ** -9)])
+def test_fp16_gradients_of_small_cotangents(lq, lk, Hq, Hk, D, size):
+    """Weights of 1/6000 times a small cotangent lie among fp16's last bits, if not below.
+
+    Rounding errors are independent: in the root mean square each rounding (of ds, of delta's out, of the
+    gradient) brings at most u, the scores 2 ds.  Small q and k at a large scale bring the gradients themselves
+    among fp16's normal numbers.
+    """
+    got, ref = _gradients(lq, lk, Hq, Hk, D, size, lk[0], qk=2.0 ** -7)
+    u, top = 2.0 ** -11, 2.0 ** -15 * ref["smax"].max()
+    rms = lambda x: float(np.sqrt(np.mean(np.square(x))))  # noqa: E731
+    for n in ("dq", "dk"):
+        # the output's own last bit: 2^-25 where the gradient is below 2^-14
+        assert rms(A.f64(got[n]) - ref[n]) <= (3 * u + top) * rms(ref[n]) + 2.0 ** -25, n
