@@ -42,7 +42,8 @@
 // 2 |dout_r| max_j |v_j|: dS is formed times a power of two that brings this bound
 // to 2^15, and dq and dk are taken back in fp32.  dq has a power for each row, dk,
 // which sums over rows, one for each sequence and key head: nothing of another
-// sequence has a part in it.  attn_range_kernel takes the norms and delta in one
+// sequence has a part in it.  P^T, at most 1, is formed 2^15 times its size for dv
+// (weights down to 2^-40 count, 2^-25 as they come).  attn_range_kernel takes the norms and delta in one
 // pass (56 us for delta's 42 at the size below); bf16 has the range and none of this.
 //
 // Measured (bf16, 64 + 8 heads of 128, 8192 tokens in 5 documents): 0.828 ms,
@@ -108,7 +109,7 @@ struct BwdItem {
   int z;       // dkv: share
   int own;     // tokens (dq) or keys of the sequence (dkv) among t0 .. t1-1
   int r_lo;    // dkv: first row that sees a key of the run
-  float fit;   // fp16: dq: the largest |v|^2 of the sequence; dkv: the power of two that dS is formed with
+  float fit;   // fp16: dq: the largest |v|^2 of the sequence; dkv: the power of two of dP - delta
 };
 static_assert(sizeof(BwdItem) <= 64, "a slot");
 
@@ -226,6 +227,10 @@ __device__ __forceinline__ int ds_exponent(float dout2, float v2) {
   return min(max(e, -60), 60);
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The power of two of P^T (dkv).
+template <typename X>
+constexpr int kProbExp = is_bf16<X>() ? 0 : 15;
 
 // Position in a ring of n tiles.
 struct Ring {
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.fit = 1.f;
       if (!is_bf16<X>() && r.seq >= 0) {
         const uint32_t* m = a.range + (static_cast<long long>(r.seq) * a.Hk + it.hk) * 2;
-        it.fit = power_of_two(15 - ds_exponent(__uint_as_float(m[0]), __uint_as_float(m[1])));
+        it.fit = power_of_two(15 - kProbExp<X> - ds_exponent(__uint_as_float(m[0]), __uint_as_float(m[1])));
       }
       return it;
     });
@@ -703,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 4; ++u) {
             const int r = u * 32 + static_cast<int>(lane);
             const bool none = l[u] == -INFINITY;
-            st[r] = none ? -INFINITY : -l[u] * 1.4426950408889634f;
+            st[r] = none ? -INFINITY : -l[u] * 1.4426950408889634f + static_cast<float>(kProbExp<X>);
             st[128 + r] = none ? 0.f : is_bf16<X>() ? de[u] : de[u] * fit;
           }
         }
@@ -834,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int t0 = it->t0;
       const long long at = key < it->t1 - t0 ? (static_cast<long long>(t0 + key) * a.Hk + it->hk) * D : -1;
-      const float fac = key < it->own ? (hf == 0 ? 1.f : is_bf16<X>() ? a.scale : a.scale / fit) : 0.f;
+      const float fac = key < it->own ? (hf == 0 ? 1.f : is_bf16<X>() ? a.scale : a.scale / fit) * (1.f / (1 << kProbExp<X>)) : 0.f;
       const uint32_t src = (hf == 0 ? t_dv : t_dk) + lane_off;
       if constexpr (SPLIT)
         store_lanes<float, D>(src, fac, (hf == 0 ? f.part_dv : f.part_dk) + it->z * (static_cast<long long>(a.Tk) * a.Hk * D),

@@ -193,3 +193,13 @@ def test_fp16_gradients_of_small_cotangents(lq, lk, Hq, Hk, D, size):
     for n in ("dq", "dk"):
         # the output's own last bit: 2^-25 where the gradient is below 2^-14
         assert rms(A.f64(got[n]) - ref[n]) <= (3 * u + top) * rms(ref[n]) + 2.0 ** -25, n
+
+
+def test_fp16_gradients_of_many_small_weights():
+    """dv of keys whose weight lies near 2^-20: p's rounding and the output's (u each), the score's error, and what
+    a weight loses below 2^-40."""
+    got, ref = _gradients([24], [200_000], 2, 1, 64, 2.0 ** 10, 5)
+    u, top = 2.0 ** -11, 2.0 ** -15 * ref["smax"].max()
+    err = np.abs(A.f64(got["dv"]) - ref["dv"])
+    bound = u * np.abs(ref["dv"]) + (u + top + 2.0 ** -18) * ref["mag_dv"] + 2.0 ** -40 * ref["sum_dv"] + 2.0 ** -25
+    assert (err <= bound).all(), float((err / bound).max())
