@@ -55,7 +55,9 @@ typedef struct {
 } csa_norm_rope_problem;
 
 /* Fills freqs[rot/2] (host memory) with theta^(-2i/rot) / (2 pi) turns as
- * 64-bit fractions; theta > 1 (up to 1e18), rot a positive even number.      */
+ * 64-bit fractions, each rounded to the nearest: an angle is off by 1.8e-19
+ * radians per position for it.  theta > 1 (up to 1e18), rot a positive even
+ * number.                                                                    */
 csa_status csa_rope_freqs(double theta, int32_t rot, uint64_t* freqs);
 
 /* q [T,Hq,D], k [T,Hk,D], q_weight [D], k_weight [D], positions [T] int64,

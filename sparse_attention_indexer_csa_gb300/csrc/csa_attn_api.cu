@@ -138,6 +138,43 @@ size_t attn_workspace_bytes(const csa_attn_problem* p, int which) {
   return plan.n_split > 1 ? static_cast<size_t>(plan.n_split) * p->Tq * p->Hq * (p->D + 1) * 4 : 0;
 }
 
+// ----------------------------------------------------------------- frequencies
+// A number as the sum of two doubles, some 100 bits: a table entry is multiplied by the position, so that the 53 bits
+// of one would be off by 6e-5 of a radian at position 1e12.
+struct Dd {
+  double hi, lo;
+};
+Dd dd_sum(double a, double b) {  // exact
+  const double s = a + b, t = s - a;
+  return Dd{s, (a - (s - t)) + (b - t)};
+}
+Dd dd_add(Dd a, Dd b) {
+  const Dd s = dd_sum(a.hi, b.hi);
+  return dd_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Dd dd_mul(Dd a, Dd b) {
+  const double p = a.hi * b.hi;
+  return dd_sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Dd dd_div(Dd a, double n) {
+  const double q = a.hi / n;
+  return dd_sum(q, (std::fma(-q, n, a.hi) + a.lo) / n);
+}
+// e^x, |x| < 64: the series at x / 1024 (below 1/16; the 18th power over 18! is below 2^-120), squared ten times.
+Dd dd_exp(Dd x) {
+  const Dd r{std::ldexp(x.hi, -10), std::ldexp(x.lo, -10)}, one{1.0, 0.0};
+  Dd e = one;
+  for (int n = 17; n > 0; --n) e = dd_add(one, dd_div(dd_mul(r, e), n));
+  for (int i = 0; i < 10; ++i) e = dd_mul(e, e);
+  return e;
+}
+// ln x by one step from the double's: y + (x e^-y - 1), whose error is the square of the first.
+Dd dd_log(double x) {
+  const double y = std::log(x);
+  const Dd d = dd_add(dd_mul(Dd{x, 0.0}, dd_exp(Dd{-y, 0.0})), Dd{-1.0, 0.0});
+  return dd_add(Dd{y, 0.0}, d);
+}
+
 }  // namespace
 }  // namespace csa
 
@@ -147,10 +184,13 @@ extern "C" {
 
 csa_status csa_rope_freqs(double theta, int32_t rot, uint64_t* freqs) {
   if (freqs == nullptr || rot < 2 || rot % 2 != 0 || !(theta > 1.0) || !(theta <= 1e18)) return CSA_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925286766559;
+  const Dd log_theta = dd_log(theta);
+  const Dd inv_two_pi{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};
   for (int i = 0; i < rot / 2; ++i) {
-    const double turns = std::pow(theta, -2.0 * i / rot) / two_pi;  // below 0.16
-    freqs[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(turns, 64)));
+    const Dd turns = dd_mul(dd_exp(dd_div(dd_mul(log_theta, Dd{-2.0 * i, 0.0}), rot)), inv_two_pi);  // below 0.16
+    const double whole = std::floor(std::ldexp(turns.hi, 64));
+    const double rest = (std::ldexp(turns.hi, 64) - whole) + std::ldexp(turns.lo, 64);
+    freqs[i] = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(rest)));
   }
   return CSA_OK;
 }
