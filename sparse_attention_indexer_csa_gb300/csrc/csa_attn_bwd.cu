@@ -1182,7 +1182,6 @@ cudaError_t run(const AttnParams& p, const AttnBwdPlan& plan, uint8_t* ws, cudaS
   f.a = p;
   f.tq = 128 / p.g;
   f.c = p.scale * 1.4426950408889634f;
-  f.wait_ns = kAttnWaitNs;
   f.n_split = plan.n_split;
   f.part_dk = reinterpret_cast<float*>(ws + plan.off_part);
   f.part_dv = f.part_dk + static_cast<long long>(plan.n_split) * p.Tk * p.Hk * D;
@@ -1220,9 +1219,11 @@ cudaError_t run(const AttnParams& p, const AttnBwdPlan& plan, uint8_t* ws, cudaS
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // dq first: it improves delta for the rows of few keys
   f.nb = nb_q;
+  f.wait_ns = attn_wait_ns(attn_steps_keys(p.Tk));
   attn_dq_kernel<X, D><<<static_cast<unsigned>(runs_q * p.Hk), kThreads, C::kSmem, stream>>>(tq, to, tk, tv, f);
   if ((e = cudaGetLastError()) != cudaSuccess || p.Tk == 0) return e;
   f.nb = nb_k;
+  f.wait_ns = attn_wait_ns(attn_steps_rows(p.Tq, f.tq));
   const unsigned grid = static_cast<unsigned>(runs_k * p.Hk * plan.n_split);
   if (plan.n_split > 1) {
     if ((e = smem_limit_once<attn_dkv_kernel<X, D, true>>(C::kSmem)) != cudaSuccess) return e;

@@ -761,7 +761,7 @@ cudaError_t run(const AttnParams& p, int n_split, void* workspace, cudaStream_t 
   f.lowest = -3.3e38f / std::max(1.f, f.c);
   f.part_o = static_cast<float*>(workspace);
   f.part_lse = f.part_o + static_cast<long long>(n_split) * p.Tq * p.Hq * D;
-  f.wait_ns = kAttnWaitNs;
+  f.wait_ns = attn_wait_ns(attn_steps_keys(p.Tk));
   if (!make_rows_map(&tq, p, p.q, p.q_st, p.q_sh, f.tq) || !make_keys_map(&tk, p, p.k, p.k_st, p.k_sh) ||
       !make_keys_map(&tv, p, p.v, p.v_st, p.v_sh) ||
       !make_rows_map(&to, p, p.out, static_cast<long long>(p.Hq) * D, D, f.tq))

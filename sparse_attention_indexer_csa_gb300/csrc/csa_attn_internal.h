@@ -3,6 +3,7 @@
 #pragma once
 
 #include "csa_attn.h"
+#include "csa_attn_limits.h"
 #include "csa_internal.h"
 
 namespace csa {

@@ -14,7 +14,6 @@
 namespace csa {
 
 constexpr uint32_t kChunkBytes = 128 * 128;  // 16 KB: 128 rows x 64 values of 2 bytes, 128-byte swizzled
-constexpr unsigned long long kAttnWaitNs = 2000000000ull;
 
 // ----------------------------------------------------------------- TMA maps (host)
 inline PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
