@@ -245,13 +245,14 @@ struct Ring {
   }
 };
 
-// Waits until the copies of the first `used` tiles of a ring have landed.
-__device__ __forceinline__ void drain_ring(uint64_t* full, int n, int used, const WaitCtl& ctl) {
-  if (*ctl.abort_flag != 0u) return;
-  volatile uint32_t dummy = 0;
+// Waits until no copy of the producer is in flight: the rings' (stages of E, then of F) and the n_res resident pairs.
+template <int D>
+__device__ __forceinline__ void drain_copies(uint64_t* bars, const Copies& copies, uint32_t n_res, const WaitCtl& ctl) {
+  using C = BwdCfg<D>;
+  volatile uint32_t dummy = 0;  // also when a role gave up
   const WaitCtl dctl{&dummy, ctl.limit_ns};
-  for (int i = 0; i < n && i < used; ++i)
-    mbar_wait(full + (used - 1 - i) % n, (static_cast<uint32_t>(used - 1 - i) / n) & 1u, dctl);
+  copies.drain([&](int st, bool mend, uint32_t parity) { mbar_wait(bars + (mend ? C::kBarLast : C::kBarE) + st, parity, dctl); });
+  if (n_res > 0) mbar_wait(bars + C::kBarRes, (n_res - 1u) & 1u, dctl);
 }
 
 // Copies tile i of a ring (rows: a block of query rows; else 128 keys).  A tile
@@ -259,12 +260,13 @@ __device__ __forceinline__ void drain_ring(uint64_t* full, int n, int used, cons
 // (null: none to clear).  Several such tiles may be on their way at once.
 template <int D>
 __device__ __forceinline__ void load_ring(uint8_t* base, uint32_t off, uint64_t* full, uint64_t* free, uint64_t* last,
-                                          const Ring& r, const CUtensorMap* map, bool rows, int at, int hk,
-                                          uint32_t bytes, uint64_t pol, const WaitCtl& ctl) {
+                                          const Ring& r, Copies& copies, int stage0, const CUtensorMap* map, bool rows,
+                                          int at, int hk, uint32_t bytes, uint64_t pol, const WaitCtl& ctl) {
   constexpr uint32_t kTile = kChunkBytes * (D / 64);
   if (!mbar_wait(free + r.at, r.phase ^ 1u, ctl)) return;
   uint64_t* bar = (last != nullptr ? last : full) + r.at;
   uint8_t* dst = base + off + r.at * kTile;
+  copies.start(stage0 + r.at, last != nullptr, r.phase);
   mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
   for (int ch = 0; ch < D / 64; ++ch) {
@@ -575,13 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring e(C::kE), o(C::kF);
     const uint32_t bytes = static_cast<uint32_t>(rows_blk) * 128u * (D / 64);
     uint32_t n_res = 0;
-    int used = 0;
+    Copies copies;
     while (const volatile BwdItem* it = ct.next()) {
       const int n = it->n, hk = it->hk, t0 = it->t0, q0 = it->s.q0 + it->r_lo + it->lo * f.tq, rows = it->s.q1 - q0;
       ct.give();
       if (lane == 0 && n > 0) {
         const bool cut = rows < n * f.tq;  // the last block is not full
         if (mbar_wait(bars + C::kBarResFree, (n_res & 1u) ^ 1u, ctl)) {
+          ++n_res;
           mbar_arrive_expect_tx(bars + C::kBarRes, 2 * C::kTile);
           for (int ch = 0; ch < D / 64; ++ch) {
             tma_load_3d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_k, bars + C::kBarRes, ch * 64, t0, hk, first);
@@ -590,24 +593,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < n; ++i) {
           const bool c = cut && i == n - 1;
-          load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, c ? bars + C::kBarLast : nullptr, e, &tmap_q,
-                       true, q0 + i * f.tq, hk, bytes, last, ctl);
+          load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, c ? bars + C::kBarLast : nullptr, e, copies, 0,
+                       &tmap_q, true, q0 + i * f.tq, hk, bytes, last, ctl);
           load_ring<D>(base, C::kOffF, bars + C::kBarF, bars + C::kBarFreeF, c ? bars + C::kBarLast + C::kE : nullptr, o,
-                       &tmap_do, true, q0 + i * f.tq, hk, bytes, last, ctl);
+                       copies, C::kE, &tmap_do, true, q0 + i * f.tq, hk, bytes, last, ctl);
           e.next();
           o.next();
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + C::kBarSoon);
-      if (n > 0) ++n_res;
-      used += n;
     }
-    if (lane == 0) {
-      drain_ring(bars + C::kBarE, C::kE, used, ctl);
-      drain_ring(bars + C::kBarF, C::kF, used, ctl);
-      if (n_res > 0) mbar_wait(bars + C::kBarRes, (n_res - 1u) & 1u, ctl);
-    }
+    if (lane == 0) drain_copies<D>(bars, copies, n_res, ctl);
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     // the warp runs as one, with uniform operands; an elected thread issues the products
@@ -896,12 +893,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t first = l2_policy_evict_first(), last = l2_policy_evict_last();
     Ring k(C::kE), v(C::kF);
     uint32_t n_res = 0;
-    int used = 0;
+    Copies copies;
     while (const volatile BwdItem* it = ct.next()) {
       const int n = it->n, hk = it->hk, t0 = it->t0, k0 = it->s.k0, lk = it->s.lk;
       ct.give();
       if (lane == 0 && n > 0) {
         if (mbar_wait(bars + C::kBarResFree, (n_res & 1u) ^ 1u, ctl)) {
+          ++n_res;
           mbar_arrive_expect_tx(bars + C::kBarRes, static_cast<uint32_t>(f.tq * a.g) * 256u * (D / 64));
           for (int ch = 0; ch < D / 64; ++ch) {
             tma_load_4d_hint(base + C::kOffA + ch * kChunkBytes, &tmap_q, bars + C::kBarRes, ch * 64, 0, t0, hk, first);
@@ -910,24 +908,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < n; ++j) {
           const bool c = j == n - 1 && n * 128 > lk;  // the tile reaches past the sequence's keys
-          load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, c ? bars + C::kBarLast : nullptr, k, &tmap_k,
-                       false, k0 + j * 128, hk, C::kTile, last, ctl);
+          load_ring<D>(base, C::kOffE, bars + C::kBarE, bars + C::kBarFreeE, c ? bars + C::kBarLast : nullptr, k, copies, 0,
+                       &tmap_k, false, k0 + j * 128, hk, C::kTile, last, ctl);
           load_ring<D>(base, C::kOffF, bars + C::kBarF, bars + C::kBarFreeF, c ? bars + C::kBarLast + C::kE : nullptr, v,
-                       &tmap_v, false, k0 + j * 128, hk, C::kTile, last, ctl);
+                       copies, C::kE, &tmap_v, false, k0 + j * 128, hk, C::kTile, last, ctl);
           k.next();
           v.next();
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + C::kBarSoon);
-      if (n > 0) ++n_res;
-      used += n;
     }
-    if (lane == 0) {
-      drain_ring(bars + C::kBarE, C::kE, used, ctl);
-      drain_ring(bars + C::kBarF, C::kF, used, ctl);
-      if (n_res > 0) mbar_wait(bars + C::kBarRes, (n_res - 1u) & 1u, ctl);
-    }
+    if (lane == 0) drain_copies<D>(bars, copies, n_res, ctl);
   } else if (warp == kMmaWarp) {
     reg_shrink();
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));

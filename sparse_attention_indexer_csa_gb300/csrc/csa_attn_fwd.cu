@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
     reg_shrink();
     if (lane == 0) {  // --------------------------------------------------- TMA producer
       const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
-      uint32_t at = 0, phase = 1, used = 0, nq[TILES] = {};
+      uint32_t at = 0, phase = 1, nq[TILES] = {};
+      Copies copies;
       while (const volatile FwdItem* it = next_item()) {
         const int lo = it->lo, hi[2] = {it->hi[0], it->hi[1]}, top = max(hi[0], hi[1]);
         const int t0 = it->t0, k0 = it->s.k0, hk = it->hk, open = it->open;
@@ -333,10 +334,11 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
               at = 0;
               phase ^= 1u;
             }
-            ++used;
             if (!mbar_wait(bars + C::kBarEmpty + st, ph, ctl)) continue;
             // a value tile that is mended lands on the stage's other barrier; who mends it completes the first
-            uint64_t* bar = bars + (kv && (j + 1) * 128 > open ? C::kBarLast : C::kBarFull) + st;
+            const bool mend = kv && (j + 1) * 128 > open;
+            uint64_t* bar = bars + (mend ? C::kBarLast : C::kBarFull) + st;
+            copies.start(static_cast<int>(st), mend, ph ^ 1u);
             mbar_arrive_expect_tx(bar, C::kTile);
             for (int ch = 0; ch < D / 64; ++ch)
               tma_load_3d_hint(base + C::kOffKv + st * C::kTile + ch * kChunkBytes, kv ? &tmap_v : &tmap_k, bar, ch * 64,
@@ -344,12 +346,14 @@ __global__ void __launch_bounds__(FwdCfg<D, TILES, ROWS>::kThreads, TILES == 2 ?
           }
         mbar_arrive(bars + C::kBarSoon);
       }
-      // no copy is in flight when the CTA ends: the last use of each stage has landed
+      // no copy is in flight when the CTA ends, a role's giving up included
       volatile uint32_t dummy = 0;
       const WaitCtl dctl{&dummy, ctl.limit_ns};
-      if (*abort_flag == 0u)
-        for (uint32_t i = 0; i < static_cast<uint32_t>(C::kStages) && i < used; ++i)
-          mbar_wait(bars + C::kBarFull + (used - 1 - i) % C::kStages, ((used - 1 - i) / C::kStages) & 1u, dctl);
+      for (int w = 0; w < TILES; ++w)
+        if (nq[w] > 0) mbar_wait(bars + C::kBarQ + w, (nq[w] - 1u) & 1u, dctl);
+      copies.drain([&](int st, bool mend, uint32_t parity) {
+        mbar_wait(bars + (mend ? C::kBarLast : C::kBarFull) + st, parity, dctl);
+      });
     }
   } else if (warp == C::kMmaWarp) {
     reg_shrink();

@@ -46,3 +46,48 @@ def test_every_launch_takes_its_limit_from_its_steps():
         text = open(os.path.join(CSRC, name)).read()
         assert len(re.findall(r"f\.wait_ns = attn_wait_ns\(attn_steps_(?:keys|rows)\(", text)) == launches
         assert len(re.findall(r"f\.wait_ns =", text)) == launches
+
+
+def test_copies_in_flight_are_waited_for_wherever_a_cta_gives_up(tmp_path):
+    """A model of the producer's rings: random tiles, some of them mended, given up after any of them.  What drain()
+    asks for is, for each stage that a copy was started into, the barrier and the parity of the phase that its last
+    copy completes."""
+    cc = shutil.which("g++")
+    if cc is None:
+        pytest.skip("no host compiler")
+    src = tmp_path / "copies.cc"
+    src.write_text(r"""
+#include <cstdio>
+#include <cstdlib>
+#include "csa_attn_limits.h"
+int main() {
+  srand(7);
+  for (int round = 0; round < 2000; ++round) {
+    const int stages = 1 + rand() % 9, tiles = rand() % 60;
+    csa::Copies c;
+    int ring[9] = {}, other[9] = {};            // phases begun on a stage's two barriers
+    int want[9], parity[9];                     // -1: no copy; 0: ring barrier; 1: the other
+    for (int s = 0; s < 9; ++s) want[s] = -1;
+    for (int i = 0; i < tiles; ++i) {
+      const int s = i % stages;
+      const bool mend = rand() % 3 == 0;
+      c.start(s, mend, (i / stages) & 1);
+      want[s] = mend;
+      parity[s] = (mend ? other[s]++ : ring[s]) & 1;
+      ++ring[s];                                // completed by the copy, or by who mends the tile
+    }
+    int asked = 0, all = 0;
+    bool good = true;
+    for (int s = 0; s < 9; ++s) all += want[s] >= 0;
+    c.drain([&](int s, bool mend, unsigned p) {
+      ++asked;
+      good = good && s < 9 && want[s] == int(mend) && parity[s] == int(p);
+    });
+    if (!good || asked != all) return printf("round %d\n", round), 1;
+  }
+  return 0;
+}
+""")
+    exe = tmp_path / "copies"
+    subprocess.run([cc, "-std=c++17", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    subprocess.run([str(exe)], check=True)
