@@ -203,3 +203,41 @@ def test_fp16_gradients_of_many_small_weights():
     err = np.abs(A.f64(got["dv"]) - ref["dv"])
     bound = u * np.abs(ref["dv"]) + (u + top + 2.0 ** -18) * ref["mag_dv"] + 2.0 ** -40 * ref["sum_dv"] + 2.0 ** -25
     assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("which", [0, 1, 2], ids=["dq", "dk", "dv"])
+def test_each_gradient_by_differences(which):
+    """sum(out * g) along the signs of the gradient's definition, so that all terms add up and the difference is
+    far above its error: steps of 2^-5 and 2^-4 from a grid that fp16 holds.
+
+    Values of out (below 4) and the weights in them are rounded to fp16 at independent points: 2^-10 / sqrt 3 each
+    in the root mean square, six sigma over the step.  The curvature's error at the smaller step is a third of
+    what the two steps differ by.  The gradient itself: four roundings of 2^-11 at most.
+    """
+    lq = [30, 21]
+    gen = torch.Generator().manual_seed(29)
+    x = [((torch.randn(51, h, 64, generator=gen)).clamp(-7, 7) * 128).round() / 128 for h in (4, 2, 2)]
+    g = torch.randn(51, 4, 64, generator=gen).to(FP16)
+    cu = _cu(*lq)
+    ref = A.attention(*(A.f64(t) for t in x), cu.cpu().numpy(), cu.cpu().numpy(), 0.125, dout=A.f64(g))
+    d = torch.from_numpy(np.sign(ref[("dq", "dk", "dv")[which]]))
+
+    def value(s):
+        y = [t.double() for t in x]
+        y[which] = y[which] + s * d
+        y16 = [t.to(FP16) for t in y]
+        assert all(torch.equal(a.double(), b) for a, b in zip(y16, y))
+        out, _ = csa.attn_forward(*(t.cuda() for t in y16), cu, cu, 0.125)
+        return float((out.double().cpu() * g.double()).sum())
+
+    base = [t.to(FP16).cuda() for t in x]
+    out, lse = csa.attn_forward(*base, cu, cu, 0.125)
+    got = csa.attn_backward(g.cuda(), *base, out, lse, cu, cu, 0.125)[which]
+    _ok()
+    along = float((got.double().cpu() * d).sum())
+    h = 2.0 ** -5
+    near, far = ((value(s) - value(-s)) / (2 * s) for s in (h, 2 * h))
+    noise = 6 * 2 * float(g.double().norm()) * 2.0 ** -10 / 3 ** 0.5 / (2 * h)
+    tol = noise + (abs(far - near) + noise) / 3 + 4 * 2.0 ** -11 * abs(near)
+    assert tol < 0.02 * abs(near)  # zero, half or turned gradients would show
+    assert abs(near - along) <= tol
