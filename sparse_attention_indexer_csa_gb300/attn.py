@@ -138,6 +138,14 @@ class _Call:
         if device.index is not None and torch.cuda.current_device() != device.index:
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
+        try:
+            self._take(stream)
+        except BaseException:
+            self.done()  # a stream that is none leaves the current device as it was
+            raise
+
+    def _take(self, stream):
+        device = self.device
         self.stream = None  # a stream other than the current one
         self.handle = _current_stream(device)
         if stream is not None:
