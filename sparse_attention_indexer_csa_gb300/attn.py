@@ -3,8 +3,9 @@
 of queries and keys, and causal attention over packed sequences.
 
 Argument marshalling only, as in ``abi.py``.  Every helper takes ``stream``
-(default: the current stream of the tensors' device); tensors it allocates are
-recorded on that stream, so they may be dropped while its work is in flight.
+(default: the current stream of the tensors' device); the tensors it takes and
+those it allocates are recorded on that stream, so they may be dropped while its
+work is in flight.
 """
 from __future__ import annotations
 
@@ -127,11 +128,11 @@ def _current_stream(device) -> int:
 
 class _Call:
     """Device and stream of one call: the stream as the library takes it, and
-    the memory that the call allocates."""
+    the memory that the call uses and allocates."""
 
     __slots__ = ("device", "stream", "handle", "guard")
 
-    def __init__(self, stream, device):
+    def __init__(self, stream, device, *used):
         self.device = device
         # kernels go to the current device, so it has to be the tensors' one
         self.guard = None
@@ -139,12 +140,12 @@ class _Call:
             self.guard = torch.cuda.device(device)
             self.guard.__enter__()
         try:
-            self._take(stream)
+            self._take(stream, used)
         except BaseException:
             self.done()  # a stream that is none leaves the current device as it was
             raise
 
-    def _take(self, stream):
+    def _take(self, stream, used):
         device = self.device
         self.stream = None  # a stream other than the current one
         self.handle = _current_stream(device)
@@ -155,6 +156,9 @@ class _Call:
                 # the allocator's memory may still be in use by work of the current stream
                 self.stream.wait_stream(torch.cuda.current_stream(device))
                 self.handle = handle
+                for t in used:
+                    if t is not None and t.numel():
+                        t.record_stream(self.stream)
 
     def new(self, shape, dtype) -> torch.Tensor:
         """An uninitialised tensor; its memory is not given to other work
@@ -223,7 +227,7 @@ def norm_rope(q, k, q_weight, k_weight, positions, freqs, eps=1e-6, rot_offset=0
     k and k_weight may be None (k_out is None).  q and k may be views."""
     dev = _check_norm_rope(q, k, q_weight, k_weight, positions, freqs)
     p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
-    c = _Call(stream, dev)
+    c = _Call(stream, dev, q, k, q_weight, k_weight, positions, freqs)
     try:
         q_out = c.new(q.shape, q.dtype)
         k_out = None if k is None else c.new(k.shape, k.dtype)
@@ -248,7 +252,7 @@ def norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, freq
     if k is not None:
         _want(dk_out, "dk_out", k.shape, q.dtype, dev)
     p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
-    c = _Call(stream, dev)
+    c = _Call(stream, dev, dq_out, dk_out, q, k, q_weight, k_weight, positions, freqs, workspace)
     try:
         D = q.shape[2]
         dq, dqw = c.new(q.shape, q.dtype), c.new((D,), torch.float32)
@@ -308,7 +312,7 @@ def attn_forward(q, k, v, cu_q, cu_k, scale, causal=True, k_len=None, workspace=
     cu_k = arange(N+1)*W.  One query row per sequence is the decode step."""
     dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
     p = make_attn_problem(q, k, v, cu_q, scale, causal)
-    c = _Call(stream, dev)
+    c = _Call(stream, dev, q, k, v, cu_q, cu_k, k_len, workspace)
     try:
         out = c.new(q.shape, q.dtype)
         lse = c.new(q.shape[:2], torch.float32)
@@ -331,7 +335,7 @@ def attn_backward(dout, q, k, v, out, lse, cu_q, cu_k, scale, causal=True, k_len
     _want(out, "out", q.shape, q.dtype, dev)
     _want(lse, "lse", q.shape[:2], torch.float32, dev)
     p = make_attn_problem(q, k, v, cu_q, scale, causal)
-    c = _Call(stream, dev)
+    c = _Call(stream, dev, dout, q, k, v, out, lse, cu_q, cu_k, k_len, workspace)
     try:
         dq = c.new(q.shape, q.dtype)
         dk, dv = c.new(k.shape, k.dtype), c.new(v.shape, v.dtype)
