@@ -241,3 +241,30 @@ def test_each_gradient_by_differences(which):
     tol = noise + (abs(far - near) + noise) / 3 + 4 * 2.0 ** -11 * abs(near)
     assert tol < 0.02 * abs(near)  # zero, half or turned gradients would show
     assert abs(near - along) <= tol
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 60000.0])
+def test_fp16_gradients_do_not_depend_on_other_sequences(bad):
+    """dS's power of two comes from a sequence's own rows and keys: neighbours, and cache entries past the lengths,
+    may hold anything; and the same call gives the same bits."""
+    lq, W = [100, 37, 130, 60], 160
+    gen = torch.Generator().manual_seed(51)
+    r = lambda *s: torch.randn(*s, generator=gen).to(FP16)  # noqa: E731
+    q, do, k, v = r(sum(lq), 8, 64), r(sum(lq), 8, 64), r(4 * W, 2, 64), r(4 * W, 2, 64)
+    cu_q, cu_k, lens = _cu(*lq), _cu(*[W] * 4), torch.tensor([110, 37, 130, 90], dtype=torch.int32, device="cuda")
+
+    def run():
+        a = [t.cuda() for t in (q, k, v)]
+        o = csa.attn_forward(*a, cu_q, cu_k, 0.125, k_len=lens)
+        return (*o, *csa.attn_backward(do.cuda(), *a, *o, cu_q, cu_k, 0.125, k_len=lens))
+
+    good, again = run(), run()
+    assert all(torch.equal(a, b) for a, b in zip(good, again))
+    rows, keys = torch.zeros(sum(lq), dtype=torch.bool), torch.arange(4 * W) // W == 1  # sequence 1
+    rows[100:137] = True
+    keys |= torch.arange(4 * W) % W >= lens.cpu().repeat_interleave(W)
+    q[rows], do[rows], k[keys], v[keys] = bad, bad, bad, bad
+    for i, (a, b) in enumerate(zip(good, run())):
+        keep = ~(rows if i < 3 else keys).cuda()
+        assert torch.equal(a[keep], b[keep])
+    _ok()
