@@ -103,6 +103,15 @@ size_t csa_norm_rope_workspace_size(const csa_norm_rope_problem* p);
  *   contiguous); the innermost dimension is contiguous.  Bases are 16-byte
  *   aligned and strides multiples of 8 elements.  out, lse, the cotangent and
  *   the gradients are contiguous, with 16-byte aligned bases.
+ * Precision: products of stored values are exact and summed in fp32, as are the
+ * softmax's sums; exponentials are fp32.  The weights p that meet v (and dout, for
+ * dv), and ds = p (dout.v - dout.out) that meets k and q, are rounded to dtype,
+ * the tensor cores' operand type: half a unit of the last place each, twice what an
+ * fp32 computation rounded once has at worst.  dout.out is taken from the rounded
+ * out, except for rows whose block sees 128 keys or fewer.  In fp16, p and ds are
+ * formed at powers of two that keep them in range: p counts down to 2^-33 of the
+ * largest in out and 2^-40 in dv, and cotangents of any size give finite gradients
+ * where these fit fp16.
  * Supported: D in {64, 128}, dtype CSA_BF16 or CSA_F16, Hq a multiple of Hk,
  * Hq / Hk <= 128.  Tq, Tk, N >= 0 (nothing to write enqueues nothing).      */
 typedef struct {

@@ -224,7 +224,8 @@ def norm_rope(q, k, q_weight, k_weight, positions, freqs, eps=1e-6, rot_offset=0
     """Norm of every head of q [T,Hq,D] and k [T,Hk,D] with the weights [D], and
     the rotation of 2*len(freqs) of its values from rot_offset on, by
     positions [T] int64 -> (q_out, k_out), contiguous, in the inputs' type.
-    k and k_weight may be None (k_out is None).  q and k may be views."""
+    k and k_weight may be None (k_out is None).  q and k may be views.  The
+    outputs have no autograd history: gradients come from norm_rope_backward."""
     dev = _check_norm_rope(q, k, q_weight, k_weight, positions, freqs)
     p = make_norm_rope_problem(q, k, q_weight, freqs, eps, rot_offset, interleaved)
     c = _Call(stream, dev, q, k, q_weight, k_weight, positions, freqs)
@@ -309,7 +310,8 @@ def attn_forward(q, k, v, cu_q, cu_k, scale, causal=True, k_len=None, workspace=
     allowed), cu_q and cu_k [N+1] int32 -> (out [Tq,Hq,D] in q's type,
     lse [Tq,Hq] fp32).  With k_len [N] int32 only the first k_len[i] keys of
     sequence i count: a cache [N,W,Hk,D] is passed as its view [N*W,Hk,D] with
-    cu_k = arange(N+1)*W.  One query row per sequence is the decode step."""
+    cu_k = arange(N+1)*W.  One query row per sequence is the decode step.  The
+    outputs have no autograd history: gradients come from attn_backward."""
     dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
     p = make_attn_problem(q, k, v, cu_q, scale, causal)
     c = _Call(stream, dev, q, k, v, cu_q, cu_k, k_len, workspace)

@@ -5,7 +5,7 @@
 //   p_j = exp(s_j - lse),  ds_j = p_j (dout.v_j - delta)
 //   dq = scale sum_j ds_j k_j,  dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dout
 //
-// Three kernels: delta (one pass over dout and out), dq, and dk with dv.  The
+// Three kernels: delta (one pass over dout and out; fp16: and v), dq, and dk with dv.  The
 // scores are formed again from q, k and lse in both of the latter; P and dS
 // never leave the SM.  That is seven products per tile where one kernel
 // for everything needs five, but every output is summed by one CTA in a fixed
@@ -46,11 +46,11 @@
 // (weights down to 2^-40 count, 2^-25 as they come).  attn_range_kernel takes the norms and delta in one
 // pass (56 us for delta's 42 at the size below); bf16 has the range and none of this.
 //
-// Measured (bf16, 64 + 8 heads of 128, 8192 tokens in 5 documents): 0.828 ms,
-// 1025 TFLOP/s of the five products that count, 1435 of the seven executed (a
-// library product: 1885).  dkv 0.405 ms, tensor pipe active 79 %: the products;
-// dq 0.366 ms, 62 %: the elementwise warps' way between two products, and short
-// items; delta 0.042 ms, 6.4 TB/s.
+// Measured (bf16, 64 + 8 heads of 128, 8192 tokens in 5 documents): 0.83 to 0.85
+// ms, 1025 TFLOP/s of the five products that count, 1435 of the seven executed (a
+// library product: 1885).  dkv 0.410 ms, tensor pipe active 79 %: the products;
+// dq 0.370 ms, 62 %: dP has one buffer, so that the next dP waits until dS of this
+// tile has been formed and read; delta 0.042 ms, 6.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

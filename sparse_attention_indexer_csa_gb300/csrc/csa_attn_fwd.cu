@@ -43,12 +43,13 @@
 // Keys may be split over n_split items (few rows, long caches): each writes
 // its normalised O and lse in fp32, and a second kernel joins them.
 //
-// Measured (bf16, 64 + 8 heads of 128): a prompt of 16384 tokens 2.76 ms, 1592
+// Measured (bf16, 64 + 8 heads of 128): a prompt of 16384 tokens 2.75 ms, 1600
 // TFLOP/s of 1885 (a library product's rate): tensor cores.  32768 tokens in 22
-// documents 1.32 ms, 1276 TFLOP/s: half of a diagonal tile's products do not
-// count, and short items end before their pipeline is full.  One token of 64
+// documents 1.31 ms, 1289 TFLOP/s: an SM takes 55 items of 13 key tiles, and between the
+// last product of one and the first P of the next some 5 us pass (diagonal tiles
+// add 5 % of products that do not count).  One token of 64
 // sequences over 2048 to 8192 cached ones 0.248 ms, 5.4 TB/s of 6.7; of one
-// sequence over 131072, 0.094 ms, 5.7 TB/s: memory, and the join's launch.
+// sequence over 131072, 0.095 ms, 5.7 TB/s: memory, and the join's launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
