@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcsa_index.so")
 SOURCES = ["csa_prefill.cu", "csa_topk.cu", "csa_gather.cu", "csa_backward.cu", "csa_api.cu", "csa_norm_rope.cu",
-           "csa_attn_fwd.cu", "csa_attn_bwd.cu", "csa_attn_api.cu"]
+           "csa_attn_fwd.cu", "csa_attn_bwd.cu", "csa_attn_api.cu", "csa_sparse_fwd.cu", "csa_sparse_bwd.cu",
+           "csa_sparse_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -11,6 +11,7 @@
 
 #include "csa_index.h"
 #include "csa_attn_internal.h"
+#include "csa_sparse_internal.h"
 #include "csa_internal.h"
 
 namespace csa {
@@ -598,7 +599,7 @@ csa_status csa_index_gather(const csa_problem* p, const void* k, const int32_t* 
 }
 
 csa_status csa_index_device_status(void* stream) {
-  uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
+  uint32_t a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0, h = 0, i = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (take_status_prefill(&a, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_other(&b, s) != cudaSuccess) return CSA_ERR_CUDA;
@@ -606,7 +607,10 @@ csa_status csa_index_device_status(void* stream) {
   if (take_status_backward(&d, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_attn_fwd(&e, s) != cudaSuccess) return CSA_ERR_CUDA;
   if (take_status_attn_bwd(&f, s) != cudaSuccess) return CSA_ERR_CUDA;
-  const uint32_t v = a | b | c | d | e | f;
+  if (take_status_sparse_fwd(&g, s) != cudaSuccess) return CSA_ERR_CUDA;
+  if (take_status_sparse_bwd(&h, s) != cudaSuccess) return CSA_ERR_CUDA;
+  if (take_status_append(&i, s) != cudaSuccess) return CSA_ERR_CUDA;
+  const uint32_t v = a | b | c | d | e | f | g | h | i;
   if (v & kErrTimeout) return CSA_ERR_TIMEOUT;
   if (v != 0u) return CSA_ERR_DEVICE;
   return CSA_OK;

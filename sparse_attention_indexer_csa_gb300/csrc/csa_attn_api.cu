@@ -176,6 +176,19 @@ Dd dd_log(double x) {
 }
 
 }  // namespace
+
+csa_status norm_rope_call(const csa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const int64_t* positions, const uint64_t* freqs, const void* q_out,
+                          const void* k_out, NormRopeParams* n) {
+  const csa_status st = check_norm_rope(p);
+  if (st != CSA_OK) return st;
+  if (!norm_rope_supported(p)) return CSA_ERR_UNSUPPORTED;
+  std::memset(n, 0, sizeof(*n));
+  if (p->T == 0) return CSA_OK;
+  *n = norm_rope_params(p, q, k, q_weight, k_weight, positions, freqs);
+  return check_norm_rope_inputs(p, q, k, q_weight, k_weight, positions, freqs, q_out, k_out);
+}
+
 }  // namespace csa
 
 using namespace csa;

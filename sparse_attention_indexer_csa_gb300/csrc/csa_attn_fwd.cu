@@ -804,6 +804,24 @@ cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace,
   return p.D == 128 ? by_plan<__half, 128>(p, workspace, s) : by_plan<__half, 64>(p, workspace, s);
 }
 
+cudaError_t launch_attn_join(const AttnParams& p, int dtype, const float* part_o, const float* part_lse, int n_split,
+                             cudaStream_t s) {
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+  if (rows > 0x7FFFFFFFll || n_split > kMaxSplit) return cudaErrorInvalidValue;
+  const unsigned grid = static_cast<unsigned>(rows);
+  if (dtype == CSA_BF16) {
+    if (p.D == 128)
+      attn_join_kernel<__nv_bfloat16, 128><<<grid, 256, 0, s>>>(p, part_o, part_lse, n_split);
+    else
+      attn_join_kernel<__nv_bfloat16, 64><<<grid, 256, 0, s>>>(p, part_o, part_lse, n_split);
+  } else if (p.D == 128) {
+    attn_join_kernel<__half, 128><<<grid, 256, 0, s>>>(p, part_o, part_lse, n_split);
+  } else {
+    attn_join_kernel<__half, 64><<<grid, 256, 0, s>>>(p, part_o, part_lse, n_split);
+  }
+  return cudaGetLastError();
+}
+
 cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
 
 }  // namespace csa

@@ -34,6 +34,11 @@ constexpr int kNormRopeBlocks = 152 * 4;  // blocks (and partial sums) of the ba
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);
 cudaError_t launch_norm_rope_backward(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream);
 
+// The checks of csa_norm_rope's arguments, and its parameters without the outputs (unset when T is 0).
+csa_status norm_rope_call(const csa_norm_rope_problem* p, const void* q, const void* k, const void* q_weight,
+                          const void* k_weight, const int64_t* positions, const uint64_t* freqs, const void* q_out,
+                          const void* k_out, NormRopeParams* n);
+
 // ----------------------------------------------------------------- attention
 struct AttnParams {
   int N, Tq, Tk, Hq, Hk, g, D;  // g = Hq / Hk
@@ -54,6 +59,9 @@ struct AttnParams {
 };
 cudaError_t launch_attn_forward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_backward(const AttnParams& p, int dtype, void* workspace, cudaStream_t stream);
+// out and lse from the outputs [n_split][Tq * Hq][D] and lse [n_split][Tq * Hq] of the shares of each row's keys (fp32).
+cudaError_t launch_attn_join(const AttnParams& p, int dtype, const float* part_o, const float* part_lse, int n_split,
+                             cudaStream_t stream);
 cudaError_t take_status_attn_fwd(uint32_t* out, cudaStream_t stream);
 cudaError_t take_status_attn_bwd(uint32_t* out, cudaStream_t stream);
 

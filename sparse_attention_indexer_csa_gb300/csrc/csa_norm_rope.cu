@@ -31,8 +31,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "csa_attn_internal.h"
 #include "csa_attn_tiles.cuh"
+#include "csa_sparse_internal.h"
 
 namespace csa {
 namespace {
@@ -45,8 +48,9 @@ constexpr int kRows = BWD && sizeof(X) == 4 ? 2 : 4;
 constexpr int kUnit = 8;
 // Blocks per SM (the registers a thread has): fp32 rows take twice the
 // registers while they are on their way, and spill at three.
-template <typename X, bool BWD>
-constexpr int kBlocks = BWD || sizeof(X) == 4 ? 2 : 3;
+// An append's rows of the cache take as many more.
+template <typename X, bool BWD, bool APPEND = false>
+constexpr int kBlocks = BWD || APPEND || sizeof(X) == 4 ? 2 : 3;
 
 // Eight consecutive values as fp32, in pairs (packed arithmetic).
 struct V8 {
@@ -104,6 +108,19 @@ __device__ __forceinline__ void store8(X* p, int gap, const V8& o) {
       __stcs(reinterpret_cast<uint2*>(p), make_uint2(a, b));
       __stcs(reinterpret_cast<uint2*>(p + gap), make_uint2(c, d));
     }
+  }
+}
+// Eight values as they were loaded.
+template <typename X, bool INTER>
+__device__ __forceinline__ void store_raw(X* p, int gap, const Raw8<X>& r) {
+  if constexpr (sizeof(X) == 4) {
+    __stcs(reinterpret_cast<uint4*>(p), r.a);
+    __stcs(reinterpret_cast<uint4*>(p + gap), r.b);
+  } else if constexpr (INTER) {
+    __stcs(reinterpret_cast<uint4*>(p), r.a);
+  } else {
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(r.a.x, r.a.y));
+    __stcs(reinterpret_cast<uint2*>(p + gap), make_uint2(r.a.z, r.a.w));
   }
 }
 // Weight e of the run-time type w_dtype (0 past D).
@@ -216,6 +233,62 @@ struct Part {
   bool is_q;
   int block, blocks;  // this block among those of its part
 };
+// What an append adds to the problem, and the blocks that work on k (those behind work on v).
+struct AppendArgs {
+  AppendParams c;
+  int k_blocks;
+};
+struct NoAppend {};
+
+// The cache row of a token.  Consecutive tokens are mostly of the sequence of
+// the one before, whose extent is kept.
+struct Places {
+  int q0 = 0, q1 = 0;  // tokens of the sequence
+  int off = 0;         // place of a token: t + off
+  int seq = -1;
+  // page * page size + row of token t; -1: it is not stored
+  __device__ __forceinline__ long long find(const AppendParams& c, int T, int t) {
+    if (t >= T || c.N <= 0) return -1;
+    if (t < q0 || t >= q1) {
+      // sequences of equal lengths (one token each, when decoding) are met at the first look
+      int lo = static_cast<int>(static_cast<long long>(t) * c.N / T);
+      int a = c.cu_q[lo], b = c.cu_q[lo + 1];
+      if (t < a || t >= b) {
+        int hi = c.N;  // the largest i with cu_q[i] <= t
+        lo = 0;
+        while (lo < hi) {
+          const int i = (lo + hi + 1) >> 1;
+          if (c.cu_q[i] <= t)
+            lo = i;
+          else
+            hi = i - 1;
+        }
+        if (lo >= c.N) return -1;
+        a = c.cu_q[lo];
+        b = c.cu_q[lo + 1];
+        if (t < a || t >= b) return -1;
+      }
+      q0 = max(a, 0);
+      q1 = min(b, T);
+      seq = lo;
+      if (a != q0 || b != q1) record_error(kErrDevice);
+      off = min(max(c.k_len[lo], 0), 0x7FFFFFFF - T) - q1;
+    }
+    const int j = t + off;
+    const int n = j >= 0 ? j / c.page : 0;
+    if (j < 0 || n >= c.table_width) {
+      record_error(kErrDevice);
+      return -1;
+    }
+    const int pg = c.table[seq * c.table_st + n];
+    if (pg < 0 || pg >= c.pages) {
+      record_error(kErrDevice);
+      return -1;
+    }
+    return static_cast<long long>(pg) * c.page + (j - n * c.page);
+  }
+};
+
 template <typename X>
 __device__ __forceinline__ Part<X> make_part(const NormRopeParams& p) {
   Part<X> a;
@@ -260,10 +333,23 @@ struct Stretch {
 // A row is requested U rows before it is worked on, as soon as its registers
 // are free.  All groups walk as far (the shuffles need whole warps); what lies
 // past a group's rows is neither read nor written.
-template <typename X, int G, bool INTER, int U, bool BWD>
-__global__ void __launch_bounds__(kThreads, kBlocks<X, BWD>) norm_rope_kernel(const NormRopeParams p) {
+//
+// APPEND: k's rows go to the cache, and a third part of the blocks copies v's rows there.
+template <typename X, int G, bool INTER, int U, bool BWD, bool APPEND = false>
+__global__ void __launch_bounds__(kThreads, kBlocks<X, BWD, APPEND>)
+    norm_rope_kernel(const NormRopeParams p, const std::conditional_t<APPEND, AppendArgs, NoAppend> more) {
   constexpr int PER = kThreads / G;
-  const Part<X> a = make_part<X>(p);
+  Part<X> a = make_part<X>(p);
+  bool is_v = false;
+  if constexpr (APPEND) {
+    is_v = !a.is_q && a.block >= more.k_blocks;
+    if (is_v) {
+      a.x = static_cast<const X*>(more.c.v);
+      a.st = more.c.v_st;
+      a.sh = more.c.v_sh;
+      a.block -= more.k_blocks;
+    }
+  }
   const Lane ln = make_lane<INTER>(p, threadIdx.x % G);
   const int e = ln.e, gap = ln.gap;
   const bool lane_ok = e < p.D;
@@ -281,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<X, BWD>) norm_rope_kernel(co
   Stretch ahead = now;                                                                // of the row requested
   const X* xp = a.x + ahead.t * a.st + ahead.h * a.sh + e;
   const X* gp = BWD ? a.g + row0 * p.D + e : nullptr;
-  X* yp = a.y + row0 * p.D + e;
+  X* yp = APPEND && !a.is_q ? nullptr : a.y + row0 * p.D + e;
   float2 acc[4] = {};  // gradients of the weights
   Raw8<X> rx[U], rg[BWD ? U : 1];
   int n_ahead = ahead.n(a.H), n_now = n_ahead;
@@ -312,6 +398,38 @@ __global__ void __launch_bounds__(kThreads, kBlocks<X, BWD>) norm_rope_kernel(co
 #pragma unroll
   for (int u = 0; u < U; ++u) request(u);
   int64_t pos = coming();
+  Places places;
+  long long y_step = p.D;  // between two rows of a stretch
+  // the cache row of a stretch (its page is looked up with the coming position), and the pointer into it
+  auto place = [&](const Stretch& s) -> long long {
+    if constexpr (APPEND) {
+      if (!a.is_q && static_cast<unsigned>(s.t) < static_cast<unsigned>(p.T)) return places.find(more.c, p.T, s.t);
+    }
+    return -1;
+  };
+  auto cache_row = [&](long long at, int h) -> X* {
+    if constexpr (APPEND) {
+      if (at < 0) return nullptr;
+      const AppendParams& c = more.c;
+      const long long page = at / c.page, row = at - page * c.page;
+      return is_v ? static_cast<X*>(c.vc) + page * c.vc_sp + row * c.vc_st + h * c.vc_sh + e
+                  : static_cast<X*>(c.kc) + page * c.kc_sp + row * c.kc_st + h * c.kc_sh + e;
+    }
+    return nullptr;
+  };
+  auto coming_place = [&]() {
+    Stretch s = now;
+    s.advance(deal, a.H);
+    return place(s);
+  };
+  long long next_at = -1;
+  if constexpr (APPEND) {
+    if (!a.is_q) {
+      y_step = is_v ? more.c.vc_sh : more.c.kc_sh;
+      if (left > 0) yp = cache_row(place(now), now.h);
+      if (left > n_now) next_at = coming_place();
+    }
+  }
   tn.set(position(now), w);
   const int most = deal.rounds * deal.R;  // all groups walk as far
   for (int i = 0; i < most; i += U) {
@@ -347,12 +465,29 @@ __global__ void __launch_bounds__(kThreads, kBlocks<X, BWD>) norm_rope_kernel(co
 #pragma unroll
         for (int i = 0; i < 4; ++i) y.p[i] = fmul2(r2, tn.turned(x, i));
       }
-      if (ok && lane_ok) store8<X, INTER>(yp, gap, y);
+      if constexpr (APPEND) {
+        if (ok && lane_ok && yp != nullptr) {
+          if (is_v)
+            store_raw<X, INTER>(yp, gap, raw);
+          else
+            store8<X, INTER>(yp, gap, y);
+        }
+        if (yp != nullptr) yp += y_step;
+      } else {
+        if (ok && lane_ok) store8<X, INTER>(yp, gap, y);
+        yp += p.D;
+      }
       --left;
-      yp += p.D;
       if (--n_now == 0) {
-        if (now.advance(deal, a.H)) yp += static_cast<long long>(deal.skip) * p.D;
+        const bool jump = now.advance(deal, a.H);
+        if (jump && !(APPEND && !a.is_q)) yp += static_cast<long long>(deal.skip) * p.D;
         n_now = now.n(a.H);
+        if constexpr (APPEND) {
+          if (!a.is_q) {
+            yp = cache_row(next_at, now.h);
+            next_at = left > n_now ? coming_place() : -1;
+          }
+        }
         tn.set(pos, w);
         pos = coming();
       }
@@ -422,12 +557,38 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
   p.q_blocks = static_cast<int>(nq);
   p.deal_q = deal_rows(static_cast<long long>(p.T) * p.Hq, nq * PER, p.Hq);
   if (nk > 0) p.deal_k = deal_rows(static_cast<long long>(p.T) * p.Hk, nk * PER, p.Hk);
-  norm_rope_kernel<X, G, INTER, U, BWD><<<static_cast<unsigned>(nq + nk), kThreads, 0, stream>>>(p);
+  norm_rope_kernel<X, G, INTER, U, BWD><<<static_cast<unsigned>(nq + nk), kThreads, 0, stream>>>(p, NoAppend{});
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !BWD) return e;
   norm_rope_dw_kernel<<<dim3((p.D + 31) / 32, p.Hk > 0 ? 2 : 1), 1024, 0, stream>>>(
       p.part, static_cast<int>(nq), static_cast<int>(nk), p.D, p.dqw, p.dkw);
   return cudaGetLastError();
+}
+
+// Blocks of q, of k and of v, in proportion to their rows.
+template <typename X, int G, bool INTER>
+cudaError_t run_append(NormRopeParams p, const AppendParams& c, cudaStream_t stream) {
+  constexpr int PER = kThreads / G, U = kRows<X, false>, CHUNK = PER * U;
+  auto chunks = [&](int H) { return (static_cast<long long>(p.T) * H + CHUNK - 1) / CHUNK; };
+  const long long cq = chunks(p.Hq), ck = chunks(p.Hk), most = 152 * kBlocks<X, false, true>;
+  long long nq = cq, nk = ck;
+  if (cq + 2 * ck > most) {
+    nk = std::max<long long>(1, std::min<long long>(ck, (most * ck + (cq + 2 * ck) / 2) / (cq + 2 * ck)));
+    nq = std::min<long long>(cq, std::max<long long>(1, most - 2 * nk));
+  }
+  p.q_blocks = static_cast<int>(nq);
+  p.deal_q = deal_rows(static_cast<long long>(p.T) * p.Hq, nq * PER, p.Hq);
+  p.deal_k = deal_rows(static_cast<long long>(p.T) * p.Hk, nk * PER, p.Hk);
+  const AppendArgs more{c, static_cast<int>(nk)};
+  norm_rope_kernel<X, G, INTER, U, false, true><<<static_cast<unsigned>(nq + 2 * nk), kThreads, 0, stream>>>(p, more);
+  return cudaGetLastError();
+}
+template <typename X, bool INTER>
+cudaError_t append_by_size(const NormRopeParams& p, const AppendParams& c, cudaStream_t s) {
+  if (p.D <= 32) return run_append<X, 4, INTER>(p, c, s);
+  if (p.D <= 64) return run_append<X, 8, INTER>(p, c, s);
+  if (p.D <= 128) return run_append<X, 16, INTER>(p, c, s);
+  return run_append<X, 32, INTER>(p, c, s);
 }
 
 template <typename X, bool INTER>
@@ -455,5 +616,13 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int dtype, bool inter, cud
 cudaError_t launch_norm_rope_backward(const NormRopeParams& p, int dtype, bool inter, cudaStream_t stream) {
   return dispatch(p, dtype, inter, true, stream);
 }
+cudaError_t launch_norm_rope_append(const NormRopeParams& p, const AppendParams& c, int dtype, bool inter,
+                                    cudaStream_t s) {
+  if (dtype == CSA_F32) return inter ? append_by_size<float, true>(p, c, s) : append_by_size<float, false>(p, c, s);
+  if (dtype == CSA_F16) return inter ? append_by_size<__half, true>(p, c, s) : append_by_size<__half, false>(p, c, s);
+  return inter ? append_by_size<__nv_bfloat16, true>(p, c, s) : append_by_size<__nv_bfloat16, false>(p, c, s);
+}
+
+cudaError_t take_status_append(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
 
 }  // namespace csa

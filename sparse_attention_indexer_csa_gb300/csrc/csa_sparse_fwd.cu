@@ -1,0 +1,611 @@
+// csa_sparse_fwd.cu -- attention over listed blocks of keys on the tensor cores.
+//
+//   s_j = scale q.k_j over the keys that a row lists, out = sum_j p_j v_j with
+//   p = softmax(s), lse = log sum_j exp(s_j).
+//
+// An item is one query row, one key head and one share of the row's list.  Its
+// g = Hq/Hk query heads are the rows of the products, and the listed keys, 128
+// at a time and packed so that hidden ones take no place, their columns:
+//   S = Q . K^T      (A = queries, B = key tile, both in shared memory, to TMEM)
+//   P = 2^(c (S - m) + shift) in the storage type, c = scale log2(e), over S
+//   O += P . V       (A = P in TMEM, B = value tile read MN-major, O in TMEM)
+// The products have 128 rows and g is often less: the queries stand there R =
+// 128 / G times (G: 32, 64 or 128 rows), and copy r takes the columns r 128/R
+// .. of each tile; P is zero in its others.  So each thread has 128/R scores
+// instead of one thread having all, each copy keeps its own reference m and sum
+// l, and the copies' outputs are joined once per item.
+//
+// m is raised (and O, l rescaled) only when a tile's largest score is 2^kRaise
+// above it; fp16 weights are formed 2^kShift times their size, so that they
+// count down to 2^-32 of the reference's.
+//
+// Roles (12 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
+//   warps 0-3   softmax, one thread per row of S
+//   warps 4-7   outputs: join, division, stores, while the next item runs
+//   warp 8      issuer of the products, one thread
+//   warp 9, 10  gathered loads of keys (and queries) and of values: four rows an
+//               instruction, by TMA, so that hidden keys are never read and what
+//               fills up a tile reads as zero
+//   warp 11     lists: the rows of the coming tiles, up to kRing tiles ahead
+// Shared memory: two query blocks, two key and two value tiles.  TMEM: S0 S1 O0 O1.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstring>
+
+#include "csa_sparse_list.cuh"
+
+namespace csa {
+namespace {
+
+template <typename X>
+constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
+constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
+
+constexpr int kRing = 4;      // tiles of rows ahead
+constexpr int kThreads = 384;
+constexpr int kOutWarp = 4, kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kListWarp = 11;
+constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
+
+// One tile of an item's keys (n of 1..128), the end of an item (n = 0) or of all (n < 0).
+struct TileHead {
+  int n, first, t, hk, z;
+};
+struct Tile {
+  int k_row[128], v_row[128];
+  TileHead h;
+  int pad[3];
+};
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kTile = kChunkBytes * (D / 64);  // 128 rows x D
+  static constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffOut = 6 * kTile;
+  static constexpr uint32_t kOffRing = kOffOut + 128 * kPitch * 4;
+  static constexpr uint32_t kOffMl = kOffRing + kRing * sizeof(Tile);  // [2][2][128] floats: m, l of two items
+  static constexpr uint32_t kOffBar = kOffMl + 2 * 2 * 128 * 4;
+  static constexpr int kBarQ = 0, kBarQFree = 2, kBarK = 4, kBarV = 6, kBarS = 8, kBarP = 10, kBarPv = 12, kBarO = 14,
+                       kBarMl = 16, kBarOFree = 18, kBarTile = 20, kBarTileFree = kBarTile + kRing,
+                       kBarMeet = kBarTileFree + kRing, kBarDone = kBarMeet + 1, kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
+};
+static_assert(Cfg<128>::kSmem <= 227 * 1024, "one CTA per SM");
+static_assert(sizeof(Tile) % 16 == 0, "rows are read 16 bytes at a time");
+
+struct FwdArgs {
+  SparseParams p;
+  long long items;  // Tq * Hk * n_split
+  long long slots;  // of a row's list
+  int n_split;
+  float c;          // scale * log2(e)
+  float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
+  float* part_lse;  // [n_split][Tq * Hq]
+  unsigned long long wait_ns;
+};
+
+// Writes the tiles of this CTA's items into the ring.  A warp.
+__device__ __forceinline__ void list_tiles(const FwdArgs& f, Tile* ring, uint64_t* full, uint64_t* free_bar,
+                                           const WaitCtl& ctl) {
+  const SparseParams& p = f.p;
+  const int lane = static_cast<int>(lane_id());
+  uint32_t n_tile = 0;
+  bool ok = true, held = false;
+  auto take = [&] {
+    if (!held) ok = ok && mbar_wait(free_bar + n_tile % kRing, ((n_tile / kRing) & 1u) ^ 1u, ctl);
+    held = true;
+  };
+  auto give = [&](const TileHead& h) {
+    if (lane == 0) ring[n_tile % kRing].h = h;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + n_tile % kRing);
+    ++n_tile;
+    held = false;
+  };
+  if (blockIdx.x == 0)
+    for (int i = lane; i < p.N; i += 32) sparse_extent(p, i);  // what is out of order or range is recorded
+  ListRow row{-1, 0, 0, -1};
+  int row_t = -1;
+  const long long chunks = (f.slots + 127) / 128;
+  for (long long item = blockIdx.x; ok && item < f.items; item += gridDim.x) {
+    const long long rest = item / f.n_split;
+    const int z = static_cast<int>(item - rest * f.n_split);
+    const int t = static_cast<int>(rest / p.Hk), hk = static_cast<int>(rest - static_cast<long long>(t) * p.Hk);
+    if (t != row_t) row = find_list_row(p, t);
+    row_t = t;
+    const int32_t* list = p.idx + t * p.idx_st;
+    const int k0 = hk * p.k.rh, v0 = hk * p.v.rh;
+    int fill = 0, first = 1;
+    if (row.lk > 0 && row.pos >= 0) {
+      int b[4];
+      Slot x[4];
+      auto blocks = [&](long long c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = c < chunks ? slot_block(p, list, c * 128 + 32 * i + lane, f.slots) : -1;
+      };
+      auto keys = [&](long long c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const long long s = c * 128 + 32 * i + lane;
+          x[i] = s < f.slots ? slot_key(p, row, s, b[i]) : Slot{-1, 0};
+        }
+      };
+      blocks(z);
+      keys(z);
+      blocks(static_cast<long long>(z) + f.n_split);
+      for (long long c = z; ok && c < chunks; c += f.n_split) {
+        Slot now[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) now[i] = x[i];
+        keys(c + f.n_split);
+        blocks(c + 2 * f.n_split);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int kr = 0, vr = 0;
+          const bool see = slot_rows(p, row, now[i], kr, vr);
+          const unsigned all = __ballot_sync(0xffffffffu, see);
+          if (all == 0u) continue;
+          take();
+          if (!ok) break;
+          const int at = fill + __popc(all & ((1u << lane) - 1u));
+          if (see && at < 128) {
+            ring[n_tile % kRing].k_row[at] = kr + k0;
+            ring[n_tile % kRing].v_row[at] = vr + v0;
+          }
+          fill += __popc(all);
+          if (fill < 128) continue;
+          give(TileHead{128, first, t, hk, z});
+          first = 0;
+          fill -= 128;
+          if (fill == 0) continue;
+          take();
+          if (!ok) break;
+          if (see && at >= 128) {
+            ring[n_tile % kRing].k_row[at - 128] = kr + k0;
+            ring[n_tile % kRing].v_row[at - 128] = vr + v0;
+          }
+        }
+      }
+      if (ok && fill > 0) {  // the products take 16 keys at a time
+        const int at = fill + lane;
+        if (at < ((fill + 15) & ~15)) {
+          ring[n_tile % kRing].k_row[at] = p.k.n;
+          ring[n_tile % kRing].v_row[at] = p.v.n;
+        }
+        give(TileHead{fill, first, t, hk, z});
+      }
+    }
+    take();
+    if (ok) give(TileHead{0, 0, t, hk, z});
+  }
+  take();
+  if (ok) give(TileHead{-1, 0, 0, 0, 0});
+}
+
+template <typename X, int D, int R, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    sparse_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ FwdArgs f) {
+  using C = Cfg<D>;
+  constexpr int G = 128 / R, CW = 128 / R;  // rows of a copy of the queries; columns that a copy takes
+  extern __shared__ __align__(1024) uint8_t base[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
+  Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
+  const SparseParams& p = f.p;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      int n = 1;
+      if (i >= C::kBarP && i < C::kBarP + 2) n = 4;
+      if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4;
+      if (i >= C::kBarOFree && i < C::kBarOFree + 2) n = 4;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 11;
+      if (i == C::kBarMeet) n = 4;
+      mbar_init(bars + i, n);
+    }
+    if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kKeyWarp && lane == 0) {
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, f.wait_ns};
+  volatile uint32_t dummy = 0;
+  const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
+  // the next tile of the stream; n < 0 after the last one or a wait that gave up
+  uint32_t n_head = 0;
+  auto next_head = [&]() -> TileHead {
+    if (!mbar_wait(bars + C::kBarTile + n_head % kRing, (n_head / kRing) & 1u, ctl)) return TileHead{-1, 0, 0, 0, 0};
+    return ring[n_head % kRing].h;
+  };
+  auto give_head = [&] {  // by one thread of a role's warp
+    mbar_arrive(bars + C::kBarTileFree + n_head % kRing);
+  };
+
+  if (warp == kListWarp) {
+    list_tiles(f, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+  } else if (warp == kKeyWarp || warp == kValueWarp) {
+    // ------------------------------------------------------------------------- gathered loads
+    const bool keys = warp == kKeyWarp;
+    const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
+    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV);
+    // a stage is free when the product that read it has completed
+    uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv);
+    uint8_t* tiles = base + (keys ? C::kOffK : C::kOffV);
+    const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
+    uint32_t j = 0, nq = 0;
+    while (true) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0) {
+        if (keys && h.first) {
+          const uint32_t b = nq & 1u;
+          if (!mbar_wait(bars + C::kBarQFree + b, ((nq >> 1) & 1u) ^ 1u, ctl)) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bars + C::kBarQ + b, static_cast<uint32_t>(R * p.g) * 128u * (D / 64));
+            for (int r = 0; r < R; ++r)
+              for (int ch = 0; ch < D / 64; ++ch)
+                tma_load_3d_hint(base + C::kOffQ + b * C::kTile + ch * kChunkBytes + r * (G * 128), &tmap_q,
+                                 bars + C::kBarQ + b, ch * 64, h.hk * p.g, h.t, q_pol);
+          }
+          ++nq;
+        }
+        const uint32_t st = j & 1u;
+        if (j >= 2 && !mbar_wait(used + st, ((j >> 1) & 1u) ^ 1u, ctl)) break;
+        const int groups = ((h.n + 15) >> 4) * 4;
+        if (lane == 0) mbar_arrive_expect_tx(full + st, static_cast<uint32_t>(groups) * 512u * (D / 64));
+        __syncwarp();
+        if (static_cast<int>(lane) < groups) {
+          const Tile& tile = ring[n_head % kRing];
+          const int4 rows = reinterpret_cast<const int4*>(keys ? tile.k_row : tile.v_row)[lane];
+#pragma unroll
+          for (int ch = 0; ch < D / 64; ++ch)
+            tma_gather4(tiles + st * C::kTile + ch * kChunkBytes + lane * 512, map, full + st, ch * 64, rows, kv_pol);
+        }
+        ++j;
+      }
+      __syncwarp();
+      if (lane == 0) give_head();
+      ++n_head;
+    }
+    // no copy is in flight when the CTA ends, a role's giving up included
+    for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait(full + (i & 1u), (i >> 1) & 1u, drain);
+    for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------------- issuer of the products
+    // S of a tile goes before the former tile's product with V, so that the
+    // softmax has one while the tensor cores have the other.
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
+    const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffK), 128);
+    const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffV), kChunkBytes, 1024u);
+    constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false), kIdO = idesc_f16<X>(128, D, true), kT = C::kTile >> 4;
+    bool alive = true;
+    auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
+    uint32_t j = 0, nq = 0, on = 0;
+    int pend = 0, pend_first = 0;  // keys of the tile whose product with V is to come
+    bool got_o = false;            // this item's O is free
+    auto take_o = [&] {
+      if (!got_o) wait(C::kBarOFree + static_cast<int>(on & 1u), ((on >> 1) & 1u) ^ 1u);
+      got_o = true;
+    };
+    auto values = [&] {
+      const uint32_t i = j - 1, st = i & 1u;
+      take_o();
+      wait(C::kBarP + static_cast<int>(st), (i >> 1) & 1u);
+      wait(C::kBarV + static_cast<int>(st), (i >> 1) & 1u);
+      tc_fence_after();
+      const int steps = (pend + 15) >> 4;
+      if (elect_one()) {
+        if (alive) {
+          for (int ks = 0; ks < steps; ++ks)
+            umma_bf16_tmem_a(tm + 256u + (on & 1u) * 128u, tm + st * 128u + 8u * ks,
+                             vd + static_cast<uint64_t>(st * kT) + static_cast<uint64_t>(128 * ks), kIdO,
+                             (!pend_first || ks != 0) ? 1u : 0u);
+        }
+        umma_commit(bars + C::kBarPv + st);
+      }
+      __syncwarp();
+      pend = 0;
+    };
+    while (alive) {
+      const TileHead h = next_head();
+      const int n = uniform(h.n), first = uniform(h.first);
+      if (n < 0) break;
+      __syncwarp();
+      if (lane == 0) give_head();
+      ++n_head;
+      if (n > 0) {
+        const uint32_t st = j & 1u;
+        if (first) {
+          wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
+          ++nq;
+        }
+        wait(C::kBarK + static_cast<int>(st), (j >> 1) & 1u);
+        tc_fence_after();
+        if (elect_one()) {
+          if (alive) {
+            const uint64_t q = qd + static_cast<uint64_t>(((nq - 1u) & 1u) * kT), k = kd + static_cast<uint64_t>(st * kT);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
+              umma_bf16(tm + st * 128u, q + o, k + o, kIdS, ks != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(bars + C::kBarS + st);
+        }
+        __syncwarp();
+        if (pend != 0) values();
+        pend = n;
+        pend_first = first;
+        ++j;
+      } else {
+        const bool any = pend != 0;
+        if (any) values();
+        take_o();
+        got_o = false;
+        if (elect_one()) {
+          umma_commit(bars + C::kBarO + (on & 1u));
+          if (any) umma_commit(bars + C::kBarQFree + ((nq - 1u) & 1u));
+        }
+        __syncwarp();
+        ++on;
+      }
+    }
+    if (elect_one()) umma_commit(bars + C::kBarDone);
+    __syncwarp();
+    mbar_wait(bars + C::kBarDone, 0u, drain);
+  } else if (warp < kOutWarp) {
+    // ------------------------------------------------------------------------- softmax
+    const int row = warp * 32 + static_cast<int>(lane), copy = row / G, col0 = copy * CW;
+    const bool used = row % G < p.g;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    float* ml = reinterpret_cast<float*>(base + C::kOffMl);
+    const float c = f.c;
+    uint32_t j = 0, on = 0;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    while (ok) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0) {
+        const uint32_t st = j & 1u;
+        ok = mbar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ts = tmem + lanes + st * 128u;
+        const int lim = h.n - col0;  // columns of this copy that are keys
+        float s[CW == 32 ? 1 : 2][32];
+        auto load = [&](int i, float (&x)[32]) {
+          tmem_ld32_start(ts + col0 + 32 * i, x);
+          tmem_wait32(x);
+          if (32 * (i + 1) > lim) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              if (32 * i + u >= lim) x[u] = -INFINITY;
+          }
+        };
+        // the tile's largest score (NaN is passed over)
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < CW / 32; ++i) {
+          float(&x)[32] = s[CW == 32 ? 0 : i & 1];
+          load(i, x);
+          float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+#pragma unroll
+          for (int u = 4; u < 32; u += 4) {
+            a = max3(a, x[u], x[u + 1]);
+            b = max3(b, x[u + 2], x[u + 3]);
+          }
+          top = max3(top, a, b);
+        }
+        if (!used) top = -INFINITY;  // no query: what stands there asks for nothing
+        if (h.first) {
+          m = top;
+          l = 0.f;
+        } else if (__any_sync(0xffffffffu, top * c > m * c + kRaise || (m == -INFINITY && top > m))) {
+          // the former tile's product with V has to be through before O is rescaled
+          ok = mbar_wait(bars + C::kBarPv + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const float mn = fmaxf(m, top), r = mn == -INFINITY ? 1.f : exp2_approx((m - mn) * c);
+          m = mn;
+          l *= r;
+          const uint32_t to = tmem + lanes + 256u + (on & 1u) * 128u;
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
+        }
+        const float ref = (m == -INFINITY ? 0.f : m) * c, bias = kShift<X> - ref;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < CW / 32; ++i) {
+          float(&x)[32] = s[CW == 32 ? 0 : i & 1];
+          if (CW == 128) load(i, x);  // P of columns before lies in columns that have been read
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float2 e = ffma2(make_float2(x[2 * u], x[2 * u + 1]), make_float2(c, c), make_float2(bias, bias));
+            const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            sum = fadd2(sum, w);
+            pk[u] = pack_pair<X>(w.x, w.y);
+          }
+          tmem_st16(ts + (col0 + 32 * i) / 2, pk);
+        }
+        l += sum.x + sum.y;
+        if (R > 1) {  // the other copies' columns, as far as the product reads
+          const uint32_t zero[16] = {};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (32 * i / CW != copy && 32 * i < h.n) tmem_st16(ts + 16 * i, zero);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarP + st);
+        ++j;
+      } else {
+        ok = mbar_wait(bars + C::kBarOFree + (on & 1u), ((on >> 1) & 1u) ^ 1u, ctl);
+        float* mine = ml + (on & 1u) * 256;
+        mine[row] = m;
+        mine[128 + row] = l;
+        m = -INFINITY;
+        l = 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarMl + (on & 1u));
+        ++on;
+      }
+      __syncwarp();
+      if (lane == 0) give_head();
+      ++n_head;
+    }
+  } else {
+    // ------------------------------------------------------------------------- outputs
+    const int w = warp - kOutWarp, row = w * 32 + static_cast<int>(lane), head = row % G, tid = row;
+    float* stage = reinterpret_cast<float*>(base + C::kOffOut);
+    const float* ml = reinterpret_cast<const float*>(base + C::kOffMl);
+    const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+    uint32_t on = 0, met = 0;
+    while (true) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n == 0) {
+        const uint32_t b = on & 1u;
+        if (!mbar_wait(bars + C::kBarMl + b, (on >> 1) & 1u, ctl) || !mbar_wait(bars + C::kBarO + b, (on >> 1) & 1u, ctl))
+          break;
+        tc_fence_after();
+        const float* mm = ml + b * 256;
+        float top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = fmaxf(top, mm[r * G + head]);
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int r = 0; r < R; ++r) l += mm[128 + r * G + head] * exp2_approx((mm[r * G + head] - ref) * f.c);
+        const bool seen = l > 0.f || l != l;
+        const float weight = seen ? exp2_approx((mm[row] - ref) * f.c) / l : 0.f;
+        const long long at = static_cast<long long>(h.t) * p.Hq + static_cast<long long>(h.hk) * p.g;
+        if (row < p.g) {
+          const float lse = seen ? (ref * f.c + __log2f(l) - kShift<X>) * 0.6931471805599453f : -INFINITY;
+          if constexpr (SPLIT)
+            f.part_lse[h.z * rows + at + row] = lse;
+          else
+            p.lse[at + row] = lse;
+        }
+        const uint32_t to = tmem + (static_cast<uint32_t>(w * 32) << 16) + 256u + b * 128u;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          float o[32];
+          tmem_ld32_start(to + 32 * ch, o);
+          tmem_wait32(o);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<float4*>(stage + row * kPitch + 4 * u) =
+                weight == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                              : make_float4(o[4 * u] * weight, o[4 * u + 1] * weight, o[4 * u + 2] * weight,
+                                            o[4 * u + 3] * weight);
+          meet(bars + C::kBarMeet, met, ctl);
+          for (int i = tid; i < p.g * 8; i += 128) {
+            const int hd = i >> 3, col = (i & 7) * 4;
+            float4 v = *reinterpret_cast<const float4*>(stage + hd * kPitch + col);
+#pragma unroll
+            for (int r = 1; r < R; ++r) {
+              const float4 x = *reinterpret_cast<const float4*>(stage + (r * G + hd) * kPitch + col);
+              v.x += x.x;
+              v.y += x.y;
+              v.z += x.z;
+              v.w += x.w;
+            }
+            const long long e = (at + hd) * D + 32 * ch + col;
+            if constexpr (SPLIT)
+              *reinterpret_cast<float4*>(f.part_o + h.z * rows * D + e) = v;
+            else
+              *reinterpret_cast<uint2*>(static_cast<X*>(p.out) + e) =
+                  make_uint2(pack_pair<X>(v.x, v.y), pack_pair<X>(v.z, v.w));
+          }
+          meet(bars + C::kBarMeet, met, ctl);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarOFree + b);
+        ++on;
+      }
+      __syncwarp();
+      if (lane == 0) give_head();
+      ++n_head;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <typename X, int D, int R, bool SPLIT>
+cudaError_t start(const FwdArgs& f, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                  cudaStream_t stream) {
+  constexpr auto kernel = sparse_fwd_kernel<X, D, R, SPLIT>;
+  const cudaError_t e = smem_limit_once<kernel>(Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(std::min(f.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, tk, tv, f);
+  return cudaGetLastError();
+}
+
+template <typename X, int D, int R>
+cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  FwdArgs f;
+  f.p = p;
+  f.slots = sparse_slots(p);
+  f.n_split = sparse_splits(p.Tq, p.Hk, f.slots);
+  f.items = static_cast<long long>(p.Tq) * p.Hk * f.n_split;
+  f.c = p.scale * 1.4426950408889634f;
+  f.part_o = static_cast<float*>(workspace);
+  f.part_lse = f.part_o + static_cast<long long>(f.n_split) * p.Tq * p.Hq * D;
+  f.wait_ns = attn_wait_ns(f.slots / 128 + 1);
+  if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, p.g) || !make_gather_map(&tk, p, p.k) || !make_gather_map(&tv, p, p.v))
+    return cudaErrorInvalidValue;
+  if (f.n_split == 1) return start<X, D, R, false>(f, tq, tk, tv, stream);
+  cudaError_t e = start<X, D, R, true>(f, tq, tk, tv, stream);
+  if (e != cudaSuccess) return e;
+  AttnParams a;
+  std::memset(&a, 0, sizeof(a));
+  a.Tq = p.Tq;
+  a.Hq = p.Hq;
+  a.D = D;
+  a.out = p.out;
+  a.lse = p.lse;
+  return launch_attn_join(a, dtype, f.part_o, f.part_lse, f.n_split, stream);
+}
+
+template <typename X, int D>
+cudaError_t by_heads(const SparseParams& p, int dtype, void* ws, cudaStream_t s) {
+  if (p.g <= 32) return run<X, D, 4>(p, dtype, ws, s);
+  return p.g <= 64 ? run<X, D, 2>(p, dtype, ws, s) : run<X, D, 1>(p, dtype, ws, s);
+}
+
+}  // namespace
+
+cudaError_t launch_sparse_forward(const SparseParams& p, int dtype, void* workspace, cudaStream_t s) {
+  if (dtype == CSA_BF16)
+    return p.D == 128 ? by_heads<__nv_bfloat16, 128>(p, dtype, workspace, s)
+                      : by_heads<__nv_bfloat16, 64>(p, dtype, workspace, s);
+  return p.D == 128 ? by_heads<__half, 128>(p, dtype, workspace, s) : by_heads<__half, 64>(p, dtype, workspace, s);
+}
+
+cudaError_t take_status_sparse_fwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
+
+}  // namespace csa
