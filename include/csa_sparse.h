@@ -53,10 +53,10 @@ extern "C" {
  *   -1 or past a row's sequence, and pages outside 0 .. pages-1, are skipped;
  *   each records CSA_ERR_DEVICE in the device status word and is never followed.
  *   Strides in elements between pages, tokens and heads (0 = contiguous); the
- *   innermost dimension is contiguous.  Bases are 16-byte aligned; q's strides are
- *   multiples of 8 elements, those of k and v multiples of D (a view of a
- *   projection's output, pages with keys and values side by side).  out, lse,
- *   the cotangent and the gradients are contiguous with 16-byte aligned bases.
+ *   innermost dimension is contiguous.  Bases are 16-byte aligned and strides of q, k
+ *   and v multiples of 8 elements (a view of a projection's output, pages with
+ *   keys and values side by side).  out, lse, the cotangent and the gradients are
+ *   contiguous with 16-byte aligned bases.
  * Precision: as for csa_attn_forward: products of stored values are exact and
  * summed in fp32, as are the softmax's sums; exponentials are fp32.  The weights
  * that meet v (and dout), and ds that meets k and q, are rounded to dtype, half a
@@ -65,7 +65,8 @@ extern "C" {
  * count down to 2^-32 of the largest in out and 2^-39 in dv.
  * Supported: D in {64, 128}, dtype CSA_BF16 or CSA_F16, Hq a multiple of Hk,
  * Hq / Hk <= 128, block a power of two up to 128, window + top_k * block up to
- * 2^20, top_k >= 0 (0: idx is NULL), Tq, Tk, N >= 0.                           */
+ * 2^20, top_k >= 0 (0: idx is NULL), Tq, Tk, N >= 0; k and v span less than 2^31
+ * times the greatest common divisor of their strides.                          */
 typedef struct {
   int32_t N, Tq, Tk, Hq, Hk, D;
   int32_t top_k, block, window;

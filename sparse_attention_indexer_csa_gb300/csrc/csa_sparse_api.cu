@@ -39,7 +39,7 @@ csa_status check_sparse(const csa_sparse_problem* p) {
   return CSA_OK;
 }
 
-// Map of the rows to gather; false where the strides do not fit one.
+// Rows to gather; false where their numbers pass 32 bits.
 bool gather_rows(const csa_sparse_problem* p, const void* base, long long sp, long long st, long long sh,
                  GatherRows* r) {
   const long long page = p->page > 0 ? p->page : p->Tk, pages = p->page > 0 ? p->Tk / p->page : 1;
@@ -52,17 +52,16 @@ bool gather_rows(const csa_sparse_problem* p, const void* base, long long sp, lo
   if (pages <= 1) sp = 0;
   long long unit = std::gcd(std::gcd(sh, st), sp);
   if (unit == 0) unit = p->D;
-  if (unit % p->D != 0) return false;
+  if (unit >= (1ll << 30)) unit = std::gcd(unit, 1ll << 29);
   const double rows = p->Tk == 0 ? 0.0
                                  : (static_cast<double>(sp) * (pages - 1) + static_cast<double>(st) * (page - 1) +
                                     static_cast<double>(sh) * (p->Hk - 1)) / static_cast<double>(unit) + 1.0;
   if (rows > 2147483000.0) return false;
   r->base = base;
-  r->unit = unit;
+  r->unit_bytes = static_cast<uint32_t>(unit * 2);
   r->rp = static_cast<int>(sp / unit);
   r->rt = static_cast<int>(st / unit);
   r->rh = static_cast<int>(sh / unit);
-  r->n = static_cast<int>(rows);
   return true;
 }
 

@@ -19,14 +19,18 @@
 // above it; fp16 weights are formed 2^kShift times their size, so that they
 // count down to 2^-32 of the reference's.
 //
-// Roles (12 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
-//   warps 0-3   softmax, one thread per row of S
-//   warps 4-7   outputs: join, division, stores, while the next item runs
-//   warp 8      issuer of the products, one thread
-//   warp 9, 10  gathered loads of keys (and queries) and of values: four rows an
-//               instruction, by TMA, so that hidden keys are never read and what
-//               fills up a tile reads as zero
-//   warp 11     lists: the rows of the coming tiles, up to kRing tiles ahead
+// Roles (16 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
+//   warps 0-3    softmax, one thread per row of S
+//   warps 4-7    outputs: join, division, stores, while the next item runs
+//   warps 8-9    loads of the listed keys' rows (and, by TMA, of the queries)
+//   warps 10-11  the same of the values' rows
+//   warps 12-13  issuers of the products with keys and with values, a thread each
+//   warps 14-15  lists: each writes the rows of every second tile, up to kRing tiles
+//                ahead
+// Rows are gathered by cp.async, 16 bytes a lane, into the layout that TMA would
+// write: hidden keys are never read, what fills up a tile is zero.  (Four warps get
+// 91 bytes a ns that way out of L2, four with TMA's gathered loads 41 to 55: those
+// take 40 to 70 cycles each to issue.)
 // Shared memory: two query blocks, two key and two value tiles.  TMEM: S0 S1 O0 O1.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,21 +42,30 @@
 namespace csa {
 namespace {
 
+// As mbar_wait, its slow part out of line: sixteen warps in seven roles run here,
+// and what they wait for is instructions.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+  return mbar_wait_u32(smem_u32(bar), parity, ctl);
+}
+
 template <typename X>
 constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
 constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
 
-constexpr int kRing = 4;      // tiles of rows ahead
-constexpr int kThreads = 384;
-constexpr int kOutWarp = 4, kMmaWarp = 8, kKeyWarp = 9, kValueWarp = 10, kListWarp = 11;
+constexpr int kLists = 2, kRing = 8;  // warps that write lists; tiles of rows ahead
+constexpr int kThreads = 512;
+constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 10, kScoreWarp = 12, kMmaWarp = 13, kListWarp = 14;
 constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
 
-// One tile of an item's keys (n of 1..128), the end of an item (n = 0) or of all (n < 0).
+// 128 slots of an item's list: the rows of those that are keys (-1: none), a bit
+// for each of them, and n: one more than the last of them (0: none).  A hidden or
+// empty slot keeps its place, as lists have few of them but at the end.
 struct TileHead {
-  int n, first, t, hk, z;
+  int n, last, t, hk, z;  // last: the item's last tile; n < 0: no more tiles
 };
 struct Tile {
   int k_row[128], v_row[128];
+  uint32_t keys[4];
   TileHead h;
   int pad[3];
 };
@@ -75,7 +88,7 @@ static_assert(sizeof(Tile) % 16 == 0, "rows are read 16 bytes at a time");
 struct FwdArgs {
   SparseParams p;
   long long items;  // Tq * Hk * n_split
-  long long slots;  // of a row's list
+  int slots, per;   // of a row's list; its tiles (of an item's share)
   int n_split;
   float c;          // scale * log2(e)
   float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
@@ -83,108 +96,125 @@ struct FwdArgs {
   unsigned long long wait_ns;
 };
 
-// Writes the tiles of this CTA's items into the ring.  A warp.
-__device__ __forceinline__ void list_tiles(const FwdArgs& f, Tile* ring, uint64_t* full, uint64_t* free_bar,
+// The tiles of a CTA: items blockIdx.x + n gridDim.x, `per` tiles each.
+__device__ __forceinline__ long long tile_count(const FwdArgs& f) {
+  return (f.items - blockIdx.x + gridDim.x - 1) / gridDim.x * f.per;
+}
+
+// Writes the tiles w, w + kLists, .. of this CTA into the ring.  A warp.
+__device__ __forceinline__ void list_tiles(const FwdArgs& f, int w, Tile* ring, uint64_t* full, uint64_t* free_bar,
                                            const WaitCtl& ctl) {
   const SparseParams& p = f.p;
   const int lane = static_cast<int>(lane_id());
-  uint32_t n_tile = 0;
-  bool ok = true, held = false;
-  auto take = [&] {
-    if (!held) ok = ok && mbar_wait(free_bar + n_tile % kRing, ((n_tile / kRing) & 1u) ^ 1u, ctl);
-    held = true;
-  };
-  auto give = [&](const TileHead& h) {
-    if (lane == 0) ring[n_tile % kRing].h = h;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + n_tile % kRing);
-    ++n_tile;
-    held = false;
-  };
-  if (blockIdx.x == 0)
+  bool bad = false;
+  if (blockIdx.x == 0 && w == 0)
     for (int i = lane; i < p.N; i += 32) sparse_extent(p, i);  // what is out of order or range is recorded
+  const long long tiles = tile_count(f);
+  // the coming tile: its item, its place in the item, its row and the blocks that its slots list
+  long long item = blockIdx.x + static_cast<long long>(w / f.per) * gridDim.x;
+  int at = w % f.per, t = 0, hk = 0, z = 0, b[4];
+  auto blocks = [&] {
+    const long long rest = item / f.n_split;
+    z = static_cast<int>(item - rest * f.n_split);
+    t = static_cast<int>(rest / p.Hk);
+    hk = static_cast<int>(rest - static_cast<long long>(t) * p.Hk);
+    const int32_t* list = p.idx + t * p.idx_st;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = slot_block(p, list, (at * f.n_split + z) * 128 + 32 * i + lane, f.slots);
+  };
   ListRow row{-1, 0, 0, -1};
   int row_t = -1;
-  const long long chunks = (f.slots + 127) / 128;
-  for (long long item = blockIdx.x; ok && item < f.items; item += gridDim.x) {
-    const long long rest = item / f.n_split;
-    const int z = static_cast<int>(item - rest * f.n_split);
-    const int t = static_cast<int>(rest / p.Hk), hk = static_cast<int>(rest - static_cast<long long>(t) * p.Hk);
+  if (w < tiles) blocks();
+  for (long long n = w; n < tiles; n += kLists) {
+    const uint32_t st = static_cast<uint32_t>(n % kRing), turn = static_cast<uint32_t>(n / kRing) & 1u;
     if (t != row_t) row = find_list_row(p, t);
     row_t = t;
-    const int32_t* list = p.idx + t * p.idx_st;
-    const int k0 = hk * p.k.rh, v0 = hk * p.v.rh;
-    int fill = 0, first = 1;
-    if (row.lk > 0 && row.pos >= 0) {
-      int b[4];
-      Slot x[4];
-      auto blocks = [&](long long c) {
+    Slot x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = c < chunks ? slot_block(p, list, c * 128 + 32 * i + lane, f.slots) : -1;
-      };
-      auto keys = [&](long long c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long s = c * 128 + 32 * i + lane;
-          x[i] = s < f.slots ? slot_key(p, row, s, b[i]) : Slot{-1, 0};
-        }
-      };
-      blocks(z);
-      keys(z);
-      blocks(static_cast<long long>(z) + f.n_split);
-      for (long long c = z; ok && c < chunks; c += f.n_split) {
-        Slot now[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) now[i] = x[i];
-        keys(c + f.n_split);
-        blocks(c + 2 * f.n_split);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int kr = 0, vr = 0;
-          const bool see = slot_rows(p, row, now[i], kr, vr);
-          const unsigned all = __ballot_sync(0xffffffffu, see);
-          if (all == 0u) continue;
-          take();
-          if (!ok) break;
-          const int at = fill + __popc(all & ((1u << lane) - 1u));
-          if (see && at < 128) {
-            ring[n_tile % kRing].k_row[at] = kr + k0;
-            ring[n_tile % kRing].v_row[at] = vr + v0;
-          }
-          fill += __popc(all);
-          if (fill < 128) continue;
-          give(TileHead{128, first, t, hk, z});
-          first = 0;
-          fill -= 128;
-          if (fill == 0) continue;
-          take();
-          if (!ok) break;
-          if (see && at >= 128) {
-            ring[n_tile % kRing].k_row[at - 128] = kr + k0;
-            ring[n_tile % kRing].v_row[at - 128] = vr + v0;
-          }
-        }
-      }
-      if (ok && fill > 0) {  // the products take 16 keys at a time
-        const int at = fill + lane;
-        if (at < ((fill + 15) & ~15)) {
-          ring[n_tile % kRing].k_row[at] = p.k.n;
-          ring[n_tile % kRing].v_row[at] = p.v.n;
-        }
-        give(TileHead{fill, first, t, hk, z});
-      }
+    for (int i = 0; i < 4; ++i) {
+      x[i] = Slot{-1, 0};
+      if (row.lk > 0 && row.pos >= 0)
+        x[i] = slot_key(p, row, (at * f.n_split + z) * 128 + 32 * i + lane, f.slots, b[i], bad);
     }
-    take();
-    if (ok) give(TileHead{0, 0, t, hk, z});
+    TileHead h{0, at == f.per - 1, t, hk, z};
+    const int k0 = hk * p.k.rh, v0 = hk * p.v.rh;
+    at += kLists;
+    while (at >= f.per) {
+      at -= f.per;
+      item += gridDim.x;
+    }
+    if (n + kLists < tiles) blocks();
+    if (!bar_wait(free_bar + st, turn ^ 1u, ctl)) break;
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int kr = 0, vr = 0;
+      const bool see = slot_rows(p, row, x[i], kr, vr, bad);
+      const unsigned all = __ballot_sync(0xffffffffu, see);
+      if (all != 0u) h.n = 32 * i + 32 - __clz(static_cast<int>(all));
+      if (lane == i) mine = all;
+      ring[st].k_row[32 * i + lane] = see ? kr + k0 : -1;
+      ring[st].v_row[32 * i + lane] = see ? vr + v0 : -1;
+    }
+    if (lane < 4) ring[st].keys[lane] = mine;
+    if (lane == 0) ring[st].h = h;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full + st);
   }
-  take();
-  if (ok) give(TileHead{-1, 0, 0, 0, 0});
+  if (bad) record_error(kErrDevice);
+}
+
+// 64 rows of a tile (from row r0 on, as far as n of the tile) by a warp.  Whole
+// stretches go without a branch or a size of their own, eight copies in a row: a
+// copy that waits for its registers' former use takes 140 cycles instead of 40.
+template <int D>
+__device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, const int* rows, int r0, int n) {
+  constexpr int P = D / 8, PER = 32 / P;  // 16-byte pieces of a row; rows an instruction takes
+  const int lane = static_cast<int>(lane_id());
+  const int mine[2] = {r0 + lane < n ? rows[r0 + lane] : -1, r0 + 32 + lane < n ? rows[r0 + 32 + lane] : -1};
+  const int piece = lane % P, sub = lane / P;
+  const char* base = static_cast<const char*>(g.base) + piece * 16;
+  const uint32_t dst = smem_u32(tile) + (piece >> 3) * kChunkBytes + (r0 + sub) * 128;
+  uint32_t at[8 / PER];  // the swizzle repeats every eight rows
+#pragma unroll
+  for (int i = 0; i < 8 / PER; ++i) at[i] = dst + (((piece & 7) ^ ((PER * i + sub) & 7)) * 16);
+  if (__all_sync(0xffffffffu, (mine[0] | mine[1]) >= 0)) {
+#pragma unroll 1
+    for (int h = 0; h < 64; h += 8 * PER) {
+      const char* src[8];
+      const int from = h < 32 ? mine[0] : mine[1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = __shfl_sync(0xffffffffu, from, (h + PER * i + sub) & 31);
+        src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * g.unit_bytes;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128), "l"(src[i])
+                     : "memory");
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 64 / PER && r0 + PER * i < n; ++i) {  // n is a multiple of 16
+      const int r = PER * i + sub;
+      const int row = __shfl_sync(0xffffffffu, PER * i < 32 ? mine[0] : mine[1], r & 31);
+      const char* src = base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * g.unit_bytes;
+      const uint32_t to = dst + PER * i * 128 + (((piece & 7) ^ (r & 7)) * 16);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(row < 0 ? 0 : 16) : "memory");
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void loaded() {  // all but the last N groups of rows are there, for the tensor cores too
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+  fence_proxy_async_shared();
+  __syncwarp();
 }
 
 template <typename X, int D, int R, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
-    sparse_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ FwdArgs f) {
+    sparse_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ FwdArgs f) {
   using C = Cfg<D>;
   constexpr int G = 128 / R, CW = 128 / R;  // rows of a copy of the queries; columns that a copy takes
   extern __shared__ __align__(1024) uint8_t base[];
@@ -202,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= C::kBarP && i < C::kBarP + 2) n = 4;
       if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4;
       if (i >= C::kBarOFree && i < C::kBarOFree + 2) n = 4;
-      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 11;
+      if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 14;
+      if (i == C::kBarDone) n = 2;
       if (i == C::kBarMeet) n = 4;
       mbar_init(bars + i, n);
     }
@@ -210,11 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0u;
     fence_mbar_init();
   }
-  if (warp == kKeyWarp && lane == 0) {
-    prefetch_tmap(&tmap_q);
-    prefetch_tmap(&tmap_k);
-    prefetch_tmap(&tmap_v);
-  }
+  if (warp == kKeyWarp && lane == 0) prefetch_tmap(&tmap_q);
   if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -226,149 +254,173 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl ctl{abort_flag, f.wait_ns};
   volatile uint32_t dummy = 0;
   const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
-  // the next tile of the stream; n < 0 after the last one or a wait that gave up
-  uint32_t n_head = 0;
+  // the next tile; n < 0 after the last one or a wait that gave up
+  unsigned long long n_tile = 0;
+  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f));
   auto next_head = [&]() -> TileHead {
-    if (!mbar_wait(bars + C::kBarTile + n_head % kRing, (n_head / kRing) & 1u, ctl)) return TileHead{-1, 0, 0, 0, 0};
-    return ring[n_head % kRing].h;
+    if (n_tile == tiles || !bar_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u, ctl))
+      return TileHead{-1, 0, 0, 0, 0};
+    return ring[n_tile % kRing].h;
   };
-  auto give_head = [&] {  // by one thread of a role's warp
-    mbar_arrive(bars + C::kBarTileFree + n_head % kRing);
+  auto give_head = [&] {  // by a role's warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + n_tile % kRing);
+    ++n_tile;
   };
 
-  if (warp == kListWarp) {
-    list_tiles(f, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
-  } else if (warp == kKeyWarp || warp == kValueWarp) {
-    // ------------------------------------------------------------------------- gathered loads
-    const bool keys = warp == kKeyWarp;
-    const CUtensorMap* map = keys ? &tmap_k : &tmap_v;
+  if (warp >= kListWarp) {
+    const int w = warp - kListWarp;
+    list_tiles(f, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+  } else if (warp >= kKeyWarp && warp < kScoreWarp) {
+    // ------------------------------------------------------------------------- rows of keys, of values
+    const bool keys = warp < kValueWarp;
+    const int r0 = 64 * (warp & 1);
+    const GatherRows& rows = keys ? p.k : p.v;
     uint64_t* full = bars + (keys ? C::kBarK : C::kBarV);
     // a stage is free when the product that read it has completed
     uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv);
-    uint8_t* tiles = base + (keys ? C::kOffK : C::kOffV);
-    const uint64_t q_pol = l2_policy_evict_first(), kv_pol = l2_policy_evict_last();
+    uint8_t* stages = base + (keys ? C::kOffK : C::kOffV);
     uint32_t j = 0, nq = 0;
+    bool flying = false;  // tile j - 1 has been asked for and not been reported
+    bool first = true;    // no tile of this item yet
+    auto report = [&](uint32_t i) {
+      if (lane == 0) mbar_arrive(full + (i & 1u));
+    };
     while (true) {
+      // the next tile is asked for before the one in flight is waited for, unless that would block
+      const bool go = n_tile != tiles && mbar_test_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u) &&
+                      (j < 2 || mbar_test_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u));
+      if (flying && __any_sync(0xffffffffu, !go)) {
+        loaded<0>();
+        report(j - 1);
+        flying = false;
+      }
       const TileHead h = next_head();
       if (h.n < 0) break;
       if (h.n > 0) {
-        if (keys && h.first) {
+        if (warp == kKeyWarp && first) {
           const uint32_t b = nq & 1u;
-          if (!mbar_wait(bars + C::kBarQFree + b, ((nq >> 1) & 1u) ^ 1u, ctl)) break;
+          if (!bar_wait(bars + C::kBarQFree + b, ((nq >> 1) & 1u) ^ 1u, ctl)) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bars + C::kBarQ + b, static_cast<uint32_t>(R * p.g) * 128u * (D / 64));
+            const uint64_t q_pol = l2_policy_evict_first();
             for (int r = 0; r < R; ++r)
               for (int ch = 0; ch < D / 64; ++ch)
                 tma_load_3d_hint(base + C::kOffQ + b * C::kTile + ch * kChunkBytes + r * (G * 128), &tmap_q,
                                  bars + C::kBarQ + b, ch * 64, h.hk * p.g, h.t, q_pol);
           }
+          __syncwarp();
           ++nq;
         }
-        const uint32_t st = j & 1u;
-        if (j >= 2 && !mbar_wait(used + st, ((j >> 1) & 1u) ^ 1u, ctl)) break;
-        const int groups = ((h.n + 15) >> 4) * 4;
-        if (lane == 0) mbar_arrive_expect_tx(full + st, static_cast<uint32_t>(groups) * 512u * (D / 64));
+        if (j >= 2 && !bar_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u, ctl)) break;
         __syncwarp();
-        if (static_cast<int>(lane) < groups) {
-          const Tile& tile = ring[n_head % kRing];
-          const int4 rows = reinterpret_cast<const int4*>(keys ? tile.k_row : tile.v_row)[lane];
-#pragma unroll
-          for (int ch = 0; ch < D / 64; ++ch)
-            tma_gather4(tiles + st * C::kTile + ch * kChunkBytes + lane * 512, map, full + st, ch * 64, rows, kv_pol);
+        const Tile& tile = ring[n_tile % kRing];
+        load_rows<D>(stages + (j & 1u) * C::kTile, rows, keys ? tile.k_row : tile.v_row, r0, (h.n + 15) & ~15);
+        if (flying) {
+          loaded<1>();
+          report(j - 1);
         }
+        flying = true;
+        first = false;
         ++j;
       }
-      __syncwarp();
-      if (lane == 0) give_head();
-      ++n_head;
+      if (h.last) first = true;
+      give_head();
     }
     // no copy is in flight when the CTA ends, a role's giving up included
-    for (uint32_t i = j > 2 ? j - 2 : 0; i < j; ++i) mbar_wait(full + (i & 1u), (i >> 1) & 1u, drain);
-    for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) mbar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------------- issuer of the products
-    // S of a tile goes before the former tile's product with V, so that the
-    // softmax has one while the tensor cores have the other.
+    loaded<0>();
+    if (flying) report(j - 1);
+    for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) bar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
+  } else if (warp == kScoreWarp || warp == kMmaWarp) {
+    // ------------------------------------------------------------------------- issuers of the products
+    // Each warp runs as one (uniform operands), one elected thread issues.  Two
+    // of them, so that neither's waits hold up the other's products: with one for
+    // both, a tile took 2400 cycles of which the tensor cores had work for 1000.
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
-    const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
-    const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffK), 128);
-    const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffV), kChunkBytes, 1024u);
-    constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false), kIdO = idesc_f16<X>(128, D, true), kT = C::kTile >> 4;
-    bool alive = true;
+    constexpr uint32_t kT = C::kTile >> 4;
+    bool alive = true, first = true;
     auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
-    uint32_t j = 0, nq = 0, on = 0;
-    int pend = 0, pend_first = 0;  // keys of the tile whose product with V is to come
-    bool got_o = false;            // this item's O is free
-    auto take_o = [&] {
-      if (!got_o) wait(C::kBarOFree + static_cast<int>(on & 1u), ((on >> 1) & 1u) ^ 1u);
-      got_o = true;
-    };
-    auto values = [&] {
-      const uint32_t i = j - 1, st = i & 1u;
-      take_o();
-      wait(C::kBarP + static_cast<int>(st), (i >> 1) & 1u);
-      wait(C::kBarV + static_cast<int>(st), (i >> 1) & 1u);
-      tc_fence_after();
-      const int steps = (pend + 15) >> 4;
-      if (elect_one()) {
-        if (alive) {
-          for (int ks = 0; ks < steps; ++ks)
-            umma_bf16_tmem_a(tm + 256u + (on & 1u) * 128u, tm + st * 128u + 8u * ks,
-                             vd + static_cast<uint64_t>(st * kT) + static_cast<uint64_t>(128 * ks), kIdO,
-                             (!pend_first || ks != 0) ? 1u : 0u);
-        }
-        umma_commit(bars + C::kBarPv + st);
-      }
-      __syncwarp();
-      pend = 0;
-    };
-    while (alive) {
-      const TileHead h = next_head();
-      const int n = uniform(h.n), first = uniform(h.first);
-      if (n < 0) break;
-      __syncwarp();
-      if (lane == 0) give_head();
-      ++n_head;
-      if (n > 0) {
-        const uint32_t st = j & 1u;
-        if (first) {
-          wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
-          ++nq;
-        }
-        wait(C::kBarK + static_cast<int>(st), (j >> 1) & 1u);
-        tc_fence_after();
-        if (elect_one()) {
-          if (alive) {
-            const uint64_t q = qd + static_cast<uint64_t>(((nq - 1u) & 1u) * kT), k = kd + static_cast<uint64_t>(st * kT);
+    uint32_t j = 0;
+    if (warp == kScoreWarp) {
+      const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);
+      const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffK), 128);
+      constexpr uint32_t kIdS = idesc_f16<X>(128, 128, false);
+      uint32_t nq = 0;
+      while (alive) {
+        const TileHead h = next_head();
+        const int n = uniform(h.n), last = uniform(h.last);
+        if (n < 0) break;
+        give_head();
+        if (n > 0) {
+          const uint32_t st = j & 1u;
+          if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
+          first = false;
+          wait(C::kBarPv + static_cast<int>(st), ((j >> 1) & 1u) ^ 1u);  // P in this S has been used
+          wait(C::kBarK + static_cast<int>(st), (j >> 1) & 1u);
+          tc_fence_after();
+          if (elect_one()) {
+            if (alive) {
+              const uint64_t q = qd + static_cast<uint64_t>((nq & 1u) * kT), k = kd + static_cast<uint64_t>(st * kT);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
-              umma_bf16(tm + st * 128u, q + o, k + o, kIdS, ks != 0 ? 1u : 0u);
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t o = static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4);
+                umma_bf16(tm + st * 128u, q + o, k + o, kIdS, ks != 0 ? 1u : 0u);
+              }
             }
+            umma_commit(bars + C::kBarS + st);
           }
-          umma_commit(bars + C::kBarS + st);
+          __syncwarp();
+          ++j;
         }
-        __syncwarp();
-        if (pend != 0) values();
-        pend = n;
-        pend_first = first;
-        ++j;
-      } else {
-        const bool any = pend != 0;
-        if (any) values();
-        take_o();
-        got_o = false;
-        if (elect_one()) {
-          umma_commit(bars + C::kBarO + (on & 1u));
-          if (any) umma_commit(bars + C::kBarQFree + ((nq - 1u) & 1u));
+        if (last && !first) {
+          if (elect_one()) umma_commit(bars + C::kBarQFree + (nq & 1u));
+          __syncwarp();
+          ++nq;
+          first = true;
         }
-        __syncwarp();
-        ++on;
+      }
+    } else {
+      const uint64_t vd = smem_desc_mn_sw128(smem_u32(base + C::kOffV), kChunkBytes, 1024u);
+      constexpr uint32_t kIdO = idesc_f16<X>(128, D, true);
+      uint32_t on = 0;
+      while (alive) {
+        const TileHead h = next_head();
+        const int n = uniform(h.n), last = uniform(h.last);
+        if (n < 0) break;
+        give_head();
+        if (first && (n > 0 || last)) wait(C::kBarOFree + static_cast<int>(on & 1u), ((on >> 1) & 1u) ^ 1u);
+        if (n > 0) {
+          const uint32_t st = j & 1u;
+          wait(C::kBarV + static_cast<int>(st), (j >> 1) & 1u);
+          wait(C::kBarP + static_cast<int>(st), (j >> 1) & 1u);
+          tc_fence_after();
+          const int steps = (n + 15) >> 4;
+          if (elect_one()) {
+            if (alive) {
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                if (ks < steps)
+                  umma_bf16_tmem_a(tm + 256u + (on & 1u) * 128u, tm + st * 128u + 8u * ks,
+                                   vd + static_cast<uint64_t>(st * kT) + static_cast<uint64_t>(128 * ks), kIdO,
+                                   (!first || ks != 0) ? 1u : 0u);
+            }
+            umma_commit(bars + C::kBarPv + st);
+          }
+          __syncwarp();
+          first = false;
+          ++j;
+        }
+        if (last) {
+          if (elect_one()) umma_commit(bars + C::kBarO + (on & 1u));
+          __syncwarp();
+          ++on;
+          first = true;
+        }
       }
     }
     if (elect_one()) umma_commit(bars + C::kBarDone);
     __syncwarp();
-    mbar_wait(bars + C::kBarDone, 0u, drain);
+    bar_wait(bars + C::kBarDone, 0u, drain);
   } else if (warp < kOutWarp) {
     // ------------------------------------------------------------------------- softmax
     const int row = warp * 32 + static_cast<int>(lane), copy = row / G, col0 = copy * CW;
@@ -378,48 +430,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = f.c;
     uint32_t j = 0, on = 0;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
+    bool ok = true, first = true;
     while (ok) {
       const TileHead h = next_head();
       if (h.n < 0) break;
       if (h.n > 0) {
         const uint32_t st = j & 1u;
-        ok = mbar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl);
+        ok = bar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl);
         if (!ok) break;
         tc_fence_after();
         const uint32_t ts = tmem + lanes + st * 128u;
-        const int lim = h.n - col0;  // columns of this copy that are keys
-        float s[CW == 32 ? 1 : 2][32];
-        auto load = [&](int i, float (&x)[32]) {
-          tmem_ld32_start(ts + col0 + 32 * i, x);
-          tmem_wait32(x);
-          if (32 * (i + 1) > lim) {
+        const uint32_t* keys = ring[n_tile % kRing].keys + copy * (CW / 32);
+        float s[32];
+        auto load = [&](int i) {  // 32 scores, those of no key at -inf
+          tmem_ld32_start(ts + col0 + 32 * i, s);
+          const uint32_t see = keys[i];
+          tmem_wait32(s);
+          if (see != 0xffffffffu) {
 #pragma unroll
             for (int u = 0; u < 32; ++u)
-              if (32 * i + u >= lim) x[u] = -INFINITY;
+              if (((see >> u) & 1u) == 0u) s[u] = -INFINITY;
           }
         };
         // the tile's largest score (NaN is passed over)
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < CW / 32; ++i) {
-          float(&x)[32] = s[CW == 32 ? 0 : i & 1];
-          load(i, x);
-          float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]);
+          load(i);
+          float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
           for (int u = 4; u < 32; u += 4) {
-            a = max3(a, x[u], x[u + 1]);
-            b = max3(b, x[u + 2], x[u + 3]);
+            a = max3(a, s[u], s[u + 1]);
+            b = max3(b, s[u + 2], s[u + 3]);
           }
           top = max3(top, a, b);
         }
         if (!used) top = -INFINITY;  // no query: what stands there asks for nothing
-        if (h.first) {
+        if (first) {
           m = top;
           l = 0.f;
         } else if (__any_sync(0xffffffffu, top * c > m * c + kRaise || (m == -INFINITY && top > m))) {
           // the former tile's product with V has to be through before O is rescaled
-          ok = mbar_wait(bars + C::kBarPv + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl);
+          ok = bar_wait(bars + C::kBarPv + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl);
           if (!ok) break;
           tc_fence_after();
           const float mn = fmaxf(m, top), r = mn == -INFINITY ? 1.f : exp2_approx((m - mn) * c);
@@ -431,14 +483,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float ref = (m == -INFINITY ? 0.f : m) * c, bias = kShift<X> - ref;
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < CW / 32; ++i) {
-          float(&x)[32] = s[CW == 32 ? 0 : i & 1];
-          if (CW == 128) load(i, x);  // P of columns before lies in columns that have been read
+          if (CW > 32) load(i);  // (again; P of the columns before lies in columns that have been read)
           uint32_t pk[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            const float2 e = ffma2(make_float2(x[2 * u], x[2 * u + 1]), make_float2(c, c), make_float2(bias, bias));
+            const float2 e = ffma2(make_float2(s[2 * u], s[2 * u + 1]), make_float2(c, c), make_float2(bias, bias));
             const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
             sum = fadd2(sum, w);
             pk[u] = pack_pair<X>(w.x, w.y);
@@ -456,21 +507,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarP + st);
+        first = false;
         ++j;
-      } else {
-        ok = mbar_wait(bars + C::kBarOFree + (on & 1u), ((on >> 1) & 1u) ^ 1u, ctl);
+      }
+      if (h.last) {
+        ok = bar_wait(bars + C::kBarOFree + (on & 1u), ((on >> 1) & 1u) ^ 1u, ctl);
         float* mine = ml + (on & 1u) * 256;
         mine[row] = m;
         mine[128 + row] = l;
         m = -INFINITY;
         l = 0.f;
+        first = true;
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarMl + (on & 1u));
         ++on;
       }
-      __syncwarp();
-      if (lane == 0) give_head();
-      ++n_head;
+      give_head();
     }
   } else {
     // ------------------------------------------------------------------------- outputs
@@ -479,12 +531,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float* ml = reinterpret_cast<const float*>(base + C::kOffMl);
     const long long rows = static_cast<long long>(p.Tq) * p.Hq;
     uint32_t on = 0, met = 0;
+    auto all_here = [&] {  // a meeting of these four warps, bounded as every wait is
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarMeet);
+      bar_wait(bars + C::kBarMeet, met, ctl);
+      met ^= 1u;
+    };
     while (true) {
       const TileHead h = next_head();
       if (h.n < 0) break;
-      if (h.n == 0) {
+      if (h.last) {
         const uint32_t b = on & 1u;
-        if (!mbar_wait(bars + C::kBarMl + b, (on >> 1) & 1u, ctl) || !mbar_wait(bars + C::kBarO + b, (on >> 1) & 1u, ctl))
+        if (!bar_wait(bars + C::kBarMl + b, (on >> 1) & 1u, ctl) || !bar_wait(bars + C::kBarO + b, (on >> 1) & 1u, ctl))
           break;
         tc_fence_after();
         const float* mm = ml + b * 256;
@@ -516,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 weight == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
                               : make_float4(o[4 * u] * weight, o[4 * u + 1] * weight, o[4 * u + 2] * weight,
                                             o[4 * u + 3] * weight);
-          meet(bars + C::kBarMeet, met, ctl);
+          all_here();
           for (int i = tid; i < p.g * 8; i += 128) {
             const int hd = i >> 3, col = (i & 7) * 4;
             float4 v = *reinterpret_cast<const float4*>(stage + hd * kPitch + col);
@@ -535,16 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint2*>(static_cast<X*>(p.out) + e) =
                   make_uint2(pack_pair<X>(v.x, v.y), pack_pair<X>(v.z, v.w));
           }
-          meet(bars + C::kBarMeet, met, ctl);
+          all_here();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarOFree + b);
         ++on;
       }
-      __syncwarp();
-      if (lane == 0) give_head();
-      ++n_head;
+      give_head();
     }
   }
   __syncwarp();
@@ -555,31 +611,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename X, int D, int R, bool SPLIT>
-cudaError_t start(const FwdArgs& f, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                  cudaStream_t stream) {
+cudaError_t start(const FwdArgs& f, const CUtensorMap& tq, cudaStream_t stream) {
   constexpr auto kernel = sparse_fwd_kernel<X, D, R, SPLIT>;
   const cudaError_t e = smem_limit_once<kernel>(Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(std::min(f.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, tk, tv, f);
+  kernel<<<static_cast<unsigned>(std::min(f.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
   return cudaGetLastError();
 }
 
 template <typename X, int D, int R>
 cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t stream) {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq;
   FwdArgs f;
   f.p = p;
-  f.slots = sparse_slots(p);
+  f.slots = static_cast<int>(sparse_slots(p));
   f.n_split = sparse_splits(p.Tq, p.Hk, f.slots);
   f.items = static_cast<long long>(p.Tq) * p.Hk * f.n_split;
+  f.per = std::max(1, ((f.slots + 127) / 128 + f.n_split - 1) / f.n_split);
   f.c = p.scale * 1.4426950408889634f;
   f.part_o = static_cast<float*>(workspace);
   f.part_lse = f.part_o + static_cast<long long>(f.n_split) * p.Tq * p.Hq * D;
   f.wait_ns = attn_wait_ns(f.slots / 128 + 1);
-  if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, p.g) || !make_gather_map(&tk, p, p.k) || !make_gather_map(&tv, p, p.v))
-    return cudaErrorInvalidValue;
-  if (f.n_split == 1) return start<X, D, R, false>(f, tq, tk, tv, stream);
-  cudaError_t e = start<X, D, R, true>(f, tq, tk, tv, stream);
+  if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, p.g)) return cudaErrorInvalidValue;
+  if (f.n_split == 1) return start<X, D, R, false>(f, tq, stream);
+  cudaError_t e = start<X, D, R, true>(f, tq, stream);
   if (e != cudaSuccess) return e;
   AttnParams a;
   std::memset(&a, 0, sizeof(a));

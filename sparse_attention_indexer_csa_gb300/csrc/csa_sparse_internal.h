@@ -10,14 +10,13 @@
 namespace csa {
 
 // ----------------------------------------------------------------- attention over listed blocks
-// Keys and values are gathered row by row from 2-D maps: row j of key head h is
-// row (page * rp +) j * rt + h * rh of the map, whose rows are `unit` elements
-// apart (the strides' greatest common divisor).
+// Rows of keys or of values: row j of key head h starts at
+// (page * rp +) j * rt + h * rh units, a unit being the strides' greatest common
+// divisor, so that a row's number fits 32 bits in a long cache.
 struct GatherRows {
   const void* base;
-  long long unit;   // elements between two rows of the map
-  int rp, rt, rh;   // rows of the map between pages, tokens, heads
-  int n;            // rows of the map; the row after the last reads as zero
+  uint32_t unit_bytes;
+  int rp, rt, rh;  // units between pages, tokens, heads
 };
 struct SparseParams {
   int N, Tq, Tk, Hq, Hk, g, D;  // g = Hq / Hk

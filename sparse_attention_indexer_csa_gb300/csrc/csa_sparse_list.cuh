@@ -1,5 +1,5 @@
 // csa_sparse_list.cuh -- what the kernels of attention over listed blocks share:
-// the keys that a row lists, gathered TMA loads and their maps.
+// the keys that a row lists, and the maps of its queries.
 #pragma once
 
 #include "csa_attn_tiles.cuh"
@@ -19,29 +19,6 @@ inline bool make_heads_map(CUtensorMap* m, const SparseParams& p, const void* x,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Rows to gather: box {64, 1}; rows past the last read as zero.  Without any key
-// the map describes a row of q that nothing loads.
-inline bool make_gather_map(CUtensorMap* m, const SparseParams& p, const GatherRows& r) {
-  auto fn = attn_encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)p.D, (cuuint64_t)(r.n > 0 ? r.n : 1)};
-  cuuint64_t strides[1] = {(cuuint64_t)r.unit * 2};
-  cuuint32_t box[2] = {64, 1}, estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(r.n > 0 ? r.base : p.q), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// ----------------------------------------------------------------- loads
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, const int4& rows,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
-      "[%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
-      "l"(m), "r"(c0), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
 // ----------------------------------------------------------------- lists
 // The sequence of a query row: keys k0 .. k0+lk-1 (counted from 0 in a paged
 // cache), the row's position, the sequence's number (-1: none, lk = 0).
@@ -77,26 +54,31 @@ __device__ __forceinline__ SeqExt sparse_extent(const SparseParams& p, int i) {
   return s;
 }
 
-// The row's sequence, by a warp (32 probes at a time): the largest i with
-// cu_q[i] <= t.  Entries out of order give some sequence or none.
+// The row's sequence, by a warp: the largest i with cu_q[i] <= t.  Sequences of
+// equal lengths (one token each, when decoding) are met at the first look, others
+// by 32 probes at a time.  Entries out of order give some sequence or none.
 __device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
   const int lane = static_cast<int>(lane_id());
   ListRow r{-1, 0, 0, -1};
-  int lo = 0, hi = p.N;
   if (p.N <= 0) return r;
-  while (lo < hi) {
-    const int span = hi - lo, stride = (span + 31) / 32;
-    const int i = lo + min(span, (lane + 1) * stride);
-    const unsigned out = __ballot_sync(0xffffffffu, p.cu_q[i] > t);
-    if (out == 0u) {
-      lo = hi;
-    } else {
-      const int n = __ffs(static_cast<int>(out)) - 1;
-      hi = lo + min(span, (n + 1) * stride) - 1;
-      lo = lo + min(span, n * stride);
+  int lo = static_cast<int>(static_cast<long long>(t) * p.N / p.Tq);
+  if (t < p.cu_q[lo] || t >= p.cu_q[lo + 1]) {
+    lo = 0;
+    int hi = p.N;
+    while (lo < hi) {
+      const int span = hi - lo, stride = (span + 31) / 32;
+      const int i = lo + min(span, (lane + 1) * stride);
+      const unsigned out = __ballot_sync(0xffffffffu, p.cu_q[i] > t);
+      if (out == 0u) {
+        lo = hi;
+      } else {
+        const int n = __ffs(static_cast<int>(out)) - 1;
+        hi = lo + min(span, (n + 1) * stride) - 1;
+        lo = lo + min(span, n * stride);
+      }
     }
+    if (lo >= p.N) return r;
   }
-  if (lo >= p.N) return r;
   const SeqExt s = sparse_extent(p, lo);
   if (t < s.q0 || t >= s.q1) return r;
   r.seq = lo;
@@ -107,39 +89,37 @@ __device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
 }
 
 // The slots of a row's list: first the window, newest key first, then top_k
-// blocks.  Slot s of the row in three steps, so that the loads of the coming
-// slots are in flight while the present ones are dealt with.
+// blocks.  A slot in three steps, so that the loads of the coming slots are in
+// flight while the present ones are dealt with.  `bad` gathers what is out of range.
 struct Slot {
   int j;     // key of the sequence; -1: none
   int page;  // its page (paged keys)
 };
-__device__ __forceinline__ int slot_block(const SparseParams& p, const int32_t* list, long long s, long long slots) {
+__device__ __forceinline__ int slot_block(const SparseParams& p, const int32_t* list, int s, int slots) {
   return s >= p.window && s < slots ? list[(s - p.window) >> p.block_shift] : -1;
 }
-__device__ __forceinline__ Slot slot_key(const SparseParams& p, const ListRow& r, long long s, int b) {
+__device__ __forceinline__ Slot slot_key(const SparseParams& p, const ListRow& r, int s, int slots, int b, bool& bad) {
   Slot x{-1, 0};
   if (s < p.window) {
-    if (s <= r.pos) x.j = r.pos - static_cast<int>(s);
-  } else if (b >= 0) {
-    const long long j = (static_cast<long long>(b) << p.block_shift) + ((s - p.window) & ((1 << p.block_shift) - 1));
-    const long long first = static_cast<long long>(b) << p.block_shift;
-    if (first >= r.lk) {
-      if (r.seq >= 0) record_error(kErrDevice);
-    } else if (j < r.lk && j <= static_cast<long long>(r.pos) - p.window) {
-      x.j = static_cast<int>(j);
+    x.j = r.pos - s;  // negative: before the first key
+  } else if (s < slots) {
+    if (static_cast<unsigned>(b) <= static_cast<unsigned>((r.lk - 1) >> p.block_shift)) {
+      const int j = (b << p.block_shift) + ((s - p.window) & ((1 << p.block_shift) - 1));
+      if (j < r.lk && j <= r.pos - p.window) x.j = j;
+    } else {
+      bad |= b != -1;
     }
-  } else if (b < -1 && r.seq >= 0) {
-    record_error(kErrDevice);
   }
-  if (x.j >= 0 && p.page > 0) x.page = p.table[r.seq * p.table_st + x.j / p.page];
+  if (p.page > 0 && x.j >= 0) x.page = p.table[r.seq * p.table_st + x.j / p.page];
   return x;
 }
-// Rows of the maps of slot x (key head 0), or none: j < 0.
-__device__ __forceinline__ bool slot_rows(const SparseParams& p, const ListRow& r, const Slot& x, int& kr, int& vr) {
+// Rows of keys and values of slot x (key head 0); false: it has none.
+__device__ __forceinline__ bool slot_rows(const SparseParams& p, const ListRow& r, const Slot& x, int& kr, int& vr,
+                                          bool& bad) {
   if (x.j < 0) return false;
   if (p.page > 0) {
-    if (x.page < 0 || x.page >= p.pages) {
-      record_error(kErrDevice);
+    if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.pages)) {
+      bad = true;
       return false;
     }
     const int off = x.j % p.page;
