@@ -93,7 +93,7 @@ csa_status csa_sparse_attn_forward(const csa_sparse_problem* p, const void* q, c
  * block that a row lists twice reaches dk and dv twice, as it does out.  The sums
  * are taken in a fixed order (the same bits on every call).  Needs `workspace`:
  * csa_sparse_attn_workspace_size(p, 1) bytes, 16-byte aligned: each row's share of
- * dk and dv for each key it lists, as many rows at a time as 2 GiB hold.       */
+ * dk and dv for each key it lists, as many rows at a time as 4 GiB hold.       */
 csa_status csa_sparse_attn_backward(const csa_sparse_problem* p, const void* dout, const void* q, const void* k,
                                     const void* v, const void* out, const float* lse, const int32_t* idx,
                                     const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* dq,

@@ -25,7 +25,8 @@ def attention(q, k, v, idx, cu_q, cu_k, scale, block=1, window=0, causal=True, k
     """Forward, and with dout the gradients, of q [Tq,Hq,D], k, v [Tk,Hk,D], idx [Tq,top_k].
 
     Returns results and magnitudes under the names of attn_oracle.attention; "bound" [Tq,Hq] is
-    2 scale |dout| max|v| (2-norms, v over the sequence), which |dout.v - dout.out| scale does not exceed.
+    2 scale max|dout| max|v| (2-norms, dout over the heads of a key head, v over the sequence), which
+    |dout.v - dout.out| scale does not exceed.
     """
     Tq, Hq, D = q.shape
     Hk = k.shape[1]
@@ -62,7 +63,8 @@ def attention(q, k, v, idx, cu_q, cu_k, scale, block=1, window=0, causal=True, k
             if dout is None:
                 continue
             G = dout[a:b, h]
-            res["bound"][a:b, h] = 2 * scale * np.linalg.norm(G, axis=1) * np.linalg.norm(V, axis=1).max()
+            most = np.linalg.norm(dout[a:b, j * g:(j + 1) * g], axis=2).max(1)
+            res["bound"][a:b, h] = 2 * scale * most * np.linalg.norm(V, axis=1).max()
             dp = G @ V.T
             ds = p * (dp - (G * o).sum(1, keepdims=True))
             dmag = np.abs(ds) + p * ((np.abs(G) * np.abs(o)).sum(1, keepdims=True) + np.abs(G) @ np.abs(V).T)

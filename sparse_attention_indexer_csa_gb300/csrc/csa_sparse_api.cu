@@ -74,7 +74,7 @@ bool sparse_supported(const csa_sparse_problem* p) {
   if (!gather_rows(p, nullptr, p->k_stride_p, p->k_stride_t, p->k_stride_h, &r)) return false;
   if (!gather_rows(p, nullptr, p->v_stride_p, p->v_stride_t, p->v_stride_h, &r)) return false;
   const double rows = std::max(static_cast<double>(p->Tq) * p->Hq, static_cast<double>(p->Tk) * p->Hk);
-  return rows < 8.0e9 && p->N < (1 << 30);
+  return rows < 8.0e9 && p->N < (1 << 30) && static_cast<long long>(p->Tk) / p->block + p->N < 0x7FFFFFF0ll;
 }
 
 SparseParams sparse_params(const csa_sparse_problem* p, const void* q, const void* k, const void* v,

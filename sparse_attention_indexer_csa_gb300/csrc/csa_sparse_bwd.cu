@@ -1,6 +1,985 @@
+// csa_sparse_bwd.cu -- gradients of attention over listed blocks of keys.
+//
+//   delta = dout.out (per row and head),  p_j = exp(s_j - lse),
+//   ds_j = p_j (dout.v_j - delta),  dq = scale sum_j ds_j k_j,
+//   dk_j = scale sum_rows ds_j q,  dv_j = sum_rows p_j dout.
+//
+// The rows that list a key are not its neighbours, and each contributes a matrix
+// product with its g heads to dk and dv.  So the work goes by rows, and every
+// row's share of dk and dv for each slot of its list goes to memory, where a
+// second kernel adds up the shares of a key in the order of the rows: no
+// atomics on values, the same bits on every call.
+//
+//   sparse_rows_kernel  an item is a row, a key head and up to 64 of its query
+//     heads; its listed keys, 128 at a time, are the rows of the products:
+//       S^T = K Q^T, dP^T = V dO^T         (operands in shared memory)
+//       P^T, dS^T in the storage type over S^T, dP^T in TMEM, dS^T to shared memory
+//       dV = P^T dO, dK = dS^T Q           (A in TMEM, B read MN-major): the shares
+//       dQ += dS K                         (A and B read MN-major)
+//     so that a group of any size costs no more than its heads.
+//   lists (sparse_count, _scan, _start, _fill)  for each block the rows that
+//     list it, in ascending order: a counting sort, the counts kept by groups of
+//     rows so that the place of each entry does not depend on timing.
+//   sparse_sum_kernel  a block of threads per key and key head adds the shares.
+//
+// Bytes: a share of dk and one of dv, D values each, per listed key, written once
+// and read once: in bf16 rounded to it (as ds and p are before), in fp16 fp32.
+// As many rows at a time as kShareBytes hold.
+//
+// fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
+// 2^15 (|dout| over the item's heads, |v| over the finite values of the sequence), and
+// P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include "csa_sparse_list.cuh"
+
 namespace csa {
-cudaError_t launch_sparse_backward(const SparseParams& p, int dtype, void* workspace, cudaStream_t stream) { return cudaErrorNotSupported; }
-size_t sparse_backward_workspace(const SparseParams& p, int dtype) { return 256; }
-cudaError_t take_status_sparse_bwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
+namespace {
+
+constexpr size_t kShareBytes = 4ull << 30;
+constexpr int kHeads = 64;  // query heads of an item at most
+constexpr int kThreads = 512;
+constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14;
+
+template <typename X>
+constexpr int kProbExp = is_bf16<X>() ? 0 : 15;  // power of two of P^T
+
+// What the shares are kept in.
+template <typename X>
+struct ShareType {
+  using T = X;
+};
+template <>
+struct ShareType<__half> {
+  using T = float;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kTile = kChunkBytes * (D / 64);           // 128 rows x D
+  static constexpr uint32_t kHeadChunk = kHeads * 128, kHeadTile = kHeadChunk * (D / 64);
+  static constexpr uint32_t kOffK = 0, kOffV = 2 * kTile, kOffDs = 4 * kTile;  // dS^T: 128 keys x 64 heads
+  // (the product that reads dS has 128 rows: what stands behind its 64 heads is read too and not used)
+  static constexpr uint32_t kOffQ = kOffDs + kChunkBytes, kOffDo = kOffQ + 2 * kHeadTile;
+  static constexpr uint32_t kOffRing = kOffDo + 2 * kHeadTile;
+  static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta; [2] power of two
+  static constexpr uint32_t kOffBar = kOffStat + 2 * kHeads * 8 + 16;
+  static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
+                       kBarKFree = 14, kBarP = 16, kBarD = 17, kBarDFree = 18, kBarDq = 19, kBarDqFree = 20,
+                       kBarTile = 21, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
+                       kBars = kBarDone + 1;
+  static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
+};
+static_assert(Cfg<128>::kSmem <= 227 * 1024, "one CTA per SM");
+static_assert(Cfg<64>::kOffRing >= Cfg<64>::kOffDs + 2 * kChunkBytes, "the second half of dS' product stays in bounds");
+static_assert(Cfg<64>::kOffStat % 16 == 0 && Cfg<128>::kOffStat % 16 == 0, "statistics are read 16 bytes at a time");
+
+struct RowsArgs {
+  SparseParams p;
+  ListArgs l;      // n_z: groups of heads of a key head
+  int heads, padded;  // of an item; the same rounded up to 16
+  int s_pad;       // slots of a row's list, rounded up to 128
+  float c;         // scale * log2(e)
+  const float *delta, *norm2;
+  const uint32_t* range;
+  void* share;     // [rows][Hk][n_z][2][s_pad][D]
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// 2 |dout| |v| < 2^E for the squares of the two norms.
+__device__ __forceinline__ int ds_exponent(float dout2, float v2) {
+  const int e = static_cast<int>((__float_as_uint(2.f * sqrtf(dout2) * sqrtf(v2)) >> 23) & 255u) - 126;
+  return min(max(e, -60), 60);
 }
+
+// Sixteen columns of this warp's lanes, requested; and eight written.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 32 columns of a warp's 32 rows, times f, stored as T: lanes 4 i .. 4 i + 3
+// exchange 16-byte pieces, so that four lanes store 64 bytes of one row.  Row r
+// goes to dst + r * D where bit r of `rows` is set.
+template <typename T, int D>
+__device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* dst, uint32_t rows) {
+  const uint32_t lane = lane_id();
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
+    uint4 q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (sizeof(T) == 4) {
+        const float* x = o + 16 * h + 4 * u;
+        q[u] = make_uint4(__float_as_uint(x[0] * f), __float_as_uint(x[1] * f), __float_as_uint(x[2] * f),
+                          __float_as_uint(x[3] * f));
+      } else {
+        const float* x = o + 8 * u;
+        q[u] = make_uint4(pack_pair<T>(x[0] * f, x[1] * f), pack_pair<T>(x[2] * f, x[3] * f),
+                          pack_pair<T>(x[4] * f, x[5] * f), pack_pair<T>(x[6] * f, x[7] * f));
+      }
+    }
+    transpose4(q, lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t r = (lane & ~3u) + u;
+      if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 16 * h)[lane & 3u] = q[u];
+    }
+  }
+}
+
+template <typename X, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    sparse_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
+                       const __grid_constant__ RowsArgs f) {
+  using C = Cfg<D>;
+  using T = typename ShareType<X>::T;
+  extern __shared__ __align__(1024) uint8_t base[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
+  Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
+  float2* stat = reinterpret_cast<float2*>(base + C::kOffStat);
+  int* fits = reinterpret_cast<int*>(base + C::kOffStat + 2 * kHeads * 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
+  const SparseParams& p = f.p;
+  const int warp = threadIdx.x / 32;
+  const uint32_t lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kBars; ++i) {
+      int n = 1;
+      if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
+      if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 8;
+      if (i == C::kBarP || i == C::kBarDFree || i == C::kBarDqFree) n = 4;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 14;
+      mbar_init(bars + i, n);
+    }
+    if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  // rows of no head: the products over heads read them, and the loads leave them as they are
+  for (uint32_t i = threadIdx.x; i < 4 * C::kHeadTile / 16; i += kThreads)
+    reinterpret_cast<uint4*>(base + C::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_shared();
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kColS = 0, kColDp = 64, kColDv = 128, kColDk = 256, kColDq = 384;
+  const WaitCtl ctl{abort_flag, f.wait_ns};
+  volatile uint32_t dummy = 0;
+  const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
+  unsigned long long n_tile = 0;
+  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f.l));
+  auto next_head = [&]() -> TileHead {
+    if (n_tile == tiles || !bar_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u, ctl))
+      return TileHead{-1, 0, 0, 0, 0, 0, 0};
+    return ring[n_tile % kRing].h;
+  };
+  auto give_head = [&] {  // by a role's warp
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + n_tile % kRing);
+    ++n_tile;
+  };
+
+  if (warp >= kListWarp) {
+    list_tiles(p, f.l, warp - kListWarp, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+  } else if (warp == kItemWarp) {
+    // ------------------------------------------------------------------------- an item's queries, cotangents, statistics
+    uint32_t ni = 0;
+    bool first = true;
+    while (true) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0 && first) {
+        const uint32_t b = ni & 1u, turn = ((ni >> 1) & 1u) ^ 1u;
+        if (!bar_wait(bars + C::kBarQFree + b, turn, ctl)) break;
+        const int head = h.hk * p.g + h.z * f.heads;
+        if (lane == 0) {
+          const uint64_t pol = l2_policy_evict_first();
+          mbar_arrive_expect_tx(bars + C::kBarQ + b, static_cast<uint32_t>(f.heads) * 256u * (D / 64));
+          for (int ch = 0; ch < D / 64; ++ch) {
+            tma_load_3d_hint(base + C::kOffQ + b * C::kHeadTile + ch * C::kHeadChunk, &tmap_q, bars + C::kBarQ + b, ch * 64,
+                             head, h.t, pol);
+            tma_load_3d_hint(base + C::kOffDo + b * C::kHeadTile + ch * C::kHeadChunk, &tmap_do, bars + C::kBarQ + b,
+                             ch * 64, head, h.t, pol);
+          }
+        }
+        __syncwarp();
+        ++ni;
+        if (!bar_wait(bars + C::kBarStatFree + b, turn, ctl)) break;
+        const long long at = static_cast<long long>(h.t) * p.Hq + head;
+        float top = 0.f;
+        for (int i = static_cast<int>(lane); i < f.padded; i += 32) {
+          float2 s = make_float2(INFINITY, 0.f);  // no head, or a row without a weight: P = 0
+          if (i < f.heads) {
+            const float l = p.lse[at + i];
+            if (l != -INFINITY) s = make_float2(l * 1.4426950408889634f, f.delta[at + i]);
+            if constexpr (!is_bf16<X>()) top = fmaxf(top, f.norm2[at + i]);
+          }
+          stat[b * kHeads + i] = s;
+        }
+        if constexpr (!is_bf16<X>()) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0)
+            fits[b] = 15 - ds_exponent(top, __uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
+        first = false;
+      }
+      if (h.last) first = true;
+      give_head();
+    }
+    for (uint32_t i = ni > 2 ? ni - 2 : 0; i < ni; ++i) bar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
+  } else if (warp >= kKeyWarp && warp < kMmaWarp) {
+    // ------------------------------------------------------------------------- rows of keys, of values
+    const bool keys = warp < kValueWarp;
+    const int r0 = 64 * (warp & 1);
+    const GatherRows& rows = keys ? p.k : p.v;
+    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV);
+    uint64_t* used = bars + (keys ? C::kBarKFree : C::kBarS);  // a stage is free when the last product that reads it is through
+    uint8_t* stages = base + (keys ? C::kOffK : C::kOffV);
+    uint32_t j = 0;
+    bool flying = false;  // tile j - 1 has been asked for and not been reported
+    auto report = [&](uint32_t i) {
+      if (lane == 0) mbar_arrive(full + (i & 1u));
+    };
+    while (true) {
+      const bool go = n_tile != tiles && mbar_test_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u) &&
+                      (j < 2 || mbar_test_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u));
+      if (flying && __any_sync(0xffffffffu, !go)) {
+        loaded<0>();
+        report(j - 1);
+        flying = false;
+      }
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0) {
+        if (j >= 2 && !bar_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u, ctl)) break;
+        __syncwarp();
+        const Tile& tile = ring[n_tile % kRing];
+        load_rows<D>(stages + (j & 1u) * C::kTile, rows, keys ? tile.k_row : tile.v_row, r0, (h.n + 15) & ~15);
+        if (flying) {
+          loaded<1>();
+          report(j - 1);
+        }
+        flying = true;
+        ++j;
+      }
+      give_head();
+    }
+    loaded<0>();  // no copy is in flight when the CTA ends, a role's giving up included
+    if (flying) report(j - 1);
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------------- issuer of the products
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128), dod = smem_desc_kmajor(smem_u32(base + C::kOffDo), 128);
+    const uint64_t qn = smem_desc_mn_sw128(smem_u32(base + C::kOffQ), C::kHeadChunk, 1024u);
+    const uint64_t don = smem_desc_mn_sw128(smem_u32(base + C::kOffDo), C::kHeadChunk, 1024u);
+    const uint64_t kd = smem_desc_kmajor(smem_u32(base + C::kOffK), 128), vd = smem_desc_kmajor(smem_u32(base + C::kOffV), 128);
+    const uint64_t kn = smem_desc_mn_sw128(smem_u32(base + C::kOffK), kChunkBytes, 1024u);
+    const uint64_t ds = smem_desc_mn_sw128(smem_u32(base + C::kOffDs), kChunkBytes, 1024u);
+    const uint32_t id_s = idesc_f16<X>(128, f.padded, false);
+    constexpr uint32_t kIdD = idesc_f16<X>(128, D, true), kIdDq = idesc_f16<X>(128, D, true) | (1u << 15);  // A MN-major too
+    constexpr uint32_t kT = C::kTile >> 4, kH = C::kHeadTile >> 4;
+    const int head_steps = uniform(f.padded >> 4);
+    bool alive = true, first = true, got_dq = false, pend_first = false;
+    int pend = 0;  // the last key of the tile whose P and dS are to come
+    uint32_t j = 0, nq = 0, on = 0;
+    auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
+    auto shares = [&] {  // dV, dK of the last tile
+      const uint32_t i = j - 1;
+      wait(C::kBarP, i & 1u);
+      wait(C::kBarDFree, (i & 1u) ^ 1u);
+      tc_fence_after();
+      if (elect_one()) {
+        if (alive) {
+          const uint64_t o = static_cast<uint64_t>((nq & 1u) * kH);
+          for (int ks = 0; ks < head_steps; ++ks)
+            umma_bf16_tmem_a(tm + kColDv, tm + kColS + 8u * ks, don + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
+          for (int ks = 0; ks < head_steps; ++ks)
+            umma_bf16_tmem_a(tm + kColDk, tm + kColDp + 8u * ks, qn + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
+        }
+        umma_commit(bars + C::kBarD);
+      }
+      __syncwarp();
+    };
+    auto take_dq = [&] {
+      if (!got_dq) wait(C::kBarDqFree, (on & 1u) ^ 1u);
+      got_dq = true;
+    };
+    auto query = [&] {  // dQ += dS K of the last tile
+      const uint32_t st = (j - 1) & 1u;
+      take_dq();
+      tc_fence_after();
+      const int steps = (pend + 15) >> 4;
+      if (elect_one()) {
+        if (alive)
+          for (int ks = 0; ks < steps; ++ks)
+            umma_bf16(tm + kColDq, ds + static_cast<uint64_t>(128 * ks), kn + static_cast<uint64_t>(st * kT + 128 * ks), kIdDq,
+                      (!pend_first || ks != 0) ? 1u : 0u);
+        umma_commit(bars + C::kBarKFree + st);
+      }
+      __syncwarp();
+      pend = 0;
+    };
+    while (alive) {
+      const TileHead h = next_head();
+      const int n = uniform(h.n), last = uniform(h.last);
+      if (n < 0) break;
+      give_head();
+      if (n > 0) {
+        const uint32_t st = j & 1u, par = (j >> 1) & 1u;
+        if (pend != 0) {
+          shares();
+          // the next scores go first, unless they would have to wait for their tile
+          if (!mbar_look_warp(bars + C::kBarK + st, par) || !mbar_look_warp(bars + C::kBarV + st, par)) query();
+        }
+        if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
+        wait(C::kBarK + static_cast<int>(st), par);
+        wait(C::kBarV + static_cast<int>(st), par);
+        tc_fence_after();
+        if (elect_one()) {
+          if (alive) {
+            const uint64_t q = static_cast<uint64_t>((nq & 1u) * kH), t = static_cast<uint64_t>(st * kT);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_bf16(tm + kColS, kd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
+                        qd + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              umma_bf16(tm + kColDp, vd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
+                        dod + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
+          }
+          umma_commit(bars + C::kBarS + st);
+        }
+        __syncwarp();
+        if (pend != 0) query();
+        pend = n;
+        pend_first = first;
+        first = false;
+        ++j;
+      }
+      if (last) {
+        if (pend != 0) {
+          shares();
+          query();
+        }
+        take_dq();
+        got_dq = false;
+        if (elect_one()) {
+          umma_commit(bars + C::kBarDq);
+          if (!first) umma_commit(bars + C::kBarQFree + (nq & 1u));
+        }
+        __syncwarp();
+        if (!first) ++nq;
+        ++on;
+        first = true;
+      }
+    }
+    if (elect_one()) umma_commit(bars + C::kBarDone);
+    __syncwarp();
+    bar_wait(bars + C::kBarDone, 0u, drain);
+  } else if (warp < kDrainWarp) {
+    // ------------------------------------------------------------------------- P and dS: a thread per key
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int key = warp * 32 + static_cast<int>(lane);
+    uint8_t* row = base + C::kOffDs + key * 128;
+    const float2 c2 = make_float2(f.c, f.c);
+    uint32_t j = 0, ni = 0;
+    bool first = true;
+    float fit = 1.f;  // power of two of dS over that of P
+    while (true) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0) {
+        const uint32_t st = j & 1u;
+        if (first) {
+          if (!bar_wait(bars + C::kBarStat + (ni & 1u), (ni >> 1) & 1u, ctl)) break;
+          if constexpr (!is_bf16<X>()) fit = power_of_two(fits[ni & 1u] - kProbExp<X>);
+        }
+        first = false;
+        if (!bar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl)) break;
+        // the former tile's product with K has read dS
+        if (j > 0 && !bar_wait(bars + C::kBarKFree + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl)) break;
+        tc_fence_after();
+        const bool see = (ring[n_tile % kRing].keys[warp] >> lane) & 1u;
+        const float4* ls = reinterpret_cast<const float4*>(stat + (ni & 1u) * kHeads);
+#pragma unroll 1
+        for (int i = 0; i < f.padded / 16; ++i) {
+          float s[16], dp[16];
+          tmem_ld16_start(tmem + lanes + kColS + 16 * i, s);
+          tmem_ld16_start(tmem + lanes + kColDp + 16 * i, dp);
+          tmem_wait16(s);
+          tmem_wait16(dp);
+          uint32_t pw[8], dw[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float4 x = ls[8 * i + u];  // lse, delta of two heads
+            const float2 e = ffma2(make_float2(s[2 * u], s[2 * u + 1]), c2,
+                                   make_float2(static_cast<float>(kProbExp<X>) - x.x, static_cast<float>(kProbExp<X>) - x.z));
+            const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
+            float2 d = fmul2(w, fadd2(make_float2(dp[2 * u], dp[2 * u + 1]), make_float2(-x.y, -x.w)));
+            if constexpr (!is_bf16<X>()) d = fmul2(d, make_float2(fit, fit));
+            pw[u] = see ? pack_pair<X>(w.x, w.y) : 0u;
+            dw[u] = see ? pack_pair<X>(d.x, d.y) : 0u;
+          }
+          tmem_st8(tmem + lanes + kColS + 8 * i, pw);
+          tmem_st8(tmem + lanes + kColDp + 8 * i, dw);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint4*>(row + (((2 * i + u) ^ (key & 7)) * 16)) =
+                make_uint4(dw[4 * u], dw[4 * u + 1], dw[4 * u + 2], dw[4 * u + 3]);
+        }
+        tmem_wait_st();
+        fence_proxy_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarP);
+        ++j;
+      }
+      if (h.last && !first) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarStatFree + (ni & 1u));
+        ++ni;
+        first = true;
+      }
+      give_head();
+    }
+  } else {
+    // ------------------------------------------------------------------------- shares of dk and dv; dq
+    const int w = warp - kDrainWarp;
+    const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+    uint32_t j = 0, ni = 0, on = 0;
+    bool first = true;
+    float back_v = 1.f, back = p.scale;  // what undoes the powers of two
+    while (true) {
+      const TileHead h = next_head();
+      if (h.n < 0) break;
+      if (h.n > 0) {
+        if (first) {
+          if (!bar_wait(bars + C::kBarStat + (ni & 1u), (ni >> 1) & 1u, ctl)) break;
+          if constexpr (!is_bf16<X>()) {
+            back_v = power_of_two(-kProbExp<X>);
+            back = p.scale * power_of_two(-fits[ni & 1u]);
+          }
+        }
+        first = false;
+        const uint32_t see = ring[n_tile % kRing].keys[w];
+        if (!bar_wait(bars + C::kBarD, j & 1u, ctl)) break;
+        tc_fence_after();
+        const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
+        T* dst = static_cast<T*>(f.share) + (item * 2 * f.s_pad + h.c * 128 + w * 32) * D;
+        if (see != 0u) {
+#pragma unroll 1
+          for (int ch = 0; ch < 2 * (D / 32); ++ch) {
+            const bool k = ch < D / 32;
+            const int col = k ? 32 * ch : 32 * ch - D;
+            float o[32];
+            tmem_ld32_start(tmem + lanes + (k ? kColDk : kColDv) + col, o);
+            tmem_wait32(o);
+            store_columns<T, D>(o, k ? back : back_v, dst + (k ? 0 : static_cast<long long>(f.s_pad) * D) + col, see);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + C::kBarDFree);
+        ++j;
+      }
+      if (h.last) {
+        if (!bar_wait(bars + C::kBarDq, on & 1u, ctl)) break;
+        tc_fence_after();
+        ++on;
+        if (w * 32 < f.heads) {
+          X* dst = static_cast<X*>(p.dq) +
+                   (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + h.z * f.heads + w * 32) * D;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            float o[32];
+            tmem_ld32_start(tmem + lanes + kColDq + 32 * ch, o);
+            tmem_wait32(o);
+            if (first) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] = 0.f;  // no key
+            }
+            store_columns<X, D>(o, back, dst + 32 * ch, low_bits(f.heads - w * 32));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars + C::kBarDqFree);
+          if (!first) mbar_arrive(bars + C::kBarStatFree + (ni & 1u));
+        }
+        if (!first) ++ni;
+        first = true;
+      }
+      give_head();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ----------------------------------------------------------------- statistics of rows, range of values
+// delta = dout.out of each row and head (and fp16: |dout|^2): D/8 lanes a head.
+template <typename X, int D>
+__global__ void __launch_bounds__(256) sparse_delta_kernel(const X* dout, const X* out, long long rows, float* delta,
+                                                          float* norm2) {
+  constexpr int G = D / 8;
+  const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
+  const int l = threadIdx.x % G;
+  float d = 0.f, n = 0.f;
+  if (r < rows) {
+    const uint4 a = reinterpret_cast<const uint4*>(dout + r * D)[l], b = reinterpret_cast<const uint4*>(out + r * D)[l];
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = unpack_pair<X>(x[i]), v = unpack_pair<X>(y[i]);
+      d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+      n = fmaf(u.x, u.x, fmaf(u.y, u.y, n));
+    }
+  }
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) {
+    d += __shfl_xor_sync(0xffffffffu, d, o);
+    n += __shfl_xor_sync(0xffffffffu, n, o);
+  }
+  if (r < rows && l == 0) {
+    delta[r] = d;
+    if (norm2 != nullptr) norm2[r] = n;
+  }
+}
+
+// The sequence of key t, by one thread: the largest i with cu_k[i] <= t (-1: none).
+__device__ __forceinline__ int key_sequence(const SparseParams& p, int t) {
+  int lo = 0, hi = p.N;
+  if (p.N <= 0 || p.cu_k[0] > t) return -1;
+  while (lo < hi) {
+    const int i = (lo + hi + 1) >> 1;
+    if (p.cu_k[i] <= t)
+      lo = i;
+    else
+      hi = i - 1;
+  }
+  return lo < p.N ? lo : -1;
+}
+
+// range[seq][key head] = the largest |v|^2 over the finite values of its keys
+// (zeroed before; as bits: these numbers are not negative).  A warp per key.
+template <typename X, int D>
+__global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p, uint32_t* range) {
+  const long long w = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
+  const int lane = threadIdx.x & 31;
+  const long long key = w / p.Hk;
+  if (key >= p.Tk) return;
+  const int hk = static_cast<int>(w - key * p.Hk), seq = key_sequence(p, static_cast<int>(key));
+  if (seq < 0) return;
+  const SeqExt s = sparse_extent(p, seq);
+  if (key < s.k0 || key >= s.k0 + s.lk) return;
+  const X* v = reinterpret_cast<const X*>(
+      static_cast<const char*>(p.v.base) +
+      static_cast<uint64_t>(key * p.v.rt + static_cast<long long>(hk) * p.v.rh) * p.v.unit_bytes);
+  float n = 0.f;
+  for (int i = lane; i < D; i += 32) {
+    const float x = static_cast<float>(v[i]);
+    if (fabsf(x) < INFINITY) n = fmaf(x, x, n);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  if (lane == 0) atomicMax(range + static_cast<long long>(seq) * p.Hk + hk, __float_as_uint(n));
+}
+
+// ----------------------------------------------------------------- who lists a block
+// Blocks of all sequences in one numbering: block b of sequence i is number
+// (k0 >> shift) + i + b, of n_blocks = (Tk >> shift) + N + 1.
+struct WhoArgs {
+  SparseParams p;
+  int t0, rows;          // this round's rows
+  int groups, per;       // groups of `per` rows whose counts are kept apart
+  int n_blocks;
+  int u_bits;            // an entry is (row - t0) << u_bits | place in the row's list
+  uint32_t *count, *total, *start, *entry;  // [groups][n_blocks], [n_blocks], [n_blocks + 1], [rows * top_k]
+};
+// Number of the block that place u of row t lists, where the row sees some of its keys; -1 else.
+__device__ __forceinline__ int listed_block(const SparseParams& p, const ListRow& r, int t, int u) {
+  const int b = p.idx[t * p.idx_st + u];
+  if (r.lk <= 0 || static_cast<unsigned>(b) > static_cast<unsigned>((r.lk - 1) >> p.block_shift)) return -1;
+  if ((b << p.block_shift) > static_cast<long long>(r.pos) - p.window) return -1;
+  return (r.k0 >> p.block_shift) + r.seq + b;
+}
+__global__ void __launch_bounds__(256) sparse_count_kernel(const WhoArgs f) {
+  const int r = (blockIdx.x * 256 + threadIdx.x) / 32, lane = threadIdx.x & 31;
+  if (r >= f.rows) return;
+  const ListRow row = find_list_row(f.p, f.t0 + r);
+  uint32_t* count = f.count + static_cast<long long>(r / f.per) * f.n_blocks;
+  for (int u = lane; u < f.p.top_k; u += 32) {
+    const int id = listed_block(f.p, row, f.t0 + r, u);
+    if (id >= 0) atomicAdd(count + id, 1u);
+  }
+}
+// Counts become places within the block's entries; totals.
+__global__ void __launch_bounds__(256) sparse_scan_kernel(const WhoArgs f) {
+  const int id = blockIdx.x * 256 + threadIdx.x;
+  if (id >= f.n_blocks) return;
+  uint32_t n = 0;
+#pragma unroll 8
+  for (int g = 0; g < f.groups; ++g) {
+    uint32_t* c = f.count + static_cast<long long>(g) * f.n_blocks + id;
+    const uint32_t x = *c;
+    *c = n;
+    n += x;
+  }
+  f.total[id] = n;
+}
+// start = running sum of total: one block of threads.
+__global__ void __launch_bounds__(1024) sparse_start_kernel(const WhoArgs f) {
+  __shared__ uint32_t sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  uint32_t before = 0;
+  for (int base = 0; base < f.n_blocks; base += 4096) {
+    uint32_t x[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = base + 4 * tid + i;
+      x[i] = id < f.n_blocks ? f.total[id] : 0u;
+      mine += x[i];
+    }
+    uint32_t run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    uint32_t off = before, all = 0;
+    for (int i = 0; i < 32; ++i) {
+      if (i < warp) off += sums[i];
+      all += sums[i];
+    }
+    run += off - mine;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = base + 4 * tid + i;
+      if (id < f.n_blocks) f.start[id] = run;
+      run += x[i];
+    }
+    before += all;
+    __syncthreads();
+  }
+  if (tid == 0) f.start[f.n_blocks] = before;
+}
+// A warp per group takes its rows in order, so that entries of a block ascend by
+// row (a block listed twice by a row: its two shares are equal).
+__global__ void __launch_bounds__(64) sparse_fill_kernel(const WhoArgs f) {
+  const int g = (blockIdx.x * 64 + threadIdx.x) / 32, lane = threadIdx.x & 31;
+  if (g >= f.groups) return;
+  uint32_t* place = f.count + static_cast<long long>(g) * f.n_blocks;
+  const int last = min(f.rows, (g + 1) * f.per);
+  for (int r = g * f.per; r < last; ++r) {
+    const ListRow row = find_list_row(f.p, f.t0 + r);
+    for (int u = lane; u < f.p.top_k; u += 32) {
+      const int id = listed_block(f.p, row, f.t0 + r, u);
+      if (id >= 0) f.entry[f.start[id] + atomicAdd(place + id, 1u)] = (static_cast<uint32_t>(r) << f.u_bits) | u;
+    }
+    __syncwarp();
+  }
+}
+
+// ----------------------------------------------------------------- sums of the shares
+struct SumArgs {
+  SparseParams p;
+  int t0, rows, u_bits, n_z, s_pad;
+  const uint32_t *start, *entry;
+  const void* share;
+  float* acc;           // [2][Tk][Hk][D]: sums of the rounds before (more than one round)
+  int opens, closes;    // the first round, the last
+};
+
+// Four values of a share.
+template <typename T>
+__device__ __forceinline__ float4 load_share(const T* x) {
+  if constexpr (sizeof(T) == 4) {
+    return __ldcs(reinterpret_cast<const float4*>(x));
+  } else {
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(x));
+    const float2 a = unpack_pair<T>(u.x), b = unpack_pair<T>(u.y);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// dk, dv of key blockIdx.x, key head blockIdx.y: eight warps take every eighth
+// (sixteenth, D = 64) share, four values a lane; their sums are joined in order.
+template <typename X, int D>
+__global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
+  using T = typename ShareType<X>::T;
+  constexpr int L = D / 4, PER = 32 / L, W = 8 * PER, U = 4;  // lanes of a share; shares of a warp, of the block; in flight
+  const SparseParams& p = f.p;
+  const int key = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, sub = tid / L, col = (tid % L) * 4;
+  __shared__ float4 red[2][W][L];
+  float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+  auto add = [](float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  };
+  const int seq = key_sequence(p, key);
+  if (seq >= 0) {
+    const SeqExt s = sparse_extent(p, seq);
+    const int j = key - s.k0, shift = s.lk - (s.q1 - s.q0) - s.q0;  // position of row t: t + shift
+    if (j >= 0 && j < s.lk) {
+      const long long share = 2ll * f.s_pad * D;  // elements of an item
+      const T* base = static_cast<const T*>(f.share) + static_cast<long long>(hk) * f.n_z * share + col;
+      // slot of row t0 + r: n shares, one after the other in groups of heads
+      auto shares = [&](const int (&r)[U], const int (&slot)[U], const bool (&ok)[U]) {
+        for (int z = 0; z < f.n_z; ++z) {
+          float4 a[U], b[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ok[i]) {
+              const T* x = base + (static_cast<long long>(r[i]) * p.Hk * f.n_z + z) * share + static_cast<long long>(slot[i]) * D;
+              a[i] = load_share<T>(x);
+              b[i] = load_share<T>(x + static_cast<long long>(f.s_pad) * D);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            add(k, a[i]);
+            add(v, b[i]);
+          }
+        }
+      };
+      if (p.top_k > 0) {
+        const int id = (s.k0 >> p.block_shift) + seq + (j >> p.block_shift), in = j & ((1 << p.block_shift) - 1);
+        const uint32_t a = f.start[id], n = f.start[id + 1] - a;
+        for (uint32_t e = sub; e < n; e += W * U) {
+          int r[U], slot[U];
+          bool ok[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            ok[i] = e + i * W < n;
+            const uint32_t x = ok[i] ? f.entry[a + e + i * W] : 0u;
+            r[i] = static_cast<int>(x >> f.u_bits);
+            const int u = static_cast<int>(x & ((1u << f.u_bits) - 1u));
+            slot[i] = p.window + (u << p.block_shift) + in;
+            ok[i] = ok[i] && (p.causal == 0 || j <= f.t0 + r[i] + shift - p.window);
+          }
+          shares(r, slot, ok);
+        }
+      }
+      // rows in whose window the key lies: positions j .. j + window - 1
+      const long long first = max(static_cast<long long>(max(s.q0, f.t0)), static_cast<long long>(j) - shift);
+      const long long end = min(static_cast<long long>(min(s.q1, f.t0 + f.rows)), static_cast<long long>(j) - shift + p.window);
+      for (long long t = first + sub; t < end; t += W * U) {
+        int r[U], slot[U];
+        bool ok[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const long long x = t + i * W;
+          ok[i] = x < end;
+          r[i] = static_cast<int>(x - f.t0);
+          slot[i] = static_cast<int>(x + shift) - j;
+        }
+        shares(r, slot, ok);
+      }
+    }
+  }
+  red[0][sub][tid % L] = k;
+  red[1][sub][tid % L] = v;
+  __syncthreads();
+  if (tid >= 2 * L) return;
+  const int which = tid / L;
+  float4 x = red[which][0][tid % L];
+#pragma unroll
+  for (int i = 1; i < W; ++i) add(x, red[which][i][tid % L]);
+  const long long at = (static_cast<long long>(key) * p.Hk + hk) * D + col;
+  float* acc = f.acc + which * static_cast<long long>(p.Tk) * p.Hk * D + at;
+  if (!f.opens) add(x, *reinterpret_cast<const float4*>(acc));
+  if (!f.closes) {
+    *reinterpret_cast<float4*>(acc) = x;
+    return;
+  }
+  uint2 u;
+  u.x = pack_pair<X>(x.x, x.y);
+  u.y = pack_pair<X>(x.z, x.w);
+  *reinterpret_cast<uint2*>(static_cast<X*>(which ? p.dv : p.dk) + at) = u;
+}
+
+// ----------------------------------------------------------------- plan and launches
+struct Plan {
+  int heads, n_z, s_pad, rows, rounds, groups, per, n_blocks, u_bits;
+  size_t norm2, range, count, total, start, entry, acc, share, bytes;
+};
+Plan make_plan(const SparseParams& p, int dtype) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  Plan a;
+  const bool fp16 = dtype == CSA_F16;
+  a.n_z = 1;
+  while (p.g / a.n_z > kHeads || p.g % a.n_z != 0) ++a.n_z;
+  a.heads = p.g / a.n_z;
+  a.s_pad = static_cast<int>((sparse_slots(p) + 127) / 128 * 128);
+  const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * (fp16 ? 4 : 2);
+  a.u_bits = 0;
+  while ((1ll << a.u_bits) < p.top_k) ++a.u_bits;
+  long long rows = row == 0 ? p.Tq : static_cast<long long>(std::max<size_t>(1, kShareBytes / row));
+  rows = std::min({rows, static_cast<long long>(p.Tq), 1ll << (32 - a.u_bits)});
+  if (p.top_k > 0) rows = std::min(rows, std::max(1ll, 0x7FFFFFFFll / p.top_k));
+  a.rows = static_cast<int>(std::max(1ll, rows));
+  a.rounds = (p.Tq + a.rows - 1) / a.rows;
+  a.rows = (p.Tq + std::max(1, a.rounds) - 1) / std::max(1, a.rounds);  // of equal size
+  a.n_blocks = (p.Tk >> p.block_shift) + p.N + 1;
+  // groups of some eight rows, their counts within 64 MB
+  const long long most = std::max(1ll, (16ll << 20) / a.n_blocks);
+  a.per = static_cast<int>(std::max(8ll, (a.rows + std::min(most, 2048ll) - 1) / std::min(most, 2048ll)));
+  a.groups = (a.rows + a.per - 1) / a.per;
+  const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
+  const bool lists = p.top_k > 0;
+  a.norm2 = per_row;
+  a.range = a.norm2 + (fp16 ? per_row : 0);
+  a.count = up(a.range + (fp16 ? static_cast<size_t>(p.N) * p.Hk * 4 : 0));
+  a.total = up(a.count + (lists ? static_cast<size_t>(a.groups) * a.n_blocks * 4 : 0));
+  a.start = up(a.total + (lists ? static_cast<size_t>(a.n_blocks) * 4 : 0));
+  a.entry = up(a.start + (lists ? static_cast<size_t>(a.n_blocks + 1) * 4 : 0));
+  a.acc = up(a.entry + static_cast<size_t>(a.rows) * p.top_k * 4);
+  a.share = a.acc + (a.rounds > 1 ? up(static_cast<size_t>(p.Tk) * p.Hk * p.D * 8) : 0);
+  a.bytes = a.share + row * a.rows;
+  return a;
+}
+
+template <typename X, int D>
+cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t stream) {
+  const Plan a = make_plan(p, dtype);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  constexpr bool fp16 = !is_bf16<X>();
+  float* delta = reinterpret_cast<float*>(ws);
+  float* norm2 = fp16 ? reinterpret_cast<float*>(ws + a.norm2) : nullptr;
+  uint32_t* range = reinterpret_cast<uint32_t*>(ws + a.range);
+  cudaError_t e;
+  const size_t dkv = static_cast<size_t>(p.Tk) * p.Hk * D * sizeof(X);
+  if (p.Tq == 0) {
+    if ((e = cudaMemsetAsync(p.dk, 0, dkv, stream)) != cudaSuccess) return e;
+    return cudaMemsetAsync(p.dv, 0, dkv, stream);
+  }
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq, blocks = (rows * (D / 8) + 255) / 256;
+  if (blocks > 0x7FFFFFFFll || p.Hk > 65535) return cudaErrorInvalidValue;
+  sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+      static_cast<const X*>(p.dout), static_cast<const X*>(p.out), rows, delta, norm2);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (fp16 && p.N > 0) {
+    if ((e = cudaMemsetAsync(range, 0, static_cast<size_t>(p.N) * p.Hk * 4, stream)) != cudaSuccess) return e;
+    const long long n = (static_cast<long long>(p.Tk) * p.Hk * 32 + 255) / 256;
+    if (n > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    if (n > 0) sparse_range_kernel<X, D><<<static_cast<unsigned>(n), 256, 0, stream>>>(p, range);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  RowsArgs f;
+  f.p = p;
+  f.l.n_z = a.n_z;
+  f.l.split = 0;
+  f.l.slots = static_cast<int>(sparse_slots(p));
+  f.l.per = std::max(1, a.s_pad / 128);
+  f.heads = a.heads;
+  f.padded = (a.heads + 15) / 16 * 16;
+  f.s_pad = a.s_pad;
+  f.c = p.scale * 1.4426950408889634f;
+  f.delta = delta;
+  f.norm2 = norm2;
+  f.range = range;
+  f.share = ws + a.share;
+  f.wait_ns = attn_wait_ns(f.l.slots / 128 + 1);
+  CUtensorMap tq, tdo;
+  if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, a.heads) ||
+      !make_heads_map(&tdo, p, p.dout, static_cast<long long>(p.Hq) * D, D, a.heads))
+    return cudaErrorInvalidValue;
+  constexpr auto kernel = sparse_rows_kernel<X, D>;
+  if ((e = smem_limit_once<kernel>(Cfg<D>::kSmem)) != cudaSuccess) return e;
+  WhoArgs who;
+  who.p = p;
+  who.per = a.per;
+  who.n_blocks = a.n_blocks;
+  who.u_bits = a.u_bits;
+  who.count = reinterpret_cast<uint32_t*>(ws + a.count);
+  who.total = reinterpret_cast<uint32_t*>(ws + a.total);
+  who.start = reinterpret_cast<uint32_t*>(ws + a.start);
+  who.entry = reinterpret_cast<uint32_t*>(ws + a.entry);
+  SumArgs sum;
+  sum.p = p;
+  sum.u_bits = a.u_bits;
+  sum.n_z = a.n_z;
+  sum.s_pad = a.s_pad;
+  sum.start = who.start;
+  sum.entry = who.entry;
+  sum.share = f.share;
+  sum.acc = reinterpret_cast<float*>(ws + a.acc);
+  for (int i = 0; i < a.rounds; ++i) {
+    const int t0 = i * a.rows, n = std::min(a.rows, p.Tq - t0);
+    f.l.t0 = who.t0 = sum.t0 = t0;
+    who.rows = sum.rows = n;
+    who.groups = (n + a.per - 1) / a.per;
+    f.l.items = static_cast<long long>(n) * p.Hk * a.n_z;
+    if (p.Tk > 0 && p.top_k > 0) {
+      if ((e = cudaMemsetAsync(who.count, 0, static_cast<size_t>(who.groups) * a.n_blocks * 4, stream)) != cudaSuccess)
+        return e;
+      sparse_count_kernel<<<static_cast<unsigned>((static_cast<long long>(n) * 32 + 255) / 256), 256, 0, stream>>>(who);
+      sparse_scan_kernel<<<(a.n_blocks + 255) / 256, 256, 0, stream>>>(who);
+      sparse_start_kernel<<<1, 1024, 0, stream>>>(who);
+      sparse_fill_kernel<<<(who.groups + 1) / 2, 64, 0, stream>>>(who);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    kernel<<<static_cast<unsigned>(std::min(f.l.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, tdo, f);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (p.Tk == 0) continue;
+    sum.opens = i == 0;
+    sum.closes = i + 1 == a.rounds;
+    sparse_sum_kernel<X, D><<<dim3(static_cast<unsigned>(p.Tk), static_cast<unsigned>(p.Hk)), 256, 0, stream>>>(sum);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t sparse_backward_workspace(const SparseParams& p, int dtype) { return make_plan(p, dtype).bytes; }
+
+cudaError_t launch_sparse_backward(const SparseParams& p, int dtype, void* workspace, cudaStream_t s) {
+  if (dtype == CSA_BF16)
+    return p.D == 128 ? run<__nv_bfloat16, 128>(p, dtype, workspace, s) : run<__nv_bfloat16, 64>(p, dtype, workspace, s);
+  return p.D == 128 ? run<__half, 128>(p, dtype, workspace, s) : run<__half, 64>(p, dtype, workspace, s);
+}
+
+cudaError_t take_status_sparse_bwd(uint32_t* out, cudaStream_t stream) { return take_status(out, stream); }
+
+}  // namespace csa

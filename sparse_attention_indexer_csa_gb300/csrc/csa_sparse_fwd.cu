@@ -42,33 +42,13 @@
 namespace csa {
 namespace {
 
-// As mbar_wait, its slow part out of line: sixteen warps in seven roles run here,
-// and what they wait for is instructions.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  return mbar_wait_u32(smem_u32(bar), parity, ctl);
-}
-
 template <typename X>
 constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
 constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
 
-constexpr int kLists = 2, kRing = 8;  // warps that write lists; tiles of rows ahead
 constexpr int kThreads = 512;
 constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 10, kScoreWarp = 12, kMmaWarp = 13, kListWarp = 14;
 constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
-
-// 128 slots of an item's list: the rows of those that are keys (-1: none), a bit
-// for each of them, and n: one more than the last of them (0: none).  A hidden or
-// empty slot keeps its place, as lists have few of them but at the end.
-struct TileHead {
-  int n, last, t, hk, z;  // last: the item's last tile; n < 0: no more tiles
-};
-struct Tile {
-  int k_row[128], v_row[128];
-  uint32_t keys[4];
-  TileHead h;
-  int pad[3];
-};
 
 template <int D>
 struct Cfg {
@@ -83,134 +63,16 @@ struct Cfg {
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024, "one CTA per SM");
-static_assert(sizeof(Tile) % 16 == 0, "rows are read 16 bytes at a time");
 
 struct FwdArgs {
   SparseParams p;
-  long long items;  // Tq * Hk * n_split
-  int slots, per;   // of a row's list; its tiles (of an item's share)
-  int n_split;
+  ListArgs l;
+  int n_split;      // shares of a row's list
   float c;          // scale * log2(e)
   float* part_o;    // [n_split][Tq * Hq][D] (n_split > 1)
   float* part_lse;  // [n_split][Tq * Hq]
   unsigned long long wait_ns;
 };
-
-// The tiles of a CTA: items blockIdx.x + n gridDim.x, `per` tiles each.
-__device__ __forceinline__ long long tile_count(const FwdArgs& f) {
-  return (f.items - blockIdx.x + gridDim.x - 1) / gridDim.x * f.per;
-}
-
-// Writes the tiles w, w + kLists, .. of this CTA into the ring.  A warp.
-__device__ __forceinline__ void list_tiles(const FwdArgs& f, int w, Tile* ring, uint64_t* full, uint64_t* free_bar,
-                                           const WaitCtl& ctl) {
-  const SparseParams& p = f.p;
-  const int lane = static_cast<int>(lane_id());
-  bool bad = false;
-  if (blockIdx.x == 0 && w == 0)
-    for (int i = lane; i < p.N; i += 32) sparse_extent(p, i);  // what is out of order or range is recorded
-  const long long tiles = tile_count(f);
-  // the coming tile: its item, its place in the item, its row and the blocks that its slots list
-  long long item = blockIdx.x + static_cast<long long>(w / f.per) * gridDim.x;
-  int at = w % f.per, t = 0, hk = 0, z = 0, b[4];
-  auto blocks = [&] {
-    const long long rest = item / f.n_split;
-    z = static_cast<int>(item - rest * f.n_split);
-    t = static_cast<int>(rest / p.Hk);
-    hk = static_cast<int>(rest - static_cast<long long>(t) * p.Hk);
-    const int32_t* list = p.idx + t * p.idx_st;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = slot_block(p, list, (at * f.n_split + z) * 128 + 32 * i + lane, f.slots);
-  };
-  ListRow row{-1, 0, 0, -1};
-  int row_t = -1;
-  if (w < tiles) blocks();
-  for (long long n = w; n < tiles; n += kLists) {
-    const uint32_t st = static_cast<uint32_t>(n % kRing), turn = static_cast<uint32_t>(n / kRing) & 1u;
-    if (t != row_t) row = find_list_row(p, t);
-    row_t = t;
-    Slot x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = Slot{-1, 0};
-      if (row.lk > 0 && row.pos >= 0)
-        x[i] = slot_key(p, row, (at * f.n_split + z) * 128 + 32 * i + lane, f.slots, b[i], bad);
-    }
-    TileHead h{0, at == f.per - 1, t, hk, z};
-    const int k0 = hk * p.k.rh, v0 = hk * p.v.rh;
-    at += kLists;
-    while (at >= f.per) {
-      at -= f.per;
-      item += gridDim.x;
-    }
-    if (n + kLists < tiles) blocks();
-    if (!bar_wait(free_bar + st, turn ^ 1u, ctl)) break;
-    uint32_t mine = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int kr = 0, vr = 0;
-      const bool see = slot_rows(p, row, x[i], kr, vr, bad);
-      const unsigned all = __ballot_sync(0xffffffffu, see);
-      if (all != 0u) h.n = 32 * i + 32 - __clz(static_cast<int>(all));
-      if (lane == i) mine = all;
-      ring[st].k_row[32 * i + lane] = see ? kr + k0 : -1;
-      ring[st].v_row[32 * i + lane] = see ? vr + v0 : -1;
-    }
-    if (lane < 4) ring[st].keys[lane] = mine;
-    if (lane == 0) ring[st].h = h;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(full + st);
-  }
-  if (bad) record_error(kErrDevice);
-}
-
-// 64 rows of a tile (from row r0 on, as far as n of the tile) by a warp.  Whole
-// stretches go without a branch or a size of their own, eight copies in a row: a
-// copy that waits for its registers' former use takes 140 cycles instead of 40.
-template <int D>
-__device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, const int* rows, int r0, int n) {
-  constexpr int P = D / 8, PER = 32 / P;  // 16-byte pieces of a row; rows an instruction takes
-  const int lane = static_cast<int>(lane_id());
-  const int mine[2] = {r0 + lane < n ? rows[r0 + lane] : -1, r0 + 32 + lane < n ? rows[r0 + 32 + lane] : -1};
-  const int piece = lane % P, sub = lane / P;
-  const char* base = static_cast<const char*>(g.base) + piece * 16;
-  const uint32_t dst = smem_u32(tile) + (piece >> 3) * kChunkBytes + (r0 + sub) * 128;
-  uint32_t at[8 / PER];  // the swizzle repeats every eight rows
-#pragma unroll
-  for (int i = 0; i < 8 / PER; ++i) at[i] = dst + (((piece & 7) ^ ((PER * i + sub) & 7)) * 16);
-  if (__all_sync(0xffffffffu, (mine[0] | mine[1]) >= 0)) {
-#pragma unroll 1
-    for (int h = 0; h < 64; h += 8 * PER) {
-      const char* src[8];
-      const int from = h < 32 ? mine[0] : mine[1];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = __shfl_sync(0xffffffffu, from, (h + PER * i + sub) & 31);
-        src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * g.unit_bytes;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128), "l"(src[i])
-                     : "memory");
-    }
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 64 / PER && r0 + PER * i < n; ++i) {  // n is a multiple of 16
-      const int r = PER * i + sub;
-      const int row = __shfl_sync(0xffffffffu, PER * i < 32 ? mine[0] : mine[1], r & 31);
-      const char* src = base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * g.unit_bytes;
-      const uint32_t to = dst + PER * i * 128 + (((piece & 7) ^ (r & 7)) * 16);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(row < 0 ? 0 : 16) : "memory");
-    }
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void loaded() {  // all but the last N groups of rows are there, for the tensor cores too
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-  fence_proxy_async_shared();
-  __syncwarp();
-}
 
 template <typename X, int D, int R, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -256,10 +118,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
   // the next tile; n < 0 after the last one or a wait that gave up
   unsigned long long n_tile = 0;
-  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f));
+  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f.l));
   auto next_head = [&]() -> TileHead {
     if (n_tile == tiles || !bar_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u, ctl))
-      return TileHead{-1, 0, 0, 0, 0};
+      return TileHead{-1, 0, 0, 0, 0, 0, 0};
     return ring[n_tile % kRing].h;
   };
   auto give_head = [&] {  // by a role's warp
@@ -270,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kListWarp) {
     const int w = warp - kListWarp;
-    list_tiles(f, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+    list_tiles(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp >= kKeyWarp && warp < kScoreWarp) {
     // ------------------------------------------------------------------------- rows of keys, of values
     const bool keys = warp < kValueWarp;
@@ -615,7 +477,7 @@ cudaError_t start(const FwdArgs& f, const CUtensorMap& tq, cudaStream_t stream) 
   constexpr auto kernel = sparse_fwd_kernel<X, D, R, SPLIT>;
   const cudaError_t e = smem_limit_once<kernel>(Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(std::min(f.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
+  kernel<<<static_cast<unsigned>(std::min(f.l.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
   return cudaGetLastError();
 }
 
@@ -624,14 +486,17 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   CUtensorMap tq;
   FwdArgs f;
   f.p = p;
-  f.slots = static_cast<int>(sparse_slots(p));
-  f.n_split = sparse_splits(p.Tq, p.Hk, f.slots);
-  f.items = static_cast<long long>(p.Tq) * p.Hk * f.n_split;
-  f.per = std::max(1, ((f.slots + 127) / 128 + f.n_split - 1) / f.n_split);
+  f.l.slots = static_cast<int>(sparse_slots(p));
+  f.n_split = sparse_splits(p.Tq, p.Hk, f.l.slots);
+  f.l.items = static_cast<long long>(p.Tq) * p.Hk * f.n_split;
+  f.l.t0 = 0;
+  f.l.n_z = f.n_split;
+  f.l.split = 1;
+  f.l.per = std::max(1, ((f.l.slots + 127) / 128 + f.n_split - 1) / f.n_split);
   f.c = p.scale * 1.4426950408889634f;
   f.part_o = static_cast<float*>(workspace);
   f.part_lse = f.part_o + static_cast<long long>(f.n_split) * p.Tq * p.Hq * D;
-  f.wait_ns = attn_wait_ns(f.slots / 128 + 1);
+  f.wait_ns = attn_wait_ns(f.l.slots / 128 + 1);
   if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, p.g)) return cudaErrorInvalidValue;
   if (f.n_split == 1) return start<X, D, R, false>(f, tq, stream);
   cudaError_t e = start<X, D, R, true>(f, tq, stream);

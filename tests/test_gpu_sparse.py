@@ -13,6 +13,8 @@ Tolerances, from the arithmetic (u = eps/2 of the storage type), as for dense at
 * fp16 weights are formed at 2^8 (in out) and 2^15 (in dv) of their size, and ds at a power of two that brings its
   bound above 2^13: subnormal spacing 2^-24, so tiny is 2^-33 per key in out, 2^-40 in dv, 2^-38 of ds' bound in
   dq and dk.  bf16 has fp32's range: 0.
+* rounding a result x to fp16 is off by u |x| for |x| >= 2^-14 and, below, where fp16's numbers are 2^-24 apart, by half
+  of that: 2^-25 is added to every fp16 bound.  (bf16's subnormals start at 2^-126: the 1e-30 of _check.)
 """
 import numpy as np
 import pytest
@@ -76,13 +78,13 @@ def _bounds(ref, dt):
     ds = 2.0 ** -16 * ref["smax"]
     lse = np.where(np.isneginf(ref["lse"]), 0, ref["lse"])
     b = dict(out=u * np.abs(ref["out"]) + (u + 2 * ds[..., None] + 2.0 ** -18) * ref["mag_out"]
-             + h * 2.0 ** -33 * ref["vsum"], lse=ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse))
+             + h * (2.0 ** -33 * ref["vsum"] + 2.0 ** -25), lse=ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse))
     top = 2 * ds.max(initial=0.0)
     rel = dict(dq=2 * u + top + 2.0 ** -15, dk=3 * u + top + 2.0 ** -15, dv=2 * u + top + 2.0 ** -18)
     tiny = dict(dq=2.0 ** -38, dk=2.0 ** -38, dv=2.0 ** -40)
     for n in ("dq", "dk", "dv"):
         if n in ref:
-            b[n] = u * np.abs(ref[n]) + rel[n] * ref["mag_" + n] + h * tiny[n] * ref["sum_" + n]
+            b[n] = u * np.abs(ref[n]) + rel[n] * ref["mag_" + n] + h * (tiny[n] * ref["sum_" + n] + 2.0 ** -25)
     return b
 
 
@@ -265,6 +267,150 @@ def test_rows_outside_every_sequence_and_bad_borders():
     out, lse = csa.sparse_attn_forward(q.cuda(), k.cuda(), v.cuda(), idx.cuda(), c([0]), c([0]), 0.125)
     _ok()
     assert not out.any() and (lse == -float("inf")).all()
+
+
+# ----------------------------------------------------------------------------- gradients
+@pytest.mark.parametrize("shape", SHAPES, ids=_shape_id)
+@pytest.mark.parametrize("lengths", LENGTHS)
+def test_gradients(lengths, shape):
+    lq, lk = LENGTHS[lengths]
+    Hq, Hk, D, dt, K, block, window = shape
+    q, k, v, do = _inputs(lq, lk, Hq, Hk, D, dt, seed=len(lq) + D)
+    idx = _lists(lq, lk, K, block, seed=K)
+    _run(q, k, v, do, idx, _cu(lq), _cu(lk), D ** -0.5, block=block, window=window)
+
+
+@pytest.mark.parametrize("Hq,Hk,D,dt", [(64, 1, 128, BF), (96, 1, 64, FP16), (134, 2, 64, BF), (8, 8, 128, FP16)])
+def test_gradients_without_causal_border_and_odd_groups(Hq, Hk, D, dt):
+    lq, lk = [40, 0, 3, 61, 1], [129, 3, 257, 40, 0]
+    q, k, v, do = _inputs(lq, lk, Hq, Hk, D, dt, seed=Hq)
+    idx = _lists(lq, lk, 50, 2, seed=5)
+    _run(q, k, v, do, idx, _cu(lq), _cu(lk), D ** -0.5, block=2, causal=False)
+
+
+def test_gradients_of_a_window_alone():
+    lq = [70, 1, 300]
+    q, k, v, do = _inputs(lq, lq, 4, 2, 64, BF, seed=9)
+    _run(q, k, v, do, None, _cu(lq), _cu(lq), 0.125, window=50)
+    _run(q, k, v, do, None, _cu(lq), _cu(lq), 0.125, window=1000)
+
+
+def test_gradients_of_a_key_that_every_row_lists():
+    T = 1500
+    q, k, v, do = _inputs([T], [300], 4, 1, 64, BF, seed=20)
+    idx = _lists([T], [300], 9, 1, seed=6, holes=0.0)
+    idx[:, 0] = torch.where((idx[:, 1:] == 7).any(1), -1, 7)
+    _run(q, k, v, do, idx, _cu([T]), _cu([300]), 0.125, causal=False)
+
+
+def test_gradients_of_a_block_listed_twice():
+    q, k, v, do = _inputs([3], [40], 4, 2, 64, BF, seed=4)
+    idx = torch.tensor([[3, 3, 1, -1], [0, 2, 0, 0], [5, 5, 5, 5]], dtype=torch.int32)
+    _run(q, k, v, do, idx, _cu([3]), _cu([40]), 0.2, block=4, causal=False)
+
+
+def test_gradients_with_lengths_of_keys():
+    lq, lk = [6, 30], [200, 100]
+    q, k, v, do = _inputs(lq, lk, 8, 2, 128, FP16, seed=6)
+    k_len = torch.tensor([150, 31], dtype=torch.int32)
+    idx = _lists(lq, [150, 31], 20, 2, seed=1)
+    r = _run(q, k, v, do, idx, _cu(lq), _cu(lk), 0.1, k_len=k_len, block=2, window=9)
+    past = torch.tensor([*range(150, 200), *range(231, 300)]).cuda()
+    assert not r[3][past].any() and not r[4][past].any()
+    k[past.cpu()], v[past.cpu()] = float("nan"), float("inf")
+    c = lambda t: t.cuda()  # noqa: E731
+    again = csa.sparse_attn_backward(c(do), c(q), c(k), c(v), r[0], r[1], c(idx), c(_cu(lq)), c(_cu(lk)), 0.1, k_len=c(k_len),
+                                     block=2, window=9)
+    _ok()
+    assert all(torch.equal(a, b) for a, b in zip(again, r[2:]))
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 14, 2.0 ** -12])
+def test_gradients_of_scaled_cotangents_fp16(size):
+    lq = [90, 33]
+    q, k, v, do = _inputs(lq, lq, 6, 2, 64, FP16, seed=22)
+    do = (do.float() * size).clamp(-60000, 60000).to(FP16)
+    if size > 1:  # gradients that fit fp16 of weights and differences that do not
+        v = (v.float() * 2.0 ** -8).to(FP16)
+        q, k = ((t.float() * 2.0 ** -5).to(FP16) for t in (q, k))
+        do = (do.float() * 2.0 ** -5).to(FP16)
+    idx = _lists(lq, lq, 12, 4, seed=8)
+    _run(q, k, v, do, idx, _cu(lq), _cu(lq), 0.125, block=4, window=3)
+
+
+def test_gradients_in_several_rounds_repeat_bit_for_bit():
+    # 6 GB of shares: two rounds; lists of all rows in a different order of places give the same sums only if the
+    # order of the sums is that of the rows
+    T, W, Hk, K = 1500, 1100, 8, 1024
+    q, k, v, do = _inputs([T], [W], Hk, Hk, 128, BF, seed=23)
+    idx = _lists([T], [W], K, 1, seed=9, holes=0.1)
+    one = _run(q, k, v, do, idx, _cu([T]), _cu([W]), 128 ** -0.5, causal=False)
+    c = lambda t: t.cuda()  # noqa: E731
+    two = csa.sparse_attn_backward(c(do), c(q), c(k), c(v), one[0], one[1], c(idx), c(_cu([T])), c(_cu([W])), 128 ** -0.5,
+                                   causal=False)
+    _ok()
+    assert all(torch.equal(a, b) for a, b in zip(one[2:], two))
+
+
+def test_gradients_against_differences():
+    """Along a direction e of one input, with the forward in 64 bits: (L(x + h e) - L(x - h e)) / 2h = sum g e.  The
+    kernel's g is off by at most the bounds of _bounds, whose magnitudes are summed here with |e|."""
+    lq, lk = [20, 7], [60, 30]
+    q, k, v, do = _inputs(lq, lk, 8, 2, 64, BF, seed=24)
+    idx = _lists(lq, lk, 9, 2, seed=10)
+    kw = dict(block=2, window=4)
+    r = _run(q, k, v, do, idx, _cu(lq), _cu(lk), 0.125, **kw)
+    a = (idx.numpy(), _cu(lq).numpy(), _cu(lk).numpy(), 0.125)
+    x = [f64(t) for t in (q, k, v)]
+    ref = S.attention(*x, *a, **kw, dout=f64(do))
+    b = _bounds(ref, BF)
+    rng = np.random.default_rng(0)
+    loss = lambda x: (S.attention(*x, *a, **kw)["out"] * f64(do)).sum()  # noqa: E731
+    for i, name in enumerate(("dq", "dk", "dv")):
+        e = rng.standard_normal(x[i].shape)
+        up, down = ([t + s * 1e-5 * e if n == i else t for n, t in enumerate(x)] for s in (1, -1))
+        want = (loss(up) - loss(down)) / 2e-5
+        assert abs((f64(r[2 + i]) * e).sum() - want) <= (b[name] * np.abs(e)).sum() + 1e-6
+
+
+def test_gradients_do_not_leak_and_replay_from_a_graph():
+    lq = [50, 37, 64]
+    q, k, v, do = (t.cuda() for t in _inputs(lq, lq, 8, 2, 128, BF, seed=25))
+    idx, cu = _lists(lq, lq, 10, 4, seed=11).cuda(), _cu(lq).cuda()
+
+    def both():
+        out, lse = csa.sparse_attn_forward(q, k, v, idx, cu, cu, 0.1, block=4, window=6)
+        return (out, lse, *csa.sparse_attn_backward(do, q, k, v, out, lse, idx, cu, cu, 0.1, block=4, window=6))
+
+    want = [t.clone() for t in both()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = both()
+    for _ in range(2):
+        g.replay()
+    _ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for t in (q, k, v, do):
+        t[50:87] = float("nan")
+    other = torch.tensor([*range(50), *range(87, 151)]).cuda()
+    assert all(torch.equal(a[other], b[other]) for a, b in zip(both(), want))
+    _ok()
+
+
+def test_gradients_without_keys_or_rows():
+    q, k, v, do = (t.cuda() for t in _inputs([5], [7], 4, 2, 64, FP16, seed=26))
+    c = lambda t: torch.tensor(t, dtype=torch.int32).cuda()  # noqa: E731
+    idx = torch.zeros(5, 2, dtype=torch.int32).cuda()
+    none = k[:0]
+    out, lse = csa.sparse_attn_forward(q, none, none, idx - 1, c([0, 5]), c([0, 0]), 0.1)
+    g = csa.sparse_attn_backward(do, q, none, none, out, lse, idx - 1, c([0, 5]), c([0, 0]), 0.1)
+    assert not out.any() and not g[0].any() and g[1].shape == none.shape
+    e = q[:0]
+    g = csa.sparse_attn_backward(e, e, k, v, e, lse[:0], idx[:0], c([0, 0]), c([0, 7]), 0.1)
+    assert not g[1].any() and not g[2].any()
+    g = csa.sparse_attn_backward(do, q, k, v, torch.zeros_like(q), torch.full_like(lse, -float("inf")), idx, c([0]), c([0]), 0.1)
+    assert not any(t.any() for t in g)
+    _ok()
 
 
 # ----------------------------------------------------------------------------- paged
