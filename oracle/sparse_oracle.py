@@ -26,7 +26,8 @@ def attention(q, k, v, idx, cu_q, cu_k, scale, block=1, window=0, causal=True, k
 
     Returns results and magnitudes under the names of attn_oracle.attention; "bound" [Tq,Hq] is
     2 scale max|dout| max|v| (2-norms, dout over the heads of a key head, v over the sequence), which
-    |dout.v - dout.out| scale does not exceed.
+    |dout.v - dout.out| scale does not exceed; "norm_dk" and "norm_dv" [Tk,Hk] are sums over rows of
+    scale m |q| and p |dout| with 2-norms (m: see there), what a row's share of a key is at most.
     """
     Tq, Hq, D = q.shape
     Hk = k.shape[1]
@@ -37,6 +38,7 @@ def attention(q, k, v, idx, cu_q, cu_k, scale, block=1, window=0, causal=True, k
     if dout is not None:
         for n, like in (("dq", q), ("dk", k), ("dv", v)):
             res[n], res["mag_" + n], res["sum_" + n] = z(like.shape), z(like.shape), z(like.shape)
+        res["norm_dk"], res["norm_dv"] = z(k.shape[:2]), z(k.shape[:2])
     for i in range(len(cu_q) - 1):
         a, b, c = int(cu_q[i]), int(cu_q[i + 1]), int(cu_k[i])
         lk = int(cu_k[i + 1]) - c if k_len is None else int(k_len[i])
@@ -78,4 +80,6 @@ def attention(q, k, v, idx, cu_q, cu_k, scale, block=1, window=0, causal=True, k
             res["dv"][c:c + lk, j] += p.T @ G
             res["mag_dv"][c:c + lk, j] += p.T @ np.abs(G)
             res["sum_dv"][c:c + lk, j] += n.T @ np.abs(G)
+            res["norm_dk"][c:c + lk, j] += scale * (dmag.T @ np.linalg.norm(Q, axis=1))
+            res["norm_dv"][c:c + lk, j] += p.T @ np.linalg.norm(G, axis=1)
     return res

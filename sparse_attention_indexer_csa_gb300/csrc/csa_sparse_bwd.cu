@@ -23,8 +23,10 @@
 //   sparse_sum_kernel  a block of threads per key and key head adds the shares.
 //
 // Bytes: a share of dk and one of dv, D values each, per listed key, written once
-// and read once: in bf16 rounded to it (as ds and p are before), in fp16 fp32.
-// As many rows at a time as kShareBytes hold.
+// and read once.  A share is kept in fp16 at a power of two of its own, from the
+// bound sum over heads of |ds| |q| (p |dout|) that its key's thread adds up on the
+// way: 11 bits, finer than ds and p have in bf16, at half of fp32's bytes.  As many
+// rows at a time as kShareBytes hold.
 //
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
 // 2^15 (|dout| over the item's heads, |v| over the finite values of the sequence), and
@@ -39,21 +41,11 @@ namespace {
 
 constexpr size_t kShareBytes = 4ull << 30;
 constexpr int kHeads = 64;  // query heads of an item at most
-constexpr int kThreads = 512;
-constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14;
+constexpr int kThreads = 640;
+constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14, kDrain2Warp = 16;
 
 template <typename X>
 constexpr int kProbExp = is_bf16<X>() ? 0 : 15;  // power of two of P^T
-
-// What the shares are kept in.
-template <typename X>
-struct ShareType {
-  using T = X;
-};
-template <>
-struct ShareType<__half> {
-  using T = float;
-};
 
 template <int D>
 struct Cfg {
@@ -63,8 +55,10 @@ struct Cfg {
   // (the product that reads dS has 128 rows: what stands behind its 64 heads is read too and not used)
   static constexpr uint32_t kOffQ = kOffDs + kChunkBytes, kOffDo = kOffQ + 2 * kHeadTile;
   static constexpr uint32_t kOffRing = kOffDo + 2 * kHeadTile;
-  static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta; [2] power of two
-  static constexpr uint32_t kOffBar = kOffStat + 2 * kHeads * 8 + 16;
+  static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta, |dout|, |q|
+  static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [2][128] factors of a key's shares
+  static constexpr uint32_t kOffFit = kOffFactor + 2 * 128 * 8;          // [2] power of two of dS
+  static constexpr uint32_t kOffBar = kOffFit + 16;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
                        kBarKFree = 14, kBarP = 16, kBarD = 17, kBarDFree = 18, kBarDq = 19, kBarDqFree = 20,
                        kBarTile = 21, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
@@ -81,17 +75,17 @@ struct RowsArgs {
   int heads, padded;  // of an item; the same rounded up to 16
   int s_pad;       // slots of a row's list, rounded up to 128
   float c;         // scale * log2(e)
-  const float *delta, *norm2;
+  const float *delta, *norm_do, *norm_q;  // [Tq][Hq]
   const uint32_t* range;
-  void* share;     // [rows][Hk][n_z][2][s_pad][D]
+  __half* share;   // [rows][Hk][n_z][2][s_pad][D]
+  uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk is its fp16 values times 2^(low byte - 143), dv: high byte
   unsigned long long wait_ns;
 };
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-// 2 |dout| |v| < 2^E for the squares of the two norms.
-__device__ __forceinline__ int ds_exponent(float dout2, float v2) {
-  const int e = static_cast<int>((__float_as_uint(2.f * sqrtf(dout2) * sqrtf(v2)) >> 23) & 255u) - 126;
-  return min(max(e, -60), 60);
+// E with x < 2^E for x >= 0, within +-most.
+__device__ __forceinline__ int exponent_above(float x, int most) {
+  return min(max(static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 126, -most), most);
 }
 
 // Sixteen columns of this warp's lanes, requested; and eight written.
@@ -118,33 +112,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
-// 32 columns of a warp's 32 rows, times f, stored as T: lanes 4 i .. 4 i + 3
-// exchange 16-byte pieces, so that four lanes store 64 bytes of one row.  Row r
-// goes to dst + r * D where bit r of `rows` is set.
+// 32 columns of a warp's 32 rows, each times its lane's f, stored as T: lanes 4 i
+// .. 4 i + 3 exchange 16-byte pieces, so that four lanes store 64 bytes of one row.
+// Row r goes to dst + r * D where bit r of `rows` is set.
 template <typename T, int D>
 __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* dst, uint32_t rows) {
   const uint32_t lane = lane_id();
+  uint4 q[4];
 #pragma unroll
-  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
-    uint4 q[4];
+  for (int u = 0; u < 4; ++u) {
+    const float* x = o + 8 * u;
+    q[u] = make_uint4(pack_pair<T>(x[0] * f, x[1] * f), pack_pair<T>(x[2] * f, x[3] * f),
+                      pack_pair<T>(x[4] * f, x[5] * f), pack_pair<T>(x[6] * f, x[7] * f));
+  }
+  transpose4(q, lane);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if constexpr (sizeof(T) == 4) {
-        const float* x = o + 16 * h + 4 * u;
-        q[u] = make_uint4(__float_as_uint(x[0] * f), __float_as_uint(x[1] * f), __float_as_uint(x[2] * f),
-                          __float_as_uint(x[3] * f));
-      } else {
-        const float* x = o + 8 * u;
-        q[u] = make_uint4(pack_pair<T>(x[0] * f, x[1] * f), pack_pair<T>(x[2] * f, x[3] * f),
-                          pack_pair<T>(x[4] * f, x[5] * f), pack_pair<T>(x[6] * f, x[7] * f));
-      }
-    }
-    transpose4(q, lane);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t r = (lane & ~3u) + u;
-      if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 16 * h)[lane & 3u] = q[u];
-    }
+  for (int u = 0; u < 4; ++u) {
+    const uint32_t r = (lane & ~3u) + u;
+    if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D)[lane & 3u] = q[u];
   }
 }
 
@@ -153,12 +138,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     sparse_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                        const __grid_constant__ RowsArgs f) {
   using C = Cfg<D>;
-  using T = typename ShareType<X>::T;
   extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
-  float2* stat = reinterpret_cast<float2*>(base + C::kOffStat);
-  int* fits = reinterpret_cast<int*>(base + C::kOffStat + 2 * kHeads * 8);
+  float4* stat = reinterpret_cast<float4*>(base + C::kOffStat);
+  float2* factor = reinterpret_cast<float2*>(base + C::kOffFactor);
+  int* fits = reinterpret_cast<int*>(base + C::kOffFit);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
   const SparseParams& p = f.p;
@@ -169,9 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kBars; ++i) {
       int n = 1;
       if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
-      if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 8;
-      if (i == C::kBarP || i == C::kBarDFree || i == C::kBarDqFree) n = 4;
-      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 14;
+      if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 12;
+      if (i == C::kBarP) n = 4;
+      if (i == C::kBarDFree || i == C::kBarDqFree) n = 8;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 18;
       mbar_init(bars + i, n);
     }
     if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
@@ -207,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++n_tile;
   };
 
-  if (warp >= kListWarp) {
+  if (warp >= kListWarp && warp < kDrain2Warp) {
     list_tiles(p, f.l, warp - kListWarp, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp == kItemWarp) {
     // ------------------------------------------------------------------------- an item's queries, cotangents, statistics
@@ -236,11 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at = static_cast<long long>(h.t) * p.Hq + head;
         float top = 0.f;
         for (int i = static_cast<int>(lane); i < f.padded; i += 32) {
-          float2 s = make_float2(INFINITY, 0.f);  // no head, or a row without a weight: P = 0
+          float4 s = make_float4(INFINITY, 0.f, 0.f, 0.f);  // no head, or a row without a weight: P = 0
           if (i < f.heads) {
-            const float l = p.lse[at + i];
-            if (l != -INFINITY) s = make_float2(l * 1.4426950408889634f, f.delta[at + i]);
-            if constexpr (!is_bf16<X>()) top = fmaxf(top, f.norm2[at + i]);
+            const float l = p.lse[at + i], n = f.norm_do[at + i];
+            if (l != -INFINITY) s = make_float4(l * 1.4426950408889634f, f.delta[at + i], n, f.norm_q[at + i]);
+            top = fmaxf(top, n);
           }
           stat[b * kHeads + i] = s;
         }
@@ -248,7 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == 0)
-            fits[b] = 15 - ds_exponent(top, __uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk]));
+            fits[b] = 15 - exponent_above(
+                               2.f * top * sqrtf(__uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk])), 60);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
@@ -415,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 c2 = make_float2(f.c, f.c);
     uint32_t j = 0, ni = 0;
     bool first = true;
-    float fit = 1.f;  // power of two of dS over that of P
+    float fit = 1.f;        // power of two of dS over that of P
+    float back = p.scale, back_v = 1.f;  // what undoes the powers of two
     while (true) {
       const TileHead h = next_head();
       if (h.n < 0) break;
@@ -423,7 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t st = j & 1u;
         if (first) {
           if (!bar_wait(bars + C::kBarStat + (ni & 1u), (ni >> 1) & 1u, ctl)) break;
-          if constexpr (!is_bf16<X>()) fit = power_of_two(fits[ni & 1u] - kProbExp<X>);
+          if constexpr (!is_bf16<X>()) {
+            fit = power_of_two(fits[ni & 1u] - kProbExp<X>);
+            back = p.scale * power_of_two(-fits[ni & 1u]);
+            back_v = power_of_two(-kProbExp<X>);
+          }
         }
         first = false;
         if (!bar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl)) break;
@@ -431,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j > 0 && !bar_wait(bars + C::kBarKFree + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl)) break;
         tc_fence_after();
         const bool see = (ring[n_tile % kRing].keys[warp] >> lane) & 1u;
-        const float4* ls = reinterpret_cast<const float4*>(stat + (ni & 1u) * kHeads);
+        const float4* ls = stat + (ni & 1u) * kHeads;
+        float2 bk = make_float2(0.f, 0.f), bv = bk;  // bounds of the key's shares
 #pragma unroll 1
         for (int i = 0; i < f.padded / 16; ++i) {
           float s[16], dp[16];
@@ -442,12 +435,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pw[8], dw[8];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const float4 x = ls[8 * i + u];  // lse, delta of two heads
+            const float4 x = ls[16 * i + 2 * u], y = ls[16 * i + 2 * u + 1];  // of two heads
             const float2 e = ffma2(make_float2(s[2 * u], s[2 * u + 1]), c2,
-                                   make_float2(static_cast<float>(kProbExp<X>) - x.x, static_cast<float>(kProbExp<X>) - x.z));
+                                   make_float2(static_cast<float>(kProbExp<X>) - x.x, static_cast<float>(kProbExp<X>) - y.x));
             const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
-            float2 d = fmul2(w, fadd2(make_float2(dp[2 * u], dp[2 * u + 1]), make_float2(-x.y, -x.w)));
+            float2 d = fmul2(w, fadd2(make_float2(dp[2 * u], dp[2 * u + 1]), make_float2(-x.y, -y.y)));
             if constexpr (!is_bf16<X>()) d = fmul2(d, make_float2(fit, fit));
+            bv = ffma2(w, make_float2(x.z, y.z), bv);
+            bk = ffma2(make_float2(fabsf(d.x), fabsf(d.y)), make_float2(x.w, y.w), bk);
             pw[u] = see ? pack_pair<X>(w.x, w.y) : 0u;
             dw[u] = see ? pack_pair<X>(d.x, d.y) : 0u;
           }
@@ -458,6 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(row + (((2 * i + u) ^ (key & 7)) * 16)) =
                 make_uint4(dw[4 * u], dw[4 * u + 1], dw[4 * u + 2], dw[4 * u + 3]);
         }
+        const int ek = exponent_above((bk.x + bk.y) * back, 110), ev = exponent_above((bv.x + bv.y) * back_v, 110);
+        factor[st * 128 + key] = make_float2(back * power_of_two(15 - ek), back_v * power_of_two(15 - ev));
+        const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
+        f.power[item * f.s_pad + h.c * 128 + key] = static_cast<uint16_t>((ek + 128) | ((ev + 128) << 8));
         tmem_wait_st();
         fence_proxy_async_shared();
         tc_fence_before();
@@ -474,38 +473,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       give_head();
     }
   } else {
-    // ------------------------------------------------------------------------- shares of dk and dv; dq
-    const int w = warp - kDrainWarp;
+    // ------------------------------------------------------------------------- shares of dk, of dv; half of dq each
+    const bool dk = warp < kDrain2Warp;
+    const int w = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
     uint32_t j = 0, ni = 0, on = 0;
     bool first = true;
-    float back_v = 1.f, back = p.scale;  // what undoes the powers of two
     while (true) {
       const TileHead h = next_head();
       if (h.n < 0) break;
       if (h.n > 0) {
-        if (first) {
-          if (!bar_wait(bars + C::kBarStat + (ni & 1u), (ni >> 1) & 1u, ctl)) break;
-          if constexpr (!is_bf16<X>()) {
-            back_v = power_of_two(-kProbExp<X>);
-            back = p.scale * power_of_two(-fits[ni & 1u]);
-          }
-        }
         first = false;
         const uint32_t see = ring[n_tile % kRing].keys[w];
         if (!bar_wait(bars + C::kBarD, j & 1u, ctl)) break;
         tc_fence_after();
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
-        T* dst = static_cast<T*>(f.share) + (item * 2 * f.s_pad + h.c * 128 + w * 32) * D;
+        __half* dst = f.share + ((2 * item + (dk ? 0 : 1)) * f.s_pad + h.c * 128 + w * 32) * D;
         if (see != 0u) {
+          const float2 both = factor[(j & 1u) * 128 + w * 32 + lane];
+          const float mine = dk ? both.x : both.y;
 #pragma unroll 1
-          for (int ch = 0; ch < 2 * (D / 32); ++ch) {
-            const bool k = ch < D / 32;
-            const int col = k ? 32 * ch : 32 * ch - D;
+          for (int ch = 0; ch < D / 32; ++ch) {
             float o[32];
-            tmem_ld32_start(tmem + lanes + (k ? kColDk : kColDv) + col, o);
+            tmem_ld32_start(tmem + lanes + (dk ? kColDk : kColDv) + 32 * ch, o);
             tmem_wait32(o);
-            store_columns<T, D>(o, k ? back : back_v, dst + (k ? 0 : static_cast<long long>(f.s_pad) * D) + col, see);
+            store_columns<__half, D>(o, mine, dst + 32 * ch, see);
           }
         }
         tc_fence_before();
@@ -518,10 +510,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         ++on;
         if (w * 32 < f.heads) {
+          float back = p.scale;
+          if (!is_bf16<X>() && !first) back *= power_of_two(-fits[ni & 1u]);
           X* dst = static_cast<X*>(p.dq) +
                    (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + h.z * f.heads + w * 32) * D;
 #pragma unroll 1
-          for (int ch = 0; ch < D / 32; ++ch) {
+          for (int ch = dk ? 0 : D / 64; ch < (dk ? D / 64 : D / 32); ++ch) {
             float o[32];
             tmem_ld32_start(tmem + lanes + kColDq + 32 * ch, o);
             tmem_wait32(o);
@@ -552,32 +546,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------- statistics of rows, range of values
-// delta = dout.out of each row and head (and fp16: |dout|^2): D/8 lanes a head.
+// delta = dout.out of each row and head, |dout| and |q|: D/8 lanes a head.
 template <typename X, int D>
-__global__ void __launch_bounds__(256) sparse_delta_kernel(const X* dout, const X* out, long long rows, float* delta,
-                                                          float* norm2) {
+__global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p, float* delta, float* norm_do, float* norm_q) {
   constexpr int G = D / 8;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
   const int l = threadIdx.x % G;
-  float d = 0.f, n = 0.f;
-  if (r < rows) {
-    const uint4 a = reinterpret_cast<const uint4*>(dout + r * D)[l], b = reinterpret_cast<const uint4*>(out + r * D)[l];
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  const bool ok = r < static_cast<long long>(p.Tq) * p.Hq;
+  float d = 0.f, n = 0.f, m = 0.f;
+  if (ok) {
+    const long long t = r / p.Hq, h = r - t * p.Hq;
+    const uint4 a = reinterpret_cast<const uint4*>(static_cast<const X*>(p.dout) + r * D)[l],
+                b = reinterpret_cast<const uint4*>(static_cast<const X*>(p.out) + r * D)[l],
+                c = reinterpret_cast<const uint4*>(static_cast<const X*>(p.q) + t * p.q_st + h * p.q_sh)[l];
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 u = unpack_pair<X>(x[i]), v = unpack_pair<X>(y[i]);
+      const float2 u = unpack_pair<X>(x[i]), v = unpack_pair<X>(y[i]), w = unpack_pair<X>(z[i]);
       d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
       n = fmaf(u.x, u.x, fmaf(u.y, u.y, n));
+      m = fmaf(w.x, w.x, fmaf(w.y, w.y, m));
     }
   }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) {
     d += __shfl_xor_sync(0xffffffffu, d, o);
     n += __shfl_xor_sync(0xffffffffu, n, o);
+    m += __shfl_xor_sync(0xffffffffu, m, o);
   }
-  if (r < rows && l == 0) {
+  if (ok && l == 0) {
     delta[r] = d;
-    if (norm2 != nullptr) norm2[r] = n;
+    norm_do[r] = sqrtf(n);
+    norm_q[r] = sqrtf(m);
   }
 }
 
@@ -648,19 +648,32 @@ __global__ void __launch_bounds__(256) sparse_count_kernel(const WhoArgs f) {
     if (id >= 0) atomicAdd(count + id, 1u);
   }
 }
-// Counts become places within the block's entries; totals.
-__global__ void __launch_bounds__(256) sparse_scan_kernel(const WhoArgs f) {
-  const int id = blockIdx.x * 256 + threadIdx.x;
-  if (id >= f.n_blocks) return;
+// Counts become places within the block's entries; totals.  32 blocks of keys and
+// 32 runs of groups per block of threads: each thread adds up its run, the runs
+// before it give where it starts.
+__global__ void __launch_bounds__(1024) sparse_scan_kernel(const WhoArgs f) {
+  __shared__ uint32_t sums[32][33];
+  const int lane = threadIdx.x & 31, run = threadIdx.x / 32, id = blockIdx.x * 32 + lane;
+  const int per = (f.groups + 31) / 32, g0 = min(f.groups, run * per), g1 = min(f.groups, g0 + per);
+  uint32_t* c = f.count + id;
   uint32_t n = 0;
+  if (id < f.n_blocks) {
 #pragma unroll 8
-  for (int g = 0; g < f.groups; ++g) {
-    uint32_t* c = f.count + static_cast<long long>(g) * f.n_blocks + id;
-    const uint32_t x = *c;
-    *c = n;
-    n += x;
+    for (int g = g0; g < g1; ++g) n += c[static_cast<long long>(g) * f.n_blocks];
   }
-  f.total[id] = n;
+  sums[run][lane] = n;
+  __syncthreads();
+  if (id >= f.n_blocks) return;
+  n = 0;
+  for (int i = 0; i < run; ++i) n += sums[i][lane];
+#pragma unroll 8
+  for (int g = g0; g < g1; ++g) {
+    uint32_t& x = c[static_cast<long long>(g) * f.n_blocks];
+    const uint32_t y = x;
+    x = n;
+    n += y;
+  }
+  if (run == 31) f.total[id] = n;
 }
 // start = running sum of total: one block of threads.
 __global__ void __launch_bounds__(1024) sparse_start_kernel(const WhoArgs f) {
@@ -700,20 +713,19 @@ __global__ void __launch_bounds__(1024) sparse_start_kernel(const WhoArgs f) {
   }
   if (tid == 0) f.start[f.n_blocks] = before;
 }
-// A warp per group takes its rows in order, so that entries of a block ascend by
-// row (a block listed twice by a row: its two shares are equal).
-__global__ void __launch_bounds__(64) sparse_fill_kernel(const WhoArgs f) {
-  const int g = (blockIdx.x * 64 + threadIdx.x) / 32, lane = threadIdx.x & 31;
-  if (g >= f.groups) return;
+// A block of threads per group takes its rows in order, so that entries of a block
+// of keys ascend by row (one listed twice by a row: its two shares are equal).
+__global__ void __launch_bounds__(256) sparse_fill_kernel(const WhoArgs f) {
+  const int g = blockIdx.x;
   uint32_t* place = f.count + static_cast<long long>(g) * f.n_blocks;
   const int last = min(f.rows, (g + 1) * f.per);
   for (int r = g * f.per; r < last; ++r) {
     const ListRow row = find_list_row(f.p, f.t0 + r);
-    for (int u = lane; u < f.p.top_k; u += 32) {
+    for (int u = threadIdx.x; u < f.p.top_k; u += 256) {
       const int id = listed_block(f.p, row, f.t0 + r, u);
       if (id >= 0) f.entry[f.start[id] + atomicAdd(place + id, 1u)] = (static_cast<uint32_t>(r) << f.u_bits) | u;
     }
-    __syncwarp();
+    __syncthreads();
   }
 }
 
@@ -722,98 +734,106 @@ struct SumArgs {
   SparseParams p;
   int t0, rows, u_bits, n_z, s_pad;
   const uint32_t *start, *entry;
-  const void* share;
+  const __half* share;
+  const uint16_t* power;
   float* acc;           // [2][Tk][Hk][D]: sums of the rounds before (more than one round)
   int opens, closes;    // the first round, the last
 };
 
-// Four values of a share.
-template <typename T>
-__device__ __forceinline__ float4 load_share(const T* x) {
-  if constexpr (sizeof(T) == 4) {
-    return __ldcs(reinterpret_cast<const float4*>(x));
-  } else {
-    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(x));
-    const float2 a = unpack_pair<T>(u.x), b = unpack_pair<T>(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-}
-
-// dk, dv of key blockIdx.x, key head blockIdx.y: eight warps take every eighth
-// (sixteenth, D = 64) share, four values a lane; their sums are joined in order.
+// dk, dv of key blockIdx.x, key head blockIdx.y.  256 shares at a time: each
+// thread finds one, with its powers of two, then eight warps add 32 each, four
+// values a lane (D = 64: half a warp a share); the warps' sums are joined in order.
 template <typename X, int D>
 __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
-  using T = typename ShareType<X>::T;
-  constexpr int L = D / 4, PER = 32 / L, W = 8 * PER, U = 4;  // lanes of a share; shares of a warp, of the block; in flight
+  constexpr int L = D / 4, PER = 32 / L, W = 8 * PER, U = 8;  // lanes of a share; shares a warp, a block adds at once; in flight
+  struct Found {
+    long long at;  // first value of the share of dk; negative: none
+    float k, v;    // factors
+  };
+  __shared__ Found found[256];
+  __shared__ float4 red[2][W][L];
   const SparseParams& p = f.p;
   const int key = blockIdx.x, hk = blockIdx.y, tid = threadIdx.x, sub = tid / L, col = (tid % L) * 4;
-  __shared__ float4 red[2][W][L];
   float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-  auto add = [](float4& a, const float4& b) {
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
-  };
   const int seq = key_sequence(p, key);
-  if (seq >= 0) {
-    const SeqExt s = sparse_extent(p, seq);
-    const int j = key - s.k0, shift = s.lk - (s.q1 - s.q0) - s.q0;  // position of row t: t + shift
-    if (j >= 0 && j < s.lk) {
-      const long long share = 2ll * f.s_pad * D;  // elements of an item
-      const T* base = static_cast<const T*>(f.share) + static_cast<long long>(hk) * f.n_z * share + col;
-      // slot of row t0 + r: n shares, one after the other in groups of heads
-      auto shares = [&](const int (&r)[U], const int (&slot)[U], const bool (&ok)[U]) {
-        for (int z = 0; z < f.n_z; ++z) {
-          float4 a[U], b[U];
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ok[i]) {
-              const T* x = base + (static_cast<long long>(r[i]) * p.Hk * f.n_z + z) * share + static_cast<long long>(slot[i]) * D;
-              a[i] = load_share<T>(x);
-              b[i] = load_share<T>(x + static_cast<long long>(f.s_pad) * D);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            add(k, a[i]);
-            add(v, b[i]);
-          }
+  SeqExt s{0, 0, 0, 0};
+  if (seq >= 0) s = sparse_extent(p, seq);
+  const int j = key - s.k0, shift = s.lk - (s.q1 - s.q0) - s.q0;  // position of row t: t + shift
+  if (seq >= 0 && j >= 0 && j < s.lk) {
+    const int in = j & ((1 << p.block_shift) - 1);
+    uint32_t a = 0, n = 0;
+    if (p.top_k > 0) {
+      const int id = (s.k0 >> p.block_shift) + seq + (j >> p.block_shift);
+      a = f.start[id];
+      n = f.start[id + 1] - a;
+    }
+    // rows in whose window the key lies: positions j .. j + window - 1
+    const long long first = max(static_cast<long long>(max(s.q0, f.t0)), static_cast<long long>(j) - shift);
+    const long long end = min(static_cast<long long>(min(s.q1, f.t0 + f.rows)), static_cast<long long>(j) - shift + p.window);
+    const long long near = max(0ll, end - first), all = (static_cast<long long>(n) + near) * f.n_z;
+    const long long dv = static_cast<long long>(f.s_pad) * D;  // from a share of dk to that of dv
+    for (long long base = 0; base < all; base += 256) {
+      Found x{-1, 0.f, 0.f};
+      if (base + tid < all) {
+        // listed rows first, then those of the window; the groups of heads of a row one after the other
+        const long long e = (base + tid) / f.n_z;
+        const int z = static_cast<int>(base + tid - e * f.n_z);
+        int r, slot;
+        bool ok = true;
+        if (e < n) {
+          const uint32_t entry = f.entry[a + static_cast<uint32_t>(e)];
+          r = static_cast<int>(static_cast<uint64_t>(entry) >> f.u_bits);
+          slot = p.window + ((entry & ((1u << f.u_bits) - 1u)) << p.block_shift) + in;
+          ok = p.causal == 0 || j <= static_cast<long long>(f.t0 + r) + shift - p.window;
+        } else {
+          const long long t = first + (e - n);
+          r = static_cast<int>(t - f.t0);
+          slot = static_cast<int>(t + shift) - j;
         }
-      };
-      if (p.top_k > 0) {
-        const int id = (s.k0 >> p.block_shift) + seq + (j >> p.block_shift), in = j & ((1 << p.block_shift) - 1);
-        const uint32_t a = f.start[id], n = f.start[id + 1] - a;
-        for (uint32_t e = sub; e < n; e += W * U) {
-          int r[U], slot[U];
-          bool ok[U];
-#pragma unroll
-          for (int i = 0; i < U; ++i) {
-            ok[i] = e + i * W < n;
-            const uint32_t x = ok[i] ? f.entry[a + e + i * W] : 0u;
-            r[i] = static_cast<int>(x >> f.u_bits);
-            const int u = static_cast<int>(x & ((1u << f.u_bits) - 1u));
-            slot[i] = p.window + (u << p.block_shift) + in;
-            ok[i] = ok[i] && (p.causal == 0 || j <= f.t0 + r[i] + shift - p.window);
-          }
-          shares(r, slot, ok);
+        if (ok) {
+          const long long item = (static_cast<long long>(r) * p.Hk + hk) * f.n_z + z;
+          const uint32_t e2 = f.power[item * f.s_pad + slot];
+          x.at = 2 * item * dv + static_cast<long long>(slot) * D;
+          x.k = power_of_two(static_cast<int>(e2 & 255u) - 143);
+          x.v = power_of_two(static_cast<int>(e2 >> 8) - 143);
         }
       }
-      // rows in whose window the key lies: positions j .. j + window - 1
-      const long long first = max(static_cast<long long>(max(s.q0, f.t0)), static_cast<long long>(j) - shift);
-      const long long end = min(static_cast<long long>(min(s.q1, f.t0 + f.rows)), static_cast<long long>(j) - shift + p.window);
-      for (long long t = first + sub; t < end; t += W * U) {
-        int r[U], slot[U];
-        bool ok[U];
+      __syncthreads();
+      found[tid] = x;
+      __syncthreads();
+      const int most = static_cast<int>(min(256ll, all - base));
+#pragma unroll 1
+      for (int i = sub; i < most; i += W * U) {
+        uint2 rk[U], rv[U];
+        float fk[U], fv[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const long long x = t + i * W;
-          ok[i] = x < end;
-          r[i] = static_cast<int>(x - f.t0);
-          slot[i] = static_cast<int>(x + shift) - j;
+        for (int u = 0; u < U; ++u) {
+          const int at = i + u * W;
+          rk[u] = rv[u] = make_uint2(0u, 0u);
+          fk[u] = fv[u] = 0.f;
+          if (at < most) {
+            const Found y = found[at];
+            if (y.at >= 0) {
+              const __half* src = f.share + y.at + col;
+              rk[u] = __ldcs(reinterpret_cast<const uint2*>(src));
+              rv[u] = __ldcs(reinterpret_cast<const uint2*>(src + dv));
+              fk[u] = y.k;
+              fv[u] = y.v;
+            }
+          }
         }
-        shares(r, slot, ok);
+        auto add = [](float4& to, const uint2& r, float by) {
+          const float2 lo = unpack_pair<__half>(r.x), hi = unpack_pair<__half>(r.y);
+          to.x = fmaf(lo.x, by, to.x);
+          to.y = fmaf(lo.y, by, to.y);
+          to.z = fmaf(hi.x, by, to.z);
+          to.w = fmaf(hi.y, by, to.w);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          add(k, rk[u], fk[u]);
+          add(v, rv[u], fv[u]);
+        }
       }
     }
   }
@@ -823,11 +843,17 @@ __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
   if (tid >= 2 * L) return;
   const int which = tid / L;
   float4 x = red[which][0][tid % L];
+  auto join = [&](const float4& b) {
+    x.x += b.x;
+    x.y += b.y;
+    x.z += b.z;
+    x.w += b.w;
+  };
 #pragma unroll
-  for (int i = 1; i < W; ++i) add(x, red[which][i][tid % L]);
-  const long long at = (static_cast<long long>(key) * p.Hk + hk) * D + col;
+  for (int i = 1; i < W; ++i) join(red[which][i][tid % L]);
+  const long long at = (static_cast<long long>(key) * p.Hk + hk) * D + (tid % L) * 4;
   float* acc = f.acc + which * static_cast<long long>(p.Tk) * p.Hk * D + at;
-  if (!f.opens) add(x, *reinterpret_cast<const float4*>(acc));
+  if (!f.opens) join(*reinterpret_cast<const float4*>(acc));
   if (!f.closes) {
     *reinterpret_cast<float4*>(acc) = x;
     return;
@@ -841,7 +867,7 @@ __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
 // ----------------------------------------------------------------- plan and launches
 struct Plan {
   int heads, n_z, s_pad, rows, rounds, groups, per, n_blocks, u_bits;
-  size_t norm2, range, count, total, start, entry, acc, share, bytes;
+  size_t norm_do, norm_q, range, count, total, start, entry, power, acc, share, bytes;
 };
 Plan make_plan(const SparseParams& p, int dtype) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -851,7 +877,7 @@ Plan make_plan(const SparseParams& p, int dtype) {
   while (p.g / a.n_z > kHeads || p.g % a.n_z != 0) ++a.n_z;
   a.heads = p.g / a.n_z;
   a.s_pad = static_cast<int>((sparse_slots(p) + 127) / 128 * 128);
-  const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * (fp16 ? 4 : 2);
+  const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * 2;  // bytes of a row's shares
   a.u_bits = 0;
   while ((1ll << a.u_bits) < p.top_k) ++a.u_bits;
   long long rows = row == 0 ? p.Tq : static_cast<long long>(std::max<size_t>(1, kShareBytes / row));
@@ -867,13 +893,15 @@ Plan make_plan(const SparseParams& p, int dtype) {
   a.groups = (a.rows + a.per - 1) / a.per;
   const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
   const bool lists = p.top_k > 0;
-  a.norm2 = per_row;
-  a.range = a.norm2 + (fp16 ? per_row : 0);
+  a.norm_do = per_row;
+  a.norm_q = 2 * per_row;
+  a.range = 3 * per_row;
   a.count = up(a.range + (fp16 ? static_cast<size_t>(p.N) * p.Hk * 4 : 0));
   a.total = up(a.count + (lists ? static_cast<size_t>(a.groups) * a.n_blocks * 4 : 0));
   a.start = up(a.total + (lists ? static_cast<size_t>(a.n_blocks) * 4 : 0));
   a.entry = up(a.start + (lists ? static_cast<size_t>(a.n_blocks + 1) * 4 : 0));
-  a.acc = up(a.entry + static_cast<size_t>(a.rows) * p.top_k * 4);
+  a.power = up(a.entry + static_cast<size_t>(a.rows) * p.top_k * 4);
+  a.acc = up(a.power + static_cast<size_t>(a.rows) * p.Hk * a.n_z * a.s_pad * 2);
   a.share = a.acc + (a.rounds > 1 ? up(static_cast<size_t>(p.Tk) * p.Hk * p.D * 8) : 0);
   a.bytes = a.share + row * a.rows;
   return a;
@@ -885,7 +913,6 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   constexpr bool fp16 = !is_bf16<X>();
   float* delta = reinterpret_cast<float*>(ws);
-  float* norm2 = fp16 ? reinterpret_cast<float*>(ws + a.norm2) : nullptr;
   uint32_t* range = reinterpret_cast<uint32_t*>(ws + a.range);
   cudaError_t e;
   const size_t dkv = static_cast<size_t>(p.Tk) * p.Hk * D * sizeof(X);
@@ -895,8 +922,8 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   }
   const long long rows = static_cast<long long>(p.Tq) * p.Hq, blocks = (rows * (D / 8) + 255) / 256;
   if (blocks > 0x7FFFFFFFll || p.Hk > 65535) return cudaErrorInvalidValue;
-  sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-      static_cast<const X*>(p.dout), static_cast<const X*>(p.out), rows, delta, norm2);
+  float *norm_do = reinterpret_cast<float*>(ws + a.norm_do), *norm_q = reinterpret_cast<float*>(ws + a.norm_q);
+  sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, delta, norm_do, norm_q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (fp16 && p.N > 0) {
     if ((e = cudaMemsetAsync(range, 0, static_cast<size_t>(p.N) * p.Hk * 4, stream)) != cudaSuccess) return e;
@@ -916,9 +943,11 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   f.s_pad = a.s_pad;
   f.c = p.scale * 1.4426950408889634f;
   f.delta = delta;
-  f.norm2 = norm2;
+  f.norm_do = norm_do;
+  f.norm_q = norm_q;
   f.range = range;
-  f.share = ws + a.share;
+  f.share = reinterpret_cast<__half*>(ws + a.share);
+  f.power = reinterpret_cast<uint16_t*>(ws + a.power);
   f.wait_ns = attn_wait_ns(f.l.slots / 128 + 1);
   CUtensorMap tq, tdo;
   if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, a.heads) ||
@@ -943,6 +972,7 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   sum.start = who.start;
   sum.entry = who.entry;
   sum.share = f.share;
+  sum.power = f.power;
   sum.acc = reinterpret_cast<float*>(ws + a.acc);
   for (int i = 0; i < a.rounds; ++i) {
     const int t0 = i * a.rows, n = std::min(a.rows, p.Tq - t0);
@@ -954,9 +984,9 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
       if ((e = cudaMemsetAsync(who.count, 0, static_cast<size_t>(who.groups) * a.n_blocks * 4, stream)) != cudaSuccess)
         return e;
       sparse_count_kernel<<<static_cast<unsigned>((static_cast<long long>(n) * 32 + 255) / 256), 256, 0, stream>>>(who);
-      sparse_scan_kernel<<<(a.n_blocks + 255) / 256, 256, 0, stream>>>(who);
+      sparse_scan_kernel<<<(a.n_blocks + 31) / 32, 1024, 0, stream>>>(who);
       sparse_start_kernel<<<1, 1024, 0, stream>>>(who);
-      sparse_fill_kernel<<<(who.groups + 1) / 2, 64, 0, stream>>>(who);
+      sparse_fill_kernel<<<who.groups, 256, 0, stream>>>(who);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     kernel<<<static_cast<unsigned>(std::min(f.l.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, tdo, f);
