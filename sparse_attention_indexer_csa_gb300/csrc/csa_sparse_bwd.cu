@@ -41,7 +41,7 @@ namespace {
 
 constexpr size_t kShareBytes = 4ull << 30;
 constexpr int kHeads = 64;  // query heads of an item at most
-constexpr int kThreads = 640;
+constexpr int kLists = 2, kThreads = 640;
 constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14, kDrain2Warp = 16;
 
 template <typename X>
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= kListWarp && warp < kDrain2Warp) {
-    list_tiles(p, f.l, warp - kListWarp, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+    list_tiles<kLists>(p, f.l, warp - kListWarp, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp == kItemWarp) {
     // ------------------------------------------------------------------------- an item's queries, cotangents, statistics
     uint32_t ni = 0;
@@ -989,7 +989,9 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
       sparse_fill_kernel<<<who.groups, 256, 0, stream>>>(who);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    kernel<<<static_cast<unsigned>(std::min(f.l.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, tdo, f);
+    const long long grid = std::min(f.l.items, 152ll);
+    set_step(f.l, p.Hk, grid);
+    kernel<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kSmem, stream>>>(tq, tdo, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.Tk == 0) continue;
     sum.opens = i == 0;

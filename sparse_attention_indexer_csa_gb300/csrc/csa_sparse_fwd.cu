@@ -19,13 +19,13 @@
 // above it; fp16 weights are formed 2^kShift times their size, so that they
 // count down to 2^-32 of the reference's.
 //
-// Roles (16 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
+// Roles (18 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
 //   warps 0-3    softmax, one thread per row of S
 //   warps 4-7    outputs: join, division, stores, while the next item runs
 //   warps 8-9    loads of the listed keys' rows (and, by TMA, of the queries)
 //   warps 10-11  the same of the values' rows
 //   warps 12-13  issuers of the products with keys and with values, a thread each
-//   warps 14-15  lists: each writes the rows of every second tile, up to kRing tiles
+//   warps 14-17  lists: each writes the rows of every fourth tile, up to kRing tiles
 //                ahead
 // Rows are gathered by cp.async, 16 bytes a lane, into the layout that TMA would
 // write: hidden keys are never read, what fills up a tile is zero.  (Four warps get
@@ -46,7 +46,7 @@ template <typename X>
 constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
 constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
 
-constexpr int kThreads = 512;
+constexpr int kLists = 4, kThreads = 576;
 constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 10, kScoreWarp = 12, kMmaWarp = 13, kListWarp = 14;
 constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
 
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kListWarp) {
     const int w = warp - kListWarp;
-    list_tiles(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
+    list_tiles<kLists>(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp >= kKeyWarp && warp < kScoreWarp) {
     // ------------------------------------------------------------------------- rows of keys, of values
     const bool keys = warp < kValueWarp;
@@ -473,11 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <typename X, int D, int R, bool SPLIT>
-cudaError_t start(const FwdArgs& f, const CUtensorMap& tq, cudaStream_t stream) {
+cudaError_t start(FwdArgs f, const CUtensorMap& tq, cudaStream_t stream) {
   constexpr auto kernel = sparse_fwd_kernel<X, D, R, SPLIT>;
   const cudaError_t e = smem_limit_once<kernel>(Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<static_cast<unsigned>(std::min(f.l.items, 152ll)), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
+  const long long grid = std::min(f.l.items, 152ll);
+  set_step(f.l, f.p.Hk, grid);
+  kernel<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
   return cudaGetLastError();
 }
 

@@ -24,6 +24,7 @@ inline bool make_heads_map(CUtensorMap* m, const SparseParams& p, const void* x,
 // cache), the row's position, the sequence's number (-1: none, lk = 0).
 struct ListRow {
   int seq, k0, lk, pos;
+  int q0, q1;  // the sequence's rows
 };
 
 // Extents of sequence i, clamped to the tensors; what was clamped is recorded.
@@ -59,7 +60,7 @@ __device__ __forceinline__ SeqExt sparse_extent(const SparseParams& p, int i) {
 // by 32 probes at a time.  Entries out of order give some sequence or none.
 __device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
   const int lane = static_cast<int>(lane_id());
-  ListRow r{-1, 0, 0, -1};
+  ListRow r{-1, 0, 0, -1, 0, 0};
   if (p.N <= 0) return r;
   int lo = static_cast<int>(static_cast<long long>(t) * p.N / p.Tq);
   if (t < p.cu_q[lo] || t >= p.cu_q[lo + 1]) {
@@ -82,6 +83,8 @@ __device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
   const SeqExt s = sparse_extent(p, lo);
   if (t < s.q0 || t >= s.q1) return r;
   r.seq = lo;
+  r.q0 = s.q0;
+  r.q1 = s.q1;
   r.k0 = s.k0;
   r.lk = s.lk;
   r.pos = p.causal ? t - s.q0 + s.lk - (s.q1 - s.q0) : s.lk - 1;
@@ -132,7 +135,7 @@ __device__ __forceinline__ bool slot_rows(const SparseParams& p, const ListRow& 
   return true;
 }
 
-constexpr int kLists = 2, kRing = 8;  // warps that write lists; tiles of rows ahead
+constexpr int kRing = 8;  // tiles of rows ahead
 
 // What the CTAs of a launch walk: items blockIdx.x + n gridDim.x, an item being
 // row t0 + item / (n_z Hk), a key head and one of n_z parts.
@@ -141,7 +144,13 @@ struct ListArgs {
   int t0, n_z;
   int split;        // the parts are shares of the row's list (tiles z, z + n_z, ..); else all have the whole list
   int slots, per;   // of a row's list; its tiles (of an item)
+  int dt, dh, dz;   // from an item to the CTA's next one: gridDim.x in rows, key heads and parts
 };
+inline void set_step(ListArgs& l, int Hk, long long grid) {
+  l.dz = static_cast<int>(grid % l.n_z);
+  l.dh = static_cast<int>(grid / l.n_z % Hk);
+  l.dt = static_cast<int>(grid / l.n_z / Hk);
+}
 
 // 128 slots of an item's list: the rows of those that are keys (-1: none), a bit
 // for each of them, and n: one more than the last of them (0: none).  A hidden or
@@ -169,65 +178,141 @@ __device__ __forceinline__ long long tile_count(const ListArgs& f) {
   return (f.items - blockIdx.x + gridDim.x - 1) / gridDim.x * f.per;
 }
 
-// Writes the tiles w, w + kLists, .. of this CTA into the ring.  A warp.
-__device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs& f, int w, Tile* ring, uint64_t* full, uint64_t* free_bar,
-                                           const WaitCtl& ctl) {
+// Writes the tiles w, w + LISTS, .. of this CTA into the ring.  A warp; a lane has
+// four consecutive slots, whose keys follow one another where blocks and window
+// allow it (one block, one page for the four).  A list warp must keep up with the
+// tensor cores: with a block, a page and 64-bit divisions for each slot, two of them
+// took 1700 cycles a tile, all that a prompt of 8192 tokens had.
+template <int LISTS>
+__device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs& f, int w, Tile* ring, uint64_t* full,
+                                           uint64_t* free_bar, const WaitCtl& ctl) {
   const int lane = static_cast<int>(lane_id());
   bool bad = false;
   if (blockIdx.x == 0 && w == 0)
     for (int i = lane; i < p.N; i += 32) sparse_extent(p, i);  // what is out of order or range is recorded
   const long long tiles = tile_count(f);
-  // the coming tile: its item, its place in the item, its row and the blocks that its slots list
-  long long item = blockIdx.x + static_cast<long long>(w / f.per) * gridDim.x;
-  int at = w % f.per, t = 0, hk = 0, z = 0, b[4];
+  const bool quads = p.block_shift >= 2 && (p.window & 3) == 0 && (p.page == 0 || ((p.page & 3) == 0 && p.window == 0));
+  // the coming tile: its row, key head and part, its place in the item, the blocks that its slots list
+  int at = w % f.per, t, hk, z, b[4];
+  {
+    const long long item = blockIdx.x + static_cast<long long>(w / f.per) * gridDim.x, rest = item / f.n_z, token = rest / p.Hk;
+    z = static_cast<int>(item - rest * f.n_z);
+    hk = static_cast<int>(rest - token * p.Hk);
+    t = f.t0 + static_cast<int>(token);
+  }
   auto tile = [&] { return f.split ? at * f.n_z + z : at; };
   auto blocks = [&] {
-    const long long rest = item / f.n_z, token = rest / p.Hk;
-    z = static_cast<int>(item - rest * f.n_z);
-    t = f.t0 + static_cast<int>(token);
-    hk = static_cast<int>(rest - token * p.Hk);
     const int32_t* list = p.idx + t * p.idx_st;
+    const int s = tile() * 128 + 4 * lane;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = slot_block(p, list, tile() * 128 + 32 * i + lane, f.slots);
+    for (int i = 0; i < 4; ++i)
+      if (i == 0 || !quads) b[i] = slot_block(p, list, s + i, f.slots);
   };
-  ListRow row{-1, 0, 0, -1};
-  int row_t = -1;
+  ListRow row{-1, 0, 0, -1, 0, 0};
   if (w < tiles) blocks();
-  for (long long n = w; n < tiles; n += kLists) {
-    const uint32_t st = static_cast<uint32_t>(n % kRing), turn = static_cast<uint32_t>(n / kRing) & 1u;
-    if (t != row_t) row = find_list_row(p, t);
-    row_t = t;
-    Slot x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = Slot{-1, 0};
-      if (row.lk > 0 && row.pos >= 0)
-        x[i] = slot_key(p, row, tile() * 128 + 32 * i + lane, f.slots, b[i], bad);
-    }
+  uint32_t st = static_cast<uint32_t>(w) % kRing, turn = static_cast<uint32_t>(w) / kRing & 1u;
+  for (long long n = w; n < tiles; n += LISTS) {
+    if (t >= row.q0 && t < row.q1)  // mostly the sequence of the row before
+      row.pos = p.causal ? t - row.q0 + row.lk - (row.q1 - row.q0) : row.lk - 1;
+    else
+      row = find_list_row(p, t);
     TileHead h{0, at == f.per - 1, t, hk, z, tile(), row.seq};
-    const int k0 = hk * p.k.rh, v0 = hk * p.v.rh;
-    at += kLists;
+    const int s = h.c * 128 + 4 * lane, k0 = hk * p.k.rh, v0 = hk * p.v.rh;
+    int kr[4], vr[4];
+    uint32_t see = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kr[i] = vr[i] = -1;
+    if (row.lk > 0 && row.pos >= 0) {
+      if (quads) {
+        int j = 0, first = 0, last = 0, step = 1;  // slot i is key j + i * step where first <= i < last
+        if (s < p.window) {
+          j = row.pos - s;
+          last = j + 1;
+          step = -1;
+        } else if (s < f.slots) {
+          if (static_cast<unsigned>(b[0]) <= static_cast<unsigned>((row.lk - 1) >> p.block_shift)) {
+            j = (b[0] << p.block_shift) + ((s - p.window) & ((1 << p.block_shift) - 1));
+            last = min(row.lk, row.pos - p.window + 1) - j;
+          } else {
+            bad |= b[0] != -1;
+          }
+        }
+        int kb = row.k0 + j, vb = kb;
+        if (p.page > 0) {
+          kb = vb = 0;
+          if (last > 0) {
+            const int n_page = j / p.page, pg = p.table[row.seq * p.table_st + n_page], off = j - n_page * p.page;
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.pages)) {
+              bad = true;
+              last = 0;
+            } else {
+              kb = pg * p.k.rp + off * p.k.rt;
+              vb = pg * p.v.rp + off * p.v.rt;
+            }
+          }
+        } else {
+          kb *= p.k.rt;
+          vb *= p.v.rt;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i >= first && i < last) {
+            kr[i] = kb + i * step * p.k.rt + k0;
+            vr[i] = vb + i * step * p.v.rt + v0;
+            see |= 1u << i;
+          }
+      } else {
+        Slot x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = slot_key(p, row, s + i, f.slots, b[i], bad);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int a = 0, c = 0;
+          if (slot_rows(p, row, x[i], a, c, bad)) {
+            kr[i] = a + k0;
+            vr[i] = c + v0;
+            see |= 1u << i;
+          }
+        }
+      }
+    }
+    at += LISTS;
     while (at >= f.per) {
       at -= f.per;
-      item += gridDim.x;
+      z += f.dz;
+      hk += f.dh;
+      t += f.dt;
+      if (z >= f.n_z) {
+        z -= f.n_z;
+        ++hk;
+      }
+      if (hk >= p.Hk) {
+        hk -= p.Hk;
+        ++t;
+      }
     }
-    if (n + kLists < tiles) blocks();
-    if (!bar_wait(free_bar + st, turn ^ 1u, ctl)) break;
-    uint32_t mine = 0u;
+    if (n + LISTS < tiles) blocks();
+    uint32_t word = see << (4 * (lane & 7));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int kr = 0, vr = 0;
-      const bool see = slot_rows(p, row, x[i], kr, vr, bad);
-      const unsigned all = __ballot_sync(0xffffffffu, see);
-      if (all != 0u) h.n = 32 * i + 32 - __clz(static_cast<int>(all));
-      if (lane == i) mine = all;
-      ring[st].k_row[32 * i + lane] = see ? kr + k0 : -1;
-      ring[st].v_row[32 * i + lane] = see ? vr + v0 : -1;
+    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    const unsigned some = __ballot_sync(0xffffffffu, see != 0u);
+    if (some != 0u) {
+      const int top = 31 - __clz(static_cast<int>(some));
+      h.n = 4 * top + 32 - __clz(__shfl_sync(0xffffffffu, static_cast<int>(see), top));
     }
-    if (lane < 4) ring[st].keys[lane] = mine;
-    if (lane == 0) ring[st].h = h;
+    if (!bar_wait(free_bar + st, turn ^ 1u, ctl)) break;
+    Tile& to = ring[st];
+    reinterpret_cast<int4*>(to.k_row)[lane] = make_int4(kr[0], kr[1], kr[2], kr[3]);
+    reinterpret_cast<int4*>(to.v_row)[lane] = make_int4(vr[0], vr[1], vr[2], vr[3]);
+    if ((lane & 7) == 0) to.keys[lane >> 3] = word;
+    if (lane == 0) to.h = h;
     __syncwarp();
     if (lane == 0) mbar_arrive(full + st);
+    st += LISTS;
+    if (st >= kRing) {
+      st -= kRing;
+      turn ^= 1u;
+    }
   }
   if (bad) record_error(kErrDevice);
 }
