@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool alive = true, first = true, got_dq = false, pend_first = false;
     int pend = 0;  // the last key of the tile whose P and dS are to come
     uint32_t j = 0, nq = 0, on = 0;
-    auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
+    auto wait = [&](int bar, uint32_t parity) { alive = alive && bar_wait(bars + bar, parity, ctl); };
     auto shares = [&] {  // dV, dK of the last tile
       const uint32_t i = j - 1;
       wait(C::kBarP, i & 1u);

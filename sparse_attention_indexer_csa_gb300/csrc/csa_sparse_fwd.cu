@@ -19,13 +19,13 @@
 // above it; fp16 weights are formed 2^kShift times their size, so that they
 // count down to 2^-32 of the reference's.
 //
-// Roles (18 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
+// Roles (20 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
 //   warps 0-3    softmax, one thread per row of S
 //   warps 4-7    outputs: join, division, stores, while the next item runs
-//   warps 8-9    loads of the listed keys' rows (and, by TMA, of the queries)
-//   warps 10-11  the same of the values' rows
-//   warps 12-13  issuers of the products with keys and with values, a thread each
-//   warps 14-17  lists: each writes the rows of every fourth tile, up to kRing tiles
+//   warps 8-11   loads of the listed keys' rows (and, by TMA, of the queries)
+//   warps 12-15  the same of the values' rows
+//   warps 16-17  issuers of the products with keys and with values, a thread each
+//   warps 18-19  lists: each writes the rows of every second tile, up to kRing tiles
 //                ahead
 // Rows are gathered by cp.async, 16 bytes a lane, into the layout that TMA would
 // write: hidden keys are never read, what fills up a tile is zero.  (Four warps get
@@ -46,8 +46,8 @@ template <typename X>
 constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
 constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
 
-constexpr int kLists = 4, kThreads = 576;
-constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 10, kScoreWarp = 12, kMmaWarp = 13, kListWarp = 14;
+constexpr int kLists = 2, kThreads = 640;
+constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 12, kScoreWarp = 16, kMmaWarp = 17, kListWarp = 18;
 constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
 
 template <int D>
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4;
       if (i >= C::kBarOFree && i < C::kBarOFree + 2) n = 4;
       if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
-      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 14;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 18;
       if (i == C::kBarDone) n = 2;
       if (i == C::kBarMeet) n = 4;
       mbar_init(bars + i, n);
@@ -135,28 +135,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     list_tiles<kLists>(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp >= kKeyWarp && warp < kScoreWarp) {
     // ------------------------------------------------------------------------- rows of keys, of values
+    // Two warps for each stage: a tile takes one of them 2000 cycles (the lists'
+    // ring, 32 copies, their way, the fence), which two tiles of work hide.
     const bool keys = warp < kValueWarp;
+    const uint32_t stage = (warp >> 1) & 1u;
     const int r0 = 64 * (warp & 1);
     const GatherRows& rows = keys ? p.k : p.v;
-    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV);
+    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV) + stage;
     // a stage is free when the product that read it has completed
-    uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv);
-    uint8_t* stages = base + (keys ? C::kOffK : C::kOffV);
+    uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv) + stage;
+    uint8_t* tile = base + (keys ? C::kOffK : C::kOffV) + stage * C::kTile;
     uint32_t j = 0, nq = 0;
-    bool flying = false;  // tile j - 1 has been asked for and not been reported
-    bool first = true;    // no tile of this item yet
-    auto report = [&](uint32_t i) {
-      if (lane == 0) mbar_arrive(full + (i & 1u));
-    };
+    bool first = true;  // no tile of this item yet
     while (true) {
-      // the next tile is asked for before the one in flight is waited for, unless that would block
-      const bool go = n_tile != tiles && mbar_test_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u) &&
-                      (j < 2 || mbar_test_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u));
-      if (flying && __any_sync(0xffffffffu, !go)) {
-        loaded<0>();
-        report(j - 1);
-        flying = false;
-      }
       const TileHead h = next_head();
       if (h.n < 0) break;
       if (h.n > 0) {
@@ -174,34 +165,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           ++nq;
         }
-        if (j >= 2 && !bar_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u, ctl)) break;
-        __syncwarp();
-        const Tile& tile = ring[n_tile % kRing];
-        load_rows<D>(stages + (j & 1u) * C::kTile, rows, keys ? tile.k_row : tile.v_row, r0, (h.n + 15) & ~15);
-        if (flying) {
-          loaded<1>();
-          report(j - 1);
-        }
-        flying = true;
         first = false;
+        if ((j & 1u) == stage) {
+          if (!bar_wait(used, ((j >> 1) & 1u) ^ 1u, ctl)) break;
+          const Tile& from = ring[n_tile % kRing];
+          load_rows<D>(tile, rows, keys ? from.k_row : from.v_row, r0, (h.n + 15) & ~15);
+          loaded<0>();
+          if (lane == 0) mbar_arrive(full);
+        }
         ++j;
       }
       if (h.last) first = true;
       give_head();
     }
-    // no copy is in flight when the CTA ends, a role's giving up included
-    loaded<0>();
-    if (flying) report(j - 1);
+    loaded<0>();  // no copy is in flight when the CTA ends, a role's giving up included
     for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) bar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
   } else if (warp == kScoreWarp || warp == kMmaWarp) {
     // ------------------------------------------------------------------------- issuers of the products
-    // Each warp runs as one (uniform operands), one elected thread issues.  Two
-    // of them, so that neither's waits hold up the other's products: with one for
+    // Each warp runs as one (uniform operands), one elected thread issues.  (They do
+    // not poll: that takes the issue slots of the warps beside them, 598 us for 500.)  Two of them, so that neither's waits hold up the other's products: with one for
     // both, a tile took 2400 cycles of which the tensor cores had work for 1000.
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     constexpr uint32_t kT = C::kTile >> 4;
     bool alive = true, first = true;
-    auto wait = [&](int bar, uint32_t parity) { alive = alive && mbar_spin_warp(bars + bar, parity, ctl); };
+    auto wait = [&](int bar, uint32_t parity) { alive = alive && bar_wait(bars + bar, parity, ctl); };
     uint32_t j = 0;
     if (warp == kScoreWarp) {
       const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128);

@@ -167,10 +167,27 @@ struct Tile {
 
 static_assert(sizeof(Tile) % 16 == 0, "tiles of a ring");
 
-// As mbar_wait, its slow part out of line: sixteen warps in seven roles run here,
-// and what they wait for is instructions.
+// As mbar_wait, its slow part out of line (sixteen warps and more in seven roles
+// run here, and what they wait for is instructions), and without a time for which
+// the thread may be suspended: a thread that gives one comes back later.
+static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try_wait_u32(bar, parity)) return true;
+    if (*ctl.abort_flag) return false;
+    if ((n & 15u) == 0u) {
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > ctl.limit_ns) {
+        *ctl.abort_flag = 1u;
+        record_error(kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  return mbar_wait_u32(smem_u32(bar), parity, ctl);
+  return mbar_try_wait_u32(smem_u32(bar), parity) || bar_wait_slow(smem_u32(bar), parity, ctl);
 }
 
 // The tiles of a CTA: items blockIdx.x + n gridDim.x, `per` tiles each.
@@ -317,43 +334,45 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
   if (bad) record_error(kErrDevice);
 }
 
-// 64 rows of a tile (from row r0 on, as far as n of the tile) by a warp.  Whole
-// stretches go without a branch or a size of their own, eight copies in a row: a
-// copy that waits for its registers' former use takes 140 cycles instead of 40.
+// 64 rows of a tile (from row r0 on, as far as n, a multiple of 16) by a warp,
+// eight copies in a row: a copy that waits for its registers' former use takes
+// 140 cycles instead of 40.  Empty slots read as zero; copies that may have one have
+// a size of their own, which costs them a quarter more.
 template <int D>
 __device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, const int* rows, int r0, int n) {
-  constexpr int P = D / 8, PER = 32 / P;  // 16-byte pieces of a row; rows an instruction takes
+  constexpr int P = D / 8, PER = 32 / P, STEP = 8 * PER;  // 16-byte pieces of a row; rows an instruction takes, and eight
   const int lane = static_cast<int>(lane_id());
   const int mine[2] = {r0 + lane < n ? rows[r0 + lane] : -1, r0 + 32 + lane < n ? rows[r0 + 32 + lane] : -1};
+  const uint32_t ok[2] = {__ballot_sync(0xffffffffu, mine[0] >= 0), __ballot_sync(0xffffffffu, mine[1] >= 0)};
   const int piece = lane % P, sub = lane / P;
   const char* base = static_cast<const char*>(g.base) + piece * 16;
   const uint32_t dst = smem_u32(tile) + (piece >> 3) * kChunkBytes + (r0 + sub) * 128;
   uint32_t at[8 / PER];  // the swizzle repeats every eight rows
 #pragma unroll
   for (int i = 0; i < 8 / PER; ++i) at[i] = dst + (((piece & 7) ^ ((PER * i + sub) & 7)) * 16);
-  if (__all_sync(0xffffffffu, (mine[0] | mine[1]) >= 0)) {
 #pragma unroll 1
-    for (int h = 0; h < 64; h += 8 * PER) {
-      const char* src[8];
-      const int from = h < 32 ? mine[0] : mine[1];
+  for (int h = 0; h < 64 && r0 + h < n; h += STEP) {
+    const int from = h < 32 ? mine[0] : mine[1];
+    const uint32_t there = (h < 32 ? ok[0] : ok[1]) >> (h & 31);
+    const char* src[8];
+    uint32_t size[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = __shfl_sync(0xffffffffu, from, (h + PER * i + sub) & 31);
-        src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(row)) * g.unit_bytes;
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int row = __shfl_sync(0xffffffffu, from, (h + PER * i + sub) & 31);
+      src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * g.unit_bytes;
+      size[i] = row < 0 ? 0u : 16u;
+    }
+    if ((~there & low_bits(STEP)) == 0u) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128), "l"(src[i])
                      : "memory");
-    }
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 64 / PER && r0 + PER * i < n; ++i) {  // n is a multiple of 16
-      const int r = PER * i + sub;
-      const int row = __shfl_sync(0xffffffffu, PER * i < 32 ? mine[0] : mine[1], r & 31);
-      const char* src = base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * g.unit_bytes;
-      const uint32_t to = dst + PER * i * 128 + (((piece & 7) ^ (r & 7)) * 16);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(row < 0 ? 0 : 16) : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128),
+                     "l"(src[i]), "r"(size[i])
+                     : "memory");
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
