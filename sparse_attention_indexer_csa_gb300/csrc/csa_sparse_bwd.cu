@@ -180,17 +180,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl ctl{abort_flag, f.wait_ns};
   volatile uint32_t dummy = 0;
   const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
-  unsigned long long n_tile = 0;
-  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f.l));
+  Place at(f.l);
   auto next_head = [&]() -> TileHead {
-    if (n_tile == tiles || !bar_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u, ctl))
-      return TileHead{-1, 0, 0, 0, 0, 0, 0};
-    return ring[n_tile % kRing].h;
+    if (at.left == 0 || !bar_wait(bars + C::kBarTile + at.slot, at.parity, ctl)) return TileHead{-1, 0, 0, 0, 0, 0, 0};
+    return ring[at.slot].h;
   };
   auto give_head = [&] {  // by a role's warp
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + n_tile % kRing);
-    ++n_tile;
+    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + at.slot);
+    at.next();
   };
 
   if (warp >= kListWarp && warp < kDrain2Warp) {
@@ -259,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(full + (i & 1u));
     };
     while (true) {
-      const bool go = n_tile != tiles && mbar_test_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u) &&
+      const bool go = at.left != 0 && mbar_test_wait(bars + C::kBarTile + at.slot, at.parity) &&
                       (j < 2 || mbar_test_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u));
       if (flying && __any_sync(0xffffffffu, !go)) {
         loaded<0>();
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (h.n > 0) {
         if (j >= 2 && !bar_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u, ctl)) break;
         __syncwarp();
-        const Tile& tile = ring[n_tile % kRing];
+        const Tile& tile = ring[at.slot];
         load_rows<D>(stages + (j & 1u) * C::kTile, rows, keys ? tile.k_row : tile.v_row, r0, (h.n + 15) & ~15);
         if (flying) {
           loaded<1>();
@@ -422,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the former tile's product with K has read dS
         if (j > 0 && !bar_wait(bars + C::kBarKFree + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl)) break;
         tc_fence_after();
-        const bool see = (ring[n_tile % kRing].keys[warp] >> lane) & 1u;
+        const bool see = (ring[at.slot].keys[warp] >> lane) & 1u;
         const float4* ls = stat + (ni & 1u) * kHeads;
         float2 bk = make_float2(0.f, 0.f), bv = bk;  // bounds of the key's shares
 #pragma unroll 1
@@ -484,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (h.n < 0) break;
       if (h.n > 0) {
         first = false;
-        const uint32_t see = ring[n_tile % kRing].keys[w];
+        const uint32_t see = ring[at.slot].keys[w];
         if (!bar_wait(bars + C::kBarD, j & 1u, ctl)) break;
         tc_fence_after();
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;

@@ -19,8 +19,12 @@
 // above it; fp16 weights are formed 2^kShift times their size, so that they
 // count down to 2^-32 of the reference's.
 //
-// Roles (20 warps, one CTA per SM, walking items blockIdx.x + n gridDim.x):
-//   warps 0-3    softmax, one thread per row of S
+// Roles (20 warps, R = 1 and 2: 24, one CTA per SM, walking items blockIdx.x + n
+// gridDim.x):
+//   warps 0-3    softmax, one thread per row of S; R = 1 and 2: warps 20-23 have the
+//                second half of a copy's columns, and the two exchange the tile's
+//                largest score (64 columns in one thread: 1750 cycles a tile, a
+//                prompt of 16384 tokens with 64 heads PROMPT1 us; in two: PROMPT2)
 //   warps 4-7    outputs: join, division, stores, while the next item runs
 //   warps 8-11   loads of the listed keys' rows (and, by TMA, of the queries)
 //   warps 12-15  the same of the values' rows
@@ -46,8 +50,12 @@ template <typename X>
 constexpr float kShift = is_bf16<X>() ? 0.f : 8.f;
 constexpr float kRaise = 6.f;  // P stays below 2^(kShift + kRaise)
 
-constexpr int kLists = 2, kThreads = 640;
-constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 12, kScoreWarp = 16, kMmaWarp = 17, kListWarp = 18;
+constexpr int kLists = 2;
+constexpr int kOutWarp = 4, kKeyWarp = 8, kValueWarp = 12, kScoreWarp = 16, kMmaWarp = 17, kListWarp = 18, kHalfWarp = 20;
+template <int R>
+constexpr int kHalves = R == 4 ? 1 : 2;  // softmax threads of a row
+template <int R>
+constexpr int kThreads = 32 * (kHalfWarp + 4 * (kHalves<R> - 1));
 constexpr int kPitch = 36;    // floats between two rows of staged outputs (32 columns)
 
 template <int D>
@@ -55,11 +63,13 @@ struct Cfg {
   static constexpr uint32_t kTile = kChunkBytes * (D / 64);  // 128 rows x D
   static constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffOut = 6 * kTile;
   static constexpr uint32_t kOffRing = kOffOut + 128 * kPitch * 4;
-  static constexpr uint32_t kOffMl = kOffRing + kRing * sizeof(Tile);  // [2][2][128] floats: m, l of two items
-  static constexpr uint32_t kOffBar = kOffMl + 2 * 2 * 128 * 4;
+  static constexpr uint32_t kOffMl = kOffRing + kRing * sizeof(Tile);  // [2][3][128] floats: m, l of two items (l by halves)
+  static constexpr uint32_t kOffTop = kOffMl + 2 * 3 * 128 * 4;          // [2][2][128] floats: a tile's largest scores
+  static constexpr uint32_t kOffItem = kOffTop + 2 * 2 * 128 * 4;          // [2] items whose outputs are to come
+  static constexpr uint32_t kOffBar = kOffItem + 64;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarK = 4, kBarV = 6, kBarS = 8, kBarP = 10, kBarPv = 12, kBarO = 14,
                        kBarMl = 16, kBarOFree = 18, kBarTile = 20, kBarTileFree = kBarTile + kRing,
-                       kBarMeet = kBarTileFree + kRing, kBarDone = kBarMeet + 1, kBars = kBarDone + 1;
+                       kBarMeet = kBarTileFree + kRing, kBarPair = kBarMeet + 1, kBarDone = kBarPair + 4, kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
 };
 static_assert(Cfg<128>::kSmem <= 227 * 1024, "one CTA per SM");
@@ -75,10 +85,11 @@ struct FwdArgs {
 };
 
 template <typename X, int D, int R, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<R>, 1)
     sparse_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ FwdArgs f) {
   using C = Cfg<D>;
   constexpr int G = 128 / R, CW = 128 / R;  // rows of a copy of the queries; columns that a copy takes
+  constexpr int H = kHalves<R>, TW = CW / H;  // columns of a softmax thread
   extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
@@ -91,11 +102,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kBars; ++i) {
       int n = 1;
-      if (i >= C::kBarP && i < C::kBarP + 2) n = 4;
-      if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4;
+      if (i >= C::kBarP && i < C::kBarP + 2) n = 4 * H;
+      if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4 * H;
+      if (i >= C::kBarPair && i < C::kBarPair + 4) n = 2;
       if (i >= C::kBarOFree && i < C::kBarOFree + 2) n = 4;
       if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
-      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 18;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 10 + 4 * H;
       if (i == C::kBarDone) n = 2;
       if (i == C::kBarMeet) n = 4;
       mbar_init(bars + i, n);
@@ -117,20 +129,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t dummy = 0;
   const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
   // the next tile; n < 0 after the last one or a wait that gave up
-  unsigned long long n_tile = 0;
-  const unsigned long long tiles = static_cast<unsigned long long>(tile_count(f.l));
+  Place at(f.l);
   auto next_head = [&]() -> TileHead {
-    if (n_tile == tiles || !bar_wait(bars + C::kBarTile + n_tile % kRing, (n_tile / kRing) & 1u, ctl))
-      return TileHead{-1, 0, 0, 0, 0, 0, 0};
-    return ring[n_tile % kRing].h;
+    if (at.left == 0 || !bar_wait(bars + C::kBarTile + at.slot, at.parity, ctl)) return TileHead{-1, 0, 0, 0, 0, 0, 0};
+    return ring[at.slot].h;
   };
   auto give_head = [&] {  // by a role's warp
     __syncwarp();
-    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + n_tile % kRing);
-    ++n_tile;
+    if (lane == 0) mbar_arrive(bars + C::kBarTileFree + at.slot);
+    at.next();
   };
 
-  if (warp >= kListWarp) {
+  if (warp >= kListWarp && warp < kHalfWarp) {
     const int w = warp - kListWarp;
     list_tiles<kLists>(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp >= kKeyWarp && warp < kScoreWarp) {
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = false;
         if ((j & 1u) == stage) {
           if (!bar_wait(used, ((j >> 1) & 1u) ^ 1u, ctl)) break;
-          const Tile& from = ring[n_tile % kRing];
+          const Tile& from = ring[at.slot];
           load_rows<D>(tile, rows, keys ? from.k_row : from.v_row, r0, (h.n + 15) & ~15);
           loaded<0>();
           if (lane == 0) mbar_arrive(full);
@@ -270,14 +280,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) umma_commit(bars + C::kBarDone);
     __syncwarp();
     bar_wait(bars + C::kBarDone, 0u, drain);
-  } else if (warp < kOutWarp) {
+  } else if (warp < kOutWarp || warp >= kHalfWarp) {
     // ------------------------------------------------------------------------- softmax
-    const int row = warp * 32 + static_cast<int>(lane), copy = row / G, col0 = copy * CW;
+    const int half = warp < kOutWarp ? 0 : 1, quarter = warp & 3;
+    const int row = quarter * 32 + static_cast<int>(lane), copy = row / G, col0 = copy * CW + half * TW;
     const bool used = row % G < p.g;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     float* ml = reinterpret_cast<float*>(base + C::kOffMl);
+    float* tops = reinterpret_cast<float*>(base + C::kOffTop);
+    TileHead* done_items = reinterpret_cast<TileHead*>(base + C::kOffItem);
     const float c = f.c;
-    uint32_t j = 0, on = 0;
+    uint32_t j = 0, on = 0, met = 0;
+    auto meet_half = [&] {  // with the warp that has the other half of these rows
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarPair + quarter);
+      const bool here = bar_wait(bars + C::kBarPair + quarter, met, ctl);
+      met ^= 1u;
+      return here;
+    };
     float m = -INFINITY, l = 0.f;
     bool ok = true, first = true;
     while (ok) {
@@ -289,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t ts = tmem + lanes + st * 128u;
-        const uint32_t* keys = ring[n_tile % kRing].keys + copy * (CW / 32);
+        const uint32_t* keys = ring[at.slot].keys + col0 / 32;
         float s[32];
         auto load = [&](int i) {  // 32 scores, those of no key at -inf
           tmem_ld32_start(ts + col0 + 32 * i, s);
@@ -304,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's largest score (NaN is passed over)
         float top = -INFINITY;
 #pragma unroll 1
-        for (int i = 0; i < CW / 32; ++i) {
+        for (int i = 0; i < TW / 32; ++i) {
           load(i);
           float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
@@ -315,10 +335,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           top = max3(top, a, b);
         }
         if (!used) top = -INFINITY;  // no query: what stands there asks for nothing
+        if constexpr (H == 2) {
+          tops[st * 256 + half * 128 + row] = top;
+          if (!(ok = meet_half())) break;
+          top = fmaxf(top, tops[st * 256 + (half ^ 1) * 128 + row]);
+        }
         if (first) {
           m = top;
           l = 0.f;
-        } else if (__any_sync(0xffffffffu, top * c > m * c + kRaise || (m == -INFINITY && top > m))) {
+        } else if (__any_sync(0xffffffffu, top * c > m * c + kRaise)) {
           // the former tile's product with V has to be through before O is rescaled
           ok = bar_wait(bars + C::kBarPv + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl);
           if (!ok) break;
@@ -328,29 +353,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= r;
           const uint32_t to = tmem + lanes + 256u + (on & 1u) * 128u;
 #pragma unroll 1
-          for (int i = 0; i < D / 16; ++i) tmem_scale16(to + 16 * i, r);
+          for (int i = half; i < D / 16; i += H) tmem_scale16(to + 16 * i, r);
         }
         const float ref = (m == -INFINITY ? 0.f : m) * c, bias = kShift<X> - ref;
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int i = 0; i < CW / 32; ++i) {
-          if (CW > 32) load(i);  // (again; P of the columns before lies in columns that have been read)
-          uint32_t pk[16];
+        // P lies over S: of this thread's columns when they have been read; of the other half's, with which the
+        // reads of the first half's second 32 columns would collide, after a second meeting
+        uint32_t pk[TW / 32][16];
+        auto weights = [&](int i) {
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
             const float2 e = ffma2(make_float2(s[2 * u], s[2 * u + 1]), make_float2(c, c), make_float2(bias, bias));
             const float2 w = make_float2(exp2_approx(e.x), exp2_approx(e.y));
             sum = fadd2(sum, w);
-            pk[u] = pack_pair<X>(w.x, w.y);
+            pk[i][u] = pack_pair<X>(w.x, w.y);
           }
-          tmem_st16(ts + (col0 + 32 * i) / 2, pk);
+        };
+        if constexpr (TW == 32) {
+          weights(0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < TW / 32; ++i) {
+            load(i);
+            weights(i);
+          }
+          if (!(ok = meet_half())) break;
         }
+#pragma unroll
+        for (int i = 0; i < TW / 32; ++i) tmem_st16(ts + (col0 + 32 * i) / 2, pk[i]);
         l += sum.x + sum.y;
         if (R > 1) {  // the other copies' columns, as far as the product reads
           const uint32_t zero[16] = {};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (32 * i / CW != copy && 32 * i < h.n) tmem_st16(ts + 16 * i, zero);
+            if (32 * i / CW != copy && 32 * i < h.n && i % H == half) tmem_st16(ts + 16 * i, zero);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -361,9 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (h.last) {
         ok = bar_wait(bars + C::kBarOFree + (on & 1u), ((on >> 1) & 1u) ^ 1u, ctl);
-        float* mine = ml + (on & 1u) * 256;
-        mine[row] = m;
-        mine[128 + row] = l;
+        float* mine = ml + (on & 1u) * 384;
+        if (half == 0) mine[row] = m;
+        if (threadIdx.x == 0) done_items[on & 1u] = h;
+        mine[128 + half * 128 + row] = l;
         m = -INFINITY;
         l = 0.f;
         first = true;
@@ -386,21 +423,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_wait(bars + C::kBarMeet, met, ctl);
       met ^= 1u;
     };
-    while (true) {
-      const TileHead h = next_head();
-      if (h.n < 0) break;
-      if (h.last) {
+    for (long long left = item_count(f.l); left > 0; --left) {
+      {
         const uint32_t b = on & 1u;
-        if (!bar_wait(bars + C::kBarMl + b, (on >> 1) & 1u, ctl) || !bar_wait(bars + C::kBarO + b, (on >> 1) & 1u, ctl))
-          break;
+        if (!bar_wait(bars + C::kBarMl + b, (on >> 1) & 1u, ctl) || !bar_wait(bars + C::kBarO + b, (on >> 1) & 1u, ctl)) break;
+        const TileHead h = reinterpret_cast<const TileHead*>(base + C::kOffItem)[b];
         tc_fence_after();
-        const float* mm = ml + b * 256;
+        const float* mm = ml + b * 384;
         float top = -INFINITY, l = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r) top = fmaxf(top, mm[r * G + head]);
         const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-        for (int r = 0; r < R; ++r) l += mm[128 + r * G + head] * exp2_approx((mm[r * G + head] - ref) * f.c);
+        for (int r = 0; r < R; ++r)
+          l += (mm[128 + r * G + head] + (H == 2 ? mm[256 + r * G + head] : 0.f)) * exp2_approx((mm[r * G + head] - ref) * f.c);
         const bool seen = l > 0.f || l != l;
         const float weight = seen ? exp2_approx((mm[row] - ref) * f.c) / l : 0.f;
         const long long at = static_cast<long long>(h.t) * p.Hq + static_cast<long long>(h.hk) * p.g;
@@ -449,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bars + C::kBarOFree + b);
         ++on;
       }
-      give_head();
     }
   }
   __syncwarp();
@@ -466,7 +501,7 @@ cudaError_t start(FwdArgs f, const CUtensorMap& tq, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long grid = std::min(f.l.items, 152ll);
   set_step(f.l, f.p.Hk, grid);
-  kernel<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kSmem, stream>>>(tq, f);
+  kernel<<<static_cast<unsigned>(grid), kThreads<R>, Cfg<D>::kSmem, stream>>>(tq, f);
   return cudaGetLastError();
 }
 

@@ -190,10 +190,24 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, const W
   return mbar_try_wait_u32(smem_u32(bar), parity) || bar_wait_slow(smem_u32(bar), parity, ctl);
 }
 
-// The tiles of a CTA: items blockIdx.x + n gridDim.x, `per` tiles each.
-__device__ __forceinline__ long long tile_count(const ListArgs& f) {
-  return (f.items - blockIdx.x + gridDim.x - 1) / gridDim.x * f.per;
+// The items and tiles of a CTA: items blockIdx.x + n gridDim.x, `per` tiles each.
+__device__ __forceinline__ long long item_count(const ListArgs& f) {
+  return (f.items - blockIdx.x + gridDim.x - 1) / gridDim.x;
 }
+__device__ __forceinline__ long long tile_count(const ListArgs& f) { return item_count(f) * f.per; }
+
+// A role's place in the ring of tiles.
+struct Place {
+  long long left;  // tiles to come
+  uint32_t slot = 0, parity = 0;
+  __device__ __forceinline__ explicit Place(const ListArgs& f) : left(tile_count(f)) {}
+  __device__ __forceinline__ void next() {
+    --left;
+    slot = (slot + 1u) & (kRing - 1u);
+    if (slot == 0u) parity ^= 1u;
+  }
+};
+static_assert((kRing & (kRing - 1)) == 0, "Place");
 
 // Writes the tiles w, w + LISTS, .. of this CTA into the ring.  A warp; a lane has
 // four consecutive slots, whose keys follow one another where blocks and window
@@ -334,46 +348,42 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
   if (bad) record_error(kErrDevice);
 }
 
-// 64 rows of a tile (from row r0 on, as far as n, a multiple of 16) by a warp,
-// eight copies in a row: a copy that waits for its registers' former use takes
-// 140 cycles instead of 40.  Empty slots read as zero; copies that may have one have
-// a size of their own, which costs them a quarter more.
+// 64 rows of a tile (from row r0 on, as far as n) by a warp: P lanes a row, each
+// group of lanes its own stretch of rows, whose numbers it reads four at a time.
+// Eight copies in a row: a copy that waits for its registers' former use takes 140
+// cycles instead of 40.  What counts beyond that are instructions (all roles of a CTA
+// together had the schedulers busy for 63 % of the time): three for a copy.  Empty slots read as
+// zero; copies that may have one have a size of their own, which costs them a quarter more.
 template <int D>
 __device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, const int* rows, int r0, int n) {
-  constexpr int P = D / 8, PER = 32 / P, STEP = 8 * PER;  // 16-byte pieces of a row; rows an instruction takes, and eight
-  const int lane = static_cast<int>(lane_id());
-  const int mine[2] = {r0 + lane < n ? rows[r0 + lane] : -1, r0 + 32 + lane < n ? rows[r0 + 32 + lane] : -1};
-  const uint32_t ok[2] = {__ballot_sync(0xffffffffu, mine[0] >= 0), __ballot_sync(0xffffffffu, mine[1] >= 0)};
-  const int piece = lane % P, sub = lane / P;
+  constexpr int P = D / 8, SPAN = 2 * P;  // 16-byte pieces of a row; rows of a group of lanes: 64 / (32 / P)
+  const int lane = static_cast<int>(lane_id()), piece = lane % P, first = r0 + SPAN * (lane / P);
   const char* base = static_cast<const char*>(g.base) + piece * 16;
-  const uint32_t dst = smem_u32(tile) + (piece >> 3) * kChunkBytes + (r0 + sub) * 128;
-  uint32_t at[8 / PER];  // the swizzle repeats every eight rows
+  uint32_t at[8];  // of the swizzle's eight rows
 #pragma unroll
-  for (int i = 0; i < 8 / PER; ++i) at[i] = dst + (((piece & 7) ^ ((PER * i + sub) & 7)) * 16);
+  for (int i = 0; i < 8; ++i)
+    at[i] = smem_u32(tile) + (piece >> 3) * kChunkBytes + (first + i) * 128 + (((piece & 7) ^ i) * 16);
 #pragma unroll 1
-  for (int h = 0; h < 64 && r0 + h < n; h += STEP) {
-    const int from = h < 32 ? mine[0] : mine[1];
-    const uint32_t there = (h < 32 ? ok[0] : ok[1]) >> (h & 31);
-    const char* src[8];
-    uint32_t size[8];
+  for (int h = 0; h < SPAN; h += 8) {
+    int4 a = reinterpret_cast<const int4*>(rows + first + h)[0], b = reinterpret_cast<const int4*>(rows + first + h)[1];
+    int row[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (__all_sync(0xffffffffu, (row[0] | row[1] | row[2] | row[3] | row[4] | row[5] | row[6] | row[7]) >= 0)) {
+      const char* src[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = __shfl_sync(0xffffffffu, from, (h + PER * i + sub) & 31);
-      src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(max(row, 0))) * g.unit_bytes;
-      size[i] = row < 0 ? 0u : 16u;
-    }
-    if ((~there & low_bits(STEP)) == 0u) {
+      for (int i = 0; i < 8; ++i) src[i] = base + static_cast<uint64_t>(static_cast<uint32_t>(row[i])) * g.unit_bytes;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128), "l"(src[i])
-                     : "memory");
-    } else {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at[i]), "l"(src[i]) : "memory");
+    } else if (__any_sync(0xffffffffu, first + h < n)) {  // (rows past n are not read by the products)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at[i % (8 / PER)] + (h + PER * i) * 128),
-                     "l"(src[i]), "r"(size[i])
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at[i]),
+                     "l"(base + static_cast<uint64_t>(static_cast<uint32_t>(max(row[i], 0))) * g.unit_bytes),
+                     "r"(row[i] < 0 ? 0 : 16)
                      : "memory");
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at[i] += 8 * 128;
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
