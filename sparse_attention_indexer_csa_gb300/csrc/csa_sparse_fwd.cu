@@ -40,6 +40,7 @@
 #include <cuda_fp16.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "csa_sparse_list.cuh"
 
@@ -447,35 +448,43 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
           else
             p.lse[at + row] = lse;
         }
-        const uint32_t to = tmem + (static_cast<uint32_t>(w * 32) << 16) + 256u + b * 128u;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(w * 32) << 16) + 256u + b * 128u;
+        using Out = std::conditional_t<SPLIT, float, X>;
+        Out* to = (SPLIT ? reinterpret_cast<Out*>(f.part_o) + h.z * rows * D : static_cast<Out*>(p.out)) +
+                  (at + (tid >> 3)) * D + (tid & 7) * 4;
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           float o[32];
-          tmem_ld32_start(to + 32 * ch, o);
+          tmem_ld32_start(acc + 32 * ch, o);
           tmem_wait32(o);
+          if (weight == 0.f) {  // no key: what stands there may be anything
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<float4*>(stage + row * kPitch + 4 * u) =
-                weight == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                              : make_float4(o[4 * u] * weight, o[4 * u + 1] * weight, o[4 * u + 2] * weight,
-                                            o[4 * u + 3] * weight);
+            for (int u = 0; u < 32; ++u) o[u] = 0.f;
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float2 w2 = make_float2(weight, weight), lo = fmul2(make_float2(o[4 * u], o[4 * u + 1]), w2),
+                         hi = fmul2(make_float2(o[4 * u + 2], o[4 * u + 3]), w2);
+            *reinterpret_cast<float4*>(stage + row * kPitch + 4 * u) = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
           all_here();
-          for (int i = tid; i < p.g * 8; i += 128) {
-            const int hd = i >> 3, col = (i & 7) * 4;
-            float4 v = *reinterpret_cast<const float4*>(stage + hd * kPitch + col);
+          // eight threads a head, 16 heads at a time
+          const float* from = stage + (tid >> 3) * kPitch + (tid & 7) * 4;
+#pragma unroll
+          for (int k = 0; k < G / 16; ++k) {
+            if ((tid >> 3) + 16 * k >= p.g) break;
+            float4 v = *reinterpret_cast<const float4*>(from + 16 * k * kPitch);
 #pragma unroll
             for (int r = 1; r < R; ++r) {
-              const float4 x = *reinterpret_cast<const float4*>(stage + (r * G + hd) * kPitch + col);
-              v.x += x.x;
-              v.y += x.y;
-              v.z += x.z;
-              v.w += x.w;
+              const float4 x = *reinterpret_cast<const float4*>(from + (r * G + 16 * k) * kPitch);
+              const float2 lo = fadd2(make_float2(v.x, v.y), make_float2(x.x, x.y)),
+                           hi = fadd2(make_float2(v.z, v.w), make_float2(x.z, x.w));
+              v = make_float4(lo.x, lo.y, hi.x, hi.y);
             }
-            const long long e = (at + hd) * D + 32 * ch + col;
             if constexpr (SPLIT)
-              *reinterpret_cast<float4*>(f.part_o + h.z * rows * D + e) = v;
+              *reinterpret_cast<float4*>(to + static_cast<long long>(16 * k) * D + 32 * ch) = v;
             else
-              *reinterpret_cast<uint2*>(static_cast<X*>(p.out) + e) =
+              *reinterpret_cast<uint2*>(to + static_cast<long long>(16 * k) * D + 32 * ch) =
                   make_uint2(pack_pair<X>(v.x, v.y), pack_pair<X>(v.z, v.w));
           }
           all_here();
