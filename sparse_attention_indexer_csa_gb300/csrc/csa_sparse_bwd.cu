@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kBars; ++i) {
       int n = 1;
-      if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
+      if (i >= C::kBarK && i < C::kBarV + 2) n = 64;  // every lane that loads
       if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 12;
       if (i == C::kBarP) n = 4;
       if (i == C::kBarDFree || i == C::kBarDqFree) n = 8;
@@ -252,36 +252,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* used = bars + (keys ? C::kBarKFree : C::kBarS);  // a stage is free when the last product that reads it is through
     uint8_t* stages = base + (keys ? C::kOffK : C::kOffV);
     uint32_t j = 0;
-    bool flying = false;  // tile j - 1 has been asked for and not been reported
-    auto report = [&](uint32_t i) {
-      if (lane == 0) mbar_arrive(full + (i & 1u));
-    };
     while (true) {
-      const bool go = at.left != 0 && mbar_test_wait(bars + C::kBarTile + at.slot, at.parity) &&
-                      (j < 2 || mbar_test_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u));
-      if (flying && __any_sync(0xffffffffu, !go)) {
-        loaded<0>();
-        report(j - 1);
-        flying = false;
-      }
       const TileHead h = next_head();
       if (h.n < 0) break;
       if (h.n > 0) {
-        if (j >= 2 && !bar_wait(used + (j & 1u), ((j >> 1) & 1u) ^ 1u, ctl)) break;
-        __syncwarp();
-        const Tile& tile = ring[at.slot];
-        load_rows<D>(stages + (j & 1u) * C::kTile, rows, keys ? tile.k_row : tile.v_row, r0, (h.n + 15) & ~15);
-        if (flying) {
-          loaded<1>();
-          report(j - 1);
-        }
-        flying = true;
+        const uint32_t st = j & 1u;
+        if (!bar_wait(used + st, ((j >> 1) & 1u) ^ 1u, ctl)) break;
+        load_rows<D, 64>(stages + st * C::kTile, rows, keys ? ring[at.slot].k_row : ring[at.slot].v_row, r0, (h.n + 15) & ~15);
+        report_rows(full + st);
         ++j;
       }
       give_head();
     }
-    loaded<0>();  // no copy is in flight when the CTA ends, a role's giving up included
-    if (flying) report(j - 1);
+    wait_rows();  // no copy is in flight when the CTA ends, a role's giving up included
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------------- issuer of the products
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
@@ -350,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
         wait(C::kBarK + static_cast<int>(st), par);
         wait(C::kBarV + static_cast<int>(st), par);
+        fence_proxy_async_shared();
         tc_fence_after();
         if (elect_one()) {
           if (alive) {

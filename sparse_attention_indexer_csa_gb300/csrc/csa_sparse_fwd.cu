@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
       if (i >= C::kBarMl && i < C::kBarMl + 2) n = 4 * H;
       if (i >= C::kBarPair && i < C::kBarPair + 4) n = 2;
       if (i >= C::kBarOFree && i < C::kBarOFree + 2) n = 4;
-      if (i >= C::kBarK && i < C::kBarV + 2) n = 2;
+      if (i >= C::kBarK && i < C::kBarV + 2) n = 128;  // every lane that loads
       if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 10 + 4 * H;
       if (i == C::kBarDone) n = 2;
       if (i == C::kBarMeet) n = 4;
@@ -146,16 +146,13 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
     list_tiles<kLists>(p, f.l, w, ring, bars + C::kBarTile, bars + C::kBarTileFree, ctl);
   } else if (warp >= kKeyWarp && warp < kScoreWarp) {
     // ------------------------------------------------------------------------- rows of keys, of values
-    // Two warps for each stage: a tile takes one of them 2000 cycles (the lists'
-    // ring, 32 copies, their way, the fence), which two tiles of work hide.
     const bool keys = warp < kValueWarp;
-    const uint32_t stage = (warp >> 1) & 1u;
-    const int r0 = 64 * (warp & 1);
+    const int r0 = 32 * (warp & 3);
     const GatherRows& rows = keys ? p.k : p.v;
-    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV) + stage;
+    uint64_t* full = bars + (keys ? C::kBarK : C::kBarV);
     // a stage is free when the product that read it has completed
-    uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv) + stage;
-    uint8_t* tile = base + (keys ? C::kOffK : C::kOffV) + stage * C::kTile;
+    uint64_t* used = bars + (keys ? C::kBarS : C::kBarPv);
+    uint8_t* stages = base + (keys ? C::kOffK : C::kOffV);
     uint32_t j = 0, nq = 0;
     bool first = true;  // no tile of this item yet
     while (true) {
@@ -177,19 +174,16 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
           ++nq;
         }
         first = false;
-        if ((j & 1u) == stage) {
-          if (!bar_wait(used, ((j >> 1) & 1u) ^ 1u, ctl)) break;
-          const Tile& from = ring[at.slot];
-          load_rows<D>(tile, rows, keys ? from.k_row : from.v_row, r0, (h.n + 15) & ~15);
-          loaded<0>();
-          if (lane == 0) mbar_arrive(full);
-        }
+        const uint32_t st = j & 1u;
+        if (!bar_wait(used + st, ((j >> 1) & 1u) ^ 1u, ctl)) break;
+        load_rows<D, 32>(stages + st * C::kTile, rows, keys ? ring[at.slot].k_row : ring[at.slot].v_row, r0, (h.n + 15) & ~15);
+        report_rows(full + st);
         ++j;
       }
       if (h.last) first = true;
       give_head();
     }
-    loaded<0>();  // no copy is in flight when the CTA ends, a role's giving up included
+    wait_rows();  // no copy is in flight when the CTA ends, a role's giving up included
     for (uint32_t i = nq > 2 ? nq - 2 : 0; i < nq; ++i) bar_wait(bars + C::kBarQ + (i & 1u), (i >> 1) & 1u, drain);
   } else if (warp == kScoreWarp || warp == kMmaWarp) {
     // ------------------------------------------------------------------------- issuers of the products
@@ -217,6 +211,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
           first = false;
           wait(C::kBarPv + static_cast<int>(st), ((j >> 1) & 1u) ^ 1u);  // P in this S has been used
           wait(C::kBarK + static_cast<int>(st), (j >> 1) & 1u);
+          fence_proxy_async_shared();
           tc_fence_after();
           if (elect_one()) {
             if (alive) {
@@ -253,6 +248,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1)
           const uint32_t st = j & 1u;
           wait(C::kBarV + static_cast<int>(st), (j >> 1) & 1u);
           wait(C::kBarP + static_cast<int>(st), (j >> 1) & 1u);
+          fence_proxy_async_shared();
           tc_fence_after();
           const int steps = (n + 15) >> 4;
           if (elect_one()) {

@@ -348,15 +348,15 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
   if (bad) record_error(kErrDevice);
 }
 
-// 64 rows of a tile (from row r0 on, as far as n) by a warp: P lanes a row, each
+// ROWS rows of a tile (from row r0 on, as far as n) by a warp: P lanes a row, each
 // group of lanes its own stretch of rows, whose numbers it reads four at a time.
 // Eight copies in a row: a copy that waits for its registers' former use takes 140
 // cycles instead of 40.  What counts beyond that are instructions (all roles of a CTA
 // together had the schedulers busy for 63 % of the time): three for a copy.  Empty slots read as
 // zero; copies that may have one have a size of their own, which costs them a quarter more.
-template <int D>
+template <int D, int ROWS>
 __device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, const int* rows, int r0, int n) {
-  constexpr int P = D / 8, SPAN = 2 * P;  // 16-byte pieces of a row; rows of a group of lanes: 64 / (32 / P)
+  constexpr int P = D / 8, SPAN = ROWS * P / 32;  // 16-byte pieces of a row; rows of a group of lanes
   const int lane = static_cast<int>(lane_id()), piece = lane % P, first = r0 + SPAN * (lane / P);
   const char* base = static_cast<const char*>(g.base) + piece * 16;
   uint32_t at[8];  // of the swizzle's eight rows
@@ -385,13 +385,12 @@ __device__ __forceinline__ void load_rows(uint8_t* tile, const GatherRows& g, co
 #pragma unroll
     for (int i = 0; i < 8; ++i) at[i] += 8 * 128;
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-template <int N>
-__device__ __forceinline__ void loaded() {  // all but the last N groups of rows are there, for the tensor cores too
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-  fence_proxy_async_shared();
-  __syncwarp();
+// Each lane arrives at `full` when its copies so far have landed; who waits there
+// has to order them before the tensor cores' reads (fence_proxy_async_shared).
+__device__ __forceinline__ void report_rows(uint64_t* full) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full)) : "memory");
 }
+__device__ __forceinline__ void wait_rows() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 }  // namespace csa
