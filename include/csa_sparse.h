@@ -60,9 +60,9 @@ extern "C" {
  * Precision: as for csa_attn_forward: products of stored values are exact and
  * summed in fp32, as are the softmax's sums; exponentials are fp32.  The weights
  * that meet v (and dout), and ds that meets k and q, are rounded to dtype, half a
- * unit of the last place each.  The share of a row in dk and dv of a key is kept
- * with 11 bits (fp16 at a power of two of its own) before the rows' shares are
- * added in fp32.  In fp16, weights
+ * unit of the last place each.  In bf16 the share of a row in dk and dv of a key is
+ * kept with 11 bits (fp16 at a power of two of its own) before the rows' shares
+ * are added in fp32; in fp16 it is fp32.  In fp16, weights
  * count down to 2^-32 of the largest in out and 2^-39 in dv.
  * Supported: D in {64, 128}, dtype CSA_BF16 or CSA_F16, Hq a multiple of Hk,
  * Hq / Hk <= 128, block a power of two up to 128, window + top_k * block up to

@@ -23,16 +23,20 @@
 //   sparse_sum_kernel  a block of threads per key and key head adds the shares.
 //
 // Bytes: a share of dk and one of dv, D values each, per listed key, written once
-// and read once.  A share is kept in fp16 at a power of two of its own, from the
-// bound sum over heads of |ds| |q| (p |dout|) that its key's thread adds up on the
-// way: 11 bits, finer than ds and p have in bf16, at half of fp32's bytes.  As many
-// rows at a time as kShareBytes hold.
+// and read once.  For bf16 a share is kept in fp16 at a power of two of its own, from
+// the bound sum over heads of |ds| |q| (p |dout|) that its key's thread adds up on the
+// way: 11 bits, finer than ds and p have, at half of fp32's bytes (in bf16 it cost
+// the gradients half of their precision, 0.0029 of their size for 0.0024).  For fp16,
+// whose own roundings are no larger, it is fp32.  As many rows at a time as
+// kShareBytes hold.
 //
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
 // 2^15 (|dout| over the item's heads, |v| over the finite values of the sequence), and
 // P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "csa_sparse_list.cuh"
 
@@ -46,6 +50,16 @@ constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kIte
 
 template <typename X>
 constexpr int kProbExp = is_bf16<X>() ? 0 : 15;  // power of two of P^T
+
+// What a share is kept in.
+template <typename X>
+struct ShareType {
+  using T = __half;
+};
+template <>
+struct ShareType<__half> {
+  using T = float;
+};
 
 template <int D>
 struct Cfg {
@@ -77,8 +91,8 @@ struct RowsArgs {
   float c;         // scale * log2(e)
   const float *delta, *norm_do, *norm_q;  // [Tq][Hq]
   const uint32_t* range;
-  __half* share;   // [rows][Hk][n_z][2][s_pad][D]
-  uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk is its fp16 values times 2^(low byte - 143), dv: high byte
+  void* share;     // [rows][Hk][n_z][2][s_pad][D] (ShareType)
+  uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk is its values times 2^(low byte - 143), dv: high byte
   unsigned long long wait_ns;
 };
 
@@ -118,18 +132,27 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 template <typename T, int D>
 __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* dst, uint32_t rows) {
   const uint32_t lane = lane_id();
-  uint4 q[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const float* x = o + 8 * u;
-    q[u] = make_uint4(pack_pair<T>(x[0] * f, x[1] * f), pack_pair<T>(x[2] * f, x[3] * f),
-                      pack_pair<T>(x[4] * f, x[5] * f), pack_pair<T>(x[6] * f, x[7] * f));
-  }
-  transpose4(q, lane);
+  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
+    uint4 q[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const uint32_t r = (lane & ~3u) + u;
-    if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D)[lane & 3u] = q[u];
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (sizeof(T) == 4) {
+        const float* x = o + 16 * h + 4 * u;
+        q[u] = make_uint4(__float_as_uint(x[0] * f), __float_as_uint(x[1] * f), __float_as_uint(x[2] * f),
+                          __float_as_uint(x[3] * f));
+      } else {
+        const float* x = o + 8 * u;
+        q[u] = make_uint4(pack_pair<T>(x[0] * f, x[1] * f), pack_pair<T>(x[2] * f, x[3] * f),
+                          pack_pair<T>(x[4] * f, x[5] * f), pack_pair<T>(x[6] * f, x[7] * f));
+      }
+    }
+    transpose4(q, lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t r = (lane & ~3u) + u;
+      if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 16 * h)[lane & 3u] = q[u];
+    }
   }
 }
 
@@ -138,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sparse_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                        const __grid_constant__ RowsArgs f) {
   using C = Cfg<D>;
+  using T = typename ShareType<X>::T;
   extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
   Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
@@ -435,7 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(row + (((2 * i + u) ^ (key & 7)) * 16)) =
                 make_uint4(dw[4 * u], dw[4 * u + 1], dw[4 * u + 2], dw[4 * u + 3]);
         }
-        const int ek = exponent_above((bk.x + bk.y) * back, 110), ev = exponent_above((bv.x + bv.y) * back_v, 110);
+        int ek = 15, ev = 15;  // (fp32: as they are)
+        if constexpr (sizeof(T) == 2) {
+          ek = exponent_above((bk.x + bk.y) * back, 110);
+          ev = exponent_above((bv.x + bv.y) * back_v, 110);
+        }
         factor[st * 128 + key] = make_float2(back * power_of_two(15 - ek), back_v * power_of_two(15 - ev));
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
         f.power[item * f.s_pad + h.c * 128 + key] = static_cast<uint16_t>((ek + 128) | ((ev + 128) << 8));
@@ -470,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!bar_wait(bars + C::kBarD, j & 1u, ctl)) break;
         tc_fence_after();
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
-        __half* dst = f.share + ((2 * item + (dk ? 0 : 1)) * f.s_pad + h.c * 128 + w * 32) * D;
+        T* dst = static_cast<T*>(f.share) + ((2 * item + (dk ? 0 : 1)) * f.s_pad + h.c * 128 + w * 32) * D;
         if (see != 0u) {
           const float2 both = factor[(j & 1u) * 128 + w * 32 + lane];
           const float mine = dk ? both.x : both.y;
@@ -479,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float o[32];
             tmem_ld32_start(tmem + lanes + (dk ? kColDk : kColDv) + 32 * ch, o);
             tmem_wait32(o);
-            store_columns<__half, D>(o, mine, dst + 32 * ch, see);
+            store_columns<T, D>(o, mine, dst + 32 * ch, see);
           }
         }
         tc_fence_before();
@@ -716,7 +744,7 @@ struct SumArgs {
   SparseParams p;
   int t0, rows, u_bits, n_z, s_pad;
   const uint32_t *start, *entry;
-  const __half* share;
+  const void* share;
   const uint16_t* power;
   float* acc;           // [2][Tk][Hk][D]: sums of the rounds before (more than one round)
   int opens, closes;    // the first round, the last
@@ -727,7 +755,8 @@ struct SumArgs {
 // values a lane (D = 64: half a warp a share); the warps' sums are joined in order.
 template <typename X, int D>
 __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
-  constexpr int L = D / 4, PER = 32 / L, W = 8 * PER, U = 8;  // lanes of a share; shares a warp, a block adds at once; in flight
+  using T = typename ShareType<X>::T;
+  constexpr int L = D / 4, PER = 32 / L, W = 8 * PER, U = sizeof(T) == 2 ? 8 : 4;  // lanes of a share; shares a warp, a block adds at once; in flight
   struct Found {
     long long at;  // first value of the share of dk; negative: none
     float k, v;    // factors
@@ -786,26 +815,34 @@ __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
       const int most = static_cast<int>(min(256ll, all - base));
 #pragma unroll 1
       for (int i = sub; i < most; i += W * U) {
-        uint2 rk[U], rv[U];
+        using Raw = std::conditional_t<sizeof(T) == 2, uint2, uint4>;  // four values
+        Raw rk[U], rv[U];
         float fk[U], fv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int at = i + u * W;
-          rk[u] = rv[u] = make_uint2(0u, 0u);
+          rk[u] = rv[u] = Raw{};
           fk[u] = fv[u] = 0.f;
           if (at < most) {
             const Found y = found[at];
             if (y.at >= 0) {
-              const __half* src = f.share + y.at + col;
-              rk[u] = __ldcs(reinterpret_cast<const uint2*>(src));
-              rv[u] = __ldcs(reinterpret_cast<const uint2*>(src + dv));
+              const T* src = static_cast<const T*>(f.share) + y.at + col;
+              rk[u] = __ldcs(reinterpret_cast<const Raw*>(src));
+              rv[u] = __ldcs(reinterpret_cast<const Raw*>(src + dv));
               fk[u] = y.k;
               fv[u] = y.v;
             }
           }
         }
-        auto add = [](float4& to, const uint2& r, float by) {
-          const float2 lo = unpack_pair<__half>(r.x), hi = unpack_pair<__half>(r.y);
+        auto add = [](float4& to, const Raw& r, float by) {
+          float2 lo, hi;
+          if constexpr (sizeof(T) == 2) {
+            lo = unpack_pair<__half>(r.x);
+            hi = unpack_pair<__half>(r.y);
+          } else {
+            lo = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+            hi = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+          }
           to.x = fmaf(lo.x, by, to.x);
           to.y = fmaf(lo.y, by, to.y);
           to.z = fmaf(hi.x, by, to.z);
@@ -859,7 +896,7 @@ Plan make_plan(const SparseParams& p, int dtype) {
   while (p.g / a.n_z > kHeads || p.g % a.n_z != 0) ++a.n_z;
   a.heads = p.g / a.n_z;
   a.s_pad = static_cast<int>((sparse_slots(p) + 127) / 128 * 128);
-  const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * 2;  // bytes of a row's shares
+  const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * (fp16 ? 4 : 2);  // bytes of a row's shares
   a.u_bits = 0;
   while ((1ll << a.u_bits) < p.top_k) ++a.u_bits;
   long long rows = row == 0 ? p.Tq : static_cast<long long>(std::max<size_t>(1, kShareBytes / row));
@@ -928,7 +965,7 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   f.norm_do = norm_do;
   f.norm_q = norm_q;
   f.range = range;
-  f.share = reinterpret_cast<__half*>(ws + a.share);
+  f.share = ws + a.share;
   f.power = reinterpret_cast<uint16_t*>(ws + a.power);
   f.wait_ns = attn_wait_ns(f.l.slots / 128 + 1);
   CUtensorMap tq, tdo;

@@ -6,11 +6,11 @@ Tolerances, from the arithmetic (u = eps/2 of the storage type), as for dense at
   by the same but u; the join of shares adds a few fp32 roundings: 2^-18 in all.
       |out - ref| <= u |ref| + (u + 2 ds + 2^-18) sum p|v| + tiny sum |v|
       |lse - ref| <= ds + 2^-19 + 2^-22 |ref|
-* gradients: as above with ds rounded to the storage type and delta from the rounded out (u each), and the shares of the
-  rows in dk and dv rounded to fp16 at a power of two that their bound (norm_dk, norm_dv) is at most twice below: 2^-11 of
+* gradients: as above with ds rounded to the storage type and delta from the rounded out (u each), and, in bf16, the shares
+  of the rows in dk and dv rounded to fp16 at a power of two that their bound (norm_dk, norm_dv) is at most twice below: 2^-11 of
   their magnitude, 2^-25 of 2^-15 of twice the bound where fp16 has no more bits:
       |dq - ref| <= u |ref| + (2u + 2 ds + 2^-15) mag + tiny (sum of the other factor)
-      dk: 2u + 2^-11 + ... and 2^-39 norm_dk;  dv: u + 2^-11 + 2 ds + 2^-18 and 2^-39 norm_dv.
+      dk: 2u + 2^-11 + ... and 2^-39 norm_dk;  dv: u + 2^-11 + 2 ds + 2^-18 and 2^-39 norm_dv  (fp16: without these).
 * fp16 weights are formed at 2^8 (in out) and 2^15 (in dv) of their size, and ds at a power of two that brings its
   bound above 2^13: subnormal spacing 2^-24, so tiny is 2^-33 per key in out, 2^-40 in dv, 2^-38 of ds' bound in
   dq and dk.  bf16 has fp32's range: 0.
@@ -81,11 +81,13 @@ def _bounds(ref, dt):
     b = dict(out=u * np.abs(ref["out"]) + (u + 2 * ds[..., None] + 2.0 ** -18) * ref["mag_out"]
              + h * (2.0 ** -33 * ref["vsum"] + 2.0 ** -25), lse=ds + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse))
     top = 2 * ds.max(initial=0.0)
-    rel = dict(dq=2 * u + top + 2.0 ** -15, dk=2 * u + 2.0 ** -11 + top + 2.0 ** -15, dv=u + 2.0 ** -11 + top + 2.0 ** -18)
+    sh = 0.0 if dt == FP16 else 1.0
+    rel = dict(dq=2 * u + top + 2.0 ** -15, dk=2 * u + sh * 2.0 ** -11 + top + 2.0 ** -15,
+               dv=u + sh * 2.0 ** -11 + top + 2.0 ** -18)
     tiny = dict(dq=2.0 ** -38, dk=2.0 ** -38, dv=2.0 ** -40)
     for n in ("dq", "dk", "dv"):
         if n in ref:
-            share = 2.0 ** -39 * ref["norm_" + n][..., None] if n != "dq" else 0.0
+            share = sh * 2.0 ** -39 * ref["norm_" + n][..., None] if n != "dq" else 0.0
             b[n] = u * np.abs(ref[n]) + rel[n] * ref["mag_" + n] + share + h * (tiny[n] * ref["sum_" + n] + 2.0 ** -25)
     return b
 
