@@ -30,6 +30,10 @@
 // whose own roundings are no larger, it is fp32.  As many rows at a time as
 // kShareBytes hold.
 //
+// Where a list is one tile, delta is taken as sum_j p_j dout.v_j from the products at
+// hand, in fp32: the rounding of out, which the forward stored, is an error of delta
+// for all keys of the row at once, and shows where these are few.
+//
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
 // 2^15 (|dout| over the item's heads, |v| over the finite values of the sequence), and
 // P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
@@ -71,11 +75,12 @@ struct Cfg {
   static constexpr uint32_t kOffRing = kOffDo + 2 * kHeadTile;
   static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta, |dout|, |q|
   static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [2][128] factors of a key's shares
-  static constexpr uint32_t kOffFit = kOffFactor + 2 * 128 * 8;          // [2] power of two of dS
+  static constexpr uint32_t kOffSum = kOffFactor + 2 * 128 * 8;          // [4][64] sums of p dout.v over a warp's keys
+  static constexpr uint32_t kOffFit = kOffSum + 4 * kHeads * 4;          // [2] power of two of dS
   static constexpr uint32_t kOffBar = kOffFit + 16;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
                        kBarKFree = 14, kBarP = 16, kBarD = 17, kBarDFree = 18, kBarDq = 19, kBarDqFree = 20,
-                       kBarTile = 21, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
+                       kBarSum = 21, kBarTile = 22, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
                        kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
 };
@@ -156,7 +161,8 @@ __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* 
   }
 }
 
-template <typename X, int D>
+// ONE: the lists are one tile.
+template <typename X, int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                        const __grid_constant__ RowsArgs f) {
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 1;
       if (i >= C::kBarK && i < C::kBarV + 2) n = 64;  // every lane that loads
       if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 12;
-      if (i == C::kBarP) n = 4;
+      if (i == C::kBarP || i == C::kBarSum) n = 4;
       if (i == C::kBarDFree || i == C::kBarDqFree) n = 8;
       if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 18;
       mbar_init(bars + i, n);
@@ -410,6 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool first = true;
     float fit = 1.f;        // power of two of dS over that of P
     float back = p.scale, back_v = 1.f;  // what undoes the powers of two
+    uint32_t met = 0;
+    auto meet_all = [&] {  // these four warps, bounded as every wait is
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + C::kBarSum);
+      const bool here = bar_wait(bars + C::kBarSum, met, ctl);
+      met ^= 1u;
+      return here;
+    };
     while (true) {
       const TileHead h = next_head();
       if (h.n < 0) break;
@@ -430,6 +444,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool see = (ring[at.slot].keys[warp] >> lane) & 1u;
         const float4* ls = stat + (ni & 1u) * kHeads;
+        if constexpr (ONE) {  // delta, see above
+          float* sums = reinterpret_cast<float*>(base + C::kOffSum);
+#pragma unroll 1
+          for (int i = 0; i < f.padded / 16; ++i) {
+            float t[16], dp[16];
+            tmem_ld16_start(tmem + lanes + kColS + 16 * i, t);
+            tmem_ld16_start(tmem + lanes + kColDp + 16 * i, dp);
+            tmem_wait16(t);
+            tmem_wait16(dp);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) t[u] = see ? exp2_approx(fmaf(t[u], f.c, -ls[16 * i + u].x)) * dp[u] : 0.f;
+            // each step adds half of the heads over half of the lanes; lanes 2 h and 2 h + 1 end with head h
+#pragma unroll
+            for (int n = 8; n > 0; n >>= 1) {
+              const bool up = (lane & (2u * n)) != 0u;
+#pragma unroll
+              for (int u = 0; u < n; ++u) {
+                const float give = up ? t[u] : t[u + n], keep = up ? t[u + n] : t[u];
+                t[u] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+              }
+            }
+            t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+            if ((lane & 1u) == 0u) sums[warp * kHeads + 16 * i + (lane >> 1)] = t[0];
+          }
+          if (!meet_all()) break;
+          if (key < f.padded)
+            stat[(ni & 1u) * kHeads + key].y = (sums[key] + sums[kHeads + key]) + (sums[2 * kHeads + key] + sums[3 * kHeads + key]);
+          if (!meet_all()) break;
+        }
         float2 bk = make_float2(0.f, 0.f), bv = bk;  // bounds of the key's shares
 #pragma unroll 1
         for (int i = 0; i < f.padded / 16; ++i) {
@@ -972,8 +1015,10 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   if (!make_heads_map(&tq, p, p.q, p.q_st, p.q_sh, a.heads) ||
       !make_heads_map(&tdo, p, p.dout, static_cast<long long>(p.Hq) * D, D, a.heads))
     return cudaErrorInvalidValue;
-  constexpr auto kernel = sparse_rows_kernel<X, D>;
-  if ((e = smem_limit_once<kernel>(Cfg<D>::kSmem)) != cudaSuccess) return e;
+  const bool one = f.l.per == 1;
+  const auto kernel = one ? sparse_rows_kernel<X, D, true> : sparse_rows_kernel<X, D, false>;
+  e = one ? smem_limit_once<sparse_rows_kernel<X, D, true>>(Cfg<D>::kSmem) : smem_limit_once<sparse_rows_kernel<X, D, false>>(Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
   WhoArgs who;
   who.p = p;
   who.per = a.per;
