@@ -94,7 +94,8 @@ csa_status csa_sparse_attn_forward(const csa_sparse_problem* p, const void* q, c
  * block that a row lists twice reaches dk and dv twice, as it does out.  The sums
  * are taken in a fixed order (the same bits on every call).  Needs `workspace`:
  * csa_sparse_attn_workspace_size(p, 1) bytes, 16-byte aligned: each row's share of
- * dk and dv for each key it lists, as many rows at a time as 4 GiB hold.       */
+ * dk and dv for each key it lists, as many rows at a time as 4 GiB hold (one at
+ * least).                                                                      */
 csa_status csa_sparse_attn_backward(const csa_sparse_problem* p, const void* dout, const void* q, const void* k,
                                     const void* v, const void* out, const float* lse, const int32_t* idx,
                                     const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* dq,
@@ -114,8 +115,8 @@ size_t csa_sparse_attn_workspace_size(const csa_sparse_problem* p, int32_t which
  * contiguous.  positions [T] give the angles, as for csa_norm_rope.
  * A token whose place is negative or past the table, whose page is outside
  * 0 .. pages-1, or that belongs to no sequence, is not stored (its q_out is); the
- * first three record CSA_ERR_DEVICE.  No other row of the cache is written.  Two
- * tokens with the same place (sequences that share a page) leave one of them there.
+ * first three record CSA_ERR_DEVICE.  No other row of the cache is written.  Of two
+ * tokens with the same place (sequences that share a page) each value is either's.
  * Cache and inputs may not overlap.  Strides in elements, multiples of 16 bytes
  * (0 = contiguous); bases are 16-byte aligned.                                 */
 typedef struct {

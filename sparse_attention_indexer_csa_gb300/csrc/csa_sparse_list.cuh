@@ -219,8 +219,8 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
                                            uint64_t* free_bar, const WaitCtl& ctl) {
   const int lane = static_cast<int>(lane_id());
   bool bad = false;
-  if (blockIdx.x == 0 && w == 0)
-    for (int i = lane; i < p.N; i += 32) sparse_extent(p, i);  // what is out of order or range is recorded
+  if (w == 0)  // what is out of order or range is recorded, also of sequences without rows
+    for (long long i = blockIdx.x * 32 + lane; i < p.N; i += 32 * gridDim.x) sparse_extent(p, static_cast<int>(i));
   const long long tiles = tile_count(f);
   const bool quads = p.block_shift >= 2 && (p.window & 3) == 0 && (p.page == 0 || ((p.page & 3) == 0 && p.window == 0));
   // the coming tile: its row, key head and part, its place in the item, the blocks that its slots list
