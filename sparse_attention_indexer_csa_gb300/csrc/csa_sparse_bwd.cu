@@ -17,7 +17,7 @@
 //       dV = P^T dO, dK = dS^T Q           (A in TMEM, B read MN-major): the shares
 //       dQ += dS K                         (A and B read MN-major)
 //     so that a group of any size costs no more than its heads.
-//   lists (sparse_count, _scan, _start, _fill)  for each block the rows that
+//   lists (sparse_count, _scan, _fill)  for each block the rows that
 //     list it, in ascending order: a counting sort, the counts kept by groups of
 //     rows so that the place of each entry does not depend on timing.
 //   sparse_sum_kernel  a block of threads per key and key head adds the shares.
@@ -683,6 +683,7 @@ struct WhoArgs {
   int n_blocks;
   int u_bits;            // an entry is (row - t0) << u_bits | place in the row's list
   uint32_t *count, *total, *start, *entry;  // [groups][n_blocks], [n_blocks], [n_blocks + 1], [rows * top_k]
+  uint32_t* ticket;                         // zero before sparse_scan_kernel, as the counts
 };
 // Number of the block that place u of row t lists, where the row sees some of its keys; -1 else.
 __device__ __forceinline__ int listed_block(const SparseParams& p, const ListRow& r, int t, int u) {
@@ -701,12 +702,14 @@ __global__ void __launch_bounds__(256) sparse_count_kernel(const WhoArgs f) {
     if (id >= 0) atomicAdd(count + id, 1u);
   }
 }
-// Counts become places within the block's entries; totals.  32 blocks of keys and
-// 32 runs of groups per block of threads: each thread adds up its run, the runs
-// before it give where it starts.
+// Counts become places within the block's entries.  32 blocks of keys and 32 runs of
+// groups per block of threads: each thread adds up its run, the runs before it give
+// where it starts.  The last block of threads to be through forms start, the running sum of
+// the totals (a launch of its own took 4 us).
 __global__ void __launch_bounds__(1024) sparse_scan_kernel(const WhoArgs f) {
   __shared__ uint32_t sums[32][33];
-  const int lane = threadIdx.x & 31, run = threadIdx.x / 32, id = blockIdx.x * 32 + lane;
+  __shared__ bool last;
+  const int tid = threadIdx.x, lane = tid & 31, run = tid / 32, id = blockIdx.x * 32 + lane;
   const int per = (f.groups + 31) / 32, g0 = min(f.groups, run * per), g1 = min(f.groups, g0 + per);
   uint32_t* c = f.count + id;
   uint32_t n = 0;
@@ -716,50 +719,54 @@ __global__ void __launch_bounds__(1024) sparse_scan_kernel(const WhoArgs f) {
   }
   sums[run][lane] = n;
   __syncthreads();
-  if (id >= f.n_blocks) return;
-  n = 0;
-  for (int i = 0; i < run; ++i) n += sums[i][lane];
+  if (id < f.n_blocks) {
+    n = 0;
+    for (int i = 0; i < run; ++i) n += sums[i][lane];
 #pragma unroll 8
-  for (int g = g0; g < g1; ++g) {
-    uint32_t& x = c[static_cast<long long>(g) * f.n_blocks];
-    const uint32_t y = x;
-    x = n;
-    n += y;
+    for (int g = g0; g < g1; ++g) {
+      uint32_t& x = c[static_cast<long long>(g) * f.n_blocks];
+      const uint32_t y = x;
+      x = n;
+      n += y;
+    }
+    if (run == 31) {
+      f.total[id] = n;
+      __threadfence();
+    }
   }
-  if (run == 31) f.total[id] = n;
-}
-// start = running sum of total: one block of threads.
-__global__ void __launch_bounds__(1024) sparse_start_kernel(const WhoArgs f) {
-  __shared__ uint32_t sums[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(f.ticket, 1u) == gridDim.x - 1u;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
   uint32_t before = 0;
   for (int base = 0; base < f.n_blocks; base += 4096) {
     uint32_t x[4], mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int id = base + 4 * tid + i;
-      x[i] = id < f.n_blocks ? f.total[id] : 0u;
+      const int at = base + 4 * tid + i;
+      x[i] = at < f.n_blocks ? __ldcg(f.total + at) : 0u;
       mine += x[i];
     }
-    uint32_t run = mine;
+    uint32_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    if (lane == 31) sums[warp] = run;
+    if (lane == 31) sums[0][run] = upto;
     __syncthreads();
     uint32_t off = before, all = 0;
     for (int i = 0; i < 32; ++i) {
-      if (i < warp) off += sums[i];
-      all += sums[i];
+      if (i < run) off += sums[0][i];
+      all += sums[0][i];
     }
-    run += off - mine;
+    upto += off - mine;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int id = base + 4 * tid + i;
-      if (id < f.n_blocks) f.start[id] = run;
-      run += x[i];
+      const int at = base + 4 * tid + i;
+      if (at < f.n_blocks) f.start[at] = upto;
+      upto += x[i];
     }
     before += all;
     __syncthreads();
@@ -949,9 +956,11 @@ Plan make_plan(const SparseParams& p, int dtype) {
   a.rounds = (p.Tq + a.rows - 1) / a.rows;
   a.rows = (p.Tq + std::max(1, a.rounds) - 1) / std::max(1, a.rounds);  // of equal size
   a.n_blocks = (p.Tk >> p.block_shift) + p.N + 1;
-  // groups of some eight rows, their counts within 64 MB
-  const long long most = std::max(1ll, (16ll << 20) / a.n_blocks);
-  a.per = static_cast<int>(std::max(8ll, (a.rows + std::min(most, 2048ll) - 1) / std::min(most, 2048ll)));
+  // Groups of few rows, which sparse_fill_kernel takes one after the other (2 us each), their counts within 8 MB,
+  // which sparse_scan_kernel reads and writes.
+  const long long most = std::min(2048ll, std::max(1ll, (2ll << 20) / a.n_blocks));
+  a.per = static_cast<int>((a.rows + most - 1) / most);
+  a.per = std::max(1, a.per);
   a.groups = (a.rows + a.per - 1) / a.per;
   const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
   const bool lists = p.top_k > 0;
@@ -959,7 +968,7 @@ Plan make_plan(const SparseParams& p, int dtype) {
   a.norm_q = 2 * per_row;
   a.range = 3 * per_row;
   a.count = up(a.range + (fp16 ? static_cast<size_t>(p.N) * p.Hk * 4 : 0));
-  a.total = up(a.count + (lists ? static_cast<size_t>(a.groups) * a.n_blocks * 4 : 0));
+  a.total = up(a.count + (lists ? (static_cast<size_t>(a.groups) * a.n_blocks + 1) * 4 : 0));  // and the ticket
   a.start = up(a.total + (lists ? static_cast<size_t>(a.n_blocks) * 4 : 0));
   a.entry = up(a.start + (lists ? static_cast<size_t>(a.n_blocks + 1) * 4 : 0));
   a.power = up(a.entry + static_cast<size_t>(a.rows) * p.top_k * 4);
@@ -1045,11 +1054,11 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
     who.groups = (n + a.per - 1) / a.per;
     f.l.items = static_cast<long long>(n) * p.Hk * a.n_z;
     if (p.Tk > 0 && p.top_k > 0) {
-      if ((e = cudaMemsetAsync(who.count, 0, static_cast<size_t>(who.groups) * a.n_blocks * 4, stream)) != cudaSuccess)
-        return e;
+      const size_t counts = static_cast<size_t>(who.groups) * a.n_blocks;
+      who.ticket = who.count + counts;
+      if ((e = cudaMemsetAsync(who.count, 0, (counts + 1) * 4, stream)) != cudaSuccess) return e;
       sparse_count_kernel<<<static_cast<unsigned>((static_cast<long long>(n) * 32 + 255) / 256), 256, 0, stream>>>(who);
       sparse_scan_kernel<<<(a.n_blocks + 31) / 32, 1024, 0, stream>>>(who);
-      sparse_start_kernel<<<1, 1024, 0, stream>>>(who);
       sparse_fill_kernel<<<who.groups, 256, 0, stream>>>(who);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
