@@ -22,6 +22,8 @@
 // rotated, 98 us (6.15 TB/s, a plain copy gives 6.69); 32768 tokens, half
 // rotated in neighbouring pairs, 189 us (6.4 TB/s), gradients 294 us (6.2
 // TB/s).  64 tokens: 4.6 us, a launch.
+// With the append of keys and values to a paged cache (APPEND): 16384 tokens, 120 us
+// (5.6 TB/s; q 81 us and, in a launch of their own, k and v 34), 64 tokens, 8 us.
 //
 // Angles: position * freq modulo 2^64 is the fraction of a turn with 64 bits
 // after the point, exactly what the table says whatever the position; its upper 32

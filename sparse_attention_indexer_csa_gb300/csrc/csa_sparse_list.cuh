@@ -167,7 +167,7 @@ struct Tile {
 
 static_assert(sizeof(Tile) % 16 == 0, "tiles of a ring");
 
-// As mbar_wait, its slow part out of line (sixteen warps and more in seven roles
+// As mbar_wait, its slow part out of line (twenty warps and more in seven roles
 // run here, and what they wait for is instructions), and without a time for which
 // the thread may be suspended: a thread that gives one comes back later.
 static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, const WaitCtl& ctl) {

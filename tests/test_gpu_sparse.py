@@ -307,6 +307,17 @@ def test_gradients_of_a_key_that_every_row_lists():
     _run(q, k, v, do, idx, _cu([T]), _cu([300]), 0.125, causal=False)
 
 
+def test_gradients_where_blocks_are_many():
+    # 90003 numbers of blocks: the running sum of the lists takes 22 steps, and groups have several rows
+    lq, lk = [450, 0, 150], [50000, 3, 39997]
+    q, k, v, do = _inputs(lq, lk, 2, 1, 64, BF, seed=24)
+    idx = _lists(lq, lk, 40, 1, seed=11)
+    idx[::3, 5] = 4095 + torch.arange(200, dtype=torch.int32) % 3  # keys with many rows, at the border of a step
+    idx[:, 6:][(idx[:, 6:] >= 4095) & (idx[:, 6:] <= 4097)] = -1
+    idx[:, :5][(idx[:, :5] >= 4095) & (idx[:, :5] <= 4097)] = -1
+    _run(q, k, v, do, idx, _cu(lq), _cu(lk), 0.125, causal=False)
+
+
 def test_gradients_of_a_block_listed_twice():
     q, k, v, do = _inputs([3], [40], 4, 2, 64, BF, seed=4)
     idx = torch.tensor([[3, 3, 1, -1], [0, 2, 0, 0], [5, 5, 5, 5]], dtype=torch.int32)
