@@ -96,6 +96,9 @@ SparseParams sparse_params(const csa_sparse_problem* p, const void* q, const voi
   a.page = p->page;
   a.pages = p->page > 0 ? p->Tk / p->page : 0;
   a.table_width = p->table_width;
+  a.page_shift = 31;
+  while (p->page > (1ll << (a.page_shift - 31))) ++a.page_shift;
+  a.page_mul = p->page > 0 ? static_cast<uint32_t>(((1ull << a.page_shift) + p->page - 1) / p->page) : 0;
   a.scale = p->scale;
   a.q = q;
   a.q_sh = p->q_stride_h ? p->q_stride_h : p->D;

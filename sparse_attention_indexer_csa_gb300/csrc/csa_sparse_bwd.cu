@@ -704,7 +704,7 @@ __device__ __forceinline__ int listed_block(const SparseParams& p, const ListRow
 __global__ void __launch_bounds__(256) sparse_count_kernel(const WhoArgs f) {
   const int r = (blockIdx.x * 256 + threadIdx.x) / 32, lane = threadIdx.x & 31;
   if (r >= f.rows) return;
-  const ListRow row = find_list_row(f.p, f.t0 + r);
+  const ListRow row = find_list_row(f.p, load_borders(f.p), f.t0 + r);
   uint32_t* count = f.count + static_cast<long long>(r / f.per) * f.n_blocks;
   for (int u = lane; u < f.p.top_k; u += 32) {
     const int id = listed_block(f.p, row, f.t0 + r, u);
@@ -788,8 +788,9 @@ __global__ void __launch_bounds__(256) sparse_fill_kernel(const WhoArgs f) {
   const int g = blockIdx.x;
   uint32_t* place = f.count + static_cast<long long>(g) * f.n_blocks;
   const int last = min(f.rows, (g + 1) * f.per);
+  const Borders border = load_borders(f.p);
   for (int r = g * f.per; r < last; ++r) {
-    const ListRow row = find_list_row(f.p, f.t0 + r);
+    const ListRow row = find_list_row(f.p, border, f.t0 + r);
     for (int u = threadIdx.x; u < f.p.top_k; u += 256) {
       const int id = listed_block(f.p, row, f.t0 + r, u);
       if (id >= 0) f.entry[f.start[id] + atomicAdd(place + id, 1u)] = (static_cast<uint32_t>(r) << f.u_bits) | u;

@@ -22,6 +22,7 @@ struct SparseParams {
   int N, Tq, Tk, Hq, Hk, g, D;  // g = Hq / Hk
   int top_k, block_shift, window, causal;
   int page, pages, table_width;
+  uint32_t page_mul, page_shift;  // division by page: multiply, shift
   float scale;
   const void* q;
   long long q_st, q_sh, idx_st, table_st;

@@ -27,19 +27,18 @@ struct ListRow {
   int q0, q1;  // the sequence's rows
 };
 
-// Extents of sequence i, clamped to the tensors; what was clamped is recorded.
-__device__ __forceinline__ SeqExt sparse_extent(const SparseParams& p, int i) {
+// Extents of a sequence with rows a .. b-1, keys c .. d-1 and n of them (where given),
+// clamped to the tensors; `bad` where anything was.
+__device__ __forceinline__ SeqExt clamp_extent(const SparseParams& p, int a, int b, int c, int d, int n, bool& bad) {
   SeqExt s;
-  const int a = p.cu_q[i], b = p.cu_q[i + 1];
   s.q0 = min(max(a, 0), p.Tq);
   s.q1 = min(max(b, s.q0), p.Tq);
-  bool bad = a != s.q0 || b != s.q1;
+  bad |= a != s.q0 || b != s.q1;
   long long most;
   if (p.page > 0) {
     s.k0 = 0;
     most = static_cast<long long>(p.table_width) * p.page;
   } else {
-    const int c = p.cu_k[i], d = p.cu_k[i + 1];
     s.k0 = min(max(c, 0), p.Tk);
     const int k1 = min(max(d, s.k0), p.Tk);
     bad |= c != s.k0 || d != k1;
@@ -47,40 +46,79 @@ __device__ __forceinline__ SeqExt sparse_extent(const SparseParams& p, int i) {
   }
   s.lk = static_cast<int>(min(most, 0x7FFFFFFFll));
   if (p.k_len != nullptr) {
-    const int n = p.k_len[i], m = min(max(n, 0), s.lk);
+    const int m = min(max(n, 0), s.lk);
     bad |= n != m;
     s.lk = m;
   }
+  return s;
+}
+// Those of sequence i; what was clamped is recorded.
+__device__ __forceinline__ SeqExt sparse_extent(const SparseParams& p, int i) {
+  bool bad = false;
+  const SeqExt s = clamp_extent(p, p.cu_q[i], p.cu_q[i + 1], p.page > 0 ? 0 : p.cu_k[i], p.page > 0 ? 0 : p.cu_k[i + 1],
+                                p.k_len != nullptr ? p.k_len[i] : 0, bad);
   if (bad) record_error(kErrDevice);
   return s;
 }
 
-// The row's sequence, by a warp: the largest i with cu_q[i] <= t.  Sequences of
-// equal lengths (one token each, when decoding) are met at the first look, others
-// by 32 probes at a time.  Entries out of order give some sequence or none.
-__device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
+// Borders and lengths of up to 31 sequences, a lane each, read once: rows of several
+// sequences in turn would wait for them three times over (1021 rows in 13
+// sequences: 41.8 us, so 38.4).
+struct Borders {
+  int q, k, n;
+};
+__device__ __forceinline__ Borders load_borders(const SparseParams& p) {
+  Borders b{0, 0, 0};
+  const int lane = static_cast<int>(lane_id());
+  if (p.N > 0 && p.N <= 31) {
+    b.q = p.cu_q[min(lane, p.N)];
+    if (p.page == 0) b.k = p.cu_k[min(lane, p.N)];
+    if (p.k_len != nullptr && lane < p.N) b.n = p.k_len[lane];
+  }
+  return b;
+}
+
+// By 32 probes at a time.
+__device__ __forceinline__ int find_far(const SparseParams& p, int t) {
+  const int lane = static_cast<int>(lane_id());
+  int lo = 0, hi = p.N;
+  while (lo < hi) {
+    const int span = hi - lo, stride = (span + 31) / 32;
+    const int i = lo + min(span, (lane + 1) * stride);
+    const unsigned out = __ballot_sync(0xffffffffu, p.cu_q[i] > t);
+    if (out == 0u) {
+      lo = hi;
+    } else {
+      const int n = __ffs(static_cast<int>(out)) - 1;
+      hi = lo + min(span, (n + 1) * stride) - 1;
+      lo = lo + min(span, n * stride);
+    }
+  }
+  return lo;
+}
+// The row's sequence, by a warp: the largest i with cu_q[i] <= t.  More than 31
+// sequences of equal lengths (one token each, when decoding) are met at the first look,
+// others are searched.  Entries out of order give some sequence or none.
+__device__ __forceinline__ ListRow find_list_row(const SparseParams& p, const Borders& border, int t) {
   const int lane = static_cast<int>(lane_id());
   ListRow r{-1, 0, 0, -1, 0, 0};
   if (p.N <= 0) return r;
-  int lo = static_cast<int>(static_cast<long long>(t) * p.N / p.Tq);
-  if (t < p.cu_q[lo] || t >= p.cu_q[lo + 1]) {
-    lo = 0;
-    int hi = p.N;
-    while (lo < hi) {
-      const int span = hi - lo, stride = (span + 31) / 32;
-      const int i = lo + min(span, (lane + 1) * stride);
-      const unsigned out = __ballot_sync(0xffffffffu, p.cu_q[i] > t);
-      if (out == 0u) {
-        lo = hi;
-      } else {
-        const int n = __ffs(static_cast<int>(out)) - 1;
-        hi = lo + min(span, (n + 1) * stride) - 1;
-        lo = lo + min(span, n * stride);
-      }
-    }
+  int lo;
+  SeqExt s;
+  if (p.N <= 31) {
+    const int next = __shfl_down_sync(0xffffffffu, border.q, 1);
+    const unsigned in = __ballot_sync(0xffffffffu, lane < p.N && border.q <= t && t < next);
+    if (in == 0u) return r;
+    lo = 31 - __clz(static_cast<int>(in));
+    auto of = [&](int x, int i) { return __shfl_sync(0xffffffffu, x, i); };
+    bool bad = false;  // (recorded for all sequences at once)
+    s = clamp_extent(p, of(border.q, lo), of(border.q, lo + 1), of(border.k, lo), of(border.k, lo + 1), of(border.n, lo), bad);
+  } else {
+    lo = static_cast<int>(static_cast<long long>(t) * p.N / p.Tq);
+    if (t < p.cu_q[lo] || t >= p.cu_q[lo + 1]) lo = find_far(p, t);
     if (lo >= p.N) return r;
+    s = sparse_extent(p, lo);
   }
-  const SeqExt s = sparse_extent(p, lo);
   if (t < s.q0 || t >= s.q1) return r;
   r.seq = lo;
   r.q0 = s.q0;
@@ -92,47 +130,13 @@ __device__ __forceinline__ ListRow find_list_row(const SparseParams& p, int t) {
 }
 
 // The slots of a row's list: first the window, newest key first, then top_k
-// blocks.  A slot in three steps, so that the loads of the coming slots are in
-// flight while the present ones are dealt with.  `bad` gathers what is out of range.
-struct Slot {
-  int j;     // key of the sequence; -1: none
-  int page;  // its page (paged keys)
-};
+// blocks.  Slot s's block (-1: none).
 __device__ __forceinline__ int slot_block(const SparseParams& p, const int32_t* list, int s, int slots) {
   return s >= p.window && s < slots ? list[(s - p.window) >> p.block_shift] : -1;
 }
-__device__ __forceinline__ Slot slot_key(const SparseParams& p, const ListRow& r, int s, int slots, int b, bool& bad) {
-  Slot x{-1, 0};
-  if (s < p.window) {
-    x.j = r.pos - s;  // negative: before the first key
-  } else if (s < slots) {
-    if (static_cast<unsigned>(b) <= static_cast<unsigned>((r.lk - 1) >> p.block_shift)) {
-      const int j = (b << p.block_shift) + ((s - p.window) & ((1 << p.block_shift) - 1));
-      if (j < r.lk && j <= r.pos - p.window) x.j = j;
-    } else {
-      bad |= b != -1;
-    }
-  }
-  if (p.page > 0 && x.j >= 0) x.page = p.table[r.seq * p.table_st + x.j / p.page];
-  return x;
-}
-// Rows of keys and values of slot x (key head 0); false: it has none.
-__device__ __forceinline__ bool slot_rows(const SparseParams& p, const ListRow& r, const Slot& x, int& kr, int& vr,
-                                          bool& bad) {
-  if (x.j < 0) return false;
-  if (p.page > 0) {
-    if (static_cast<unsigned>(x.page) >= static_cast<unsigned>(p.pages)) {
-      bad = true;
-      return false;
-    }
-    const int off = x.j % p.page;
-    kr = x.page * p.k.rp + off * p.k.rt;
-    vr = x.page * p.v.rp + off * p.v.rt;
-  } else {
-    kr = (r.k0 + x.j) * p.k.rt;
-    vr = (r.k0 + x.j) * p.v.rt;
-  }
-  return true;
+// The page of key j >= 0 of a sequence: j * ceil(2^n / page) / 2^n with 2^(n - 31) >= page, which is exact below 2^31.
+__device__ __forceinline__ int page_of(const SparseParams& p, int j) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * p.page_mul) >> p.page_shift);
 }
 
 constexpr int kRing = 8;  // tiles of rows ahead
@@ -240,13 +244,14 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
       if (i == 0 || !quads) b[i] = slot_block(p, list, s + i, f.slots);
   };
   ListRow row{-1, 0, 0, -1, 0, 0};
+  const Borders border = load_borders(p);
   if (w < tiles) blocks();
   uint32_t st = static_cast<uint32_t>(w) % kRing, turn = static_cast<uint32_t>(w) / kRing & 1u;
   for (long long n = w; n < tiles; n += LISTS) {
     if (t >= row.q0 && t < row.q1)  // mostly the sequence of the row before
       row.pos = p.causal ? t - row.q0 + row.lk - (row.q1 - row.q0) : row.lk - 1;
     else
-      row = find_list_row(p, t);
+      row = find_list_row(p, border, t);
     TileHead h{0, at == f.per - 1, t, hk, z, tile(), row.seq};
     const int s = h.c * 128 + 4 * lane, k0 = hk * p.k.rh, v0 = hk * p.v.rh;
     int kr[4], vr[4];
@@ -272,7 +277,7 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
         if (p.page > 0) {
           kb = vb = 0;
           if (last > 0) {
-            const int n_page = j / p.page, pg = p.table[row.seq * p.table_st + n_page], off = j - n_page * p.page;
+            const int n_page = page_of(p, j), pg = p.table[row.seq * p.table_st + n_page], off = j - n_page * p.page;
             if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.pages)) {
               bad = true;
               last = 0;
@@ -293,16 +298,46 @@ __device__ __forceinline__ void list_tiles(const SparseParams& p, const ListArgs
             see |= 1u << i;
           }
       } else {
-        Slot x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = slot_key(p, row, s + i, f.slots, b[i], bad);
+        // straight on, a select for each border: branches for each slot took 2000 cycles a tile (38.4 us for 33.3, as above)
+        const int lim = min(row.lk - 1, row.pos - p.window), mask = (1 << p.block_shift) - 1;
+        const unsigned most = static_cast<unsigned>((row.lk - 1) >> p.block_shift);
+        int j[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          int a = 0, c = 0;
-          if (slot_rows(p, row, x[i], a, c, bad)) {
-            kr[i] = a + k0;
-            vr[i] = c + v0;
-            see |= 1u << i;
+          const bool listed = static_cast<unsigned>(b[i]) <= most;
+          const int key = static_cast<int>(static_cast<unsigned>(b[i]) << p.block_shift) + ((s + i - p.window) & mask);
+          bad |= !listed && b[i] != -1;
+          j[i] = listed && key <= lim ? key : -1;
+          if (s + i < p.window) j[i] = row.pos - s - i;
+        }
+        if (p.page > 0) {
+          const int32_t* table = p.table + row.seq * p.table_st;
+          int n_page[4], pg[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            n_page[i] = page_of(p, j[i]);
+            pg[i] = j[i] >= 0 ? table[n_page[i]] : 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int off = j[i] - n_page[i] * p.page;
+            const bool has = static_cast<unsigned>(pg[i]) < static_cast<unsigned>(p.pages);
+            bad |= j[i] >= 0 && !has;
+            if (j[i] >= 0 && has) {
+              kr[i] = pg[i] * p.k.rp + off * p.k.rt + k0;
+              vr[i] = pg[i] * p.v.rp + off * p.v.rt + v0;
+              see |= 1u << i;
+            }
+          }
+        } else {
+          const int kb = row.k0 * p.k.rt + k0, vb = row.k0 * p.v.rt + v0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (j[i] >= 0) {
+              kr[i] = kb + j[i] * p.k.rt;
+              vr[i] = vb + j[i] * p.v.rt;
+              see |= 1u << i;
+            }
           }
         }
       }
