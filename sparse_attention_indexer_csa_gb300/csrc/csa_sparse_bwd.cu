@@ -58,8 +58,10 @@ namespace {
 
 constexpr size_t kShareBytes = 4ull << 30;
 constexpr int kHeads = 64;  // query heads of an item at most
-constexpr int kLists = 2, kThreads = 640;
-constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14, kDrain2Warp = 16;
+constexpr int kLists = 2;
+constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14, kDrain2Warp = 16, kMma2Warp = 20;
+template <bool TWO>
+constexpr int kThreads = 32 * (kMma2Warp + (TWO ? 1 : 0));
 
 template <typename X>
 constexpr int kProbExp = is_bf16<X>() ? 0 : 15;  // power of two of P^T
@@ -74,28 +76,34 @@ struct ShareType<__half> {
   using T = float;
 };
 
-template <int D>
+// TWO: items of up to 32 heads, whose scores and dS have two buffers each.
+template <int D, bool TWO>
 struct Cfg {
+  static constexpr int kBufs = TWO ? 2 : 1, kFactors = TWO ? 4 : 2;
   static constexpr uint32_t kTile = kChunkBytes * (D / 64);           // 128 rows x D
-  static constexpr uint32_t kHeadChunk = kHeads * 128, kHeadTile = kHeadChunk * (D / 64);
+  static constexpr uint32_t kHeadChunk = (TWO ? 32 : kHeads) * 128, kHeadTile = kHeadChunk * (D / 64);
   static constexpr uint32_t kOffK = 0, kOffV = 2 * kTile, kOffDs = 4 * kTile;  // dS^T: 128 keys x 64 heads
   // (the product that reads dS has 128 rows: what stands behind its 64 heads is read too and not used)
-  static constexpr uint32_t kOffQ = kOffDs + kChunkBytes, kOffDo = kOffQ + 2 * kHeadTile;
+  static constexpr uint32_t kOffQ = kOffDs + kBufs * kChunkBytes, kOffDo = kOffQ + 2 * kHeadTile;
   static constexpr uint32_t kOffRing = kOffDo + 2 * kHeadTile;
   static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta, |dout|, |q|
-  static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [2][128] factors of a key's shares
-  static constexpr uint32_t kOffSum = kOffFactor + 2 * 128 * 8;          // [4][64] sums of p dout.v over a warp's keys
+  static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [kFactors][128] factors of a key's shares
+  static constexpr uint32_t kOffSum = kOffFactor + kFactors * 128 * 8;          // [4][64] sums of p dout.v over a warp's keys
   static constexpr uint32_t kOffFit = kOffSum + 4 * kHeads * 4;          // [2] power of two of dS
   static constexpr uint32_t kOffBar = kOffFit + 16;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
-                       kBarKFree = 14, kBarP = 16, kBarD = 17, kBarDFree = 18, kBarDq = 19, kBarDqFree = 20,
-                       kBarSum = 21, kBarTile = 22, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
+                       kBarKFree = 14, kBarP = 16, kBarD = 18, kBarDFree = 20, kBarDq = 21, kBarDqFree = 22,
+                       kBarSum = 23, kBarTile = 24, kBarTileFree = kBarTile + kRing, kBarDone = kBarTileFree + kRing,
                        kBars = kBarDone + 1;
   static constexpr uint32_t kOffMisc = kOffBar + 8 * kBars, kSmem = kOffMisc + 16;
 };
-static_assert(Cfg<128>::kSmem <= 227 * 1024, "one CTA per SM");
-static_assert(Cfg<64>::kOffRing >= Cfg<64>::kOffDs + 2 * kChunkBytes, "the second half of dS' product stays in bounds");
-static_assert(Cfg<64>::kOffStat % 16 == 0 && Cfg<128>::kOffStat % 16 == 0, "statistics are read 16 bytes at a time");
+template <typename C>
+constexpr bool fits_layout() {
+  return C::kSmem <= 227 * 1024 && C::kOffRing >= C::kOffDs + (C::kBufs + 1) * kChunkBytes && C::kOffStat % 16 == 0;
+}
+static_assert(fits_layout<Cfg<128, false>>() && fits_layout<Cfg<128, true>>() && fits_layout<Cfg<64, false>>() &&
+                  fits_layout<Cfg<64, true>>(),
+              "one CTA per SM; the second half of dS' product stays in bounds; statistics are read 16 bytes at a time");
 
 struct RowsArgs {
   SparseParams p;
@@ -170,12 +178,16 @@ __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* 
   }
 }
 
-// ONE: the lists are one tile.
-template <typename X, int D, bool ONE>
-__global__ void __launch_bounds__(kThreads, 1)
+// ONE: the lists are one tile.  TWO: see Cfg.  Then a tile's scores are formed while the
+// tile before is in its softmax, which mends what a row of few heads waits for most: the
+// way from P through its products to the next scores (3100 cycles of 4500 a tile).
+// (4096 rows of 2 x 16 heads, 16 blocks of 16, window 64: this kernel 348 -> 336 us, where
+// its shares go out at 4 TB/s; 517 rows of 2 x 5 heads of 64: 28 -> 24; with one issuer 375 and 23.)
+template <typename X, int D, bool ONE, bool TWO>
+__global__ void __launch_bounds__(kThreads<TWO>, 1)
     sparse_rows_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_do,
                        const __grid_constant__ RowsArgs f) {
-  using C = Cfg<D>;
+  using C = Cfg<D, TWO>;
   using T = typename ShareType<X>::T;
   extern __shared__ __align__(1024) uint8_t base[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBar);
@@ -194,9 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 1;
       if (i >= C::kBarK && i < C::kBarV + 2) n = 64;  // every lane that loads
       if (i >= C::kBarStatFree && i < C::kBarStatFree + 2) n = 12;
-      if (i == C::kBarP || i == C::kBarSum) n = 4;
+      if (i == C::kBarP || i == C::kBarP + 1 || i == C::kBarSum) n = 4;
       if (i == C::kBarDFree || i == C::kBarDqFree) n = 8;
-      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = 18;
+      if (i >= C::kBarTileFree && i < C::kBarTileFree + kRing) n = TWO ? 19 : 18;
+      if (i == C::kBarDone) n = TWO ? 2 : 1;
       mbar_init(bars + i, n);
     }
     if ((smem_u32(base) & 1023u) != 0u) record_error(kErrDevice);  // the swizzled tiles would be misread
@@ -204,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   // rows of no head: the products over heads read them, and the loads leave them as they are
-  for (uint32_t i = threadIdx.x; i < 4 * C::kHeadTile / 16; i += kThreads)
+  for (uint32_t i = threadIdx.x; i < 4 * C::kHeadTile / 16; i += kThreads<TWO>)
     reinterpret_cast<uint4*>(base + C::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_shared();
   if (warp == kMmaWarp) {
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  constexpr uint32_t kColS = 0, kColDp = 64, kColDv = 128, kColDk = 256, kColDq = 384;
+  constexpr uint32_t kColS = 0, kColDp = TWO ? 32 : 64, kColBuf = TWO ? 64 : 0, kColDv = 128, kColDk = 256, kColDq = 384;
   const WaitCtl ctl{abort_flag, f.wait_ns};
   volatile uint32_t dummy = 0;
   const WaitCtl drain{&dummy, f.wait_ns};  // for what has to be waited for even when a role gave up
@@ -304,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       give_head();
     }
     wait_rows();  // no copy is in flight when the CTA ends, a role's giving up included
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------------- issuer of the products
+  } else if (warp == kMmaWarp || warp >= kMma2Warp) {
+    // ------------------------------------------------------------------------- issuers of the products
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     const uint64_t qd = smem_desc_kmajor(smem_u32(base + C::kOffQ), 128), dod = smem_desc_kmajor(smem_u32(base + C::kOffDo), 128);
     const uint64_t qn = smem_desc_mn_sw128(smem_u32(base + C::kOffQ), C::kHeadChunk, 1024u);
@@ -317,24 +330,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdD = idesc_f16<X>(128, D, true), kIdDq = idesc_f16<X>(128, D, true) | (1u << 15);  // A MN-major too
     constexpr uint32_t kT = C::kTile >> 4, kH = C::kHeadTile >> 4;
     const int head_steps = uniform(f.padded >> 4);
-    bool alive = true, first = true, got_dq = false, pend_first = false;
-    int pend = 0;  // the last key of the tile whose P and dS are to come
+    bool alive = true, first = true, got_dq = false;
+    struct {  // the tile whose P and dS are to come: its last key (0: none), whether it is the item's first; gives dQ
+      int n;
+      bool first, last;
+      uint32_t j, q;  // its number, its item's
+    } pend{0, false, false, 0, 0};
     uint32_t j = 0, nq = 0, on = 0;
     auto wait = [&](int bar, uint32_t parity) { alive = alive && bar_wait(bars + bar, parity, ctl); };
-    auto shares = [&] {  // dV, dK of the last tile
-      const uint32_t i = j - 1;
-      wait(C::kBarP, i & 1u);
+    auto scores = [&] {  // S^T, dP^T of tile j, whose rows have been waited for
+      const uint32_t st = j & 1u;
+      fence_proxy_async_shared();
+      tc_fence_after();
+      if (elect_one()) {
+        if (alive) {
+          const uint64_t q = static_cast<uint64_t>((nq & 1u) * kH), t = static_cast<uint64_t>(st * kT);
+          const uint32_t to = tm + st * kColBuf;
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16(to + kColS, kd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
+                      qd + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            umma_bf16(to + kColDp, vd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
+                      dod + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
+        }
+        umma_commit(bars + C::kBarS + st);
+      }
+      __syncwarp();
+    };
+    auto shares = [&] {  // dV, dK
+      const uint32_t i = pend.j;
+      wait(C::kBarP + static_cast<int>(i & 1u), (i >> 1) & 1u);
       wait(C::kBarDFree, (i & 1u) ^ 1u);
       tc_fence_after();
       if (elect_one()) {
         if (alive) {
-          const uint64_t o = static_cast<uint64_t>((nq & 1u) * kH);
+          const uint64_t o = static_cast<uint64_t>((pend.q & 1u) * kH);
+          const uint32_t from = tm + (i & 1u) * kColBuf;
           for (int ks = 0; ks < head_steps; ++ks)
-            umma_bf16_tmem_a(tm + kColDv, tm + kColS + 8u * ks, don + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
+            umma_bf16_tmem_a(tm + kColDv, from + kColS + 8u * ks, don + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
           for (int ks = 0; ks < head_steps; ++ks)
-            umma_bf16_tmem_a(tm + kColDk, tm + kColDp + 8u * ks, qn + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
+            umma_bf16_tmem_a(tm + kColDk, from + kColDp + 8u * ks, qn + o + static_cast<uint64_t>(128 * ks), kIdD, ks != 0 ? 1u : 0u);
         }
-        umma_commit(bars + C::kBarD);
+        umma_commit(bars + C::kBarD + (i & 1u));
       }
       __syncwarp();
     };
@@ -342,73 +381,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!got_dq) wait(C::kBarDqFree, (on & 1u) ^ 1u);
       got_dq = true;
     };
-    auto query = [&] {  // dQ += dS K of the last tile
-      const uint32_t st = (j - 1) & 1u;
+    auto give_dq = [&](bool any, uint32_t q) {  // the item's dQ is complete, and so is what its queries are read for
+      take_dq();
+      got_dq = false;
+      if (elect_one()) {
+        umma_commit(bars + C::kBarDq);
+        if (any) umma_commit(bars + C::kBarQFree + (q & 1u));
+      }
+      __syncwarp();
+      ++on;
+    };
+    auto query = [&] {  // dQ += dS K
+      const uint32_t st = pend.j & 1u;
       take_dq();
       tc_fence_after();
-      const int steps = (pend + 15) >> 4;
+      const int steps = (pend.n + 15) >> 4;
       if (elect_one()) {
         if (alive)
           for (int ks = 0; ks < steps; ++ks)
-            umma_bf16(tm + kColDq, ds + static_cast<uint64_t>(128 * ks), kn + static_cast<uint64_t>(st * kT + 128 * ks), kIdDq,
-                      (!pend_first || ks != 0) ? 1u : 0u);
+            umma_bf16(tm + kColDq, ds + static_cast<uint64_t>((TWO ? st * (kChunkBytes >> 4) : 0u) + 128 * ks),
+                      kn + static_cast<uint64_t>(st * kT + 128 * ks), kIdDq, (!pend.first || ks != 0) ? 1u : 0u);
         umma_commit(bars + C::kBarKFree + st);
       }
       __syncwarp();
-      pend = 0;
+      pend.n = 0;
+      if (pend.last) give_dq(true, pend.q);
     };
+    // One issuer: the products of a tile's P and dS are issued when the next tile has come
     while (alive) {
       const TileHead h = next_head();
       const int n = uniform(h.n), last = uniform(h.last);
       if (n < 0) break;
       give_head();
-      if (n > 0) {
-        const uint32_t st = j & 1u, par = (j >> 1) & 1u;
-        if (pend != 0) {
+      const uint32_t st = j & 1u, par = (j >> 1) & 1u;
+      if (TWO && warp == kMmaWarp) {
+        if (n > 0) {
+          if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
+          wait(C::kBarD + static_cast<int>(st), par ^ 1u);  // P and dS of the tile before the last have been used
+          wait(C::kBarK + static_cast<int>(st), par);
+          wait(C::kBarV + static_cast<int>(st), par);
+          scores();
+        }
+      } else if (TWO) {
+        if (n > 0) {
+          pend = {n, first, last != 0, j, nq};
+          wait(C::kBarK + static_cast<int>(st), par);
+          fence_proxy_async_shared();
           shares();
-          // the next scores go first, unless they would have to wait for their tile
-          if (!mbar_look_warp(bars + C::kBarK + st, par) || !mbar_look_warp(bars + C::kBarV + st, par)) query();
+          query();
+        } else if (last != 0) {
+          give_dq(!first, nq);
         }
-        if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
-        wait(C::kBarK + static_cast<int>(st), par);
-        wait(C::kBarV + static_cast<int>(st), par);
-        fence_proxy_async_shared();
-        tc_fence_after();
-        if (elect_one()) {
-          if (alive) {
-            const uint64_t q = static_cast<uint64_t>((nq & 1u) * kH), t = static_cast<uint64_t>(st * kT);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16(tm + kColS, kd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
-                        qd + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              umma_bf16(tm + kColDp, vd + t + static_cast<uint64_t>(((ks >> 2) * kChunkBytes + (ks & 3) * 32) >> 4),
-                        dod + q + static_cast<uint64_t>(((ks >> 2) * C::kHeadChunk + (ks & 3) * 32) >> 4), id_s, ks != 0 ? 1u : 0u);
+      } else {
+        if (n > 0) {
+          if (pend.n != 0) {
+            shares();  // reads P and dS where the scores will be
+            // the next scores go first, unless they would have to wait for their tile
+            if (!mbar_look_warp(bars + C::kBarK + st, par) || !mbar_look_warp(bars + C::kBarV + st, par)) query();
           }
-          umma_commit(bars + C::kBarS + st);
+          if (first) wait(C::kBarQ + static_cast<int>(nq & 1u), (nq >> 1) & 1u);
+          wait(C::kBarK + static_cast<int>(st), par);
+          wait(C::kBarV + static_cast<int>(st), par);
+          scores();
+          if (pend.n != 0) query();
+          pend = {n, first, false, j, nq};
         }
-        __syncwarp();
-        if (pend != 0) query();
-        pend = n;
-        pend_first = first;
+        if (last != 0) {
+          if (pend.n != 0) {
+            shares();
+            query();
+          }
+          give_dq(n > 0 || !first, nq);
+        }
+      }
+      if (n > 0) {
         first = false;
         ++j;
       }
-      if (last) {
-        if (pend != 0) {
-          shares();
-          query();
-        }
-        take_dq();
-        got_dq = false;
-        if (elect_one()) {
-          umma_commit(bars + C::kBarDq);
-          if (!first) umma_commit(bars + C::kBarQFree + (nq & 1u));
-        }
-        __syncwarp();
+      if (last != 0) {
         if (!first) ++nq;
-        ++on;
         first = true;
       }
     }
@@ -419,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------------- P and dS: a thread per key
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int key = warp * 32 + static_cast<int>(lane);
-    uint8_t* row = base + C::kOffDs + key * 128;
     const float2 c2 = make_float2(f.c, f.c);
     uint32_t j = 0, ni = 0;
     bool first = true;
@@ -448,18 +498,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         first = false;
         if (!bar_wait(bars + C::kBarS + st, (j >> 1) & 1u, ctl)) break;
-        // the former tile's product with K has read dS
-        if (j > 0 && !bar_wait(bars + C::kBarKFree + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl)) break;
+        // the former tile's product with K has read dS (TWO: the one before that has, or K would not be here)
+        if (!TWO && j > 0 && !bar_wait(bars + C::kBarKFree + (st ^ 1u), ((j - 1) >> 1) & 1u, ctl)) break;
         tc_fence_after();
         const bool see = (ring[at.slot].keys[warp] >> lane) & 1u;
+        uint8_t* row = base + C::kOffDs + (TWO ? st * kChunkBytes : 0u) + key * 128;
+        const uint32_t ts = tmem + lanes + kColS + st * kColBuf, td = tmem + lanes + kColDp + st * kColBuf;
         const float4* ls = stat + (ni & 1u) * kHeads;
         if constexpr (ONE) {  // delta, see above
           float* sums = reinterpret_cast<float*>(base + C::kOffSum);
 #pragma unroll 1
           for (int i = 0; i < f.padded / 16; ++i) {
             float t[16], dp[16];
-            tmem_ld16_start(tmem + lanes + kColS + 16 * i, t);
-            tmem_ld16_start(tmem + lanes + kColDp + 16 * i, dp);
+            tmem_ld16_start(ts + 16 * i, t);
+            tmem_ld16_start(td + 16 * i, dp);
             tmem_wait16(t);
             tmem_wait16(dp);
 #pragma unroll
@@ -486,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < f.padded / 16; ++i) {
           float s[16], dp[16];
-          tmem_ld16_start(tmem + lanes + kColS + 16 * i, s);
-          tmem_ld16_start(tmem + lanes + kColDp + 16 * i, dp);
+          tmem_ld16_start(ts + 16 * i, s);
+          tmem_ld16_start(td + 16 * i, dp);
           tmem_wait16(s);
           tmem_wait16(dp);
           uint32_t pw[8], dw[8];
@@ -504,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             pw[u] = see ? pack_pair<X>(w.x, w.y) : 0u;
             dw[u] = see ? pack_pair<X>(d.x, d.y) : 0u;
           }
-          tmem_st8(tmem + lanes + kColS + 8 * i, pw);
-          tmem_st8(tmem + lanes + kColDp + 8 * i, dw);
+          tmem_st8(ts + 8 * i, pw);
+          tmem_st8(td + 8 * i, dw);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             *reinterpret_cast<uint4*>(row + (((2 * i + u) ^ (key & 7)) * 16)) =
@@ -516,14 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ek = exponent_above((bk.x + bk.y) * back, 110);
           ev = exponent_above((bv.x + bv.y) * back_v, 110);
         }
-        factor[st * 128 + key] = make_float2(back * power_of_two(15 - ek), back_v * power_of_two(15 - ev));
+        factor[(j % C::kFactors) * 128 + key] = make_float2(back * power_of_two(15 - ek), back_v * power_of_two(15 - ev));
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
         f.power[item * f.s_pad + h.c * 128 + key] = static_cast<uint16_t>((ek + 128) | ((ev + 128) << 8));
         tmem_wait_st();
         fence_proxy_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bars + C::kBarP);
+        if (lane == 0) mbar_arrive(bars + C::kBarP + st);
         ++j;
       }
       if (h.last && !first) {
@@ -547,12 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (h.n > 0) {
         first = false;
         const uint32_t see = ring[at.slot].keys[w];
-        if (!bar_wait(bars + C::kBarD, j & 1u, ctl)) break;
+        if (!bar_wait(bars + C::kBarD + (j & 1u), (j >> 1) & 1u, ctl)) break;
         tc_fence_after();
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;
         T* dst = static_cast<T*>(f.share) + ((2 * item + (dk ? 0 : 1)) * f.s_pad + h.c * 128 + w * 32) * D;
         if (see != 0u) {
-          const float2 both = factor[(j & 1u) * 128 + w * 32 + lane];
+          const float2 both = factor[(j % C::kFactors) * 128 + w * 32 + lane];
           const float mine = dk ? both.x : both.y;
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -1038,8 +1090,20 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
       !make_heads_map(&tdo, p, p.dout, static_cast<long long>(p.Hq) * D, D, a.heads))
     return cudaErrorInvalidValue;
   const bool one = f.l.per == 1;
-  const auto kernel = one ? sparse_rows_kernel<X, D, true> : sparse_rows_kernel<X, D, false>;
-  e = one ? smem_limit_once<sparse_rows_kernel<X, D, true>>(Cfg<D>::kSmem) : smem_limit_once<sparse_rows_kernel<X, D, false>>(Cfg<D>::kSmem);
+  void (*kernel)(CUtensorMap, CUtensorMap, RowsArgs) = nullptr;
+  uint32_t smem = 0, threads = 0;
+  const bool two = f.padded <= 32;
+  auto take = [&](auto k1, auto k2) {
+    constexpr bool ONE = decltype(k1)::value, TWO = decltype(k2)::value;
+    constexpr auto k = sparse_rows_kernel<X, D, ONE, TWO>;
+    kernel = k;
+    smem = Cfg<D, TWO>::kSmem;
+    threads = kThreads<TWO>;
+    return smem_limit_once<k>(smem);
+  };
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  e = one ? (two ? take(yes, yes) : take(yes, no)) : (two ? take(no, yes) : take(no, no));
   if (e != cudaSuccess) return e;
   WhoArgs who;
   who.p = p;
@@ -1077,7 +1141,7 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
     }
     const long long grid = std::min(f.l.items, 152ll);
     set_step(f.l, p.Hk, grid);
-    kernel<<<static_cast<unsigned>(grid), kThreads, Cfg<D>::kSmem, stream>>>(tq, tdo, f);
+    kernel<<<static_cast<unsigned>(grid), threads, smem, stream>>>(tq, tdo, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (p.Tk == 0) continue;
     sum.opens = i == 0;
