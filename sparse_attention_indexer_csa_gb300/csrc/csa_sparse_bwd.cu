@@ -150,7 +150,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 
 // 32 columns of a warp's 32 rows, each times its lane's f, stored as T: lanes 4 i
 // .. 4 i + 3 exchange 16-byte pieces, so that four lanes store 64 bytes of one row.
-// Row r goes to dst + r * D where bit r of `rows` is set.
+// Row r goes to dst + r * D where bit r of `rows` is set.  (Streaming stores: what is written is
+// read once, much later; 722 -> 716 us and 853 -> 848.)
 template <typename T, int D>
 __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* dst, uint32_t rows) {
   const uint32_t lane = lane_id();
@@ -173,7 +174,7 @@ __device__ __forceinline__ void store_columns(const float (&o)[32], float f, T* 
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t r = (lane & ~3u) + u;
-      if ((rows >> r) & 1u) reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 16 * h)[lane & 3u] = q[u];
+      if ((rows >> r) & 1u) __stcs(reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * D + 16 * h) + (lane & 3u), q[u]);
     }
   }
 }
@@ -1025,7 +1026,7 @@ Plan make_plan(const SparseParams& p, int dtype) {
   // 304: 870.
   const double even = std::sqrt(static_cast<double>(a.rows) * 750000.0 / a.n_blocks);
   const long long most = std::max(1ll, static_cast<long long>(std::min(even, 1024.0)));
-  a.per = static_cast<int>((a.rows + most - 1) / most);
+  a.per = std::max(1, static_cast<int>((a.rows + most - 1) / most));  // (no rows: one group of none)
   a.groups = (a.rows + a.per - 1) / a.per;
   const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
   const bool lists = p.top_k > 0;
