@@ -35,10 +35,11 @@
 // for all keys of the row at once, and shows where these are few.
 //
 // Measured (bf16, D 128): 8192 rows of 64 heads and one key head, 256 listed entries
-// each, 650 us: delta 59, lists 50, rows 372, sums 203 (1 GB of shares, which
-// rows writes at 2.7 TB/s, forming 161 GFLOP, and sums reads at 5.0 TB/s).  4096 rows of 2 x
-// 16 heads, 16 blocks of 16 and a window of 64: 570 us, of which rows 352 and sums 180.
-// The rows kernel is bound by its roles' steps one behind the other (P and dS of a tile
+// each, 680 us: delta 60 to 69, lists 45, rows 355, sums 205 (1 GB of shares, which
+// rows writes at 2.8 TB/s, forming 161 GFLOP, and sums reads at 5.0 TB/s).  4096 rows of 2 x
+// 16 heads, 16 blocks of 16 and a window of 64: 550 us, of which rows 331 (4 TB/s of
+// shares) and sums 181.
+// With 64 heads the rows kernel is bound by its roles' steps one behind the other (P and dS of a tile
 // wait for its scores, its shares for both, and one buffer holds each: tensor cores 22
 // %, schedulers 43 %, HBM 39 %).
 //

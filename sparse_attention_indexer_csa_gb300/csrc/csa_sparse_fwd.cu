@@ -38,11 +38,11 @@
 // Shared memory: two query blocks, two key and two value tiles.  TMEM: S0 S1 O0 O1.
 //
 // Measured (bf16, D 128): 16384 rows of 64 heads and one key head over 512 listed
-// entries, 453 us (569 TFLOP/s of counted work, twice that with the copies of the
+// entries, 425 us (606 TFLOP/s of counted work, twice that with the copies of the
 // queries); 8192 rows of 2 x 16 heads over 256 blocks of 4 keys and a window of 128,
-// 724 us (12 TB/s out of L2; 16 heads of 128 rows count); one token of 64 sequences, 8
-// key heads, 512 blocks of 4 of a cache of 32768, 102 us (5.6 TB/s of HBM, 84 % of a
-// copy); one token, 131072 cached, 13 us and 4 for the join.  Prompts are bound by what
+// 688 us (13 TB/s out of L2; 16 heads of 128 rows count); one token of 64 sequences, 8
+// key heads, 512 blocks of 4 of a cache of 32768, 97 us (5.9 TB/s of HBM, 88 % of a
+// copy); one token, 131072 cached, 12 us with the join.  Prompts are bound by what
 // a tile costs in instructions (schedulers busy 63 % of the time, tensor cores 41 %)
 // and in meetings of the roles, 200 to 300 cycles each; wide blocks by the gathered
 // rows out of L2.
