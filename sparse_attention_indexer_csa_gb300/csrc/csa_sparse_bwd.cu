@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p,
 // (k0 >> shift) + i + b, of n_blocks = (Tk >> shift) + N + 1.
 struct WhoArgs {
   SparseParams p;
-  int t0, rows;          // this round's rows
+  int t0, rows;          // rows t0 .. t0 + rows - 1
   int groups, per;       // groups of `per` rows whose counts are kept apart
   int n_blocks;
   int u_bits;            // an entry is (row - t0) << u_bits | place in the row's list

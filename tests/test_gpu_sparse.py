@@ -307,6 +307,31 @@ def test_gradients_of_a_key_that_every_row_lists():
     _run(q, k, v, do, idx, _cu([T]), _cu([300]), 0.125, causal=False)
 
 
+@pytest.mark.parametrize("N", [31, 32, 75])
+def test_gradients_of_many_sequences(N):
+    # up to 31 are held by the lanes, more are searched; lengths of zero to 13 rows, so no row's sequence is guessed
+    rng = np.random.default_rng(N)
+    lq = rng.integers(0, 14, N).tolist()
+    lk = [n + int(m) for n, m in zip(lq, rng.integers(0, 60, N))]
+    q, k, v, do = _inputs(lq, lk, 6, 2, 64, BF, seed=25)
+    idx = _lists(lq, lk, 11, 2, seed=12)
+    out = _run(q, k, v, do, idx, _cu(lq), _cu(lk), 0.125, block=2, window=7)
+    # the same keys in pages, in another order
+    page, width = 8, -(-max(lk) // 8)
+    table = torch.randperm(N * width, generator=torch.Generator().manual_seed(1)).reshape(N, width).to(torch.int32)
+    kp, vp = (torch.full((N * width, page, 2, 64), float("nan"), dtype=BF) for _ in range(2))
+    at = 0
+    for i, n in enumerate(lk):
+        for j in range(n):
+            kp[table[i, j // page], j % page], vp[table[i, j // page], j % page] = k[at + j], v[at + j]
+        at += n
+    c = lambda t: t.cuda()  # noqa: E731
+    paged = csa.sparse_attn_paged(c(q), c(kp), c(vp), c(table), c(idx), c(_cu(lq)), torch.tensor(lk, dtype=torch.int32).cuda(),
+                                  0.125, block=2, window=7)
+    _ok()
+    assert all(torch.equal(a, b) for a, b in zip(paged, out))
+
+
 def test_gradients_where_blocks_are_many():
     # 90003 numbers of blocks: the running sum of the lists takes 22 steps, and groups have several rows
     lq, lk = [450, 0, 150], [50000, 3, 39997]
