@@ -35,7 +35,7 @@
 // for all keys of the row at once, and shows where these are few.
 //
 // Measured (bf16, D 128): 8192 rows of 64 heads and one key head, 256 listed entries
-// each, 680 us: delta 60 to 69, lists 45, rows 355, sums 205 (1 GB of shares, which
+// each, 670 us: delta 60 to 69, lists 36, rows 355, sums 205 (1 GB of shares, which
 // rows writes at 2.8 TB/s, forming 161 GFLOP, and sums reads at 5.0 TB/s).  4096 rows of 2 x
 // 16 heads, 16 blocks of 16 and a window of 64: 550 us, of which rows 331 (4 TB/s of
 // shares) and sums 181.
@@ -59,6 +59,7 @@ namespace {
 
 constexpr size_t kShareBytes = 4ull << 30;
 constexpr int kHeads = 64;  // query heads of an item at most
+constexpr int kGroups = 1024;  // groups of rows in the lists' sort at most
 constexpr int kLists = 2;
 constexpr int kDrainWarp = 4, kKeyWarp = 8, kValueWarp = 10, kMmaWarp = 12, kItemWarp = 13, kListWarp = 14, kDrain2Warp = 16, kMma2Warp = 20;
 template <bool TWO>
@@ -748,9 +749,8 @@ struct WhoArgs {
   uint32_t *count, *total, *start, *entry;  // [groups][n_blocks], [n_blocks], [n_blocks + 1], [rows * top_k]
   uint32_t* ticket;                         // zero before sparse_scan_kernel, as the counts
 };
-// Number of the block that place u of row t lists, where the row sees some of its keys; -1 else.
-__device__ __forceinline__ int listed_block(const SparseParams& p, const ListRow& r, int t, int u) {
-  const int b = p.idx[t * p.idx_st + u];
+// Number of the listed block b of a row, where the row sees some of its keys; -1 else.
+__device__ __forceinline__ int listed_block(const SparseParams& p, const ListRow& r, int b) {
   if (r.lk <= 0 || static_cast<unsigned>(b) > static_cast<unsigned>((r.lk - 1) >> p.block_shift)) return -1;
   if ((b << p.block_shift) > static_cast<long long>(r.pos) - p.window) return -1;
   return (r.k0 >> p.block_shift) + r.seq + b;
@@ -761,36 +761,36 @@ __global__ void __launch_bounds__(256) sparse_count_kernel(const WhoArgs f) {
   const ListRow row = find_list_row(f.p, load_borders(f.p), f.t0 + r);
   uint32_t* count = f.count + static_cast<long long>(r / f.per) * f.n_blocks;
   for (int u = lane; u < f.p.top_k; u += 32) {
-    const int id = listed_block(f.p, row, f.t0 + r, u);
+    const int id = listed_block(f.p, row, f.p.idx[(f.t0 + r) * f.p.idx_st + u]);
     if (id >= 0) atomicAdd(count + id, 1u);
   }
 }
 // Counts become places within the block's entries.  32 blocks of keys and 32 runs of
-// groups per block of threads: each thread adds up its run, the runs before it give
-// where it starts.  The last block of threads to be through forms start, the running sum of
+// groups per block of threads: each thread adds up its run of groups, the runs before it
+// give where it starts.  The last block of threads to be through forms start, the running sum of
 // the totals (a launch of its own took 4 us).
 __global__ void __launch_bounds__(1024) sparse_scan_kernel(const WhoArgs f) {
   __shared__ uint32_t sums[32][33];
   __shared__ bool last;
   const int tid = threadIdx.x, lane = tid & 31, run = tid / 32, id = blockIdx.x * 32 + lane;
   const int per = (f.groups + 31) / 32, g0 = min(f.groups, run * per), g1 = min(f.groups, g0 + per);
-  uint32_t* c = f.count + id;
-  uint32_t n = 0;
-  if (id < f.n_blocks) {
-#pragma unroll 8
-    for (int g = g0; g < g1; ++g) n += c[static_cast<long long>(g) * f.n_blocks];
-  }
+  uint32_t* c = f.count + static_cast<long long>(g0) * f.n_blocks + id;
+  uint32_t n = 0, x[kGroups / 32];
+#pragma unroll
+  for (int g = 0; g < kGroups / 32; ++g)
+    x[g] = id < f.n_blocks && g < g1 - g0 ? c[static_cast<long long>(g) * f.n_blocks] : 0u;
+#pragma unroll
+  for (int g = 0; g < kGroups / 32; ++g) n += x[g];
   sums[run][lane] = n;
   __syncthreads();
   if (id < f.n_blocks) {
     n = 0;
-    for (int i = 0; i < run; ++i) n += sums[i][lane];
-#pragma unroll 8
-    for (int g = g0; g < g1; ++g) {
-      uint32_t& x = c[static_cast<long long>(g) * f.n_blocks];
-      const uint32_t y = x;
-      x = n;
-      n += y;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) n += i < run ? sums[i][lane] : 0u;
+#pragma unroll
+    for (int g = 0; g < kGroups / 32; ++g) {
+      if (g < g1 - g0) c[static_cast<long long>(g) * f.n_blocks] = n;
+      n += x[g];
     }
     if (run == 31) {
       f.total[id] = n;
@@ -820,6 +820,7 @@ __global__ void __launch_bounds__(1024) sparse_scan_kernel(const WhoArgs f) {
     if (lane == 31) sums[0][run] = upto;
     __syncthreads();
     uint32_t off = before, all = 0;
+#pragma unroll
     for (int i = 0; i < 32; ++i) {
       if (i < run) off += sums[0][i];
       all += sums[0][i];
@@ -843,10 +844,15 @@ __global__ void __launch_bounds__(256) sparse_fill_kernel(const WhoArgs f) {
   uint32_t* place = f.count + static_cast<long long>(g) * f.n_blocks;
   const int last = min(f.rows, (g + 1) * f.per);
   const Borders border = load_borders(f.p);
+  const int u0 = threadIdx.x;
+  auto list = [&](int r, int u) { return u < f.p.top_k && r < last ? f.p.idx[(f.t0 + r) * f.p.idx_st + u] : -1; };
+  int next = list(g * f.per, u0);  // of the coming row, on its way while this one's places are taken
   for (int r = g * f.per; r < last; ++r) {
     const ListRow row = find_list_row(f.p, border, f.t0 + r);
-    for (int u = threadIdx.x; u < f.p.top_k; u += 256) {
-      const int id = listed_block(f.p, row, f.t0 + r, u);
+    const int here = next;
+    next = list(r + 1, u0);
+    for (int u = u0; u < f.p.top_k; u += 256) {
+      const int id = listed_block(f.p, row, u == u0 ? here : list(r, u));
       if (id >= 0) f.entry[f.start[id] + atomicAdd(place + id, 1u)] = (static_cast<uint32_t>(r) << f.u_bits) | u;
     }
     __syncthreads();
@@ -1023,10 +1029,10 @@ Plan make_plan(const SparseParams& p, int dtype) {
   // sparse_fill_kernel takes a group's rows one after the other, 2 us each; the counts of a group are cleared, added to,
   // read and written once each, 16 bytes for a block of keys, at 6 bytes a ps.  Both cost the same where groups^2 = rows *
   // 750000 / n_blocks.  (Of 16384 rows over 131072 blocks of one key: 308 groups, 110 us each; as many groups as 8 MB of
-  // counts hold, 16, would take 2 ms.)  1024 groups fill the SMs: 8192 rows, 256 listed entries, 863 us in all, 2048: 895,
-  // 304: 870.
+  // counts hold, 16, would take 2 ms.)  1024 groups fill the SMs (8192 rows, 256 listed entries, with the forward: 863 us, 2048:
+  // 895, 304: 870).
   const double even = std::sqrt(static_cast<double>(a.rows) * 750000.0 / a.n_blocks);
-  const long long most = std::max(1ll, static_cast<long long>(std::min(even, 1024.0)));
+  const long long most = std::max(1ll, static_cast<long long>(std::min(even, static_cast<double>(kGroups))));
   a.per = std::max(1, static_cast<int>((a.rows + most - 1) / most));  // (no rows: one group of none)
   a.groups = (a.rows + a.per - 1) / a.per;
   const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
