@@ -95,7 +95,8 @@ csa_status csa_sparse_attn_forward(const csa_sparse_problem* p, const void* q, c
  * are taken in a fixed order (the same bits on every call).  Needs `workspace`:
  * csa_sparse_attn_workspace_size(p, 1) bytes, 16-byte aligned: each row's share of
  * dk and dv for each key it lists, as many rows at a time as 4 GiB hold (one at
- * least).                                                                      */
+ * least; where not all, also fp32 sums of dk and dv), and the rows by key, up to
+ * 1 GiB and 12 bytes for each block of keys.                                    */
 csa_status csa_sparse_attn_backward(const csa_sparse_problem* p, const void* dout, const void* q, const void* k,
                                     const void* v, const void* out, const float* lse, const int32_t* idx,
                                     const int32_t* cu_q, const int32_t* cu_k, const int32_t* k_len, void* dq,

@@ -1030,9 +1030,9 @@ Plan make_plan(const SparseParams& p, int dtype) {
   // read and written once each, 16 bytes for a block of keys, at 6 bytes a ps.  Both cost the same where groups^2 = rows *
   // 750000 / n_blocks.  (Of 16384 rows over 131072 blocks of one key: 308 groups, 110 us each; as many groups as 8 MB of
   // counts hold, 16, would take 2 ms.)  1024 groups fill the SMs (8192 rows, 256 listed entries, with the forward: 863 us, 2048:
-  // 895, 304: 870).
+  // 895, 304: 870), and 1 GiB of counts is the most there is for them.
   const double even = std::sqrt(static_cast<double>(a.rows) * 750000.0 / a.n_blocks);
-  const long long most = std::max(1ll, static_cast<long long>(std::min(even, static_cast<double>(kGroups))));
+  const long long most = std::max(1ll, static_cast<long long>(std::min({even, static_cast<double>(kGroups), 268435456.0 / a.n_blocks})));
   a.per = std::max(1, static_cast<int>((a.rows + most - 1) / most));  // (no rows: one group of none)
   a.groups = (a.rows + a.per - 1) / a.per;
   const size_t per_row = up(static_cast<size_t>(p.Tq) * p.Hq * 4);
