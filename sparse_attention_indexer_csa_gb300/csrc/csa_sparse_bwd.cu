@@ -27,7 +27,9 @@
 // the bound sum over heads of |ds| |q| (p |dout|) that its key's thread adds up on the
 // way: 11 bits, finer than ds and p have, at half of fp32's bytes (in bf16 it cost
 // the gradients half of their precision, 0.0029 of their size for 0.0024).  For fp16,
-// whose own roundings are no larger, it is fp32.  As many rows at a time as
+// whose own roundings are no larger, it is fp32.  The scale meets dk when its shares have
+// been added: a large one would take the power of two of a share whose bound is zero
+// past fp32's range (0 * inf from a scale of 8 on).  As many rows at a time as
 // kShareBytes hold.
 //
 // Where a list is one tile, delta is taken as sum_j p_j dout.v_j from the products at
@@ -116,7 +118,7 @@ struct RowsArgs {
   const float *delta, *norm_do, *norm_q;  // [Tq][Hq]
   const uint32_t* range;
   void* share;     // [rows][Hk][n_z][2][s_pad][D] (ShareType)
-  uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk is its values times 2^(low byte - 143), dv: high byte
+  uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk / scale is its values times 2^(low byte - 143), dv: high byte
   unsigned long long wait_ns;
 };
 
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
     uint32_t j = 0, ni = 0;
     bool first = true;
     float fit = 1.f;        // power of two of dS over that of P
-    float back = p.scale, back_v = 1.f;  // what undoes the powers of two
+    float back = 1.f, back_v = 1.f;  // what undoes the powers of two
     uint32_t met = 0;
     auto meet_all = [&] {  // these four warps, bounded as every wait is
       __syncwarp();
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
           if (!bar_wait(bars + C::kBarStat + (ni & 1u), (ni >> 1) & 1u, ctl)) break;
           if constexpr (!is_bf16<X>()) {
             fit = power_of_two(fits[ni & 1u] - kProbExp<X>);
-            back = p.scale * power_of_two(-fits[ni & 1u]);
+            back = power_of_two(-fits[ni & 1u]);
             back_v = power_of_two(-kProbExp<X>);
           }
         }
@@ -627,8 +629,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         tc_fence_after();
         ++on;
         if (w * 32 < f.heads) {
-          float back = p.scale;
-          if (!is_bf16<X>() && !first) back *= power_of_two(-fits[ni & 1u]);
+          const float back = !is_bf16<X>() && !first ? power_of_two(-fits[ni & 1u]) : 1.f;
           X* dst = static_cast<X*>(p.dq) +
                    (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + h.z * f.heads + w * 32) * D;
 #pragma unroll 1
@@ -639,8 +640,11 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             if (first) {
 #pragma unroll
               for (int u = 0; u < 32; ++u) o[u] = 0.f;  // no key
+            } else if constexpr (!is_bf16<X>()) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[u] *= back;
             }
-            store_columns<X, D>(o, back, dst + 32 * ch, low_bits(f.heads - w * 32));
+            store_columns<X, D>(o, p.scale, dst + 32 * ch, low_bits(f.heads - w * 32));
           }
         }
         tc_fence_before();
@@ -866,7 +870,7 @@ struct SumArgs {
   const uint32_t *start, *entry;
   const void* share;
   const uint16_t* power;
-  float* acc;           // [2][Tk][Hk][D]: sums of the rounds before (more than one round)
+  float* acc;           // [2][Tk][Hk][D]: sums of the rounds before (more than one round), dk's without the scale
   int opens, closes;    // the first round, the last
 };
 
@@ -996,6 +1000,12 @@ __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
   if (!f.closes) {
     *reinterpret_cast<float4*>(acc) = x;
     return;
+  }
+  if (which == 0) {
+    x.x *= p.scale;
+    x.y *= p.scale;
+    x.z *= p.scale;
+    x.w *= p.scale;
   }
   uint2 u;
   u.x = pack_pair<X>(x.x, x.y);
