@@ -667,19 +667,23 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
 }
 
 // ----------------------------------------------------------------- statistics of rows, range of values
-// delta = dout.out of each row and head, |dout| and |q|: D/8 lanes a head.
+// delta = dout.out of each row and head, |dout| and |q|: D/8 lanes a head.  The norms bound the shares whose powers of
+// two they give, so they hold over all of bf16's range: squares that leave fp32's (of values below 2^-48 or above 2^48)
+// are formed again of the values times a power of two.
 template <typename X, int D>
 __global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p, float* delta, float* norm_do, float* norm_q) {
   constexpr int G = D / 8;
+  constexpr float kLow = 0x1p-96f, kHigh = 0x1p96f, kUp = 0x1p80f, kDown = 0x1p-80f;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
   const int l = threadIdx.x % G;
   const bool ok = r < static_cast<long long>(p.Tq) * p.Hq;
   float d = 0.f, n = 0.f, m = 0.f;
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, c = a;
   if (ok) {
     const long long t = r / p.Hq, h = r - t * p.Hq;
-    const uint4 a = reinterpret_cast<const uint4*>(static_cast<const X*>(p.dout) + r * D)[l],
-                b = reinterpret_cast<const uint4*>(static_cast<const X*>(p.out) + r * D)[l],
-                c = reinterpret_cast<const uint4*>(static_cast<const X*>(p.q) + t * p.q_st + h * p.q_sh)[l];
+    a = reinterpret_cast<const uint4*>(static_cast<const X*>(p.dout) + r * D)[l];
+    b = reinterpret_cast<const uint4*>(static_cast<const X*>(p.out) + r * D)[l];
+    c = reinterpret_cast<const uint4*>(static_cast<const X*>(p.q) + t * p.q_st + h * p.q_sh)[l];
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -695,10 +699,29 @@ __global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p,
     n += __shfl_xor_sync(0xffffffffu, n, o);
     m += __shfl_xor_sync(0xffffffffu, m, o);
   }
+  float back_n = 1.f, back_m = 1.f;
+  const bool far = !(n >= kLow && n <= kHigh) || !(m >= kLow && m <= kHigh);
+  if (is_bf16<X>() && __any_sync(0xffffffffu, ok && far)) {
+    auto again = [&](const uint4& v, float& s, float& back) {
+      const float by = s < kLow ? kUp : s <= kHigh ? 1.f : kDown;
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = unpack_pair<X>(x[i]);
+        s = fmaf(u.x * by, u.x * by, fmaf(u.y * by, u.y * by, s));
+      }
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      back = 1.f / by;
+    };
+    again(a, n, back_n);
+    again(c, m, back_m);
+  }
   if (ok && l == 0) {
     delta[r] = d;
-    norm_do[r] = sqrtf(n);
-    norm_q[r] = sqrtf(m);
+    norm_do[r] = sqrtf(n) * back_n;
+    norm_q[r] = sqrtf(m) * back_m;
   }
 }
 
