@@ -123,9 +123,9 @@ struct RowsArgs {
 };
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-// E with x < 2^E for x >= 0, within +-most.
-__device__ __forceinline__ int exponent_above(float x, int most) {
-  return min(max(static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 126, -most), most);
+// E with x < 2^E for x >= 0, within lo .. hi.
+__device__ __forceinline__ int exponent_above(float x, int lo, int hi) {
+  return min(max(static_cast<int>((__float_as_uint(x) >> 23) & 255u) - 126, lo), hi);
 }
 
 // Sixteen columns of this warp's lanes, requested; and eight written.
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == 0)
             fits[b] = 15 - exponent_above(
-                               2.f * top * sqrtf(__uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk])), 60);
+                               2.f * top * sqrtf(__uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk])), -60, 60);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
@@ -570,8 +570,9 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         }
         int ek = 15, ev = 15;  // (fp32: as they are)
         if constexpr (sizeof(T) == 2) {
-          ek = exponent_above((bk.x + bk.y) * back, 110);
-          ev = exponent_above((bv.x + bv.y) * back_v, 110);
+          // (down to where 2^(15 - E) is finite; up to the largest that a byte holds)
+          ek = exponent_above((bk.x + bk.y) * back, -110, 127);
+          ev = exponent_above((bv.x + bv.y) * back_v, -110, 127);
         }
         factor[(j % C::kFactors) * 128 + key] = make_float2(back * power_of_two(15 - ek), back_v * power_of_two(15 - ev));
         const long long item = (static_cast<long long>(h.t - f.l.t0) * p.Hk + h.hk) * f.l.n_z + h.z;

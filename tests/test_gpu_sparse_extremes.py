@@ -66,3 +66,14 @@ def test_gradients_of_rows_of_many_sizes():
     do = (do.float() * (2.0 ** torch.arange(-100, 80, 3.0))[:60, None, None]).to(BF)
     idx = torch.arange(60, dtype=torch.int32)[:, None]  # a key has the rows of one size
     _run(q, k, v, do, idx, _cu(lq), _cu(lk), 0.125, causal=False)
+
+
+@pytest.mark.parametrize("Hq,Hk,K", [(6, 2, 20), (64, 1, 150)])
+def test_gradients_up_to_the_end_of_the_range(Hq, Hk, K):
+    """dk and dv above 2^110."""
+    lq, lk = [30, 9], [200, 31]
+    q, k, v, do = _inputs(lq, lk, Hq, Hk, 64, BF, seed=36)
+    do = (do.float() * 2.0 ** 112).to(BF)
+    v = (v.float() * 2.0 ** -4).to(BF)
+    r = _run(q, k, v, do, _lists(lq, lk, K, 1, seed=17), _cu(lq), _cu(lk), 0.125, causal=False)
+    assert r[4].abs().max() > 2.0 ** 111
