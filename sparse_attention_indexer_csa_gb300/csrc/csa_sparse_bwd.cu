@@ -46,7 +46,7 @@
 // %, schedulers 43 %, HBM 39 %).
 //
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
-// 2^15 (|dout| over the item's heads, |v| over the finite values of the sequence), and
+// 2^15 (|dout| over the item's heads, |v| over the finite values of the row's keys), and
 // P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -116,7 +116,7 @@ struct RowsArgs {
   int s_pad;       // slots of a row's list, rounded up to 128
   float c;         // scale * log2(e)
   const float *delta, *norm_do, *norm_q;  // [Tq][Hq]
-  const uint32_t* range;
+  const float* range;  // [Tq][Hk]: the largest |v|^2 of a row's keys (fp16)
   void* share;     // [rows][Hk][n_z][2][s_pad][D] (ShareType)
   uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk / scale is its values times 2^(low byte - 143), dv: high byte
   unsigned long long wait_ns;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == 0)
             fits[b] = 15 - exponent_above(
-                               2.f * top * sqrtf(__uint_as_float(f.range[static_cast<long long>(h.seq) * p.Hk + h.hk])), -60, 60);
+                               2.f * top * sqrtf(f.range[static_cast<long long>(h.t) * p.Hk + h.hk]), -60, 60);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarStat + b);
@@ -740,18 +740,14 @@ __device__ __forceinline__ int key_sequence(const SparseParams& p, int t) {
   return lo < p.N ? lo : -1;
 }
 
-// range[seq][key head] = the largest |v|^2 over the finite values of its keys
-// (zeroed before; as bits: these numbers are not negative).  A warp per key.
+// norm[key][key head] = |v|^2 over the finite ones of a key's values.  A warp per key.
 template <typename X, int D>
-__global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p, uint32_t* range) {
+__global__ void __launch_bounds__(256) sparse_value_kernel(const SparseParams p, float* norm) {
   const long long w = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
   const int lane = threadIdx.x & 31;
   const long long key = w / p.Hk;
   if (key >= p.Tk) return;
-  const int hk = static_cast<int>(w - key * p.Hk), seq = key_sequence(p, static_cast<int>(key));
-  if (seq < 0) return;
-  const SeqExt s = sparse_extent(p, seq);
-  if (key < s.k0 || key >= s.k0 + s.lk) return;
+  const int hk = static_cast<int>(w - key * p.Hk);
   const X* v = reinterpret_cast<const X*>(
       static_cast<const char*>(p.v.base) +
       static_cast<uint64_t>(key * p.v.rt + static_cast<long long>(hk) * p.v.rh) * p.v.unit_bytes);
@@ -762,7 +758,36 @@ __global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  if (lane == 0) atomicMax(range + static_cast<long long>(seq) * p.Hk + hk, __float_as_uint(n));
+  if (lane == 0) norm[w] = n;
+}
+// range[row][key head] = the largest of them over the keys that the row sees: what else its sequence holds does not
+// count.  A warp per row, a lane per slot of its list.
+__global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p, const float* norm, float* range) {
+  const long long w = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32, t = w / p.Hk;
+  if (t >= p.Tq) return;
+  const int lane = threadIdx.x & 31, hk = static_cast<int>(w - t * p.Hk);
+  const ListRow row = find_list_row(p, load_borders(p), static_cast<int>(t));
+  float top = 0.f;
+  if (row.lk > 0 && row.pos >= 0) {
+    const int slots = p.window + (p.top_k << p.block_shift), lim = min(row.lk - 1, row.pos - p.window);
+    const int32_t* list = p.idx + t * p.idx_st;
+#pragma unroll 4
+    for (int s = lane; s < slots; s += 32) {
+      int j = row.pos - s;
+      if (s >= p.window) {
+        const int b = list[(s - p.window) >> p.block_shift];
+        j = -1;
+        if (static_cast<unsigned>(b) <= static_cast<unsigned>((row.lk - 1) >> p.block_shift)) {
+          const int key = (b << p.block_shift) + ((s - p.window) & ((1 << p.block_shift) - 1));
+          if (key <= lim) j = key;
+        }
+      }
+      if (j >= 0) top = fmaxf(top, norm[static_cast<long long>(row.k0 + j) * p.Hk + hk]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) range[w] = top;
 }
 
 // ----------------------------------------------------------------- who lists a block
@@ -1074,7 +1099,7 @@ Plan make_plan(const SparseParams& p, int dtype) {
   a.norm_do = per_row;
   a.norm_q = 2 * per_row;
   a.range = 3 * per_row;
-  a.count = up(a.range + (fp16 ? static_cast<size_t>(p.N) * p.Hk * 4 : 0));
+  a.count = up(a.range + (fp16 ? (static_cast<size_t>(p.Tq) + p.Tk) * p.Hk * 4 : 0));  // of rows, and the norms of keys
   a.total = up(a.count + (lists ? (static_cast<size_t>(a.groups) * a.n_blocks + 1) * 4 : 0));  // and the ticket
   a.start = up(a.total + (lists ? static_cast<size_t>(a.n_blocks) * 4 : 0));
   a.entry = up(a.start + (lists ? static_cast<size_t>(a.n_blocks + 1) * 4 : 0));
@@ -1091,7 +1116,7 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   constexpr bool fp16 = !is_bf16<X>();
   float* delta = reinterpret_cast<float*>(ws);
-  uint32_t* range = reinterpret_cast<uint32_t*>(ws + a.range);
+  float *range = reinterpret_cast<float*>(ws + a.range), *norm_v = range + static_cast<long long>(p.Tq) * p.Hk;
   cudaError_t e;
   const size_t dkv = static_cast<size_t>(p.Tk) * p.Hk * D * sizeof(X);
   if (p.Tq == 0) {
@@ -1103,11 +1128,11 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   float *norm_do = reinterpret_cast<float*>(ws + a.norm_do), *norm_q = reinterpret_cast<float*>(ws + a.norm_q);
   sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, delta, norm_do, norm_q);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (fp16 && p.N > 0) {
-    if ((e = cudaMemsetAsync(range, 0, static_cast<size_t>(p.N) * p.Hk * 4, stream)) != cudaSuccess) return e;
-    const long long n = (static_cast<long long>(p.Tk) * p.Hk * 32 + 255) / 256;
-    if (n > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    if (n > 0) sparse_range_kernel<X, D><<<static_cast<unsigned>(n), 256, 0, stream>>>(p, range);
+  if (fp16 && p.N > 0 && p.Tk > 0) {
+    const long long nk = (static_cast<long long>(p.Tk) * p.Hk + 7) / 8, nq = (static_cast<long long>(p.Tq) * p.Hk + 7) / 8;
+    if (nk > 0x7FFFFFFFll || nq > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    sparse_value_kernel<X, D><<<static_cast<unsigned>(nk), 256, 0, stream>>>(p, norm_v);
+    sparse_range_kernel<<<static_cast<unsigned>(nq), 256, 0, stream>>>(p, norm_v, range);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   RowsArgs f;

@@ -2,10 +2,12 @@
 
 Tolerances are those of test_gpu_sparse (its docstring derives them); they scale with the inputs.
 """
+import numpy as np
 import pytest
 import torch
 
 import sparse_attention_indexer_csa_gb300 as csa
+from oracle import sparse_oracle as S
 from test_gpu_sparse import BF, FP16, _cu, _inputs, _lists, _run
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +79,57 @@ def test_gradients_up_to_the_end_of_the_range(Hq, Hk, K):
     v = (v.float() * 2.0 ** -4).to(BF)
     r = _run(q, k, v, do, _lists(lq, lk, K, 1, seed=17), _cu(lq), _cu(lk), 0.125, causal=False)
     assert r[4].abs().max() > 2.0 ** 111
+
+
+@pytest.mark.parametrize("paths", [(6, 2, 64, 20, 2, 9), (64, 1, 128, 150, 1, 0), (40, 1, 64, 0, 1, 33)],
+                         ids=["one_tile", "several_tiles", "window"])
+@pytest.mark.parametrize("dt", [BF, FP16], ids=["bf16", "fp16"])
+def test_gradients_do_not_depend_on_values_that_a_row_does_not_see(paths, dt):
+    """Finite large values, infinities and NaN at keys that no row sees, and at one that a single row sees: the other
+    rows' dq and the other keys' dk and dv keep their bits."""
+    Hq, Hk, D, K, block, window = paths
+    lq, lk = [30, 9], [400, 90]
+    q, k, v, do = (t.cuda() for t in _inputs(lq, lk, Hq, Hk, D, dt, seed=37))
+    idx = None
+    if K:
+        idx = _lists(lq, [n - 60 for n in lk], K, block, seed=18)
+        first = idx[:30]
+        first[first == 5] = -1  # of the first sequence only row 7 lists block 5
+        first[7, 0] = 5
+        first[7, 1:][first[7, 1:] == 5] = -1
+    cq, ck = _cu(lq), _cu(lk)
+    lists = np.zeros((39, 0), dtype=np.int32) if idx is None else idx.numpy()
+    n = [S.counts(lists[a:b], np.arange(b - a) + m - (b - a), m, block, window, window > 0)
+         for a, b, m in ((0, 30, 400), (30, 39, 90))]
+    seen = np.concatenate([x.any(0) for x in n])
+    assert (~seen).sum() > 50
+    if idx is not None:
+        idx = idx.cuda()
+    kw = dict(block=block, window=window, causal=window > 0)
+
+    def grads(k, v):
+        out, lse = csa.sparse_attn_forward(q, k, v, idx, cq.cuda(), ck.cuda(), 0.1, **kw)
+        g = csa.sparse_attn_backward(do, q, k, v, out, lse, idx, cq.cuda(), ck.cuda(), 0.1, **kw)
+        torch.cuda.synchronize()
+        assert csa.device_status() == csa.CSA_OK
+        return g
+
+    want = grads(k, v)
+    hidden = torch.tensor(~seen).cuda()
+    for bad in (6e4, float("inf"), float("nan")):
+        k2, v2 = k.clone(), v.clone()
+        k2[hidden], v2[hidden] = bad, bad
+        assert all(torch.equal(a, b) for a, b in zip(grads(k2, v2), want)), bad
+    # a key that few rows see
+    key = int(np.argmin(np.where(n[0].any(0), n[0].sum(0), 99)))
+    rows = torch.zeros(39, dtype=torch.bool)
+    rows[:30] = torch.tensor(n[0][:, key] > 0)
+    keys = torch.zeros(490, dtype=torch.bool)
+    keys[:400] = torch.tensor(n[0][rows[:30].numpy()].any(0))
+    assert 0 < rows.sum() < 30 and 0 < keys.sum() < seen.sum()
+    v2 = v.clone()
+    v2[key] = 6e4
+    got = grads(k, v2)
+    rows, keys = rows.cuda(), keys.cuda()
+    assert torch.equal(got[0][~rows], want[0][~rows])
+    assert torch.equal(got[1][~keys], want[1][~keys]) and torch.equal(got[2][~keys], want[2][~keys])
