@@ -89,7 +89,9 @@ csa_status csa_sparse_attn_forward(const csa_sparse_problem* p, const void* q, c
                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Gradients for the cotangent dout [Tq,Hq,D] of out, from the forward's out
- * and lse: dq [Tq,Hq,D], dk, dv [Tk,Hk,D] (dtype, every element; zero where
+ * and lse, or from those of several calls over different keys joined by their lse
+ * (out = sum exp(lse_i - lse) out_i): then dq, dk and dv are this call's keys' part
+ * of the gradients of the joined out.  dq [Tq,Hq,D], dk, dv [Tk,Hk,D] (dtype, every element; zero where
  * nothing reaches them).  Packed keys only (page > 0: CSA_ERR_UNSUPPORTED).  A
  * block that a row lists twice reaches dk and dv twice, as it does out.  The sums
  * are taken in a fixed order (the same bits on every call).  Needs `workspace`:

@@ -34,7 +34,9 @@
 //
 // Where a list is one tile, delta is taken as sum_j p_j dout.v_j from the products at
 // hand, in fp32: the rounding of out, which the forward stored, is an error of delta
-// for all keys of the row at once, and shows where these are few.
+// for all keys of the row at once, and shows where these are few.  That holds while the
+// list is all that the softmax has, sum_j p_j = 1: with out and lse of several calls
+// joined, delta is dout.out, as it is for longer lists.
 //
 // Measured (bf16, D 128): 8192 rows of 64 heads and one key head, 256 listed entries
 // each, 670 us: delta 60 to 69, lists 36, rows 355, sums 205 (1 GB of shares, which
@@ -92,8 +94,8 @@ struct Cfg {
   static constexpr uint32_t kOffRing = kOffDo + 2 * kHeadTile;
   static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta, |dout|, |q|
   static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [kFactors][128] factors of a key's shares
-  static constexpr uint32_t kOffSum = kOffFactor + kFactors * 128 * 8;          // [4][64] sums of p dout.v over a warp's keys
-  static constexpr uint32_t kOffFit = kOffSum + 4 * kHeads * 4;          // [2] power of two of dS
+  static constexpr uint32_t kOffSum = kOffFactor + kFactors * 128 * 8;  // [2][4][64] sums of p dout.v, of p over a warp's keys
+  static constexpr uint32_t kOffFit = kOffSum + 8 * kHeads * 4;         // [2] power of two of dS
   static constexpr uint32_t kOffBar = kOffFit + 16;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
                        kBarKFree = 14, kBarP = 16, kBarD = 18, kBarDFree = 20, kBarDq = 21, kBarDqFree = 22,
@@ -520,23 +522,38 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             tmem_wait16(t);
             tmem_wait16(dp);
 #pragma unroll
-            for (int u = 0; u < 16; ++u) t[u] = see ? exp2_approx(fmaf(t[u], f.c, -ls[16 * i + u].x)) * dp[u] : 0.f;
-            // each step adds half of the heads over half of the lanes; lanes 2 h and 2 h + 1 end with head h
-#pragma unroll
-            for (int n = 8; n > 0; n >>= 1) {
-              const bool up = (lane & (2u * n)) != 0u;
-#pragma unroll
-              for (int u = 0; u < n; ++u) {
-                const float give = up ? t[u] : t[u + n], keep = up ? t[u + n] : t[u];
-                t[u] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
-              }
+            for (int u = 0; u < 16; ++u) {
+              t[u] = see ? exp2_approx(fmaf(t[u], f.c, -ls[16 * i + u].x)) : 0.f;
+              dp[u] = see ? t[u] * dp[u] : 0.f;
             }
-            t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
-            if ((lane & 1u) == 0u) sums[warp * kHeads + 16 * i + (lane >> 1)] = t[0];
+            // each step adds half of the heads over half of the lanes; lanes 2 h and 2 h + 1 end with head h
+            auto add_up = [&](float (&x)[16]) {
+#pragma unroll
+              for (int n = 8; n > 0; n >>= 1) {
+                const bool up = (lane & (2u * n)) != 0u;
+#pragma unroll
+                for (int u = 0; u < n; ++u) {
+                  const float give = up ? x[u] : x[u + n], keep = up ? x[u + n] : x[u];
+                  x[u] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+                }
+              }
+              return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+            };
+            const float sum = add_up(dp), weight = add_up(t);
+            if ((lane & 1u) == 0u) {
+              sums[warp * kHeads + 16 * i + (lane >> 1)] = sum;
+              sums[(4 + warp) * kHeads + 16 * i + (lane >> 1)] = weight;
+            }
           }
           if (!meet_all()) break;
-          if (key < f.padded)
-            stat[(ni & 1u) * kHeads + key].y = (sums[key] + sums[kHeads + key]) + (sums[2 * kHeads + key] + sums[3 * kHeads + key]);
+          if (key < f.padded) {
+            auto all = [&](const float* x) { return (x[0] + x[kHeads]) + (x[2 * kHeads] + x[3 * kHeads]); };
+            float4& x = stat[(ni & 1u) * kHeads + key];
+            // The weights add up to 1 within the errors of scores and lse (2^-23 of their size each) and of the sum.  Keys of
+            // other calls that weigh less than that change delta by 2^-16 of their dout.v, where out's rounding (fp16's
+            // 2^-11, bf16's 2^-8 of its size) counts for more.  (No head: lse is inf, nothing is read.)
+            if (fabsf(all(sums + 4 * kHeads + key) - 1.f) <= 0x1p-16f + 0x1p-21f * fabsf(x.x)) x.y = all(sums + key);
+          }
           if (!meet_all()) break;
         }
         float2 bk = make_float2(0.f, 0.f), bv = bk;  // bounds of the key's shares

@@ -200,7 +200,8 @@ def sparse_attn_backward(dout, q, k, v, out, lse, idx, cu_q, cu_k, scale, block=
                          workspace=None, stream=None):
     """Gradients of sparse_attn_forward for the cotangent dout of out
     (contiguous), from the forward's out and lse -> (dq, dk, dv), contiguous, in
-    q's type."""
+    q's type.  With out and lse of several calls joined (lse by logaddexp, out by
+    exp(lse_i - lse)), the gradients are this call's part of those of the joined out."""
     dev, idx = _check_packed(q, k, v, idx, cu_q, cu_k, k_len)
     _want(dout, "dout", q.shape, q.dtype, dev)
     _want(out, "out", q.shape, q.dtype, dev)

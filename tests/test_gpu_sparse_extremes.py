@@ -1,4 +1,5 @@
-"""Gradients of attention over listed blocks where scales, magnitudes or hidden values are extreme.
+"""Gradients of attention over listed blocks where scales, magnitudes or hidden values are extreme, and where the
+softmax spans the keys of two calls.
 
 Tolerances are those of test_gpu_sparse (its docstring derives them); they scale with the inputs.
 """
@@ -8,6 +9,7 @@ import torch
 
 import sparse_attention_indexer_csa_gb300 as csa
 from oracle import sparse_oracle as S
+from oracle.attn_oracle import f64
 from test_gpu_sparse import BF, FP16, _cu, _inputs, _lists, _run
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +135,72 @@ def test_gradients_do_not_depend_on_values_that_a_row_does_not_see(paths, dt):
     rows, keys = rows.cuda(), keys.cuda()
     assert torch.equal(got[0][~rows], want[0][~rows])
     assert torch.equal(got[1][~keys], want[1][~keys]) and torch.equal(got[2][~keys], want[2][~keys])
+
+
+def _masked(q, k, v, do, out, lse, see, scale, dt):
+    """Gradients in 64 bits of a call whose rows see the keys `see` [rows,keys] (one sequence), as a part of a softmax
+    whose out and lse are given: p = exp(s - lse), ds = p (dp - dout.out).  With their bounds, those of test_gpu_sparse:
+    u |ref| + (2u + 2 ds + 2^-15 of the magnitudes), the shares' 2^-11 and 2^-39, fp16's spacing."""
+    u = torch.finfo(dt).eps / 2
+    h = 1.0 if dt == FP16 else 0.0
+    Q, K, V, G, O, L = (f64(t) for t in (q, k, v, do, out, lse))
+    g = Q.shape[1] // K.shape[1]
+    val = {n: np.zeros(x.shape) for n, x in (("dq", Q), ("dk", K), ("dv", V))}
+    err = {n: np.zeros(x.shape) for n, x in (("dq", Q), ("dk", K), ("dv", V))}
+    for x in range(Q.shape[1]):
+        j = x // g
+        s = scale * Q[:, x] @ K[:, j].T
+        ds = 2.0 ** -16 * np.where(see, scale * np.abs(Q[:, x]) @ np.abs(K[:, j]).T, 0).max(1, keepdims=True)
+        p = np.where(see, np.exp(s - L[:, x][:, None]), 0.0)
+        dp = G[:, x] @ V[:, j].T
+        d = p * (dp - (G[:, x] * O[:, x]).sum(1, keepdims=True))
+        m = p * (np.abs(G[:, x]) @ np.abs(V[:, j]).T + (np.abs(G[:, x]) * np.abs(O[:, x])).sum(1, keepdims=True)) + np.abs(d)
+        top = 2 * np.linalg.norm(G[:, j * g:(j + 1) * g], axis=2).max(1, keepdims=True) * np.linalg.norm(V[:, j], axis=1).max()
+        tiny = h * 2.0 ** -38 * see * top
+        e = (2 * u + 2 * ds + 2.0 ** -15) * m + tiny
+        val["dq"][:, x] = scale * d @ K[:, j]
+        err["dq"][:, x] = scale * e @ np.abs(K[:, j])
+        e = e + (1 - h) * 2.0 ** -11 * m
+        val["dk"][:, j] += scale * d.T @ Q[:, x]
+        err["dk"][:, j] += scale * (e.T @ np.abs(Q[:, x]) + (1 - h) * 2.0 ** -39 * (m.T @ np.linalg.norm(Q[:, x], axis=1))[:, None])
+        val["dv"][:, j] += p.T @ G[:, x]
+        err["dv"][:, j] += (((u + (1 - h) * 2.0 ** -11 + 2 * ds + 2.0 ** -18) * p + h * 2.0 ** -40 * see).T @ np.abs(G[:, x])
+                            + (1 - h) * 2.0 ** -39 * (p.T @ np.linalg.norm(G[:, x], axis=1))[:, None])
+    for n in val:
+        err[n] += u * np.abs(val[n]) + h * 2.0 ** -25
+    return val, err
+
+
+@pytest.mark.parametrize("dt", [BF, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Hk,D", [(6, 2, 64), (64, 1, 128), (20, 1, 128)])
+@pytest.mark.parametrize("K,window", [(40, 128), (128, 33), (200, 200)])
+def test_gradients_of_two_calls_joined_by_lse(K, window, Hq, Hk, D, dt):
+    """One softmax over selected entries and the last tokens, which are two calls: each call's gradients, from the
+    joined out and lse, are its keys' part, whatever the lengths of its list."""
+    T, W = 230, 300
+    q, kt, vt, do = _inputs([T], [T], Hq, Hk, D, dt, seed=38)
+    _, ke, ve, _ = _inputs([T], [W], Hq, Hk, D, dt, seed=39)
+    idx = _lists([T], [W], K, 1, seed=19)
+    idx[:3] = -1  # rows of no entry
+    scale = D ** -0.5
+    c = lambda t: t.cuda()  # noqa: E731
+    entries = lambda: (c(q), c(ke), c(ve))  # noqa: E731
+    ae, aw = (c(idx), c(_cu([T])), c(_cu([W])), scale), (None, c(_cu([T])), c(_cu([T])), scale)
+    oe, le = csa.sparse_attn_forward(*entries(), *ae, causal=False)
+    ow, lw = csa.sparse_attn_forward(c(q), c(kt), c(vt), *aw, window=window)
+    lse = torch.logaddexp(le, lw)
+    out = ((le - lse).exp()[..., None] * oe + (lw - lse).exp()[..., None] * ow).to(dt)
+    ge = csa.sparse_attn_backward(c(do), *entries(), out, lse, *ae, causal=False)
+    gw = csa.sparse_attn_backward(c(do), c(q), c(kt), c(vt), out, lse, *aw, window=window)
+    torch.cuda.synchronize()
+    assert csa.device_status() == csa.CSA_OK
+    see_e = np.zeros((T, W), dtype=bool)
+    r, s = np.nonzero(idx.numpy() >= 0)
+    see_e[r, idx.numpy()[r, s]] = True
+    at = np.arange(T)
+    see_w = (at[None] <= at[:, None]) & (at[None] > at[:, None] - window)
+    for name, got, k, v, see in (("entries", ge, ke, ve, see_e), ("window", gw, kt, vt, see_w)):
+        val, err = _masked(q, k, v, do, out, lse, see, scale, dt)
+        for n, t in zip(("dq", "dk", "dv"), got):
+            x = np.abs(f64(t) - val[n]) / (err[n] + 1e-30)
+            assert x.max() <= 1, (name, n, float(x.max()))
