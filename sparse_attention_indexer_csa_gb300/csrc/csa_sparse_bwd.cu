@@ -48,8 +48,8 @@
 // %, schedulers 43 %, HBM 39 %).
 //
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
-// 2^15 (|dout| over the item's heads, |v| over the finite values of the row's keys), and
-// P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
+// 2^15 (|dout| over the item's heads, |v| over the finite values of the row's keys), or
+// |dout| max|v| + |delta| where that is larger (out of joined calls), and P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -277,22 +277,25 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         ++ni;
         if (!bar_wait(bars + C::kBarStatFree + b, turn, ctl)) break;
         const long long at = static_cast<long long>(h.t) * p.Hq + head;
-        float top = 0.f;
+        float top = 0.f, most = 0.f;  // of |dout|, |delta|
         for (int i = static_cast<int>(lane); i < f.padded; i += 32) {
           float4 s = make_float4(INFINITY, 0.f, 0.f, 0.f);  // no head, or a row without a weight: P = 0
           if (i < f.heads) {
             const float l = p.lse[at + i], n = f.norm_do[at + i];
             if (l != -INFINITY) s = make_float4(l * 1.4426950408889634f, f.delta[at + i], n, f.norm_q[at + i]);
             top = fmaxf(top, n);
+            most = fmaxf(most, fabsf(s.y));
           }
           stat[b * kHeads + i] = s;
         }
         if constexpr (!is_bf16<X>()) {
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0)
-            fits[b] = 15 - exponent_above(
-                               2.f * top * sqrtf(f.range[static_cast<long long>(h.t) * p.Hk + h.hk]), -60, 60);
+          for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          }
+          const float dp = top * sqrtf(f.range[static_cast<long long>(h.t) * p.Hk + h.hk]);
+          if (lane == 0) fits[b] = 15 - exponent_above(dp + fmaxf(dp, most), -60, 60);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + C::kBarStat + b);

@@ -137,12 +137,14 @@ def test_gradients_do_not_depend_on_values_that_a_row_does_not_see(paths, dt):
     assert torch.equal(got[1][~keys], want[1][~keys]) and torch.equal(got[2][~keys], want[2][~keys])
 
 
-def _masked(q, k, v, do, out, lse, see, scale, dt):
+def masked(q, k, v, do, out, lse, see, scale, dt, shares=True):
     """Gradients in 64 bits of a call whose rows see the keys `see` [rows,keys] (one sequence), as a part of a softmax
     whose out and lse are given: p = exp(s - lse), ds = p (dp - dout.out).  With their bounds, those of test_gpu_sparse:
-    u |ref| + (2u + 2 ds + 2^-15 of the magnitudes), the shares' 2^-11 and 2^-39, fp16's spacing."""
+    u |ref| + (2u + 2 ds + 2^-15 of the magnitudes), the shares' 2^-11 and 2^-39, fp16's spacing (ds is bounded by
+    |dout| max|v| + |dout.out| too, as out may hold other calls' values)."""
     u = torch.finfo(dt).eps / 2
     h = 1.0 if dt == FP16 else 0.0
+    sh = 1.0 if shares and dt != FP16 else 0.0
     Q, K, V, G, O, L = (f64(t) for t in (q, k, v, do, out, lse))
     g = Q.shape[1] // K.shape[1]
     val = {n: np.zeros(x.shape) for n, x in (("dq", Q), ("dk", K), ("dv", V))}
@@ -155,17 +157,19 @@ def _masked(q, k, v, do, out, lse, see, scale, dt):
         dp = G[:, x] @ V[:, j].T
         d = p * (dp - (G[:, x] * O[:, x]).sum(1, keepdims=True))
         m = p * (np.abs(G[:, x]) @ np.abs(V[:, j]).T + (np.abs(G[:, x]) * np.abs(O[:, x])).sum(1, keepdims=True)) + np.abs(d)
-        top = 2 * np.linalg.norm(G[:, j * g:(j + 1) * g], axis=2).max(1, keepdims=True) * np.linalg.norm(V[:, j], axis=1).max()
+        heads = slice(j * g, (j + 1) * g)
+        top = np.linalg.norm(G[:, heads], axis=2).max(1, keepdims=True) * np.linalg.norm(V[:, j], axis=1).max()
+        top = top + np.maximum(top, np.abs((G * O).sum(2))[:, heads].max(1, keepdims=True))
         tiny = h * 2.0 ** -38 * see * top
         e = (2 * u + 2 * ds + 2.0 ** -15) * m + tiny
         val["dq"][:, x] = scale * d @ K[:, j]
         err["dq"][:, x] = scale * e @ np.abs(K[:, j])
-        e = e + (1 - h) * 2.0 ** -11 * m
+        e = e + sh * 2.0 ** -11 * m
         val["dk"][:, j] += scale * d.T @ Q[:, x]
-        err["dk"][:, j] += scale * (e.T @ np.abs(Q[:, x]) + (1 - h) * 2.0 ** -39 * (m.T @ np.linalg.norm(Q[:, x], axis=1))[:, None])
+        err["dk"][:, j] += scale * (e.T @ np.abs(Q[:, x]) + sh * 2.0 ** -39 * (m.T @ np.linalg.norm(Q[:, x], axis=1))[:, None])
         val["dv"][:, j] += p.T @ G[:, x]
-        err["dv"][:, j] += (((u + (1 - h) * 2.0 ** -11 + 2 * ds + 2.0 ** -18) * p + h * 2.0 ** -40 * see).T @ np.abs(G[:, x])
-                            + (1 - h) * 2.0 ** -39 * (p.T @ np.linalg.norm(G[:, x], axis=1))[:, None])
+        err["dv"][:, j] += (((u + sh * 2.0 ** -11 + 2 * ds + 2.0 ** -18) * p + h * 2.0 ** -40 * see).T @ np.abs(G[:, x])
+                            + sh * 2.0 ** -39 * (p.T @ np.linalg.norm(G[:, x], axis=1))[:, None])
     for n in val:
         err[n] += u * np.abs(val[n]) + h * 2.0 ** -25
     return val, err
@@ -173,13 +177,14 @@ def _masked(q, k, v, do, out, lse, see, scale, dt):
 
 @pytest.mark.parametrize("dt", [BF, FP16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("Hq,Hk,D", [(6, 2, 64), (64, 1, 128), (20, 1, 128)])
-@pytest.mark.parametrize("K,window", [(40, 128), (128, 33), (200, 200)])
-def test_gradients_of_two_calls_joined_by_lse(K, window, Hq, Hk, D, dt):
+@pytest.mark.parametrize("K,window,size", [(40, 128, 1), (128, 33, 1), (200, 200, 1), (40, 128, 2 ** 10), (200, 33, 2 ** 10)])
+def test_gradients_of_two_calls_joined_by_lse(K, window, size, Hq, Hk, D, dt):
     """One softmax over selected entries and the last tokens, which are two calls: each call's gradients, from the
-    joined out and lse, are its keys' part, whatever the lengths of its list."""
+    joined out and lse, are its keys' part, whatever the lengths of its list and the sizes of the other's values."""
     T, W = 230, 300
     q, kt, vt, do = _inputs([T], [T], Hq, Hk, D, dt, seed=38)
     _, ke, ve, _ = _inputs([T], [W], Hq, Hk, D, dt, seed=39)
+    vt, do = (vt.float() * size).to(dt), (do.float() / min(size, 16)).to(dt)
     idx = _lists([T], [W], K, 1, seed=19)
     idx[:3] = -1  # rows of no entry
     scale = D ** -0.5
@@ -200,7 +205,7 @@ def test_gradients_of_two_calls_joined_by_lse(K, window, Hq, Hk, D, dt):
     at = np.arange(T)
     see_w = (at[None] <= at[:, None]) & (at[None] > at[:, None] - window)
     for name, got, k, v, see in (("entries", ge, ke, ve, see_e), ("window", gw, kt, vt, see_w)):
-        val, err = _masked(q, k, v, do, out, lse, see, scale, dt)
+        val, err = masked(q, k, v, do, out, lse, see, scale, dt)
         for n, t in zip(("dq", "dk", "dv"), got):
             x = np.abs(f64(t) - val[n]) / (err[n] + 1e-30)
             assert x.max() <= 1, (name, n, float(x.max()))
