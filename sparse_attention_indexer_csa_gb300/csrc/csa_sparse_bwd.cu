@@ -35,8 +35,8 @@
 // Where a list is one tile, delta is taken as sum_j p_j dout.v_j from the products at
 // hand, in fp32: the rounding of out, which the forward stored, is an error of delta
 // for all keys of the row at once, and shows where these are few.  That holds while the
-// list is all that the softmax has, sum_j p_j = 1: with out and lse of several calls
-// joined, delta is dout.out, as it is for longer lists.
+// list is all that the softmax has, sum_j p_j = 1, and dout.out differs by no more than out's
+// rounding: with out and lse of several calls joined, delta is dout.out, as it is for longer lists.
 //
 // Measured (bf16, D 128): 8192 rows of 64 heads and one key head, 256 listed entries
 // each, 670 us: delta 60 to 69, lists 36, rows 355, sums 205 (1 GB of shares, which
@@ -95,7 +95,8 @@ struct Cfg {
   static constexpr uint32_t kOffStat = kOffRing + kRing * sizeof(Tile);  // [2][64] lse, delta, |dout|, |q|
   static constexpr uint32_t kOffFactor = kOffStat + 2 * kHeads * 16;     // [kFactors][128] factors of a key's shares
   static constexpr uint32_t kOffSum = kOffFactor + kFactors * 128 * 8;  // [2][4][64] sums of p dout.v, of p over a warp's keys
-  static constexpr uint32_t kOffFit = kOffSum + 8 * kHeads * 4;         // [2] power of two of dS
+  static constexpr uint32_t kOffTol = kOffSum + 8 * kHeads * 4;         // [2][64] what out's rounding is in delta
+  static constexpr uint32_t kOffFit = kOffTol + 2 * kHeads * 4;         // [2] power of two of dS
   static constexpr uint32_t kOffBar = kOffFit + 16;
   static constexpr int kBarQ = 0, kBarQFree = 2, kBarStat = 4, kBarStatFree = 6, kBarK = 8, kBarV = 10, kBarS = 12,
                        kBarKFree = 14, kBarP = 16, kBarD = 18, kBarDFree = 20, kBarDq = 21, kBarDqFree = 22,
@@ -117,7 +118,7 @@ struct RowsArgs {
   int heads, padded;  // of an item; the same rounded up to 16
   int s_pad;       // slots of a row's list, rounded up to 128
   float c;         // scale * log2(e)
-  const float *delta, *norm_do, *norm_q;  // [Tq][Hq]
+  const float *delta, *norm_do, *norm_q, *tol;  // [Tq][Hq] (tol: lists of one tile)
   const float* range;  // [Tq][Hk]: the largest |v|^2 of a row's keys (fp16)
   void* share;     // [rows][Hk][n_z][2][s_pad][D] (ShareType)
   uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk / scale is its values times 2^(low byte - 143), dv: high byte
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
   Tile* ring = reinterpret_cast<Tile*>(base + C::kOffRing);
   float4* stat = reinterpret_cast<float4*>(base + C::kOffStat);
   float2* factor = reinterpret_cast<float2*>(base + C::kOffFactor);
+  float* tols = reinterpret_cast<float*>(base + C::kOffTol);
   int* fits = reinterpret_cast<int*>(base + C::kOffFit);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(base + C::kOffMisc + 4);
@@ -285,6 +287,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             if (l != -INFINITY) s = make_float4(l * 1.4426950408889634f, f.delta[at + i], n, f.norm_q[at + i]);
             top = fmaxf(top, n);
             most = fmaxf(most, fabsf(s.y));
+            if constexpr (ONE) tols[b * kHeads + i] = f.tol[at + i];
           }
           stat[b * kHeads + i] = s;
         }
@@ -549,13 +552,12 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             }
           }
           if (!meet_all()) break;
-          if (key < f.padded) {
+          if (key < f.heads) {
             auto all = [&](const float* x) { return (x[0] + x[kHeads]) + (x[2 * kHeads] + x[3 * kHeads]); };
             float4& x = stat[(ni & 1u) * kHeads + key];
-            // The weights add up to 1 within the errors of scores and lse (2^-23 of their size each) and of the sum.  Keys of
-            // other calls that weigh less than that change delta by 2^-16 of their dout.v, where out's rounding (fp16's
-            // 2^-11, bf16's 2^-8 of its size) counts for more.  (No head: lse is inf, nothing is read.)
-            if (fabsf(all(sums + 4 * kHeads + key) - 1.f) <= 0x1p-16f + 0x1p-21f * fabsf(x.x)) x.y = all(sums + key);
+            const float sum = all(sums + key), left = fabsf(all(sums + 4 * kHeads + key) - 1.f);
+            // the weights add up to 1 within the errors of scores and lse (2^-23 of their size each) and of the sum
+            if (left <= 0x1p-16f + 0x1p-21f * fabsf(x.x) && fabsf(sum - x.y) <= tols[(ni & 1u) * kHeads + key]) x.y = sum;
           }
           if (!meet_all()) break;
         }
@@ -690,15 +692,18 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
 // ----------------------------------------------------------------- statistics of rows, range of values
 // delta = dout.out of each row and head, |dout| and |q|: D/8 lanes a head.  The norms bound the shares whose powers of
 // two they give, so they hold over all of bf16's range: squares that leave fp32's (of values below 2^-48 or above 2^48)
-// are formed again of the values times a power of two.
+// are formed again of the values times a power of two.  tol (where given): 4 u sum |dout||out|, where
+// rounding out to X adds at most u sum |dout||out| to delta; the rest is room for the rounded weights.
 template <typename X, int D>
-__global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p, float* delta, float* norm_do, float* norm_q) {
+__global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p, float* delta, float* norm_do, float* norm_q,
+                                                           float* tol) {
   constexpr int G = D / 8;
   constexpr float kLow = 0x1p-96f, kHigh = 0x1p96f, kUp = 0x1p80f, kDown = 0x1p-80f;
   const long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / G;
   const int l = threadIdx.x % G;
   const bool ok = r < static_cast<long long>(p.Tq) * p.Hq;
-  float d = 0.f, n = 0.f, m = 0.f;
+  constexpr float kTol = is_bf16<X>() ? 0x1p-6f : 0x1p-9f;
+  float d = 0.f, n = 0.f, m = 0.f, s = 0.f;
   uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, c = a;
   if (ok) {
     const long long t = r / p.Hq, h = r - t * p.Hq;
@@ -710,6 +715,7 @@ __global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p,
     for (int i = 0; i < 4; ++i) {
       const float2 u = unpack_pair<X>(x[i]), v = unpack_pair<X>(y[i]), w = unpack_pair<X>(z[i]);
       d = fmaf(u.x, v.x, fmaf(u.y, v.y, d));
+      s = fmaf(fabsf(u.x), fabsf(v.x), fmaf(fabsf(u.y), fabsf(v.y), s));
       n = fmaf(u.x, u.x, fmaf(u.y, u.y, n));
       m = fmaf(w.x, w.x, fmaf(w.y, w.y, m));
     }
@@ -719,6 +725,7 @@ __global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p,
     d += __shfl_xor_sync(0xffffffffu, d, o);
     n += __shfl_xor_sync(0xffffffffu, n, o);
     m += __shfl_xor_sync(0xffffffffu, m, o);
+    if (tol != nullptr) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
   float back_n = 1.f, back_m = 1.f;
   const bool far = !(n >= kLow && n <= kHigh) || !(m >= kLow && m <= kHigh);
@@ -743,6 +750,7 @@ __global__ void __launch_bounds__(256) sparse_delta_kernel(const SparseParams p,
     delta[r] = d;
     norm_do[r] = sqrtf(n) * back_n;
     norm_q[r] = sqrtf(m) * back_m;
+    if (tol != nullptr) tol[r] = kTol * s;
   }
 }
 
@@ -1085,7 +1093,7 @@ __global__ void __launch_bounds__(256) sparse_sum_kernel(const SumArgs f) {
 // ----------------------------------------------------------------- plan and launches
 struct Plan {
   int heads, n_z, s_pad, rows, rounds, groups, per, n_blocks, u_bits;
-  size_t norm_do, norm_q, range, count, total, start, entry, power, acc, share, bytes;
+  size_t norm_do, norm_q, tol, range, count, total, start, entry, power, acc, share, bytes;
 };
 Plan make_plan(const SparseParams& p, int dtype) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -1118,7 +1126,8 @@ Plan make_plan(const SparseParams& p, int dtype) {
   const bool lists = p.top_k > 0;
   a.norm_do = per_row;
   a.norm_q = 2 * per_row;
-  a.range = 3 * per_row;
+  a.tol = 3 * per_row;
+  a.range = a.tol + (a.s_pad <= 128 ? per_row : 0);
   a.count = up(a.range + (fp16 ? (static_cast<size_t>(p.Tq) + p.Tk) * p.Hk * 4 : 0));  // of rows, and the norms of keys
   a.total = up(a.count + (lists ? (static_cast<size_t>(a.groups) * a.n_blocks + 1) * 4 : 0));  // and the ticket
   a.start = up(a.total + (lists ? static_cast<size_t>(a.n_blocks) * 4 : 0));
@@ -1146,7 +1155,8 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   const long long rows = static_cast<long long>(p.Tq) * p.Hq, blocks = (rows * (D / 8) + 255) / 256;
   if (blocks > 0x7FFFFFFFll || p.Hk > 65535) return cudaErrorInvalidValue;
   float *norm_do = reinterpret_cast<float*>(ws + a.norm_do), *norm_q = reinterpret_cast<float*>(ws + a.norm_q);
-  sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, delta, norm_do, norm_q);
+  float* tol = a.s_pad <= 128 ? reinterpret_cast<float*>(ws + a.tol) : nullptr;
+  sparse_delta_kernel<X, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, delta, norm_do, norm_q, tol);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (fp16 && p.N > 0 && p.Tk > 0) {
     const long long nk = (static_cast<long long>(p.Tk) * p.Hk + 7) / 8, nq = (static_cast<long long>(p.Tq) * p.Hk + 7) / 8;
@@ -1168,6 +1178,7 @@ cudaError_t run(const SparseParams& p, int dtype, void* workspace, cudaStream_t 
   f.delta = delta;
   f.norm_do = norm_do;
   f.norm_q = norm_q;
+  f.tol = tol;
   f.range = range;
   f.share = ws + a.share;
   f.power = reinterpret_cast<uint16_t*>(ws + a.power);

@@ -177,10 +177,13 @@ def masked(q, k, v, do, out, lse, see, scale, dt, shares=True):
 
 @pytest.mark.parametrize("dt", [BF, FP16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("Hq,Hk,D", [(6, 2, 64), (64, 1, 128), (20, 1, 128)])
-@pytest.mark.parametrize("K,window,size", [(40, 128, 1), (128, 33, 1), (200, 200, 1), (40, 128, 2 ** 10), (200, 33, 2 ** 10)])
-def test_gradients_of_two_calls_joined_by_lse(K, window, size, Hq, Hk, D, dt):
+@pytest.mark.parametrize("K,window,size,nats", [(40, 128, 1, 0), (128, 33, 1, 0), (200, 200, 1, 0), (40, 128, 2 ** 10, 0),
+                                                (200, 33, 2 ** 10, 0), (40, 33, 2 ** 13, 12.5), (40, 33, 2 ** 13, 15),
+                                                (200, 33, 2 ** 13, 15)])
+def test_gradients_of_two_calls_joined_by_lse(K, window, size, nats, Hq, Hk, D, dt):
     """One softmax over selected entries and the last tokens, which are two calls: each call's gradients, from the
-    joined out and lse, are its keys' part, whatever the lengths of its list and the sizes of the other's values."""
+    joined out and lse, are its keys' part, whatever the lengths of its list and the weights and sizes of the other's
+    values (nats: what the entries' scores are above)."""
     T, W = 230, 300
     q, kt, vt, do = _inputs([T], [T], Hq, Hk, D, dt, seed=38)
     _, ke, ve, _ = _inputs([T], [W], Hq, Hk, D, dt, seed=39)
@@ -188,6 +191,8 @@ def test_gradients_of_two_calls_joined_by_lse(K, window, size, Hq, Hk, D, dt):
     idx = _lists([T], [W], K, 1, seed=19)
     idx[:3] = -1  # rows of no entry
     scale = D ** -0.5
+    if nats:
+        q[..., 0], ke[..., 0], kt[..., 0] = 4.0, nats / (4 * scale), 0.0
     c = lambda t: t.cuda()  # noqa: E731
     entries = lambda: (c(q), c(ke), c(ve))  # noqa: E731
     ae, aw = (c(idx), c(_cu([T])), c(_cu([W])), scale), (None, c(_cu([T])), c(_cu([T])), scale)
