@@ -16,7 +16,8 @@
 //       P^T, dS^T in the storage type over S^T, dP^T in TMEM, dS^T to shared memory
 //       dV = P^T dO, dK = dS^T Q           (A in TMEM, B read MN-major): the shares
 //       dQ += dS K                         (A and B read MN-major)
-//     so that a group of any size costs no more than its heads.
+//     so that a group of up to 64 heads costs no more than its heads; a larger one is two
+//     items, each with shares of its own.
 //   lists (sparse_count, _scan, _fill)  for each block the rows that
 //     list it, in ascending order: a counting sort, the counts kept by groups of
 //     rows so that the place of each entry does not depend on timing.
@@ -114,8 +115,8 @@ static_assert(fits_layout<Cfg<128, false>>() && fits_layout<Cfg<128, true>>() &&
 
 struct RowsArgs {
   SparseParams p;
-  ListArgs l;      // n_z: groups of heads of a key head
-  int heads, padded;  // of an item; the same rounded up to 16
+  ListArgs l;      // n_z: parts of a key head's query heads
+  int heads, padded;  // of a part; the same rounded up to 16
   int s_pad;       // slots of a row's list, rounded up to 128
   float c;         // scale * log2(e)
   const float *delta, *norm_do, *norm_q, *tol;  // [Tq][Hq] (tol: lists of one tile)
@@ -124,6 +125,10 @@ struct RowsArgs {
   uint16_t* power; // [rows][Hk][n_z][s_pad]: the share of dk / scale is its values times 2^(low byte - 143), dv: high byte
   unsigned long long wait_ns;
 };
+
+// First head of a key head's part z.  All parts have as many; the last of an odd group begins with the last head of the
+// part before, which counts there and weighs nothing here.
+__device__ __forceinline__ int first_head(const RowsArgs& f, int z) { return min(z * f.heads, f.p.g - f.heads); }
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 // E with x < 2^E for x >= 0, within lo .. hi.
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
       if (h.n > 0 && first) {
         const uint32_t b = ni & 1u, turn = ((ni >> 1) & 1u) ^ 1u;
         if (!bar_wait(bars + C::kBarQFree + b, turn, ctl)) break;
-        const int head = h.hk * p.g + h.z * f.heads;
+        const int own = first_head(f, h.z), head = h.hk * p.g + own, skip = h.z * f.heads - own;
         if (lane == 0) {
           const uint64_t pol = l2_policy_evict_first();
           mbar_arrive_expect_tx(bars + C::kBarQ + b, static_cast<uint32_t>(f.heads) * 256u * (D / 64));
@@ -282,13 +287,13 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         float top = 0.f, most = 0.f;  // of |dout|, |delta|
         for (int i = static_cast<int>(lane); i < f.padded; i += 32) {
           float4 s = make_float4(INFINITY, 0.f, 0.f, 0.f);  // no head, or a row without a weight: P = 0
-          if (i < f.heads) {
+          if (i >= skip && i < f.heads) {
             const float l = p.lse[at + i], n = f.norm_do[at + i];
             if (l != -INFINITY) s = make_float4(l * 1.4426950408889634f, f.delta[at + i], n, f.norm_q[at + i]);
             top = fmaxf(top, n);
             most = fmaxf(most, fabsf(s.y));
-            if constexpr (ONE) tols[b * kHeads + i] = f.tol[at + i];
           }
+          if constexpr (ONE) tols[b * kHeads + i] = i < f.heads ? f.tol[at + i] : 0.f;
           stat[b * kHeads + i] = s;
         }
         if constexpr (!is_bf16<X>()) {
@@ -653,8 +658,9 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         ++on;
         if (w * 32 < f.heads) {
           const float back = !is_bf16<X>() && !first ? power_of_two(-fits[ni & 1u]) : 1.f;
-          X* dst = static_cast<X*>(p.dq) +
-                   (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + h.z * f.heads + w * 32) * D;
+          const int own = first_head(f, h.z), skip = h.z * f.heads - own;
+          const uint32_t rows = low_bits(f.heads - w * 32) & ~low_bits(max(0, skip - w * 32));
+          X* dst = static_cast<X*>(p.dq) + (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + own + w * 32) * D;
 #pragma unroll 1
           for (int ch = dk ? 0 : D / 64; ch < (dk ? D / 64 : D / 32); ++ch) {
             float o[32];
@@ -667,7 +673,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
 #pragma unroll
               for (int u = 0; u < 32; ++u) o[u] *= back;
             }
-            store_columns<X, D>(o, p.scale, dst + 32 * ch, low_bits(f.heads - w * 32));
+            store_columns<X, D>(o, p.scale, dst + 32 * ch, rows);
           }
         }
         tc_fence_before();
@@ -1099,9 +1105,8 @@ Plan make_plan(const SparseParams& p, int dtype) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   Plan a;
   const bool fp16 = dtype == CSA_F16;
-  a.n_z = 1;
-  while (p.g / a.n_z > kHeads || p.g % a.n_z != 0) ++a.n_z;
-  a.heads = p.g / a.n_z;
+  a.n_z = (p.g + kHeads - 1) / kHeads;
+  a.heads = (p.g + a.n_z - 1) / a.n_z;
   a.s_pad = static_cast<int>((sparse_slots(p) + 127) / 128 * 128);
   const size_t row = static_cast<size_t>(p.Hk) * a.n_z * 2 * a.s_pad * p.D * (fp16 ? 4 : 2);  // bytes of a row's shares
   a.u_bits = 0;

@@ -214,3 +214,11 @@ def test_gradients_of_two_calls_joined_by_lse(K, window, size, nats, Hq, Hk, D, 
         for n, t in zip(("dq", "dk", "dv"), got):
             x = np.abs(f64(t) - val[n]) / (err[n] + 1e-30)
             assert x.max() <= 1, (name, n, float(x.max()))
+
+
+@pytest.mark.parametrize("Hq,Hk,D,dt,K,block", [(65, 1, 128, BF, 20, 2), (134, 2, 64, FP16, 150, 1), (101, 1, 128, FP16, 9, 4),
+                                                (254, 2, 64, BF, 70, 4)])
+def test_gradients_of_odd_groups_of_more_than_64_heads(Hq, Hk, D, dt, K, block):
+    lq, lk = [13, 0, 5], [129, 3, 300]
+    q, k, v, do = _inputs(lq, lk, Hq, Hk, D, dt, seed=42)
+    _run(q, k, v, do, _lists(lq, lk, K, block, seed=20), _cu(lq), _cu(lk), D ** -0.5, block=block, causal=False)
