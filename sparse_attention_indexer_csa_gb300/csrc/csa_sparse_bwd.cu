@@ -657,7 +657,8 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         tc_fence_after();
         ++on;
         if (w * 32 < f.heads) {
-          const float back = !is_bf16<X>() && !first ? power_of_two(-fits[ni & 1u]) : 1.f;
+          float back = p.scale;  // (finite: no inf meets a zero)
+          if (!is_bf16<X>() && !first) back = fminf(back * power_of_two(-fits[ni & 1u]), 0x1.fffffep127f);
           const int own = first_head(f, h.z), skip = h.z * f.heads - own;
           const uint32_t rows = low_bits(f.heads - w * 32) & ~low_bits(max(0, skip - w * 32));
           X* dst = static_cast<X*>(p.dq) + (static_cast<long long>(h.t) * p.Hq + h.hk * p.g + own + w * 32) * D;
@@ -669,11 +670,8 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             if (first) {
 #pragma unroll
               for (int u = 0; u < 32; ++u) o[u] = 0.f;  // no key
-            } else if constexpr (!is_bf16<X>()) {
-#pragma unroll
-              for (int u = 0; u < 32; ++u) o[u] *= back;
             }
-            store_columns<X, D>(o, p.scale, dst + 32 * ch, rows);
+            store_columns<X, D>(o, back, dst + 32 * ch, rows);
           }
         }
         tc_fence_before();
