@@ -268,8 +268,26 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
       if (h.n < 0) break;
       if (h.n > 0 && first) {
         const uint32_t b = ni & 1u, turn = ((ni >> 1) & 1u) ^ 1u;
-        if (!bar_wait(bars + C::kBarQFree + b, turn, ctl)) break;
         const int own = first_head(f, h.z), head = h.hk * p.g + own, skip = h.z * f.heads - own;
+        // on their way while the buffers become free (loaded one behind the other after that, they were what short items
+        // waited for: 4096 rows of 8 x 8 heads of 64, 256 entries each, 1229 us; so 1188)
+        const long long at = static_cast<long long>(h.t) * p.Hq + head;
+        float l[kHeads / 32], de[kHeads / 32], n[kHeads / 32], nq[kHeads / 32], tol[kHeads / 32], range = 0.f;
+#pragma unroll
+        for (int u = 0; u < kHeads / 32; ++u) {
+          const int i = static_cast<int>(lane) + 32 * u;
+          l[u] = -INFINITY;
+          de[u] = n[u] = nq[u] = tol[u] = 0.f;
+          if (i >= skip && i < f.heads) {
+            l[u] = p.lse[at + i];
+            de[u] = f.delta[at + i];
+            n[u] = f.norm_do[at + i];
+            nq[u] = f.norm_q[at + i];
+            if constexpr (ONE) tol[u] = f.tol[at + i];
+          }
+        }
+        if constexpr (!is_bf16<X>()) range = f.range[static_cast<long long>(h.t) * p.Hk + h.hk];
+        if (!bar_wait(bars + C::kBarQFree + b, turn, ctl)) break;
         if (lane == 0) {
           const uint64_t pol = l2_policy_evict_first();
           mbar_arrive_expect_tx(bars + C::kBarQ + b, static_cast<uint32_t>(f.heads) * 256u * (D / 64));
@@ -283,18 +301,19 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
         __syncwarp();
         ++ni;
         if (!bar_wait(bars + C::kBarStatFree + b, turn, ctl)) break;
-        const long long at = static_cast<long long>(h.t) * p.Hq + head;
         float top = 0.f, most = 0.f;  // of |dout|, |delta|
-        for (int i = static_cast<int>(lane); i < f.padded; i += 32) {
-          float4 s = make_float4(INFINITY, 0.f, 0.f, 0.f);  // no head, or a row without a weight: P = 0
-          if (i >= skip && i < f.heads) {
-            const float l = p.lse[at + i], n = f.norm_do[at + i];
-            if (l != -INFINITY) s = make_float4(l * 1.4426950408889634f, f.delta[at + i], n, f.norm_q[at + i]);
-            top = fmaxf(top, n);
-            most = fmaxf(most, fabsf(s.y));
+#pragma unroll
+        for (int u = 0; u < kHeads / 32; ++u) {
+          const int i = static_cast<int>(lane) + 32 * u;
+          if (i < f.padded) {
+            const bool some = l[u] != -INFINITY;  // else no head, or a row without a weight: P = 0
+            if (!some) de[u] = 0.f;
+            stat[b * kHeads + i] = some ? make_float4(l[u] * 1.4426950408889634f, de[u], n[u], nq[u])
+                                        : make_float4(INFINITY, 0.f, 0.f, 0.f);
+            if constexpr (ONE) tols[b * kHeads + i] = tol[u];
+            top = fmaxf(top, n[u]);
+            most = fmaxf(most, fabsf(de[u]));
           }
-          if constexpr (ONE) tols[b * kHeads + i] = i < f.heads ? f.tol[at + i] : 0.f;
-          stat[b * kHeads + i] = s;
         }
         if constexpr (!is_bf16<X>()) {
 #pragma unroll
@@ -302,7 +321,7 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           }
-          const float dp = top * sqrtf(f.range[static_cast<long long>(h.t) * p.Hk + h.hk]);
+          const float dp = top * sqrtf(range);
           if (lane == 0) fits[b] = 15 - exponent_above(dp + fmaxf(dp, most), -60, 60);
         }
         __syncwarp();
