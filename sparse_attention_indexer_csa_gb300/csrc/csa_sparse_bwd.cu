@@ -557,27 +557,25 @@ __global__ void __launch_bounds__(kThreads<TWO>, 1)
               dp[u] = see ? t[u] * dp[u] : 0.f;
             }
             // each step adds half of the heads over half of the lanes; lanes 2 h and 2 h + 1 end with head h
-            auto add_up = [&](float (&x)[16]) {
 #pragma unroll
-              for (int n = 8; n > 0; n >>= 1) {
-                const bool up = (lane & (2u * n)) != 0u;
+            for (int n = 8; n > 0; n >>= 1) {
+              const bool up = (lane & (2u * n)) != 0u;
 #pragma unroll
-                for (int u = 0; u < n; ++u) {
-                  const float give = up ? x[u] : x[u + n], keep = up ? x[u + n] : x[u];
-                  x[u] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
-                }
+              for (int u = 0; u < n; ++u) {
+                const float give = up ? dp[u] : dp[u + n], keep = up ? dp[u + n] : dp[u];
+                const float give2 = up ? t[u] : t[u + n], keep2 = up ? t[u + n] : t[u];
+                dp[u] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * n);
+                t[u] = keep2 + __shfl_xor_sync(0xffffffffu, give2, 2 * n);
               }
-              return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
-            };
-            const float sum = add_up(dp), weight = add_up(t);
-            if ((lane & 1u) == 0u) {
-              sums[warp * kHeads + 16 * i + (lane >> 1)] = sum;
-              sums[(4 + warp) * kHeads + 16 * i + (lane >> 1)] = weight;
             }
+            // (even lanes end with sums of p dP, odd ones with those of p; sums of p by integer reductions took 10 us more)
+            const bool odd = (lane & 1u) != 0u;
+            const float give = odd ? dp[0] : t[0], keep = odd ? t[0] : dp[0];
+            sums[(4 * (lane & 1u) + warp) * kHeads + 16 * i + (lane >> 1)] = keep + __shfl_xor_sync(0xffffffffu, give, 1);
           }
           if (!meet_all()) break;
           if (key < f.heads) {
-            auto all = [&](const float* x) { return (x[0] + x[kHeads]) + (x[2 * kHeads] + x[3 * kHeads]); };
+            auto all = [&](const auto* x) { return (x[0] + x[kHeads]) + (x[2 * kHeads] + x[3 * kHeads]); };
             float4& x = stat[(ni & 1u) * kHeads + key];
             const float sum = all(sums + key), left = fabsf(all(sums + 4 * kHeads + key) - 1.f);
             // the weights add up to 1 within the errors of scores and lse (2^-23 of their size each) and of the sum
