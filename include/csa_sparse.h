@@ -66,14 +66,14 @@ extern "C" {
  * count down to 2^-32 of the largest in out and 2^-39 in dv.
  * Supported: D in {64, 128}, dtype CSA_BF16 or CSA_F16, Hq a multiple of Hk,
  * Hq / Hk <= 128, block a power of two up to 128, window + top_k * block up to
- * 2^20, top_k >= 0 (0: idx is NULL), Tq, Tk, N >= 0; k and v span less than 2^31
+ * 2^20, scale up to 2^127, top_k >= 0 (0: idx is NULL), Tq, Tk, N >= 0; k and v span less than 2^31
  * times the greatest common divisor of their strides.                          */
 typedef struct {
   int32_t N, Tq, Tk, Hq, Hk, D;
   int32_t top_k, block, window;
   int32_t page, table_width; /* page = 0: packed keys, no table */
   int32_t dtype, causal;
-  float scale; /* > 0, finite */
+  float scale; /* > 0, up to 2^127 */
   int64_t idx_stride, table_stride; /* between rows of idx and table (0 = contiguous) */
   int64_t q_stride_t, q_stride_h;
   int64_t k_stride_p, k_stride_t, k_stride_h; /* _p: between pages */

@@ -70,6 +70,7 @@ bool sparse_supported(const csa_sparse_problem* p) {
   if (p->dtype != CSA_BF16 && p->dtype != CSA_F16) return false;
   if (p->Hq / p->Hk > 128 || p->Hq > 65535 || p->block > 128 || (p->block & (p->block - 1)) != 0) return false;
   if (p->window + static_cast<long long>(p->top_k) * p->block > (1 << 20)) return false;
+  if (p->scale > 0x1p127f) return false;  // scale * log2(e) is finite
   GatherRows r;
   if (!gather_rows(p, nullptr, p->k_stride_p, p->k_stride_t, p->k_stride_h, &r)) return false;
   if (!gather_rows(p, nullptr, p->v_stride_p, p->v_stride_t, p->v_stride_h, &r)) return false;
