@@ -131,9 +131,9 @@ csa_status csa_attn_forward(const csa_attn_problem* p, const void* q, const void
 
 /* Gradients for the cotangent dout [Tq,Hq,D] of out, from the out and lse of
  * this call's forward (not of several calls joined by their lse: rows of few keys
- * take dout.out as the sum over their own): dq [Tq,Hq,D], dk, dv [Tk,Hk,D] (dtype, every element; zero where
- * nothing reaches them).  The sums are taken in a fixed order (the same bits
- * on every call).  Needs `workspace`: csa_attn_workspace_size(p, 1) bytes.    */
+ * take dout.out as the sum over their own): dq [Tq,Hq,D], dk, dv [Tk,Hk,D] (dtype,
+ * every element; zero where nothing reaches them).  The sums are taken in a fixed
+ * order (the same bits on every call).  Needs `workspace`: csa_attn_workspace_size(p, 1) bytes.    */
 csa_status csa_attn_backward(const csa_attn_problem* p, const void* dout, const void* q, const void* k,
                              const void* v, const void* out, const float* lse, const int32_t* cu_q,
                              const int32_t* cu_k, const int32_t* k_len, void* dq, void* dk, void* dv,

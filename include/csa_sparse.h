@@ -63,7 +63,8 @@ extern "C" {
  * unit of the last place each.  In bf16 the share of a row in dk and dv of a key is
  * kept with 11 bits (fp16 at a power of two of its own) before the rows' shares
  * are added in fp32; in fp16 it is fp32.  In fp16, weights
- * count down to 2^-32 of the largest in out and 2^-39 in dv.
+ * count down to 2^-32 of the largest in out and 2^-39 in dv; ds' range is set by the
+ * values that the row sees.  Groups of more than 64 heads have two shares.
  * Supported: D in {64, 128}, dtype CSA_BF16 or CSA_F16, Hq a multiple of Hk,
  * Hq / Hk <= 128, block a power of two up to 128, window + top_k * block up to
  * 2^20, scale up to 2^127, top_k >= 0 (0: idx is NULL), Tq, Tk, N >= 0; k and v span less than 2^31

@@ -331,7 +331,8 @@ def attn_forward(q, k, v, cu_q, cu_k, scale, causal=True, k_len=None, workspace=
 
 def attn_backward(dout, q, k, v, out, lse, cu_q, cu_k, scale, causal=True, k_len=None, workspace=None, stream=None):
     """Gradients of attn_forward for the cotangent dout of out (contiguous),
-    from the forward's out and lse -> (dq, dk, dv), contiguous, in q's type."""
+    from this forward's out and lse (not joined with other calls') -> (dq, dk, dv),
+    contiguous, in q's type."""
     dev = _check_attn(q, k, v, cu_q, cu_k, k_len)
     _want(dout, "dout", q.shape, q.dtype, dev)
     _want(out, "out", q.shape, q.dtype, dev)

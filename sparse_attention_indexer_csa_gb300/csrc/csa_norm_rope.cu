@@ -23,7 +23,7 @@
 // rotated in neighbouring pairs, 189 us (6.4 TB/s), gradients 294 us (6.2
 // TB/s).  64 tokens: 4.6 us, a launch.
 // With the append of keys and values to a paged cache (APPEND): 16384 tokens, 120 us
-// (5.6 TB/s; q 81 us and, in a launch of their own, k and v 34), 64 tokens, 8 us.
+// (5.6 TB/s; q 81 us and, in a launch of their own, k and v 34), 64 tokens, 5.7 us.
 //
 // Angles: position * freq modulo 2^64 is the fraction of a turn with 64 bits
 // after the point, exactly what the table says whatever the position; its upper 32
@@ -568,7 +568,7 @@ cudaError_t run(NormRopeParams p, cudaStream_t stream) {
 }
 
 // Blocks of q, of k and of v, in proportion to their rows, in one launch where all
-// of them are on the GPU at once (64 tokens: 8 us).  More rows go in two: q as in
+// of them are on the GPU at once (64 tokens: 5.7 us).  More rows go in two: q as in
 // norm_rope, with three blocks per SM, since the cache's rows take registers that
 // leave room for two (16384 tokens, 64 + 8 heads: 140 us in one launch, 121 in two).
 template <typename X, int G, bool INTER>

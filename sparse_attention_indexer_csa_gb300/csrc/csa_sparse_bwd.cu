@@ -50,7 +50,8 @@
 //
 // fp16: dS is formed times a power of two that brings its bound 2 |dout| max|v| to
 // 2^15 (|dout| over the item's heads, |v| over the finite values of the row's keys), or
-// |dout| max|v| + |delta| where that is larger (out of joined calls), and P^T, at most 1, at 2^15 times its size; both are taken back in fp32.
+// |dout| max|v| + |delta| where that is larger (out of joined calls), and P^T, at most
+// 1, at 2^15 times its size; both are taken back in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -810,7 +811,8 @@ __global__ void __launch_bounds__(256) sparse_value_kernel(const SparseParams p,
   if (lane == 0) norm[w] = n;
 }
 // range[row][key head] = the largest of them over the keys that the row sees: what else its sequence holds does not
-// count.  A warp for a row and four key heads, a lane per slot of its list (4096 rows of 256 keys, 8 heads: 11.5 us, a warp for each head 32).
+// count.  A warp for a row and four key heads, a lane per slot of its list (4096 rows of 256 keys, 8 heads: 11.5 us, a
+// warp for each head 32).
 __global__ void __launch_bounds__(256) sparse_range_kernel(const SparseParams p, const float* norm, float* range) {
   const int parts = (p.Hk + 3) / 4;
   const long long w = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32, t = w / parts;

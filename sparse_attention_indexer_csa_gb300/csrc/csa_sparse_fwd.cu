@@ -4,8 +4,9 @@
 //   p = softmax(s), lse = log sum_j exp(s_j).
 //
 // An item is one query row, one key head and one share of the row's list.  Its
-// g = Hq/Hk query heads are the rows of the products, and the listed keys, 128
-// at a time and packed so that hidden ones take no place, their columns:
+// g = Hq/Hk query heads are the rows of the products, and its list's slots, 128
+// at a time, their columns; a slot that names no visible key keeps its place, reads
+// as zero and weighs nothing:
 //   S = Q . K^T      (A = queries, B = key tile, both in shared memory, to TMEM)
 //   P = 2^(c (S - m) + shift) in the storage type, c = scale log2(e), over S
 //   O += P . V       (A = P in TMEM, B = value tile read MN-major, O in TMEM)
